@@ -70,13 +70,17 @@ enum {
   PA_ERR_WORKSPACE = -4    /* workspace pointer NULL or smaller than required */
 };
 
-enum { PA_F16 = 0, PA_BF16 = 1 };
+/* PA_E4M3: 8-bit cache values (four exponent, three mantissa bits, largest 448), each
+ * standing for itself times its kv head's fp32 scale; only where a call says so.
+ * PA_F32: rotary tables of pa_rotary_append_varlen. */
+enum { PA_F16 = 0, PA_BF16 = 1, PA_E4M3 = 2, PA_F32 = 3 };
 
 /* Codes written to err_word[0] by the kernels. */
 enum {
   PA_DEVERR_PAGE_OOB = 1,    /* block_table entry < 0 or >= num_pages            */
   PA_DEVERR_LENGTH = 2,      /* length < 0, beyond the table, cache or max_seqlen_k */
-  PA_DEVERR_TIMEOUT = 3      /* a pipeline wait exceeded its time limit          */
+  PA_DEVERR_TIMEOUT = 3,     /* a pipeline wait exceeded its time limit          */
+  PA_DEVERR_CAPACITY = 4     /* the page pool or the packed rows do not suffice  */
 };
 
 /* A 4-D cache view.  Paged: [num_pages, page_size, Hkv, D] with stride_b =
@@ -313,6 +317,151 @@ PA_API size_t pa_fwd_varlen_workspace_size(int B, int total_q, int max_seqlen_q,
 PA_API int pa_split_combine(const float* o_partial, const float* lse_partial,
                             const int32_t* splits_per_seq, int S, int B, int Lq, int Hq, int D,
                             void* out, float* lse, int dtype, pa_stream_t stream);
+
+/*
+ * pa_plan_step -- pages, block tables, slots and positions of a step's new
+ * tokens, from the lengths alone, on the GPU (one launch).  The metadata that
+ * vLLM #6052 builds on the host for its single varlen launch: block tables,
+ * cumulative query lengths with repeated entries for padding, and the slots of
+ * the cache write.
+ *
+ * Request b has cache_seqlens[b] tokens in the cache and brings q_lens[b] >= 0
+ * new ones (0: it rests, or is a padding entry).  It needs
+ *   ceil((cached + new) / page_size) - ceil(cached / page_size)
+ * pages of the pool.  Requests are admitted in order while the free pages and
+ * token_capacity suffice; the first one that does not fit and every later one
+ * get no rows in this step and keep their lengths (PA_DEVERR_CAPACITY with the
+ * first one's index and its needed pages).  A request with a negative length,
+ * or more tokens than its table row holds, is left out the same way
+ * (PA_DEVERR_LENGTH) and does not stop those behind it.
+ *
+ *   cache_seqlens, q_lens  int32 [B].
+ *   block_table   int32 [B, >= max_pages] rows of stride bt_stride; the new
+ *                 pages are written behind each request's own, nothing else.
+ *   free_pages    int32 [num_pages], of which the first *free_count are the
+ *                 free pages, a stack: the step's k-th new page (by request,
+ *                 then by position) is free_pages[*free_count - 1 - k].  Not
+ *                 written.
+ *   cu_seqlens_q  int32 [B+1] out: first packed row of each request.
+ *   seqlens_k     int32 [B] out: tokens in the cache after the step's append
+ *                 (pa_fwd_varlen_unified's argument); may be cache_seqlens.
+ *   slot_mapping  int64 [token_capacity] out: page * page_size + place in it
+ *                 of each packed row's token; -1 behind the last row, and for a
+ *                 token whose table entry lies outside the pool
+ *                 (PA_DEVERR_PAGE_OOB with the request and the entry's column).
+ *   positions     int32 [token_capacity] out: the token's position in its
+ *                 sequence; 0 behind the last row.
+ *   free_count_out  int32 [1] out: free pages left; may be free_count.
+ * At most 4096 requests (PA_ERR_UNSUPPORTED).  A *free_count outside
+ * [0, num_pages] is reported (PA_DEVERR_CAPACITY, index -1) and clamped.
+ * err_word[1] is the request, [2] the offending value.  Pages belong to one
+ * request each; two calls on the same pool must be ordered by the caller.
+ */
+PA_API int pa_plan_step(const int32_t* cache_seqlens, const int32_t* q_lens, int B,
+                        int32_t* block_table, int64_t bt_stride, int max_pages, int page_size,
+                        const int32_t* free_pages, const int32_t* free_count, int64_t num_pages,
+                        int32_t* cu_seqlens_q, int32_t* seqlens_k, int64_t* slot_mapping,
+                        int32_t* positions, int token_capacity, int32_t* free_count_out,
+                        int32_t* err_word, pa_stream_t stream);
+
+/*
+ * pa_release_pages -- gives pages back to pa_plan_step's pool (one launch):
+ * those of finished requests (keep_lens[b] == 0) and of requests that take
+ * tokens back, such as rejected speculative ones.
+ *
+ * Request b keeps min(keep_lens[b], cache_seqlens[b]) tokens; its table entries
+ * from ceil(keep / page_size) up to ceil(cached / page_size) are pushed onto
+ * free_pages behind the first *free_count, by request, then by position.
+ *   seqlens_out     int32 [B] out: tokens kept; may be cache_seqlens.
+ *   free_count_out  int32 [1] out; may be free_count.
+ * block_table is not written: entries behind a sequence's pages mean nothing.
+ * A negative or too long cached length and a negative keep_lens[b] leave the
+ * request as it is (PA_DEVERR_LENGTH).  An entry outside the pool is not given
+ * back (PA_DEVERR_PAGE_OOB).  Where the list would hold more than num_pages
+ * pages, the first request that does not fit and every later one stay as they
+ * are (PA_DEVERR_CAPACITY).  Limits as pa_plan_step.
+ */
+PA_API int pa_release_pages(const int32_t* cache_seqlens, const int32_t* keep_lens, int B,
+                            const int32_t* block_table, int64_t bt_stride, int max_pages,
+                            int page_size, int32_t* free_pages, const int32_t* free_count,
+                            int64_t num_pages, int32_t* seqlens_out, int32_t* free_count_out,
+                            int32_t* err_word, pa_stream_t stream);
+
+/*
+ * pa_rotary_append_varlen -- rotary embedding of a ragged batch's new tokens
+ * by positions with one or several axes, and the write of their k and v into
+ * the slots of a paged cache, in 16 bits or as e4m3 (one launch).  The step
+ * before pa_fwd_varlen_unified and pa_fwd_varlen_e4m3, whose chunks must
+ * already be in the cache.
+ *
+ * Token t's pair p (paired as in pa_fwd_kvcache_rotary) turns by row
+ * positions[pair_axis[p]][t] of the tables: c = rotary_cos[row][p].  Images and
+ * video have a position on each axis (time, height, width); text has one.
+ *
+ *   q, k, v       [T, H, D] views, element strides *_st, *_sh (multiples of
+ *                 8), D contiguous, 16-byte aligned; slices of one projection
+ *                 will do.  q may be NULL (k and v only).
+ *   q_out         the rotated q, with its own strides; may be q.
+ *   k_cache, v_cache  paged, of `dtype` or PA_E4M3 (cache_dtype); for PA_E4M3
+ *                 strides are multiples of 16 elements.  Stored is
+ *                 e4m3(x / scale of the kv head), nearest, saturating at
+ *                 +-448; NaN stays NaN.
+ *   k_scale, v_scale  fp32 [Hkv] on the device (PA_E4M3 only); NULL: 1.
+ *   slot_mapping  int64 [T]: page * page_size + place; negative: the token's k
+ *                 and v are not stored.  A slot outside the pool is skipped
+ *                 and reported (PA_DEVERR_PAGE_OOB, token, page).  Two tokens
+ *                 with one slot race.
+ *   positions     int32 [n_axes, T], rows of stride pos_stride; n_axes 1 to 4.
+ *                 A token with a position outside [0, rotary_len) on any axis
+ *                 is not rotated (PA_DEVERR_LENGTH, token, position).
+ *   pair_axis     HOST array of rotary_dim / 2 axis numbers, read before the
+ *                 call returns; NULL: axis 0 for every pair.
+ *   rotary_cos, rotary_sin  [rotary_len, rotary_dim / 2] of `dtype` or PA_F32
+ *                 (rotary_dtype); rotary_cos NULL: nothing is rotated, q is
+ *                 copied.
+ * The rotation is computed in fp32 and rounded once to what is stored.
+ */
+PA_API int pa_rotary_append_varlen(
+    const void* q, int64_t q_st, int64_t q_sh, const void* k, int64_t k_st, int64_t k_sh,
+    const void* v, int64_t v_st, int64_t v_sh, void* q_out, int64_t qo_st, int64_t qo_sh,
+    pa_tensor4 k_cache, pa_tensor4 v_cache, const float* k_scale, const float* v_scale,
+    const int64_t* slot_mapping, int page_size, int64_t num_pages, const int32_t* positions,
+    int64_t pos_stride, int n_axes, const uint8_t* pair_axis, const void* rotary_cos,
+    const void* rotary_sin, int rotary_len, int rotary_dim, int rotary_interleaved,
+    int rotary_dtype, int T, int Hq, int Hkv, int D, int dtype, int cache_dtype,
+    int32_t* err_word, pa_stream_t stream);
+
+/*
+ * pa_fwd_varlen_e4m3 -- pa_fwd_varlen_unified over an e4m3 cache: attention of
+ * a ragged batch of prompt chunks and single tokens over paged 8-bit K and V,
+ * with half the cache's bytes to read.
+ *
+ * Arguments as pa_fwd_varlen_unified, with k_cache and v_cache of e4m3 values
+ * (strides multiples of 16 elements) and
+ *   k_scale, v_scale  fp32 [Hkv] on the device: what a stored value of the kv
+ *                     head is multiplied by; NULL: 1.
+ *   workspace         pa_fwd_varlen_e4m3_workspace_size bytes, 256-byte
+ *                     aligned, always; its contents on entry do not matter.
+ *                     Calls that may overlap on the GPU need one each.
+ * q and out are fp16 or bf16; both products are computed in fp16 with fp32
+ * accumulation (e4m3 is exact in fp16; a bf16 row of q is scaled by a power of
+ * two first), so the result is that of the dequantised cache up to the rounding
+ * of the probabilities to fp16.  Keys that a row does not see have no effect on
+ * it, whatever they hold.  Rows behind cu_seqlens_q[B] are not written.  At most
+ * 4096 entries; more return PA_ERR_UNSUPPORTED.
+ */
+PA_API int pa_fwd_varlen_e4m3(const void* q, int64_t q_st, int64_t q_sh, pa_tensor4 k_cache,
+                              pa_tensor4 v_cache, const float* k_scale, const float* v_scale,
+                              const int32_t* cu_seqlens_q, const int32_t* seqlens_k,
+                              const int32_t* block_table, int64_t bt_stride, int max_pages,
+                              int page_size, int B, int total_q, int max_seqlen_q,
+                              int max_seqlen_k, int Hq, int Hkv, int D, int64_t num_pages,
+                              float scale, int causal, void* out, float* lse, void* workspace,
+                              size_t workspace_bytes, int32_t* err_word, int dtype,
+                              pa_stream_t stream);
+
+PA_API size_t pa_fwd_varlen_e4m3_workspace_size(int B, int total_q, int max_seqlen_q, int Hq,
+                                                int Hkv, int D, int max_seqlen_k);
 
 /* Human-readable text of the last non-OK return on the calling thread. */
 PA_API const char* pa_last_error_string(void);

@@ -1,0 +1,754 @@
+// Attention of a ragged batch over a paged e4m3 cache (sm_103a): single
+// tokens and short query blocks, split over the keys.  The interface is that
+// of the mixed launch of vLLM #6052 "Unify the kernel used in flash attention
+// backend"; the cache holds 8-bit values with a scale for each kv head.
+//
+// Mathematics.  For a query row q (head h of kv head j) over its visible keys
+//   s_t = (scale ks_j) q . K_t,  O = vs_j sum_t e^{s_t - LSE} V_t,
+// computed as one pass with a running reference m (log2 domain) and sum l.
+// e4m3 values are exact in fp16, so both products run on fp16 tensor-core
+// MMAs with fp32 accumulation.  fp16 q is used as it is; a bf16 q row is
+// first scaled by a power of two to a largest magnitude in [1, 2), which
+// leaves every bf16 significand exact and loses only what lies 2^-24 below
+// the row's largest value.  Probabilities are rounded to fp16 (half a unit is
+// 2^-12) as 2^(s - m + 10): the ten powers of two move the smallest normal
+// fp16 probability from 2^-14 to 2^-24 of the row's largest.  m follows the
+// maximum only when it is passed by 2^5, so that p stays below 2^15 and the
+// accumulators are hardly ever rescaled; l sums the unrounded values in fp32.
+//
+// Bound: HBM, 2 D bytes a key and kv head; half of a 16-bit cache's.  A warp
+// takes 16 keys at a time:
+//   copy     cp.async 16 bytes a lane into the warp's own ring of stages --
+//            no producer warp, no barrier: a warp waits for its own copies
+//   S        [16 rows][16 keys] = Q K^T, MMAs m16n8k16, Q in registers.  A
+//            lane's 16 bytes of a key are four MMAs' operands as they stand:
+//            which feature an MMA calls k is free, as long as Q agrees
+//   softmax  in the accumulator fragments, which are PV's operand layout
+//   O        [16 rows][D] += P V: V's operand pairs two keys' bytes (a byte
+//            permute), then the same conversion
+// The 16-byte slots of a stage are permuted so that both reads touch every
+// bank once.
+//
+// Work.  The streams (sequence, kv head, 16-row tile) are laid end to end in
+// units of 16 keys and cut into equal shares, one a CTA; the cut is made on
+// the GPU from the lengths.  A CTA has at most one stream that began earlier
+// and one that goes on, so two partial results a CTA hold every split, and the
+// CTA that finishes a split stream last merges it.
+#include <cuda_fp8.h>
+
+#include <algorithm>
+#include <cmath>
+#include <type_traits>
+
+#include "pa_common.cuh"
+#include "pa_internal.h"
+
+namespace pa {
+int set_error(int code, const char* fmt, ...);
+
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kRows = 16;       // query rows of a tile
+constexpr int kKeys = 16;       // keys of a unit
+constexpr int kStages = 5;      // units in a warp's ring
+constexpr int kMaxB = 4096;
+constexpr float kShift = 10.f;  // log2 of what probabilities are scaled by
+constexpr float kSlack = 5.f;   // log2 of how far they may pass that
+constexpr int kMinShare = 32;   // units
+
+struct AttendParams {
+  const void* q;
+  int64_t q_st, q_sh;
+  const uint8_t *k_cache, *v_cache;
+  int64_t k_sb, k_st, k_sh, v_sb, v_st, v_sh;
+  const float *k_scale, *v_scale;
+  const int32_t *cu_seqlens_q, *seqlens_k, *block_table;
+  int64_t bt_stride, num_pages;
+  int B, total_q, Hq, Hkv, G, max_pages, page_shift, max_seqlen_k, causal;
+  float scale_log2;
+  void* out;
+  float* lse;
+  unsigned long long* words;  // [CTAs] arrivals on the stream that starts in the CTA and goes on
+  float2* part_ml;            // [2 CTAs][16] reference and sum
+  float* part_o;              // [2 CTAs][16][D]
+  int32_t* err;
+};
+
+template <int D>
+struct Layout {
+  static constexpr int kHalf = kKeys * D;                  // bytes of K (or V) in a stage
+  static constexpr int kStage = 2 * kHalf;
+  static constexpr int kRing = kStages * kStage;           // of a warp
+  static constexpr int kOffO = kWarps * kRing;             // float [kWarps][kRows][D]
+  static constexpr int kOffM = kOffO + kWarps * kRows * D * 4;
+  static constexpr int kOffL = kOffM + kWarps * kRows * 4;
+  static constexpr int kOffFlag = kOffL + kWarps * kRows * 4;
+  static constexpr int kOffSums = kOffO;  // long long [kThreads + kWarps], before the first merge
+  static constexpr int kBytes = kOffFlag + 16;
+};
+
+struct Seq {
+  int q0, qlen, lk, units, tiles;  // tiles: 16-row tiles of a kv head
+};
+
+__device__ __forceinline__ Seq load_seq(const AttendParams& p, int b, bool tell) {
+  Seq s{};
+  const int c0 = __ldg(p.cu_seqlens_q + b), c1 = __ldg(p.cu_seqlens_q + b + 1);
+  s.q0 = min(max(c0, 0), p.total_q);
+  s.qlen = min(max(c1, s.q0), p.total_q) - s.q0;
+  if (s.qlen == 0) return s;
+  s.lk = __ldg(p.seqlens_k + b);
+  const long long cap = (long long)(p.max_pages << p.page_shift) * kKeys;
+  if (s.lk < 0 || s.lk > p.max_seqlen_k || s.lk > cap) {
+    if (tell) report(p.err, PA_DEVERR_LENGTH, b, s.lk);
+    s.lk = 0;
+  }
+  s.units = max(1, (s.lk + kKeys - 1) / kKeys);
+  s.tiles = (s.qlen * p.G + kRows - 1) / kRows;
+  return s;
+}
+
+__device__ __forceinline__ long long units_of(const AttendParams& p, const Seq& s) {
+  return (long long)s.units * s.tiles * p.Hkv;
+}
+
+// A position in a CTA's share: one segment (units [u, u + len) of a stream).
+struct Cursor {
+  int b, h, tile, u, len;
+  long long left;  // units of the share from u on
+  Seq s;
+
+  // Units of the segment that hold a key some row of the tile sees.
+  __device__ __forceinline__ int seen(const AttendParams& p) const {
+    if (!p.causal) return len;
+    const int last = min((tile + 1) * kRows, s.qlen * p.G) - 1;
+    const int end = min(s.lk, last / p.G + s.lk - s.qlen + 1);
+    return min(len, max(0, (end + kKeys - 1) / kKeys - u));
+  }
+  __device__ __forceinline__ void next(const AttendParams& p) {
+    left -= len;
+    u = len = 0;
+    if (left <= 0) return;
+    if (++tile == s.tiles) {
+      tile = 0;
+      if (++h == p.Hkv) {
+        h = 0;
+        do {
+          if (++b >= p.B) {  // (lengths that change under the launch)
+            left = 0;
+            return;
+          }
+          s = load_seq(p, b, false);
+        } while (s.units == 0);
+      }
+    }
+    len = (int)min((long long)s.units, left);
+  }
+};
+
+__device__ __forceinline__ uint32_t f16x2_of(uint32_t e4m3x2) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)e4m3x2, __NV_E4M3);
+  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+}
+
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
+  const int n = take ? 16 : 0;  // 0: the slot is filled with zeros, nothing is read
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Byte offset of 16-byte chunk c of row r (a key) in a stage.  D = 128: a row
+// fills all banks; D = 64: two rows do.
+template <int D>
+__device__ __forceinline__ int slot_of(int r, int c) {
+  if constexpr (D == 128) return r * 128 + ((c ^ ((2 * (r & 3)) ^ (r & 4))) << 4);
+  const int line = r >> 1;
+  return line * 128 + (((((r & 1) << 2) | c) ^ (2 * (line & 3))) << 4);
+}
+
+// Key (of 16) of accumulator column j (0, 1) of key tile n (0, 1) in lane
+// group position t.
+template <int D>
+__device__ __forceinline__ int key_of(int n, int j, int t) {
+  return D == 128 ? 8 * n + t + 4 * j : 8 * n + 2 * t + j;
+}
+
+template <int D, typename T>
+__global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_constant__
+                                                                 AttendParams p) {
+  using L = Layout<D>;
+  using E = Elem<T>;
+  constexpr int kQ = D / 16;   // QK^T steps
+  constexpr int kO = D / 8;    // PV column tiles; a lane holds columns [kO 2t, kO 2t + 2 kO)
+  extern __shared__ __align__(128) uint8_t smem[];
+  float* sO = reinterpret_cast<float*>(smem + L::kOffO);
+  float* sM = reinterpret_cast<float*>(smem + L::kOffM);
+  float* sL = reinterpret_cast<float*>(smem + L::kOffL);
+  long long* sSums = reinterpret_cast<long long*>(smem + L::kOffSums);
+  int* sFlag = reinterpret_cast<int*>(smem + L::kOffFlag);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, t = lane & 3;
+
+  // ---- the CTA's share
+  const int per = (p.B + kThreads - 1) / kThreads;
+  long long mine = 0;
+  for (int i = 0; i < per; ++i) {
+    const int b = tid * per + i;
+    if (b < p.B) mine += units_of(p, load_seq(p, b, blockIdx.x == 0));
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) sSums[kThreads + warp] = incl;
+  __syncthreads();
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const long long x = sSums[kThreads + w];
+    if (w < warp) incl += x;
+    total += x;
+  }
+  sSums[tid] = incl;
+  __syncthreads();
+  long long share = (total + gridDim.x - 1) / gridDim.x;
+  share = max((share + kWarps - 1) / kWarps * kWarps, (long long)kMinShare);
+  const long long first = share * blockIdx.x;
+  if (first >= total) return;
+  Cursor at{};
+  {
+    int lo = 0;  // the first thread whose sum passes `first`
+    for (int step = kThreads / 2; step > 0; step >>= 1)
+      if (sSums[lo + step - 1] <= first) lo += step;
+    long long off = first - (lo > 0 ? sSums[lo - 1] : 0);
+    at.b = lo * per;
+    at.s = load_seq(p, at.b, false);
+    while (off >= units_of(p, at.s) && at.b + 1 < p.B) {
+      off -= units_of(p, at.s);
+      at.s = load_seq(p, ++at.b, false);
+    }
+    at.h = (int)(off / ((long long)at.s.units * at.s.tiles));
+    const int rest = (int)(off % ((long long)at.s.units * at.s.tiles));
+    at.tile = rest / at.s.units;
+    at.u = rest % at.s.units;
+    at.left = min(share, total - first);
+    at.len = (int)min((long long)(at.s.units - at.u), at.left);
+  }
+
+  __syncthreads();  // sSums lies where the segments' results go
+
+  // ---- the warp's copies: unit i of a segment, i = warp, warp + 8, ...
+  const uint32_t ring = smem_u32(smem) + warp * L::kRing;
+  Cursor ahead = at;
+  int a_i = warp, a_seen = ahead.seen(p), entry = 0;
+  auto find = [&]() {  // moves to the warp's next unit and reads its table entry
+    while (ahead.left > 0 && a_i >= a_seen) {
+      ahead.next(p);
+      a_i = warp;
+      a_seen = ahead.left > 0 ? ahead.seen(p) : 0;
+    }
+    if (ahead.left > 0)
+      entry = __ldg(p.block_table + (int64_t)ahead.b * p.bt_stride +
+                    ((ahead.u + a_i) >> p.page_shift));
+  };
+  auto copy = [&](int stage) {
+    if (ahead.left > 0) {
+      const int unit = ahead.u + a_i;
+      int page = entry;
+      if (page < 0 || page >= p.num_pages) {
+        if (lane == 0 && unit * kKeys < ahead.s.lk) report(p.err, PA_DEVERR_PAGE_OOB, ahead.b, unit);
+        page = 0;
+      }
+      const int row0 = (unit & ((1 << p.page_shift) - 1)) * kKeys;
+      const uint32_t dst = ring + stage * L::kStage;
+      constexpr int kChunks = D / 16, kRowsAt = 32 / kChunks;
+      const int c = lane % kChunks, r0 = lane / kChunks;
+      const uint8_t* ks = p.k_cache + page * p.k_sb + ahead.h * p.k_sh + (row0 + r0) * p.k_st + c * 16;
+      const uint8_t* vs = p.v_cache + page * p.v_sb + ahead.h * p.v_sh + (row0 + r0) * p.v_st + c * 16;
+      const int valid = ahead.s.lk - unit * kKeys;  // rows of the unit that hold a key
+#pragma unroll
+      for (int i = 0; i < kKeys / kRowsAt; ++i) {
+        const int r = r0 + i * kRowsAt;
+        cp_async16(dst + slot_of<D>(r, c), ks + (int64_t)(i * kRowsAt) * p.k_st, r < valid);
+      }
+#pragma unroll
+      for (int i = 0; i < kKeys / kRowsAt; ++i) {
+        const int r = r0 + i * kRowsAt;
+        cp_async16(dst + L::kHalf + slot_of<D>(r, c), vs + (int64_t)(i * kRowsAt) * p.v_st, r < valid);
+      }
+      a_i += kWarps;
+      find();
+    }
+    cp_commit();  // an empty group where nothing is left keeps the count
+  };
+  find();
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) copy(i);
+  int stage = 0;
+
+  // ---- segments
+  long long stream0 = first - at.u;  // first unit of the segment's stream
+  for (;;) {
+    const int R = min(kRows, at.s.qlen * p.G - at.tile * kRows);
+    const float ks = p.k_scale != nullptr ? __ldg(p.k_scale + at.h) : 1.f;
+    uint32_t qa[kQ][4];
+    float f[2];  // score factor of rows g, g + 8 (log2 domain)
+    int lim[2];  // keys they see
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int r = g + 8 * j;
+      const int row = at.tile * kRows + r;
+      const bool live = r < R;
+      const int i = row / p.G, h = at.h * p.G + row % p.G;
+      lim[j] = p.causal && live ? min(at.s.lk, i + at.s.lk - at.s.qlen + 1) : at.s.lk;
+      const T* src = reinterpret_cast<const T*>(p.q) + (int64_t)(at.s.q0 + (live ? i : 0)) * p.q_st +
+                     (int64_t)(live ? h : 0) * p.q_sh;
+      uint32_t w[D / 64][8];
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (live) x = __ldg(reinterpret_cast<const uint4*>(src + c * 64 + t * 16) + e);
+          w[c][4 * e] = x.x; w[c][4 * e + 1] = x.y; w[c][4 * e + 2] = x.z; w[c][4 * e + 3] = x.w;
+        }
+      f[j] = fabsf(ks) * p.scale_log2;
+      if constexpr (sizeof(T) == 2 && !std::is_same<T, __half>::value) {
+        uint32_t top = 0;  // bits of the largest magnitude
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            top = max(top, max((w[c][e] & 0x7fffu) << 16, w[c][e] & 0x7fff0000u));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int ex = (int)(top >> 23);  // biased exponent
+        // 2^(127 - ex) scales the row to [1, 2) (to [2, 4) at the top of the
+        // range); rows of zeros, of subnormals and rows with an infinity or
+        // NaN stay as they are
+        const bool turn = ex > 0 && ex < 255;
+        const int by = min(ex, 253);
+        const float down = turn ? __uint_as_float((uint32_t)(254 - by) << 23) : 1.f;
+        if (turn) f[j] *= __uint_as_float((uint32_t)by << 23);
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float2 x = E::to_f2(w[c][e]);
+            w[c][e] = Elem<__half>::from_f2(x.x * down, x.y * down);
+          }
+      }
+      const uint32_t flip = ks < 0.f ? 0x80008000u : 0u;
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          qa[c * 4 + e][j] = w[c][2 * e] ^ flip;
+          qa[c * 4 + e][2 + j] = w[c][2 * e + 1] ^ flip;
+        }
+    }
+    // every row of the tile sees the keys below this
+    const int all = p.causal ? max(0, min(at.s.lk, at.tile * kRows / p.G + at.s.lk - at.s.qlen + 1))
+                             : at.s.lk;
+    float o[kO][4];
+#pragma unroll
+    for (int e = 0; e < kO; ++e)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[e][i] = 0.f;
+    float m[2] = {neg_inf(), neg_inf()}, l[2] = {0.f, 0.f};  // m: the reference less kShift
+
+    const int n = at.seen(p);
+    for (int i = warp; i < n; i += kWarps) {
+      cp_wait<kStages - 2>();
+      __syncwarp();  // every lane's copies of the unit; and the last unit's stage is free
+      copy(stage == 0 ? kStages - 1 : stage - 1);
+      const uint8_t* sk = smem + warp * L::kRing + stage * L::kStage;
+      const uint8_t* sv = sk + L::kHalf;
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+      // S
+      float c[2][4];
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c[nt][e] = 0.f;
+        // column g of the tile: the inverse of key_of
+        const int key = D == 128 ? 8 * nt + (g >> 1) + 4 * (g & 1) : 8 * nt + g;
+#pragma unroll
+        for (int hf = 0; hf < D / 64; ++hf) {
+          const uint4 x = *reinterpret_cast<const uint4*>(sk + slot_of<D>(key, hf * 4 + t));
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            mma16816(c[nt], qa[hf * 4 + e], f16x2_of(w[e] & 0xffffu), f16x2_of(w[e] >> 16));
+        }
+      }
+      // softmax
+      const int key0 = (at.u + i) * kKeys;
+      const bool part = key0 + kKeys > all;  // some row does not see all of the unit
+      if (part) {
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (key0 + key_of<D>(nt, e & 1, t) >= lim[e >> 1]) c[nt][e] = neg_inf();
+      }
+      const float top0 = fmaxf(fmaxf(c[0][0], c[0][1]), fmaxf(c[1][0], c[1][1])) * f[0];
+      const float top1 = fmaxf(fmaxf(c[0][2], c[0][3]), fmaxf(c[1][2], c[1][3])) * f[1];
+      if (__any_sync(0xffffffffu, top0 > m[0] + (kShift + kSlack) || top1 > m[1] + (kShift + kSlack))) {
+        float top[2] = {top0, top1};
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], 1));
+          top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], 2));
+          const float to = fmaxf(m[j], top[j] - kShift);
+          const float by = m[j] == to ? 1.f : ex2(m[j] - to);
+          m[j] = to;
+          l[j] *= by;
+#pragma unroll
+          for (int e = 0; e < kO; ++e) {
+            o[e][2 * j] *= by;
+            o[e][2 * j + 1] *= by;
+          }
+        }
+      }
+      // a row that has seen no key yet has the reference -inf: 0 stands in
+      const float m0 = m[0] == neg_inf() ? 0.f : m[0], m1 = m[1] == neg_inf() ? 0.f : m[1];
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        c[nt][0] = ex2(fmaf(c[nt][0], f[0], -m0));
+        c[nt][1] = ex2(fmaf(c[nt][1], f[0], -m0));
+        c[nt][2] = ex2(fmaf(c[nt][2], f[1], -m1));
+        c[nt][3] = ex2(fmaf(c[nt][3], f[1], -m1));
+      }
+      if (part) {  // (a factor of zero turns -inf into NaN)
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (key0 + key_of<D>(nt, e & 1, t) >= lim[e >> 1]) c[nt][e] = 0.f;
+      }
+      l[0] += (c[0][0] + c[0][1]) + (c[1][0] + c[1][1]);
+      l[1] += (c[0][2] + c[0][3]) + (c[1][2] + c[1][3]);
+      const uint32_t pa[4] = {Elem<__half>::from_f2(c[0][0], c[0][1]),
+                              Elem<__half>::from_f2(c[0][2], c[0][3]),
+                              Elem<__half>::from_f2(c[1][0], c[1][1]),
+                              Elem<__half>::from_f2(c[1][2], c[1][3])};
+      // O
+      constexpr int kWords = kO / 4;
+      uint32_t v[4][kWords];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int key = key_of<D>(e >> 1, e & 1, t);
+        if constexpr (D == 128) {
+          const uint4 x = *reinterpret_cast<const uint4*>(sv + slot_of<D>(key, g));
+          v[e][0] = x.x; v[e][1] = x.y; v[e][2] = x.z; v[e][3] = x.w;
+        } else {
+          const uint2 x = *reinterpret_cast<const uint2*>(sv + slot_of<D>(key, g >> 1) + (g & 1) * 8);
+          v[e][0] = x.x; v[e][1] = x.y;
+        }
+      }
+      if (part) {
+        // A NaN in V at a key that only some rows see must not reach the
+        // others through 0 x NaN: it is taken out of the product here and put
+        // into the accumulators of the rows that do see it.
+        uint32_t bad = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int w = 0; w < kWords; ++w)
+            bad |= ((v[e][w] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+        if (__any_sync(0xffffffffu, bad != 0)) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int w = 0; w < kWords; ++w) {
+              const uint32_t hit = (((v[e][w] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;
+              v[e][w] &= ~(hit * 0xffu);
+            }
+          const int end0 = min(lim[0] - key0, kKeys), end1 = min(lim[1] - key0, kKeys);
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf)  // the lane's two runs of columns
+#pragma unroll
+            for (int e = 0; e < kO; ++e) {
+              const int col = (2 * t + hf) * kO + e;
+              for (int key = 0; key < kKeys; ++key) {
+                const uint8_t x = sv[slot_of<D>(key, col >> 4) + (col & 15)];
+                if ((x & 0x7f) != 0x7f) continue;
+                if (key < end0) o[e][hf] = __int_as_float(0x7fffffff);
+                if (key < end1) o[e][2 + hf] = __int_as_float(0x7fffffff);
+              }
+            }
+        }
+      }
+#pragma unroll
+      for (int w = 0; w < kWords; ++w) {
+        const uint32_t x0 = __byte_perm(v[0][w], v[1][w], 0x5140);
+        const uint32_t x1 = __byte_perm(v[2][w], v[3][w], 0x5140);
+        const uint32_t y0 = __byte_perm(v[0][w], v[1][w], 0x7362);
+        const uint32_t y1 = __byte_perm(v[2][w], v[3][w], 0x7362);
+        mma16816(o[4 * w], pa, f16x2_of(x0 & 0xffffu), f16x2_of(x1 & 0xffffu));
+        mma16816(o[4 * w + 1], pa, f16x2_of(x0 >> 16), f16x2_of(x1 >> 16));
+        mma16816(o[4 * w + 2], pa, f16x2_of(y0 & 0xffffu), f16x2_of(y1 & 0xffffu));
+        mma16816(o[4 * w + 3], pa, f16x2_of(y0 >> 16), f16x2_of(y1 >> 16));
+      }
+    }
+
+    // ---- the warps' results: (m, l, O) of each, merged by column
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      l[j] += __shfl_xor_sync(0xffffffffu, l[j], 1);
+      l[j] += __shfl_xor_sync(0xffffffffu, l[j], 2);
+      const int r = g + 8 * j;
+      if (t == 0) {
+        sM[warp * kRows + r] = m[j];
+        sL[warp * kRows + r] = l[j];
+      }
+      if (r < R) {
+        float* dst = sO + (warp * kRows + r) * D;
+#pragma unroll
+        for (int q4 = 0; q4 < kO / 2; ++q4) {  // 16-byte chunks of the lane's 2 kO columns
+          const int hf = q4 / (kO / 4), e = (q4 % (kO / 4)) * 4;
+          const int c = t * (kO / 2) + q4;
+          const int to = c ^ ((r & 1) | ((t << 1) & (D / 32 * 2 - 1)));
+          *reinterpret_cast<float4*>(dst + to * 4) =
+              make_float4(o[e][2 * j + hf], o[e + 1][2 * j + hf], o[e + 2][2 * j + hf],
+                          o[e + 3][2 * j + hf]);
+        }
+      }
+    }
+    __syncthreads();
+    const bool whole = at.u == 0 && at.len == at.s.units;
+    const long long stream1 = stream0 + at.s.units;
+    const int cta0 = (int)(stream0 / share), cta1 = (int)((stream1 - 1) / share);
+    const int slot = 2 * blockIdx.x + (at.u == 0 ? 1 : 0);
+    const float vs = p.v_scale != nullptr ? __ldg(p.v_scale + at.h) : 1.f;
+    constexpr int kChunksO = D / 4;
+    auto write_row = [&](int r, int c, float4 x, float ref, float sum) {
+      const int row = at.tile * kRows + r;
+      const int i = row / p.G, h = at.h * p.G + row % p.G;
+      const float by = sum == 0.f ? 0.f : vs / sum;  // NaN sums stay NaN
+      T* dst = reinterpret_cast<T*>(p.out) + ((int64_t)(at.s.q0 + i) * p.Hq + h) * D + c * 4;
+      uint2 y;
+      y.x = E::from_f2(x.x * by, x.y * by);
+      y.y = E::from_f2(x.z * by, x.w * by);
+      *reinterpret_cast<uint2*>(dst) = y;
+      if (c == 0 && p.lse != nullptr)
+        p.lse[(int64_t)h * p.total_q + at.s.q0 + i] =
+            sum == 0.f ? neg_inf() : (ref + log2f(sum)) * kLn2;
+    };
+    for (int x = tid; x < R * kChunksO; x += kThreads) {
+      const int r = x / kChunksO, c = x % kChunksO;
+      const int from = c ^ ((r & 1) | (((c / (kO / 2)) << 1) & (D / 32 * 2 - 1)));
+      float ref = neg_inf();
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) ref = fmaxf(ref, sM[w * kRows + r]);
+      float sum = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float mw = sM[w * kRows + r];
+        const float by = mw == ref ? 1.f : ex2(mw - ref);
+        const float4 y = *reinterpret_cast<const float4*>(sO + (w * kRows + r) * D + from * 4);
+        sum = fmaf(by, sL[w * kRows + r], sum);
+        acc.x = fmaf(by, y.x, acc.x);
+        acc.y = fmaf(by, y.y, acc.y);
+        acc.z = fmaf(by, y.z, acc.z);
+        acc.w = fmaf(by, y.w, acc.w);
+      }
+      if (whole) {
+        write_row(r, c, acc, ref, sum);
+      } else {
+        *reinterpret_cast<float4*>(p.part_o + ((int64_t)slot * kRows + r) * D + c * 4) = acc;
+        if (c == 0) p.part_ml[slot * kRows + r] = make_float2(ref, sum);
+      }
+    }
+    if (!whole) {
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) *sFlag = arrive_last(p.words + cta0, launch_tag(), cta1 - cta0 + 1) ? 1 : 0;
+      __syncthreads();
+      if (*sFlag) {
+        __threadfence();
+        for (int x = tid; x < R * kChunksO; x += kThreads) {
+          const int r = x / kChunksO, c = x % kChunksO;
+          float ref = neg_inf(), sum = 0.f;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int cta = cta0; cta <= cta1; ++cta) {
+            const int from = 2 * cta + (cta == cta0 ? 1 : 0);
+            const float2 ml = __ldcg(p.part_ml + from * kRows + r);
+            const float4 y = __ldcg(reinterpret_cast<const float4*>(
+                p.part_o + ((int64_t)from * kRows + r) * D + c * 4));
+            const float to = fmaxf(ref, ml.x);
+            const float b0 = ref == to ? 1.f : ex2(ref - to), b1 = ml.x == to ? 1.f : ex2(ml.x - to);
+            ref = to;
+            sum = fmaf(b1, ml.y, sum * b0);
+            acc.x = fmaf(b1, y.x, acc.x * b0);
+            acc.y = fmaf(b1, y.y, acc.y * b0);
+            acc.z = fmaf(b1, y.z, acc.z * b0);
+            acc.w = fmaf(b1, y.w, acc.w * b0);
+          }
+          write_row(r, c, acc, ref, sum);
+        }
+      }
+    }
+    at.next(p);
+    if (at.left <= 0) break;
+    stream0 = stream1;
+    __syncthreads();  // the merge has read what the next segment's overwrites
+  }
+  cp_wait<0>();
+}
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+struct Workspace {
+  size_t ml, o, total;
+};
+Workspace workspace_of(int D) {
+  const size_t ctas = (size_t)num_sms();
+  Workspace w{};
+  w.ml = align256(ctas * 8);
+  w.o = w.ml + align256(ctas * 2 * kRows * 8);
+  w.total = w.o + align256(ctas * 2 * kRows * D * 4);
+  return w;
+}
+
+template <int D, typename T>
+cudaError_t launch(const AttendParams& p, cudaStream_t st) {
+  const int bytes = Layout<D>::kBytes;
+  cudaError_t e = cudaFuncSetAttribute(attend_kernel<D, T>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  attend_kernel<D, T><<<(unsigned)num_sms(), kThreads, bytes, st>>>(p);
+  return cudaGetLastError();
+}
+
+bool aligned16(const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15u) == 0; }
+
+int check_cache8(const pa_tensor4& t, const char* name) {
+  if (t.ptr == nullptr) return set_error(PA_ERR_INVALID_ARG, "%s.ptr is NULL", name);
+  if (!aligned16(t.ptr) || t.stride_b <= 0 || t.stride_t <= 0 || t.stride_h <= 0 ||
+      t.stride_b % 16 != 0 || t.stride_t % 16 != 0 || t.stride_h % 16 != 0)
+    return set_error(PA_ERR_INVALID_ARG,
+                     "%s must be 16-byte aligned with positive strides in multiples of 16 elements",
+                     name);
+  return PA_OK;
+}
+
+}  // namespace
+}  // namespace pa
+
+using namespace pa;
+
+extern "C" {
+
+PA_API size_t pa_fwd_varlen_e4m3_workspace_size(int B, int total_q, int max_seqlen_q, int Hq,
+                                                int Hkv, int D, int max_seqlen_k) {
+  (void)max_seqlen_q;
+  (void)max_seqlen_k;
+  if (B <= 0 || total_q <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0) return 0;
+  return workspace_of(D).total;
+}
+
+PA_API int pa_fwd_varlen_e4m3(const void* q, int64_t q_st, int64_t q_sh, pa_tensor4 k_cache,
+                              pa_tensor4 v_cache, const float* k_scale, const float* v_scale,
+                              const int32_t* cu_seqlens_q, const int32_t* seqlens_k,
+                              const int32_t* block_table, int64_t bt_stride, int max_pages,
+                              int page_size, int B, int total_q, int max_seqlen_q,
+                              int max_seqlen_k, int Hq, int Hkv, int D, int64_t num_pages,
+                              float scale, int causal, void* out, float* lse, void* workspace,
+                              size_t workspace_bytes, int32_t* err_word, int dtype,
+                              pa_stream_t stream) {
+  if (dtype != PA_F16 && dtype != PA_BF16) return set_error(PA_ERR_UNSUPPORTED, "dtype %d", dtype);
+  if (D != 64 && D != 128) return set_error(PA_ERR_UNSUPPORTED, "head_dim %d (64 or 128)", D);
+  if (Hq < 1 || Hkv < 1) return set_error(PA_ERR_INVALID_ARG, "head counts must be >= 1");
+  if (Hq % Hkv != 0)
+    return set_error(PA_ERR_UNSUPPORTED, "Hq %d not a multiple of Hkv %d", Hq, Hkv);
+  if (B < 0 || total_q < 0 || max_seqlen_q < 0 || max_seqlen_k < 0)
+    return set_error(PA_ERR_INVALID_ARG, "negative size argument");
+  if (B == 0 || total_q == 0) return PA_OK;
+  if (B > kMaxB) return set_error(PA_ERR_UNSUPPORTED, "more than %d sequences", kMaxB);
+  int rc = 0;
+  if ((rc = check_cache8(k_cache, "k_cache")) || (rc = check_cache8(v_cache, "v_cache"))) return rc;
+  if (q == nullptr || out == nullptr || cu_seqlens_q == nullptr || seqlens_k == nullptr ||
+      block_table == nullptr)
+    return set_error(PA_ERR_INVALID_ARG,
+                     "q, out, cu_seqlens_q, seqlens_k and block_table must be non-NULL");
+  if (!aligned16(q) || !aligned16(out))
+    return set_error(PA_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
+  if (q_st <= 0 || q_sh <= 0 || q_st % 8 != 0 || q_sh % 8 != 0)
+    return set_error(PA_ERR_INVALID_ARG, "q strides must be positive multiples of 8 elements");
+  if (max_pages < 1 || bt_stride < max_pages || num_pages < 1)
+    return set_error(PA_ERR_INVALID_ARG, "block table / pool sizes");
+  if (!(scale > 0.f) || !std::isfinite(scale))
+    return set_error(PA_ERR_INVALID_ARG, "scale must be finite and > 0");
+  AttendParams p{};
+  p.page_shift = -1;
+  for (int s = 0; s <= 4; ++s)
+    if (page_size == kPage << s) p.page_shift = s;
+  if (p.page_shift < 0)
+    return set_error(PA_ERR_UNSUPPORTED, "page_size must be 16, 32, 64, 128 or 256");
+  if ((long long)max_pages * page_size > 0x7fffffff)
+    return set_error(PA_ERR_UNSUPPORTED, "a block table row must hold fewer than 2^31 tokens");
+  const Workspace ws = workspace_of(D);
+  if (workspace == nullptr || workspace_bytes < ws.total)
+    return set_error(PA_ERR_WORKSPACE, "workspace of %zu bytes required (got %zu)", ws.total,
+                     workspace_bytes);
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return set_error(PA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  uint8_t* wsb = reinterpret_cast<uint8_t*>(workspace);
+  p.q = q;
+  p.q_st = q_st; p.q_sh = q_sh;
+  p.k_cache = reinterpret_cast<const uint8_t*>(k_cache.ptr);
+  p.v_cache = reinterpret_cast<const uint8_t*>(v_cache.ptr);
+  p.k_sb = k_cache.stride_b; p.k_st = k_cache.stride_t; p.k_sh = k_cache.stride_h;
+  p.v_sb = v_cache.stride_b; p.v_st = v_cache.stride_t; p.v_sh = v_cache.stride_h;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.cu_seqlens_q = cu_seqlens_q;
+  p.seqlens_k = seqlens_k;
+  p.block_table = block_table;
+  p.bt_stride = bt_stride;
+  p.num_pages = num_pages;
+  p.B = B;
+  p.total_q = total_q;
+  p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv;
+  p.max_pages = max_pages;
+  p.max_seqlen_k = max_seqlen_k;
+  p.causal = causal ? 1 : 0;
+  p.scale_log2 = scale * kLog2e;
+  p.out = out;
+  p.lse = lse;
+  p.words = reinterpret_cast<unsigned long long*>(wsb);
+  p.part_ml = reinterpret_cast<float2*>(wsb + ws.ml);
+  p.part_o = reinterpret_cast<float*>(wsb + ws.o);
+  p.err = err_word;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (dtype == PA_F16)
+    e = D == 128 ? launch<128, __half>(p, st) : launch<64, __half>(p, st);
+  else
+    e = D == 128 ? launch<128, __nv_bfloat16>(p, st) : launch<64, __nv_bfloat16>(p, st);
+  if (e != cudaSuccess) return set_error(PA_ERR_CUDA, "attend launch: %s", cudaGetErrorString(e));
+  return PA_OK;
+}
+
+}  // extern "C"

@@ -245,6 +245,62 @@ __device__ __forceinline__ PageRef resolve_page(const CacheGeom& g, int b, int l
   return r;
 }
 
+// ---------------------------------------------------------------- split merge
+// The splits of a stream (one sequence, one kv head) are merged by the CTA
+// that finishes last, inside this launch: no combine kernel and no state
+// that has to start at zero.  Each stream has a 64-bit arrival word in the
+// workspace holding (launch tag, count).  The launch tag is %gridid, a per-
+// context launch number that every CTA of a grid reads alike, so a word
+// holding arbitrary bytes or left by another launch counts as zero
+// arrivals.  Replays of one CUDA graph may share a tag, so the arrival that
+// completes a stream also resets its word to (tag, 0): every completed call
+// leaves the words it used at zero arrivals for a replay.  The 48 low bits
+// of %gridid are the tag; 16 bits count up to the split count.  No CTA
+// waits on another: an arrival's compare-and-swap loop repeats only when
+// another arrival changed the word, so it ends after at most as many rounds
+// as there are splits.
+__device__ __forceinline__ unsigned long long launch_tag() {
+  unsigned long long id;
+  asm volatile("mov.u64 %0, %%gridid;" : "=l"(id));
+  return id & 0xffffffffffffull;
+}
+
+// One arrival on `word` for this launch; true for the arrival that makes
+// `nb` of them, which leaves the word at (tag, 0).  The common case is one
+// atomic add: a word that already carries this launch's tag counts the
+// arrival.  An add that finds another tag (the first arrival after another
+// launch, or bytes never written) went to a stale value; that arrival then
+// installs (tag, 1) by compare-and-swap, unless another arrival of this
+// launch has installed the tag meanwhile, in which case it adds itself to
+// the installed count.  Every arrival is counted exactly once: by the one
+// successful installation or by an add to a tagged word.
+__device__ __forceinline__ bool arrive_last(unsigned long long* word, unsigned long long tag,
+                                            int nb) {
+  const unsigned long long mine = tag << 16;
+  const unsigned long long old = atomicAdd(word, 1ull);
+  unsigned long long cnt;
+  if ((old >> 16) == tag) {
+    cnt = (old & 0xffffull) + 1ull;
+  } else {
+    unsigned long long cur = old + 1ull;
+    for (;;) {
+      const unsigned long long prev = atomicCAS(word, cur, mine | 1ull);
+      if (prev == cur) {
+        cnt = 1ull;
+        break;
+      }
+      if ((prev >> 16) == tag) {
+        cnt = (atomicAdd(word, 1ull) & 0xffffull) + 1ull;
+        break;
+      }
+      cur = prev;
+    }
+  }
+  if (cnt < (unsigned long long)nb) return false;
+  atomicExch(word, mine);
+  return true;
+}
+
 // ---------------------------------------------------------------- split-KV schedule
 // Pages per split when a sequence of `pages` pages is cut into splits of at
 // most `chunk` pages (rounded up to 4 pages, at most s_max splits); writes
