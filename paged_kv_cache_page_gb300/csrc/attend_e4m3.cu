@@ -34,14 +34,11 @@
 // the GPU from the lengths.  A CTA has at most one stream that began earlier
 // and one that goes on, so two partial results a CTA hold every split, and the
 // CTA that finishes a split stream last merges it.
-#include <cuda_fp8.h>
-
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
 
-#include "pa_common.cuh"
-#include "pa_internal.h"
+#include "attend_e4m3.cuh"
 
 namespace pa {
 int set_error(int code, const char* fmt, ...);
@@ -54,27 +51,11 @@ constexpr int kRows = 16;       // query rows of a tile
 constexpr int kKeys = 16;       // keys of a unit
 constexpr int kStages = 5;      // units in a warp's ring
 constexpr int kMaxB = 4096;
-constexpr float kShift = 10.f;  // log2 of what probabilities are scaled by
-constexpr float kSlack = 5.f;   // log2 of how far they may pass that
+constexpr float kShift = kE4m3Shift, kSlack = kE4m3Slack;
 constexpr int kMinShare = 32;   // units
-
-struct AttendParams {
-  const void* q;
-  int64_t q_st, q_sh;
-  const uint8_t *k_cache, *v_cache;
-  int64_t k_sb, k_st, k_sh, v_sb, v_st, v_sh;
-  const float *k_scale, *v_scale;
-  const int32_t *cu_seqlens_q, *seqlens_k, *block_table;
-  int64_t bt_stride, num_pages;
-  int B, total_q, Hq, Hkv, G, max_pages, page_shift, max_seqlen_k, causal;
-  float scale_log2;
-  void* out;
-  float* lse;
-  unsigned long long* words;  // [CTAs] arrivals on the stream that starts in the CTA and goes on
-  float2* part_ml;            // [2 CTAs][16] reference and sum
-  float* part_o;              // [2 CTAs][16][D]
-  int32_t* err;
-};
+// Rows per kv head up to which a sequence runs here; longer query blocks fill
+// the 128-row tiles of the tcgen05 kernel.
+constexpr int kSmallRows = 64;
 
 template <int D>
 struct Layout {
@@ -94,17 +75,10 @@ struct Seq {
 };
 
 __device__ __forceinline__ Seq load_seq(const AttendParams& p, int b, bool tell) {
-  Seq s{};
-  const int c0 = __ldg(p.cu_seqlens_q + b), c1 = __ldg(p.cu_seqlens_q + b + 1);
-  s.q0 = min(max(c0, 0), p.total_q);
-  s.qlen = min(max(c1, s.q0), p.total_q) - s.q0;
+  const SeqRows r = seq_rows(p, b, tell);
+  Seq s{r.q0, r.qlen, r.lk, 0, 0};
+  if ((long long)s.qlen * p.G > p.small_rows) s.qlen = 0;  // not this kernel's
   if (s.qlen == 0) return s;
-  s.lk = __ldg(p.seqlens_k + b);
-  const long long cap = (long long)(p.max_pages << p.page_shift) * kKeys;
-  if (s.lk < 0 || s.lk > p.max_seqlen_k || s.lk > cap) {
-    if (tell) report(p.err, PA_DEVERR_LENGTH, b, s.lk);
-    s.lk = 0;
-  }
   s.units = max(1, (s.lk + kKeys - 1) / kKeys);
   s.tiles = (s.qlen * p.G + kRows - 1) / kRows;
   return s;
@@ -147,11 +121,6 @@ struct Cursor {
     len = (int)min((long long)s.units, left);
   }
 };
-
-__device__ __forceinline__ uint32_t f16x2_of(uint32_t e4m3x2) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)e4m3x2, __NV_E4M3);
-  return (uint32_t)h.x | ((uint32_t)h.y << 16);
-}
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
@@ -232,7 +201,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   long long share = (total + gridDim.x - 1) / gridDim.x;
   share = max((share + kWarps - 1) / kWarps * kWarps, (long long)kMinShare);
   const long long first = share * blockIdx.x;
-  if (first >= total) return;
+  if (first >= total) {
+    griddep_wait();
+    return;
+  }
   Cursor at{};
   {
     int lo = 0;  // the first thread whose sum passes `first`
@@ -474,14 +446,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         for (int e = 0; e < 4; ++e)
 #pragma unroll
           for (int w = 0; w < kWords; ++w)
-            bad |= ((v[e][w] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+            bad |= nan_bytes(v[e][w]);
         if (__any_sync(0xffffffffu, bad != 0)) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
 #pragma unroll
             for (int w = 0; w < kWords; ++w) {
-              const uint32_t hit = (((v[e][w] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;
-              v[e][w] &= ~(hit * 0xffu);
+              v[e][w] &= ~((nan_bytes(v[e][w]) >> 7) * 0xffu);
             }
           const int end0 = min(lim[0] - key0, kKeys), end1 = min(lim[1] - key0, kKeys);
 #pragma unroll
@@ -615,30 +586,55 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     __syncthreads();  // the merge has read what the next segment's overwrites
   }
   cp_wait<0>();
+  // Launched behind the chunks' kernel this one may start before that one
+  // ends; it must not end before it, for the stream's next kernel waits for
+  // this one alone.
+  griddep_wait();
 }
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct Workspace {
-  size_t ml, o, total;
+  size_t ml, o, chunk_words, chunk_ml, chunk_o, total;
 };
-Workspace workspace_of(int D) {
+Workspace workspace_of(int D, bool chunks) {
   const size_t ctas = (size_t)num_sms();
   Workspace w{};
   w.ml = align256(ctas * 8);
   w.o = w.ml + align256(ctas * 2 * kRows * 8);
   w.total = w.o + align256(ctas * 2 * kRows * D * 4);
+  if (chunks) {
+    w.chunk_words = w.total;
+    w.chunk_ml = w.chunk_words + align256(ctas * 8);
+    w.chunk_o = w.chunk_ml + align256(ctas * 2 * kChunkRows * 8);
+    w.total = w.chunk_o + align256(ctas * 2 * kChunkRows * D * 4);
+  }
   return w;
 }
 
 template <int D, typename T>
-cudaError_t launch(const AttendParams& p, cudaStream_t st) {
+cudaError_t launch(const AttendParams& p, bool dependent, cudaStream_t st) {
   const int bytes = Layout<D>::kBytes;
   cudaError_t e = cudaFuncSetAttribute(attend_kernel<D, T>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  attend_kernel<D, T><<<(unsigned)num_sms(), kThreads, bytes, st>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)num_sms());
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)bytes;
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = dependent ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, attend_kernel<D, T>, p);
+}
+
+// Whether a sequence of the call may have more rows per kv head than the
+// warp-level kernel takes.
+bool has_chunks(int max_seqlen_q, int Hq, int Hkv) {
+  return (long long)max_seqlen_q * (Hq / Hkv) > kSmallRows;
 }
 
 bool aligned16(const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15u) == 0; }
@@ -662,10 +658,9 @@ extern "C" {
 
 PA_API size_t pa_fwd_varlen_e4m3_workspace_size(int B, int total_q, int max_seqlen_q, int Hq,
                                                 int Hkv, int D, int max_seqlen_k) {
-  (void)max_seqlen_q;
   (void)max_seqlen_k;
   if (B <= 0 || total_q <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0) return 0;
-  return workspace_of(D).total;
+  return workspace_of(D, has_chunks(max_seqlen_q, Hq, Hkv)).total;
 }
 
 PA_API int pa_fwd_varlen_e4m3(const void* q, int64_t q_st, int64_t q_sh, pa_tensor4 k_cache,
@@ -698,6 +693,8 @@ PA_API int pa_fwd_varlen_e4m3(const void* q, int64_t q_st, int64_t q_sh, pa_tens
     return set_error(PA_ERR_INVALID_ARG, "q strides must be positive multiples of 8 elements");
   if (max_pages < 1 || bt_stride < max_pages || num_pages < 1)
     return set_error(PA_ERR_INVALID_ARG, "block table / pool sizes");
+  if ((long long)total_q * (Hq / Hkv) > 0x7fffffff)
+    return set_error(PA_ERR_UNSUPPORTED, "total_q * Hq / Hkv must be below 2^31");
   if (!(scale > 0.f) || !std::isfinite(scale))
     return set_error(PA_ERR_INVALID_ARG, "scale must be finite and > 0");
   AttendParams p{};
@@ -708,7 +705,8 @@ PA_API int pa_fwd_varlen_e4m3(const void* q, int64_t q_st, int64_t q_sh, pa_tens
     return set_error(PA_ERR_UNSUPPORTED, "page_size must be 16, 32, 64, 128 or 256");
   if ((long long)max_pages * page_size > 0x7fffffff)
     return set_error(PA_ERR_UNSUPPORTED, "a block table row must hold fewer than 2^31 tokens");
-  const Workspace ws = workspace_of(D);
+  const bool chunks = has_chunks(max_seqlen_q, Hq, Hkv);
+  const Workspace ws = workspace_of(D, chunks);
   if (workspace == nullptr || workspace_bytes < ws.total)
     return set_error(PA_ERR_WORKSPACE, "workspace of %zu bytes required (got %zu)", ws.total,
                      workspace_bytes);
@@ -737,16 +735,27 @@ PA_API int pa_fwd_varlen_e4m3(const void* q, int64_t q_st, int64_t q_sh, pa_tens
   p.scale_log2 = scale * kLog2e;
   p.out = out;
   p.lse = lse;
+  p.err = err_word;
+  // sequences of more rows than max_seqlen_q said run on the warp-level kernel
+  p.small_rows = chunks ? kSmallRows : 0x7fffffff;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (chunks) {
+    p.words = reinterpret_cast<unsigned long long*>(wsb + ws.chunk_words);
+    p.part_ml = reinterpret_cast<float2*>(wsb + ws.chunk_ml);
+    p.part_o = reinterpret_cast<float*>(wsb + ws.chunk_o);
+    e = launch_chunks_e4m3(p, D, dtype, st);
+    if (e != cudaSuccess)
+      return set_error(PA_ERR_CUDA, "chunk launch: %s", cudaGetErrorString(e));
+  }
   p.words = reinterpret_cast<unsigned long long*>(wsb);
   p.part_ml = reinterpret_cast<float2*>(wsb + ws.ml);
   p.part_o = reinterpret_cast<float*>(wsb + ws.o);
-  p.err = err_word;
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e;
   if (dtype == PA_F16)
-    e = D == 128 ? launch<128, __half>(p, st) : launch<64, __half>(p, st);
+    e = D == 128 ? launch<128, __half>(p, chunks, st) : launch<64, __half>(p, chunks, st);
   else
-    e = D == 128 ? launch<128, __nv_bfloat16>(p, st) : launch<64, __nv_bfloat16>(p, st);
+    e = D == 128 ? launch<128, __nv_bfloat16>(p, chunks, st)
+                 : launch<64, __nv_bfloat16>(p, chunks, st);
   if (e != cudaSuccess) return set_error(PA_ERR_CUDA, "attend launch: %s", cudaGetErrorString(e));
   return PA_OK;
 }

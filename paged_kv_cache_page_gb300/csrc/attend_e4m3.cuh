@@ -1,0 +1,73 @@
+// Shared by the two kernels of pa_fwd_varlen_e4m3: parameters, the sequences
+// of a ragged batch, and the conversion of e4m3 values.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "pa_common.cuh"
+#include "pa_internal.h"
+
+namespace pa {
+
+constexpr float kE4m3Shift = 10.f;  // log2 of what probabilities are scaled by
+constexpr float kE4m3Slack = 5.f;   // log2 of how far they may pass that
+
+struct AttendParams {
+  const void* q;
+  int64_t q_st, q_sh;
+  const uint8_t *k_cache, *v_cache;
+  int64_t k_sb, k_st, k_sh, v_sb, v_st, v_sh;
+  const float *k_scale, *v_scale;
+  const int32_t *cu_seqlens_q, *seqlens_k, *block_table;
+  int64_t bt_stride, num_pages;
+  int B, total_q, Hq, Hkv, G, max_pages, page_shift, max_seqlen_k, causal;
+  int small_rows;  // sequences of at most this many rows per kv head run on the warp-level kernel
+  float scale_log2;
+  void* out;
+  float* lse;
+  // Split results: two a CTA, one of the stream that began before its share
+  // and one of the stream that goes on behind it.
+  unsigned long long* words;  // [CTAs] arrivals on the stream that starts in the CTA and goes on
+  float2* part_ml;            // reference and sum of each row
+  float* part_o;
+  int32_t* err;
+};
+
+struct SeqRows {
+  int q0, qlen, lk;
+};
+
+// The rows and keys of sequence b: offsets kept within the packed rows, a
+// length that the table or max_seqlen_k does not hold run as 0.
+__device__ __forceinline__ SeqRows seq_rows(const AttendParams& p, int b, bool tell) {
+  SeqRows s{};
+  const int c0 = __ldg(p.cu_seqlens_q + b), c1 = __ldg(p.cu_seqlens_q + b + 1);
+  s.q0 = min(max(c0, 0), p.total_q);
+  s.qlen = min(max(c1, s.q0), p.total_q) - s.q0;
+  if (s.qlen == 0) return s;
+  s.lk = __ldg(p.seqlens_k + b);
+  const long long cap = (long long)p.max_pages * (kPage << p.page_shift);
+  if (s.lk < 0 || s.lk > p.max_seqlen_k || s.lk > cap) {
+    if (tell) report(p.err, PA_DEVERR_LENGTH, b, s.lk);
+    s.lk = 0;
+  }
+  return s;
+}
+
+// Two e4m3 values (the low byte first) as two fp16 values.
+__device__ __forceinline__ uint32_t f16x2_of(uint32_t e4m3x2) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)e4m3x2, __NV_E4M3);
+  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+}
+// The sign bits (moved to bit 7) of the NaN bytes among four e4m3 values.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
+  return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+
+// The attention of sequences of more than small_rows rows per kv head
+// (chunk_e4m3.cu).
+cudaError_t launch_chunks_e4m3(const AttendParams& p, int D, int dtype, cudaStream_t st);
+constexpr int kChunkRows = 256;  // rows of its pair of query tiles: part_ml [2 CTAs][256],
+                                 // part_o [2 CTAs][2 tiles][D / 4][128][4]
+
+}  // namespace pa

@@ -1,0 +1,740 @@
+// Attention of prompt chunks over a paged e4m3 cache on the 5th-generation
+// tensor cores (sm_103a): sequences of more query rows per kv head than the
+// warp-level kernel (attend_e4m3.cu) takes.
+//
+// Mathematics as there: both products in fp16 with fp32 accumulation, e4m3
+// being exact in fp16.  The rows of a tile are packed over the heads of a kv
+// head, row i G + g of a sequence, so that all 256 rows of a CTA's two tiles
+// share every K and V tile and its conversion.
+//
+// Bound: the tensor cores and the exponentials, 4 D operations and one
+// exponential a visible (row, key) pair.  Warps:
+//   0-7    softmax: one thread a row, group g = warp / 4 takes tile g
+//   8-11   converters: the pair's Q (a bf16 row scaled by a power of two), then
+//          K and V tiles in turn -- 16 bytes a load from the pages, two fp16
+//          chunks a store into the 128-byte-swizzled operand tile -- into a
+//          ring of fp16 tiles K0 V0 K1 V1 ...
+//   12     S_g = Q_g K^T          13  O_g += P_g V (P_g from TMEM over S_g)
+// TMEM: S_0, S_1, O_0, O_1.  While one group's softmax runs, the tensor core
+// works on the other group.  The registers are dealt by setmaxnreg: 184 for
+// the softmax threads, 88 for the converters, 56 for the issuers, in all what
+// the block was launched with (512 x 128).
+//
+// Work: the streams (sequence, kv head, pair of tiles) laid end to end in
+// 128-key tiles, as many as the pair's last row sees, and cut into equal
+// shares, one a CTA, as in the warp-level kernel; split streams are joined by
+// the CTA that finishes last.
+#include <algorithm>
+#include <type_traits>
+
+#include "attend_e4m3.cuh"
+#include "pa_tcgen05.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kM = 128;          // rows of a query tile
+constexpr int kN = 128;          // keys of a tile
+constexpr int kUnits = kN / kPage;
+constexpr int kWarpConv = 8, kWarpQK = 12, kWarpPV = 13;
+constexpr int kThreads = 512;
+constexpr int kMinShare = 4;     // tiles
+
+template <int D>
+struct Layout {
+  static constexpr int kHalves = D / 64;          // 64-column slabs of a row
+  static constexpr int kSlab = 128 * 128;         // 128 rows x 128 bytes
+  static constexpr int kTile = kHalves * kSlab;   // a fp16 operand tile
+  static constexpr int kRing = D == 128 ? 4 : 8;  // K and V tiles in the ring
+  static constexpr int kOffQ = 0;                 // [2]
+  static constexpr int kOffKV = 2 * kTile;
+  static constexpr int kOffF = kOffKV + kRing * kTile;      // float [256] factor of a row's scores
+  static constexpr int kOffNan = kOffF + kChunkRows * 4;    // int [kRing][4]
+  static constexpr int kOffBar = kOffNan + kRing * 16;
+  // q_full, q_empty, f_empty; full, empty [kRing]; s_full, p_full, pv_done, o_free [2]
+  static constexpr int kBars = 3 + 2 * kRing + 8;
+  static constexpr int kOffMisc = kOffBar + kBars * 8;      // TMEM base, merge flag
+  static constexpr int kOffSums = kOffKV;                   // long long [kThreads + 16], prologue
+  static constexpr int kBytes = kOffMisc + 16 + 1024;
+  static_assert(kBytes <= 232448, "shared memory");
+};
+
+struct Stream {  // a sequence with rows of this kernel's, and its share of tiles
+  SeqRows s;
+  int rows;      // qlen * G, 0: not this kernel's
+  int pairs;
+};
+
+__device__ __forceinline__ Stream load_stream(const AttendParams& p, int b, bool tell) {
+  Stream x{seq_rows(p, b, tell), 0, 0};
+  const long long rows = (long long)x.s.qlen * p.G;
+  if (rows > p.small_rows) {
+    x.rows = (int)rows;
+    x.pairs = (x.rows + kChunkRows - 1) / kChunkRows;
+  }
+  return x;
+}
+
+// Keys that row `row` of the sequence sees.
+__device__ __forceinline__ int seen(const AttendParams& p, const Stream& x, int row) {
+  return p.causal ? max(0, min(x.s.lk, row / p.G + x.s.lk - x.s.qlen + 1)) : x.s.lk;
+}
+// Key tiles of rows [row0, row0 + n) of the sequence.
+__device__ __forceinline__ int tiles_of(const AttendParams& p, const Stream& x, int row0, int n) {
+  const int last = min(row0 + n, x.rows) - 1;
+  return last < row0 ? 0 : (seen(p, x, last) + kN - 1) / kN;
+}
+__device__ __forceinline__ int pair_tiles(const AttendParams& p, const Stream& x, int pair) {
+  return max(1, tiles_of(p, x, pair * kChunkRows, kChunkRows));
+}
+__device__ __forceinline__ long long head_tiles(const AttendParams& p, const Stream& x) {
+  long long n = 0;
+  for (int i = 0; i < x.pairs; ++i) n += pair_tiles(p, x, i);
+  return n;
+}
+
+// A segment of a CTA's share: tiles [t0, t0 + n) of a stream.
+struct Walk {
+  int b, h, pair, t0, n, all;  // all: tiles of the stream
+  long long left;              // tiles of the share from t0 on
+  long long begin;             // first tile of the stream, counted over all streams
+  Stream x;
+
+  __device__ __forceinline__ int rows0() const { return pair * kChunkRows; }
+  // End of the tiles that group g has work in.
+  __device__ __forceinline__ int group_end(const AttendParams& p, int g) const {
+    return min(t0 + n, tiles_of(p, x, rows0() + g * kM, kM));
+  }
+  __device__ __forceinline__ void next(const AttendParams& p) {
+    left -= n;
+    begin += all;
+    t0 = n = 0;
+    if (left <= 0) return;
+    if (++pair == x.pairs) {
+      pair = 0;
+      if (++h == p.Hkv) {
+        h = 0;
+        do {
+          if (++b >= p.B) {  // (lengths that change under the launch)
+            left = 0;
+            return;
+          }
+          x = load_stream(p, b, false);
+        } while (x.rows == 0);
+      }
+    }
+    all = pair_tiles(p, x, pair);
+    n = (int)min((long long)all, left);
+  }
+};
+
+template <int R>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+
+template <int D, typename T>
+__global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constant__
+                                                                AttendParams p) {
+  using L = Layout<D>;
+  using E = Elem<T>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint8_t* sQ = smem + L::kOffQ;
+  uint8_t* sKV = smem + L::kOffKV;
+  float* sF = reinterpret_cast<float*>(smem + L::kOffF);
+  int* sNan = reinterpret_cast<int*>(smem + L::kOffNan);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
+  uint64_t* q_full = bars;
+  uint64_t* q_empty = bars + 1;
+  uint64_t* f_empty = bars + 2;
+  uint64_t* full = bars + 3;
+  uint64_t* empty = full + L::kRing;
+  uint64_t* s_full = empty + L::kRing;
+  uint64_t* p_full = s_full + 2;
+  uint64_t* pv_done = p_full + 2;
+  uint64_t* o_free = pv_done + 2;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
+  int* sFlag = reinterpret_cast<int*>(smem + L::kOffMisc) + 1;
+  long long* sSums = reinterpret_cast<long long*>(smem + L::kOffSums);
+
+  griddep_launch_dependents();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    mbar_init(q_full, 4);
+    mbar_init(q_empty, 1);
+    mbar_init(f_empty, 8);
+    for (int i = 0; i < L::kRing; ++i) {
+      mbar_init(&full[i], 4);
+      mbar_init(&empty[i], 1);
+    }
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(&s_full[g], 1);
+      mbar_init(&p_full[g], 4);
+      mbar_init(&pv_done[g], 1);
+      mbar_init(&o_free[g], 4);
+    }
+    fence_mbar_init();
+  }
+
+  // ---- the CTA's share
+  const int per = (p.B + kThreads - 1) / kThreads;
+  long long incl = 0;
+  for (int i = 0; i < per; ++i) {
+    const int b = tid * per + i;
+    if (b < p.B) incl += head_tiles(p, load_stream(p, b, false)) * p.Hkv;
+  }
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) sSums[kThreads + warp] = incl;
+  __syncthreads();
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    const long long x = sSums[kThreads + w];
+    if (w < warp) incl += x;
+    total += x;
+  }
+  sSums[tid] = incl;
+  __syncthreads();
+  const long long share = max((total + gridDim.x - 1) / gridDim.x, (long long)kMinShare);
+  const long long first = share * blockIdx.x;
+  if (first >= total) return;
+  Walk at{};
+  {
+    int lo = 0;
+    for (int step = kThreads / 2; step > 0; step >>= 1)
+      if (sSums[lo + step - 1] <= first) lo += step;
+    long long off = first - (lo > 0 ? sSums[lo - 1] : 0);
+    at.b = lo * per;
+    at.x = load_stream(p, at.b, false);
+    long long head = head_tiles(p, at.x);
+    while (off >= head * p.Hkv && at.b + 1 < p.B) {
+      off -= head * p.Hkv;
+      at.x = load_stream(p, ++at.b, false);
+      head = head_tiles(p, at.x);
+    }
+    at.h = (int)(off / head);
+    off %= head;
+    at.all = pair_tiles(p, at.x, 0);
+    while (off >= at.all) {
+      off -= at.all;
+      at.all = pair_tiles(p, at.x, ++at.pair);
+    }
+    at.t0 = (int)off;
+    at.left = min(share, total - first);
+    at.n = (int)min((long long)(at.all - at.t0), at.left);
+    at.begin = first - at.t0;
+  }
+  if (warp == kWarpPV) {
+    tc::tmem_alloc(tslot, 512);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();  // (and sSums has been read)
+  tc::fence_after_sync();
+  const uint32_t tbase = *tslot;
+  auto tS = [&](int g) { return tbase + (uint32_t)(g * 128); };
+  auto tO = [&](int g) { return tbase + 256u + (uint32_t)(g * D); };
+  bool failed = false;
+  auto wait = [&](uint64_t* bar, uint32_t par, int where) {
+    if (!failed && !mbar_wait(bar, par)) {
+      report(p.err, PA_DEVERR_TIMEOUT, -1, where);
+      failed = true;
+    }
+  };
+
+  if (warp >= kWarpQK) {
+    regs_dec<56>();
+    if (warp == kWarpQK) {
+      // ======================= S = Q K^T =======================
+      const uint32_t id = tc::idesc_f16(kM, kN, false, false);
+      const uint64_t dQ0 = tc::smem_desc(smem_u32(sQ), 16, 1024);
+      const uint64_t dK0 = tc::smem_desc(smem_u32(sKV), 16, 1024);
+      int k = 0, a = 0, n0 = 0, n1 = 0;
+      for (; at.left > 0; at.next(p), ++a) {
+        const int end0 = at.group_end(p, 0), end1 = at.group_end(p, 1);
+        wait(q_full, (uint32_t)(a & 1), 40);
+        for (int t = at.t0; t < at.t0 + at.n; ++t, k += 2) {
+          const int s = k % L::kRing;
+          wait(&full[s], (uint32_t)((k / L::kRing) & 1), 41);
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            if (t >= (g ? end1 : end0)) continue;
+            int& n = g ? n1 : n0;
+            if (n >= 1) wait(&pv_done[g], (uint32_t)((n - 1) & 1), 42 + g);
+            tc::fence_after_sync();
+            if (lane == 0) {
+              const uint64_t dQ = dQ0 + (uint32_t)((g * L::kTile) >> 4);
+              const uint64_t dK = dK0 + (uint32_t)((s * L::kTile) >> 4);
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = ((kk >> 2) * L::kSlab + (kk & 3) * 32) >> 4;
+                tc::mma_f16_ss(tS(g), dQ + off, dK + off, id, kk > 0);
+              }
+              tc::commit(&s_full[g]);
+            }
+            __syncwarp();
+            ++n;
+          }
+          if (lane == 0) tc::commit(&empty[s]);
+          __syncwarp();
+        }
+        if (lane == 0) tc::commit(q_empty);
+        __syncwarp();
+      }
+    } else if (warp == kWarpPV) {
+      // ======================= O += P V =======================
+      const uint32_t id = tc::idesc_f16(kM, D, false, true);
+      const uint64_t dV0 = tc::smem_desc(smem_u32(sKV), L::kSlab, 1024);
+      int k = 1, n0 = 0, n1 = 0, m0 = 0, m1 = 0;
+      for (; at.left > 0; at.next(p)) {
+        const int end0 = at.group_end(p, 0), end1 = at.group_end(p, 1);
+        for (int t = at.t0; t < at.t0 + at.n; ++t, k += 2) {
+          const int s = k % L::kRing;
+          wait(&full[s], (uint32_t)((k / L::kRing) & 1), 50);
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            if (t >= (g ? end1 : end0)) continue;
+            int& n = g ? n1 : n0;
+            const int m = g ? m1 : m0;
+            wait(&p_full[g], (uint32_t)(n & 1), 51 + g);
+            if (t == at.t0 && m >= 1) wait(&o_free[g], (uint32_t)((m - 1) & 1), 53 + g);
+            tc::fence_after_sync();
+            if (lane == 0) {
+              const uint64_t dV = dV0 + (uint32_t)((s * L::kTile) >> 4);
+#pragma unroll
+              for (int kk = 0; kk < kN / 16; ++kk)
+                tc::mma_f16_ts(tO(g), tS(g) + kk * 8, dV + (kk * 2048 >> 4), id,
+                               (t > at.t0 || kk > 0) ? 1u : 0u);
+              tc::commit(&pv_done[g]);
+            }
+            __syncwarp();
+            ++n;
+          }
+          if (lane == 0) tc::commit(&empty[s]);
+          __syncwarp();
+        }
+        if (end0 > at.t0) ++m0;
+        if (end1 > at.t0) ++m1;
+      }
+    }
+  } else if (warp >= kWarpConv) {
+    regs_dec<88>();
+    // ======================= converters =======================
+    const int ct = tid - kWarpConv * 32;  // 0 .. 127
+    constexpr int kChunks = D / 16;       // 16-byte chunks of a key
+    constexpr int kRowsAt = 128 / kChunks;
+    constexpr int kLoads = kN / kRowsAt;  // of a thread and tile
+    const int c = ct % kChunks, r0 = ct / kChunks;
+    int k = 0, a = 0;
+    for (; at.left > 0; at.next(p), ++a) {
+      const int32_t* trow = p.block_table + (int64_t)at.b * p.bt_stride;
+      const int lk = at.x.s.lk;
+      auto table = [&](int t, int (&pg)[kUnits]) {
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) {
+          const int unit = t * kUnits + i;
+          pg[i] = unit * kPage < lk ? __ldg(trow + (unit >> p.page_shift)) : 0;
+        }
+      };
+      int pages[kUnits];
+      table(at.t0, pages);
+      // Q: 16 (8 for D = 64) lanes a row
+      if (a >= 1) wait(q_empty, (uint32_t)((a - 1) & 1), 10);
+      if (a >= 1) wait(f_empty, (uint32_t)((a - 1) & 1), 11);
+      {
+        constexpr int kLanes = D / 8, kAt = 128 / kLanes;
+        // a negative scale of K turns Q's sign, so that the scores' factor is none
+        const uint32_t flip =
+            p.k_scale != nullptr && __ldg(p.k_scale + at.h) < 0.f ? 0x80008000u : 0u;
+        const int qc = ct % kLanes;
+#pragma unroll 1
+        for (int i0 = 0; i0 < kChunkRows / kAt; i0 += 4) {
+          uint4 x[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int row = at.rows0() + (i0 + i) * kAt + ct / kLanes;
+            x[i] = make_uint4(0, 0, 0, 0);
+            if (row < at.x.rows) {
+              const int qi = row / p.G, h = at.h * p.G + row % p.G;
+              x[i] = __ldg(reinterpret_cast<const uint4*>(
+                  reinterpret_cast<const T*>(p.q) + (int64_t)(at.x.s.q0 + qi) * p.q_st +
+                  (int64_t)h * p.q_sh + qc * 8));
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = (i0 + i) * kAt + ct / kLanes;  // of the pair's 256 rows
+            float f = 1.f;
+            uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            if constexpr (!std::is_same<T, __half>::value) {
+              uint32_t top = 0;
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                top = max(top, max((w[e] & 0x7fffu) << 16, w[e] & 0x7fff0000u));
+#pragma unroll
+              for (int o = 1; o < kLanes; o <<= 1)
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+              const int ex = (int)(top >> 23);
+              const bool turn = ex > 0 && ex < 255;
+              const int by = min(ex, 253);
+              const float down = turn ? __uint_as_float((uint32_t)(254 - by) << 23) : 1.f;
+              if (turn) f = __uint_as_float((uint32_t)by << 23);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 y = E::to_f2(w[e]);
+                w[e] = Elem<__half>::from_f2(y.x * down, y.y * down);
+              }
+            }
+            const int rt = r & 127;
+            *reinterpret_cast<uint4*>(sQ + (r >> 7) * L::kTile + (qc >> 3) * L::kSlab + rt * 128 +
+                                      (((qc & 7) ^ (rt & 7)) << 4)) =
+                make_uint4(w[0] ^ flip, w[1] ^ flip, w[2] ^ flip, w[3] ^ flip);
+            if (qc == 0) sF[r] = f;
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
+      }
+      // the first row of the pair sees the least
+      const int least = seen(p, at.x, at.rows0());
+      auto load = [&](const uint8_t* cache, int64_t sb, int64_t st, int64_t sh, int t, bool tell,
+                      uint4 (&x)[kLoads]) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          const int r = i * kRowsAt + r0;  // key of the tile
+          const int unit = t * kUnits + (r >> 4);
+          int page = D == 128 ? pages[i % kUnits]
+                              : (r0 < 16 ? pages[2 * i % kUnits] : pages[(2 * i + 1) % kUnits]);
+          if (page < 0 || page >= p.num_pages) {
+            if (tell && c == 0 && (r & 15) == 0) report(p.err, PA_DEVERR_PAGE_OOB, at.b, unit);
+            page = 0;
+          }
+          const int row = (unit & ((1 << p.page_shift) - 1)) * kPage + (r & 15);
+          x[i] = make_uint4(0, 0, 0, 0);
+          if (t * kN + r < lk)
+            x[i] = __ldg(reinterpret_cast<const uint4*>(cache + page * sb + (int64_t)row * st +
+                                                        at.h * sh + c * 16));
+        }
+      };
+      auto store = [&](uint8_t* tile, const uint4 (&x)[kLoads]) {
+        // Eight lanes store a row of D = 128: those of the two slabs would meet
+        // in the same banks, so they store their two chunks in opposite order.
+        const int odd = D == 128 ? (c >> 2) : 0;
+        uint8_t* slab = tile + (c >> 2) * L::kSlab;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          const int r = i * kRowsAt + r0;
+          const uint4 lo = make_uint4(f16x2_of(x[i].x & 0xffffu), f16x2_of(x[i].x >> 16),
+                                      f16x2_of(x[i].y & 0xffffu), f16x2_of(x[i].y >> 16));
+          const uint4 hi = make_uint4(f16x2_of(x[i].z & 0xffffu), f16x2_of(x[i].z >> 16),
+                                      f16x2_of(x[i].w & 0xffffu), f16x2_of(x[i].w >> 16));
+          const int c0 = 2 * (c & 3) + odd, c1 = 2 * (c & 3) + 1 - odd;
+          *reinterpret_cast<uint4*>(slab + r * 128 + ((c0 ^ (r & 7)) << 4)) = odd ? hi : lo;
+          *reinterpret_cast<uint4*>(slab + r * 128 + ((c1 ^ (r & 7)) << 4)) = odd ? lo : hi;
+        }
+      };
+      auto done = [&](int s) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[s]);
+      };
+      for (int t = at.t0; t < at.t0 + at.n; ++t) {
+        uint4 x[kLoads];
+        load(p.k_cache, p.k_sb, p.k_st, p.k_sh, t, true, x);
+        int s = k % L::kRing;
+        wait(&empty[s], (uint32_t)(((k / L::kRing) & 1) ^ 1), 20);
+        store(sKV + s * L::kTile, x);
+        done(s);
+        ++k;
+        load(p.v_cache, p.v_sb, p.v_st, p.v_sh, t, false, x);
+        if (t + 1 < at.t0 + at.n) table(t + 1, pages);
+        s = k % L::kRing;
+        wait(&empty[s], (uint32_t)(((k / L::kRing) & 1) ^ 1), 21);
+        if ((t + 1) * kN > least) {
+          // Some row does not see all of the tile: a NaN in V is taken out of
+          // the product (0 x NaN) and told to the rows, which put it into
+          // their results if they see it.
+          uint32_t bad = 0;
+#pragma unroll
+          for (int i = 0; i < kLoads; ++i) {
+            uint32_t* w = reinterpret_cast<uint32_t*>(&x[i]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t hit = nan_bytes(w[e]);
+              bad |= hit;
+              w[e] &= ~((hit >> 7) * 0xffu);
+            }
+          }
+          const bool any = __any_sync(0xffffffffu, bad != 0);
+          if (lane == 0) sNan[s * 4 + warp - kWarpConv] = any ? 1 : 0;
+        }
+        store(sKV + s * L::kTile, x);
+        done(s);
+        ++k;
+      }
+    }
+    // nothing in flight may outlive the CTA: the last reads of Q and the ring
+    if (a >= 1) wait(q_empty, (uint32_t)((a - 1) & 1), 12);
+    for (int i = 0; i < L::kRing; ++i, ++k)
+      wait(&empty[k % L::kRing], (uint32_t)(((k / L::kRing) & 1) ^ 1), 22);
+  } else {
+    regs_inc<184>();
+    // ======================= softmax =======================
+    const int g = warp >> 2, quarter = warp & 3;
+    const int r = quarter * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    int n = 0, a = 0, k = 1;  // k: the V tile's place in the ring
+    for (; at.left > 0; ++a) {
+      const int row = at.rows0() + g * kM + r;
+      const bool valid = row < at.x.rows;
+      const int qi = valid ? row / p.G : 0, h = at.h * p.G + (valid ? row % p.G : 0);
+      const float ks = p.k_scale != nullptr ? __ldg(p.k_scale + at.h) : 1.f;
+      const float vs = p.v_scale != nullptr ? __ldg(p.v_scale + at.h) : 1.f;
+      wait(q_full, (uint32_t)(a & 1), 59);
+      const float f = sF[g * kM + r] * (fabsf(ks) * p.scale_log2);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(f_empty);
+      const int sees = valid ? seen(p, at.x, row) : 0;
+      const int least = seen(p, at.x, at.rows0());
+      const int end = at.group_end(p, g);
+      float m = neg_inf(), l = 0.f;
+      uint32_t nans[D / 32];  // columns of the row that a NaN in V reaches
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) nans[i] = 0;
+      for (int t = at.t0; t < end; ++t) {
+        wait(&s_full[g], (uint32_t)(n & 1), 60 + g);
+        tc::fence_after_sync();
+        float v[kN];
+#pragma unroll
+        for (int i = 0; i < kN / 32; ++i) tc::tmem_ld32(tS(g) + lane_off + i * 32, v + i * 32);
+        tc::tmem_wait_ld();
+        const int lim = sees - t * kN;  // keys [0, lim) of the tile are seen
+        const bool whole = lim >= kN;
+        float top8[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top8[i] = neg_inf();
+        if (!whole) {
+#pragma unroll
+          for (int i = 0; i < kN; ++i) v[i] = i < lim ? v[i] : neg_inf();
+        }
+#pragma unroll
+        for (int i = 0; i < kN; ++i) top8[i & 7] = fmaxf(top8[i & 7], v[i]);
+        const float top = fmaxf(fmaxf(fmaxf(top8[0], top8[1]), fmaxf(top8[2], top8[3])),
+                                fmaxf(fmaxf(top8[4], top8[5]), fmaxf(top8[6], top8[7]))) *
+                          f;
+        float alpha = 1.f;
+        if (top > m + (kE4m3Shift + kE4m3Slack)) {
+          const float to = top - kE4m3Shift;
+          if (m != neg_inf()) alpha = ex2(m - to);
+          l *= alpha;
+          m = to;
+        }
+        const float neg_m = m == neg_inf() ? 0.f : -m;
+        float sum8[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum8[i] = 0.f;
+#pragma unroll
+        for (int i = 0; i < kN / 32; ++i) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int at_key = i * 32 + 2 * e;
+            float e0 = ex2(fmaf(v[at_key], f, neg_m));
+            float e1 = ex2(fmaf(v[at_key + 1], f, neg_m));
+            if (!whole) {
+              e0 = at_key < lim ? e0 : 0.f;
+              e1 = at_key + 1 < lim ? e1 : 0.f;
+            }
+            sum8[e & 7] += e0 + e1;
+            pk[e] = Elem<__half>::from_f2(e0, e1);
+          }
+          tc::tmem_st16u(tS(g) + lane_off + i * 16, pk);
+        }
+        l += ((sum8[0] + sum8[1]) + (sum8[2] + sum8[3])) +
+             ((sum8[4] + sum8[5]) + (sum8[6] + sum8[7]));
+        if (t > at.t0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+          // O_g is still once P V of the group's previous tile is done
+          wait(&pv_done[g], (uint32_t)((n - 1) & 1), 62 + g);
+          tc::fence_after_sync();
+#pragma unroll 1
+          for (int i = 0; i < D / 32; ++i) {
+            float o[32];
+            tc::tmem_ld32(tO(g) + lane_off + i * 32, o);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= alpha;
+            tc::tmem_st32(tO(g) + lane_off + i * 32, o);
+          }
+        }
+        if ((t + 1) * kN > least) {
+          const int s = (k + 2 * (t - at.t0)) % L::kRing;
+          wait(&full[s], (uint32_t)(((k + 2 * (t - at.t0)) / L::kRing) & 1), 66);
+          const int4 bad = *reinterpret_cast<const int4*>(sNan + s * 4);
+          if ((bad.x | bad.y | bad.z | bad.w) != 0) {
+            for (int key = t * kN; key < min(sees, (t + 1) * kN); ++key) {
+              const int unit = key / kPage;
+              int page = __ldg(p.block_table + (int64_t)at.b * p.bt_stride + (unit >> p.page_shift));
+              if (page < 0 || page >= p.num_pages) page = 0;
+              const uint8_t* src = p.v_cache + page * p.v_sb +
+                                   (int64_t)((unit & ((1 << p.page_shift) - 1)) * kPage +
+                                             key % kPage) * p.v_st + at.h * p.v_sh;
+#pragma unroll
+              for (int i = 0; i < D / 32; ++i)
+                for (int e = 0; e < 8; ++e) {
+                  const uint32_t hit = nan_bytes(__ldg(reinterpret_cast<const uint32_t*>(src) +
+                                                       i * 8 + e));
+                  // bits 7, 15, 23, 31 to bits 0 to 3
+                  nans[i] |= (((hit >> 7) * 0x00204081u >> 21) & 0xfu) << (4 * e);
+                }
+            }
+          }
+          __syncwarp();
+        }
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[g]);
+        ++n;
+      }
+      // ---- the segment's result
+      const bool whole = at.n == at.all;
+      const int slot = 2 * blockIdx.x + (at.t0 == 0 ? 1 : 0);
+      const int64_t my_part = ((int64_t)slot * 2 + g) * kM;
+      auto out_row = [&]() {
+        return reinterpret_cast<T*>(p.out) + ((int64_t)(at.x.s.q0 + qi) * p.Hq + h) * D;
+      };
+      auto put_lse = [&](float ref, float sum) {
+        if (p.lse != nullptr)
+          p.lse[(int64_t)h * p.total_q + at.x.s.q0 + qi] =
+              sum == 0.f ? neg_inf() : (ref + log2f(sum)) * kLn2;
+      };
+      const float nan = __int_as_float(0x7fffffff);
+      if (end > at.t0) {
+        wait(&pv_done[g], (uint32_t)((n - 1) & 1), 64 + g);
+        tc::fence_after_sync();
+        const float by = l == 0.f ? 0.f : vs / l;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          float o[32];
+          tc::tmem_ld32(tO(g) + lane_off + i * 32, o);
+          tc::tmem_wait_ld();
+          if (nans[i] != 0) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if ((nans[i] >> e) & 1) o[e] = nan;
+          }
+          if (whole) {
+            if (valid) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 8)
+                *reinterpret_cast<uint4*>(out_row() + i * 32 + e) = make_uint4(
+                    E::from_f2(o[e] * by, o[e + 1] * by), E::from_f2(o[e + 2] * by, o[e + 3] * by),
+                    E::from_f2(o[e + 4] * by, o[e + 5] * by),
+                    E::from_f2(o[e + 6] * by, o[e + 7] * by));
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              *reinterpret_cast<float4*>(p.part_o + (my_part * (D / 4) + (i * 8 + e) * kM + r) * 4) =
+                  make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          }
+        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&o_free[g]);
+      } else if (whole && valid) {
+#pragma unroll
+        for (int i = 0; i < D; i += 8)
+          *reinterpret_cast<uint4*>(out_row() + i) = make_uint4(0, 0, 0, 0);
+      }
+      if (whole) {
+        if (valid) put_lse(m, l);
+      } else {
+        p.part_ml[my_part + r] = make_float2(m, l);
+        const int cta0 = (int)(at.begin / share);
+        const int cta1 = (int)((at.begin + at.all - 1) / share);
+        __threadfence();
+        named_barrier(1, 256);
+        if (tid == 0) *sFlag = arrive_last(p.words + cta0, launch_tag(), cta1 - cta0 + 1) ? 1 : 0;
+        named_barrier(1, 256);
+        if (*sFlag) {
+          __threadfence();
+          float ref = neg_inf(), sum = 0.f;
+          for (int cta = cta0; cta <= cta1; ++cta) {
+            const int64_t from = ((int64_t)(2 * cta + (cta == cta0 ? 1 : 0)) * 2 + g) * kM;
+            ref = fmaxf(ref, __ldcg(p.part_ml + from + r).x);
+          }
+          float4 acc[D / 16];  // a quarter of the row at a time
+#pragma unroll 1
+          for (int part = 0; part < 4; ++part) {
+#pragma unroll
+            for (int e = 0; e < D / 16; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+            sum = 0.f;
+            for (int cta = cta0; cta <= cta1; ++cta) {
+              const int64_t from = ((int64_t)(2 * cta + (cta == cta0 ? 1 : 0)) * 2 + g) * kM;
+              const float2 ml = __ldcg(p.part_ml + from + r);
+              if (ml.y == 0.f && ml.x == neg_inf()) continue;  // no tile of the group's: O unset
+              const float w = ml.x == ref ? 1.f : ex2(ml.x - ref);
+              sum = fmaf(w, ml.y, sum);
+#pragma unroll
+              for (int e = 0; e < D / 16; ++e) {
+                const float4 y = __ldcg(reinterpret_cast<const float4*>(
+                    p.part_o + (from * (D / 4) + (part * (D / 16) + e) * kM + r) * 4));
+                acc[e].x = fmaf(w, y.x, acc[e].x);
+                acc[e].y = fmaf(w, y.y, acc[e].y);
+                acc[e].z = fmaf(w, y.z, acc[e].z);
+                acc[e].w = fmaf(w, y.w, acc[e].w);
+              }
+            }
+            const float by = sum == 0.f ? 0.f : vs / sum;
+            if (valid) {
+#pragma unroll
+              for (int e = 0; e < D / 16; e += 2)
+                *reinterpret_cast<uint4*>(out_row() + part * (D / 4) + e * 4) = make_uint4(
+                    E::from_f2(acc[e].x * by, acc[e].y * by), E::from_f2(acc[e].z * by, acc[e].w * by),
+                    E::from_f2(acc[e + 1].x * by, acc[e + 1].y * by),
+                    E::from_f2(acc[e + 1].z * by, acc[e + 1].w * by));
+            }
+          }
+          if (valid) put_lse(ref, sum);
+        }
+      }
+      k += 2 * at.n;
+      at.next(p);
+    }
+  }
+
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == kWarpPV) tc::tmem_dealloc(tbase, 512);
+}
+
+template <int D, typename T>
+cudaError_t launch(const AttendParams& p, cudaStream_t st) {
+  const cudaError_t e = cudaFuncSetAttribute(
+      chunk_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::kBytes);
+  if (e != cudaSuccess) return e;
+  chunk_kernel<D, T><<<(unsigned)num_sms(), kThreads, Layout<D>::kBytes, st>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_chunks_e4m3(const AttendParams& p, int D, int dtype, cudaStream_t st) {
+  if (dtype == PA_F16) return D == 128 ? launch<128, __half>(p, st) : launch<64, __half>(p, st);
+  return D == 128 ? launch<128, __nv_bfloat16>(p, st) : launch<64, __nv_bfloat16>(p, st);
+}
+
+}  // namespace pa
