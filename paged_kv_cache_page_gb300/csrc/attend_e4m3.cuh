@@ -56,8 +56,9 @@ __device__ __forceinline__ SeqRows seq_rows(const AttendParams& p, int b, bool t
 
 // Two e4m3 values (the low byte first) as two fp16 values.
 __device__ __forceinline__ uint32_t f16x2_of(uint32_t e4m3x2) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)e4m3x2, __NV_E4M3);
-  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)e4m3x2));
+  return h;
 }
 // The sign bits (moved to bit 7) of the NaN bytes among four e4m3 values.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {

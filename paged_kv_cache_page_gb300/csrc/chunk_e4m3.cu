@@ -16,9 +16,9 @@
 //          ring of fp16 tiles K0 V0 K1 V1 ...
 //   12     S_g = Q_g K^T          13  O_g += P_g V (P_g from TMEM over S_g)
 // TMEM: S_0, S_1, O_0, O_1.  While one group's softmax runs, the tensor core
-// works on the other group.  The registers are dealt by setmaxnreg: 184 for
-// the softmax threads, 88 for the converters, 56 for the issuers, in all what
-// the block was launched with (512 x 128).
+// works on the other group.  A softmax thread holds 64 of its row's 128 scores
+// at a time and reads the others twice: with all of them in registers the 128 that
+// 14 warps leave a thread do not suffice.
 //
 // Work: the streams (sequence, kv head, pair of tiles) laid end to end in
 // 128-key tiles, as many as the pair's last row sees, and cut into equal
@@ -37,7 +37,7 @@ constexpr int kM = 128;          // rows of a query tile
 constexpr int kN = 128;          // keys of a tile
 constexpr int kUnits = kN / kPage;
 constexpr int kWarpConv = 8, kWarpQK = 12, kWarpPV = 13;
-constexpr int kThreads = 512;
+constexpr int kThreads = 14 * 32;
 constexpr int kMinShare = 4;     // tiles
 
 template <int D>
@@ -128,13 +128,30 @@ struct Walk {
   }
 };
 
-template <int R>
-__device__ __forceinline__ void regs_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+// Adds the columns in which one of keys [key0, key1) of the sequence has a NaN
+// in V (one bit a column).
+template <int D>
+__device__ __noinline__ void nan_columns(const AttendParams& p, int b, int h, int key0, int key1,
+                                         uint32_t (&nans)[D / 32]) {
+  for (int key = key0; key < key1; ++key) {
+    const int unit = key / kPage;
+    int page = __ldg(p.block_table + (int64_t)b * p.bt_stride + (unit >> p.page_shift));
+    if (page < 0 || page >= p.num_pages) page = 0;
+    const int row = (unit & ((1 << p.page_shift) - 1)) * kPage + key % kPage;
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(p.v_cache + page * p.v_sb +
+                                                            (int64_t)row * p.v_st + h * p.v_sh);
+    for (int i = 0; i < D / 32; ++i)
+      for (int e = 0; e < 8; ++e)  // bits 7, 15, 23, 31 to bits 0 to 3
+        nans[i] |= ((((nan_bytes(__ldg(src + i * 8 + e)) >> 7) * 0x00204081u) >> 21) & 0xfu)
+                   << (4 * e);
+  }
 }
-template <int R>
-__device__ __forceinline__ void regs_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+
+// Ties 32 values of an asynchronous TMEM load to the wait in front of it, so
+// that nothing computed from them moves ahead of the wait.
+__device__ __forceinline__ void arrived(float* v) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(v[i]));
 }
 
 template <int D, typename T>
@@ -211,8 +228,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   Walk at{};
   {
     int lo = 0;
-    for (int step = kThreads / 2; step > 0; step >>= 1)
-      if (sSums[lo + step - 1] <= first) lo += step;
+    for (int step = 256; step > 0; step >>= 1)
+      if (lo + step <= kThreads && sSums[lo + step - 1] <= first) lo += step;
     long long off = first - (lo > 0 ? sSums[lo - 1] : 0);
     at.b = lo * per;
     at.x = load_stream(p, at.b, false);
@@ -253,7 +270,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   };
 
   if (warp >= kWarpQK) {
-    regs_dec<56>();
     if (warp == kWarpQK) {
       // ======================= S = Q K^T =======================
       const uint32_t id = tc::idesc_f16(kM, kN, false, false);
@@ -328,7 +344,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       }
     }
   } else if (warp >= kWarpConv) {
-    regs_dec<88>();
     // ======================= converters =======================
     const int ct = tid - kWarpConv * 32;  // 0 .. 127
     constexpr int kChunks = D / 16;       // 16-byte chunks of a key
@@ -339,15 +354,46 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     for (; at.left > 0; at.next(p), ++a) {
       const int32_t* trow = p.block_table + (int64_t)at.b * p.bt_stride;
       const int lk = at.x.s.lk;
-      auto table = [&](int t, int (&pg)[kUnits]) {
+      // Table entries of 32 units (four tiles) from `unit` on, one a lane.
+      auto table = [&](int unit) {
+        unit += lane;
+        return unit * kPage < lk ? __ldg(trow + (unit >> p.page_shift)) : 0;
+      };
+      const uint8_t* kbase = p.k_cache + (int64_t)at.h * p.k_sh + c * 16;
+      const uint8_t* vbase = p.v_cache + (int64_t)at.h * p.v_sh + c * 16;
+      // An entry outside the pool is reported and read as page 0.
+      auto checked = [&](int entry, int unit) {
+        if (entry >= 0 && entry < p.num_pages) return entry;
+        if (ct < 32) report(p.err, PA_DEVERR_PAGE_OOB, at.b, unit + lane);
+        return 0;
+      };
+      // The thread's 16 bytes of each of its keys of tile t: loads without a
+      // condition (rows behind the last key lie in its page or in page 0, and
+      // are cleared before they are stored), so that all are in flight at
+      // once.  `entries` holds the table from tile t0 + 4 j on.
+      auto load = [&](const uint8_t* base, int64_t sb, int64_t st, int t, int entries,
+                      uint4 (&x)[kLoads]) {
 #pragma unroll
-        for (int i = 0; i < kUnits; ++i) {
-          const int unit = t * kUnits + i;
-          pg[i] = unit * kPage < lk ? __ldg(trow + (unit >> p.page_shift)) : 0;
+        for (int i = 0; i < kLoads; ++i) {
+          const int r = i * kRowsAt + r0;  // key of the tile
+          const int unit = t * kUnits + (r >> 4);
+          const int page =
+              __shfl_sync(0xffffffffu, entries, ((t - at.t0) & 3) * kUnits + (r >> 4));
+          const int row = (unit & ((1 << p.page_shift) - 1)) * kPage + (r & 15);
+          x[i] = __ldg(reinterpret_cast<const uint4*>(base + page * sb + (int64_t)row * st));
         }
       };
-      int pages[kUnits];
-      table(at.t0, pages);
+      // Zeros at keys of tile t behind the last one.
+      auto clear = [&](int t, uint4 (&x)[kLoads]) {
+        if ((t + 1) * kN <= lk) return;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+          if (t * kN + i * kRowsAt + r0 >= lk) x[i] = make_uint4(0, 0, 0, 0);
+      };
+      int cur = checked(table(at.t0 * kUnits), at.t0 * kUnits);
+      int nxt = at.n > 4 ? table((at.t0 + 4) * kUnits) : 0;
+      uint4 xk[kLoads], xv[kLoads];
+      load(kbase, p.k_sb, p.k_st, at.t0, cur, xk);
       // Q: 16 (8 for D = 64) lanes a row
       if (a >= 1) wait(q_empty, (uint32_t)((a - 1) & 1), 10);
       if (a >= 1) wait(f_empty, (uint32_t)((a - 1) & 1), 11);
@@ -408,25 +454,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       }
       // the first row of the pair sees the least
       const int least = seen(p, at.x, at.rows0());
-      auto load = [&](const uint8_t* cache, int64_t sb, int64_t st, int64_t sh, int t, bool tell,
-                      uint4 (&x)[kLoads]) {
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-          const int r = i * kRowsAt + r0;  // key of the tile
-          const int unit = t * kUnits + (r >> 4);
-          int page = D == 128 ? pages[i % kUnits]
-                              : (r0 < 16 ? pages[2 * i % kUnits] : pages[(2 * i + 1) % kUnits]);
-          if (page < 0 || page >= p.num_pages) {
-            if (tell && c == 0 && (r & 15) == 0) report(p.err, PA_DEVERR_PAGE_OOB, at.b, unit);
-            page = 0;
-          }
-          const int row = (unit & ((1 << p.page_shift) - 1)) * kPage + (r & 15);
-          x[i] = make_uint4(0, 0, 0, 0);
-          if (t * kN + r < lk)
-            x[i] = __ldg(reinterpret_cast<const uint4*>(cache + page * sb + (int64_t)row * st +
-                                                        at.h * sh + c * 16));
-        }
-      };
       auto store = [&](uint8_t* tile, const uint4 (&x)[kLoads]) {
         // Eight lanes store a row of D = 128: those of the two slabs would meet
         // in the same banks, so they store their two chunks in opposite order.
@@ -435,13 +462,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
           const int r = i * kRowsAt + r0;
-          const uint4 lo = make_uint4(f16x2_of(x[i].x & 0xffffu), f16x2_of(x[i].x >> 16),
-                                      f16x2_of(x[i].y & 0xffffu), f16x2_of(x[i].y >> 16));
-          const uint4 hi = make_uint4(f16x2_of(x[i].z & 0xffffu), f16x2_of(x[i].z >> 16),
-                                      f16x2_of(x[i].w & 0xffffu), f16x2_of(x[i].w >> 16));
+          const uint32_t w0 = odd ? x[i].z : x[i].x, w1 = odd ? x[i].w : x[i].y;
+          const uint32_t w2 = odd ? x[i].x : x[i].z, w3 = odd ? x[i].y : x[i].w;
           const int c0 = 2 * (c & 3) + odd, c1 = 2 * (c & 3) + 1 - odd;
-          *reinterpret_cast<uint4*>(slab + r * 128 + ((c0 ^ (r & 7)) << 4)) = odd ? hi : lo;
-          *reinterpret_cast<uint4*>(slab + r * 128 + ((c1 ^ (r & 7)) << 4)) = odd ? lo : hi;
+          *reinterpret_cast<uint4*>(slab + r * 128 + ((c0 ^ (r & 7)) << 4)) =
+              make_uint4(f16x2_of(w0 & 0xffffu), f16x2_of(w0 >> 16), f16x2_of(w1 & 0xffffu),
+                         f16x2_of(w1 >> 16));
+          *reinterpret_cast<uint4*>(slab + r * 128 + ((c1 ^ (r & 7)) << 4)) =
+              make_uint4(f16x2_of(w2 & 0xffffu), f16x2_of(w2 >> 16), f16x2_of(w3 & 0xffffu),
+                         f16x2_of(w3 >> 16));
         }
       };
       auto done = [&](int s) {
@@ -450,17 +479,25 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         if (lane == 0) mbar_arrive(&full[s]);
       };
       for (int t = at.t0; t < at.t0 + at.n; ++t) {
-        uint4 x[kLoads];
-        load(p.k_cache, p.k_sb, p.k_st, p.k_sh, t, true, x);
+        // V of this tile and K of the next are on their way while K of this one
+        // is converted
+        load(vbase, p.v_sb, p.v_st, t, cur, xv);
         int s = k % L::kRing;
         wait(&empty[s], (uint32_t)(((k / L::kRing) & 1) ^ 1), 20);
-        store(sKV + s * L::kTile, x);
+        clear(t, xk);
+        store(sKV + s * L::kTile, xk);
         done(s);
         ++k;
-        load(p.v_cache, p.v_sb, p.v_st, p.v_sh, t, false, x);
-        if (t + 1 < at.t0 + at.n) table(t + 1, pages);
+        if (t + 1 < at.t0 + at.n) {
+          if (((t + 1 - at.t0) & 3) == 0) {
+            cur = checked(nxt, (t + 1) * kUnits);
+            if (t + 5 < at.t0 + at.n) nxt = table((t + 5) * kUnits);
+          }
+          load(kbase, p.k_sb, p.k_st, t + 1, cur, xk);
+        }
         s = k % L::kRing;
         wait(&empty[s], (uint32_t)(((k / L::kRing) & 1) ^ 1), 21);
+        clear(t, xv);
         if ((t + 1) * kN > least) {
           // Some row does not see all of the tile: a NaN in V is taken out of
           // the product (0 x NaN) and told to the rows, which put it into
@@ -468,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           uint32_t bad = 0;
 #pragma unroll
           for (int i = 0; i < kLoads; ++i) {
-            uint32_t* w = reinterpret_cast<uint32_t*>(&x[i]);
+            uint32_t* w = reinterpret_cast<uint32_t*>(&xv[i]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const uint32_t hit = nan_bytes(w[e]);
@@ -479,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           const bool any = __any_sync(0xffffffffu, bad != 0);
           if (lane == 0) sNan[s * 4 + warp - kWarpConv] = any ? 1 : 0;
         }
-        store(sKV + s * L::kTile, x);
+        store(sKV + s * L::kTile, xv);
         done(s);
         ++k;
       }
@@ -489,7 +526,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     for (int i = 0; i < L::kRing; ++i, ++k)
       wait(&empty[k % L::kRing], (uint32_t)(((k / L::kRing) & 1) ^ 1), 22);
   } else {
-    regs_inc<184>();
     // ======================= softmax =======================
     const int g = warp >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane;
@@ -515,21 +551,25 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       for (int t = at.t0; t < end; ++t) {
         wait(&s_full[g], (uint32_t)(n & 1), 60 + g);
         tc::fence_after_sync();
-        float v[kN];
-#pragma unroll
-        for (int i = 0; i < kN / 32; ++i) tc::tmem_ld32(tS(g) + lane_off + i * 32, v + i * 32);
-        tc::tmem_wait_ld();
+        const uint32_t ts = tS(g) + lane_off;
         const int lim = sees - t * kN;  // keys [0, lim) of the tile are seen
         const bool whole = lim >= kN;
-        float top8[8];
+        // keys 64 .. 127 for the maximum alone, then 0 .. 63, which stay
+        float v[64], top8[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) top8[i] = neg_inf();
-        if (!whole) {
 #pragma unroll
-          for (int i = 0; i < kN; ++i) v[i] = i < lim ? v[i] : neg_inf();
+        for (int hf = 1; hf >= 0; --hf) {
+          tc::tmem_ld32(ts + hf * 64, v);
+          tc::tmem_ld32(ts + hf * 64 + 32, v + 32);
+          tc::tmem_wait_ld();
+          if (!whole) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) v[i] = hf * 64 + i < lim ? v[i] : neg_inf();
+          }
+#pragma unroll
+          for (int i = 0; i < 64; ++i) top8[i & 7] = fmaxf(top8[i & 7], v[i]);
         }
-#pragma unroll
-        for (int i = 0; i < kN; ++i) top8[i & 7] = fmaxf(top8[i & 7], v[i]);
         const float top = fmaxf(fmaxf(fmaxf(top8[0], top8[1]), fmaxf(top8[2], top8[3])),
                                 fmaxf(fmaxf(top8[4], top8[5]), fmaxf(top8[6], top8[7]))) *
                           f;
@@ -544,22 +584,36 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         float sum8[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum8[i] = 0.f;
-#pragma unroll
-        for (int i = 0; i < kN / 32; ++i) {
+        // P of keys key0 .. key0 + 31 over the columns from key0 / 2 on: scores
+        // that are in registers or have been used
+        auto probabilities = [&](const float* x, int key0) {
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const int at_key = i * 32 + 2 * e;
-            float e0 = ex2(fmaf(v[at_key], f, neg_m));
-            float e1 = ex2(fmaf(v[at_key + 1], f, neg_m));
+            const int key = key0 + 2 * e;
+            float e0 = ex2(fmaf(x[2 * e], f, neg_m));
+            float e1 = ex2(fmaf(x[2 * e + 1], f, neg_m));
             if (!whole) {
-              e0 = at_key < lim ? e0 : 0.f;
-              e1 = at_key + 1 < lim ? e1 : 0.f;
+              e0 = key < lim ? e0 : 0.f;
+              e1 = key + 1 < lim ? e1 : 0.f;
             }
             sum8[e & 7] += e0 + e1;
             pk[e] = Elem<__half>::from_f2(e0, e1);
           }
-          tc::tmem_st16u(tS(g) + lane_off + i * 16, pk);
+          tc::tmem_st16u(ts + key0 / 2, pk);
+        };
+        {
+          float w[32];
+          tc::tmem_ld32(ts + 64, w);
+          probabilities(v, 0);
+          probabilities(v + 32, 32);
+          tc::tmem_wait_ld();
+          arrived(w);
+          tc::tmem_ld32(ts + 96, v);
+          probabilities(w, 64);
+          tc::tmem_wait_ld();
+          arrived(v);
+          probabilities(v, 96);
         }
         l += ((sum8[0] + sum8[1]) + (sum8[2] + sum8[3])) +
              ((sum8[4] + sum8[5]) + (sum8[6] + sum8[7]));
@@ -582,22 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           wait(&full[s], (uint32_t)(((k + 2 * (t - at.t0)) / L::kRing) & 1), 66);
           const int4 bad = *reinterpret_cast<const int4*>(sNan + s * 4);
           if ((bad.x | bad.y | bad.z | bad.w) != 0) {
-            for (int key = t * kN; key < min(sees, (t + 1) * kN); ++key) {
-              const int unit = key / kPage;
-              int page = __ldg(p.block_table + (int64_t)at.b * p.bt_stride + (unit >> p.page_shift));
-              if (page < 0 || page >= p.num_pages) page = 0;
-              const uint8_t* src = p.v_cache + page * p.v_sb +
-                                   (int64_t)((unit & ((1 << p.page_shift) - 1)) * kPage +
-                                             key % kPage) * p.v_st + at.h * p.v_sh;
-#pragma unroll
-              for (int i = 0; i < D / 32; ++i)
-                for (int e = 0; e < 8; ++e) {
-                  const uint32_t hit = nan_bytes(__ldg(reinterpret_cast<const uint32_t*>(src) +
-                                                       i * 8 + e));
-                  // bits 7, 15, 23, 31 to bits 0 to 3
-                  nans[i] |= (((hit >> 7) * 0x00204081u >> 21) & 0xfu) << (4 * e);
-                }
-            }
+            nan_columns<D>(p, at.b, at.h, t * kN, min(sees, (t + 1) * kN), nans);
           }
           __syncwarp();
         }
