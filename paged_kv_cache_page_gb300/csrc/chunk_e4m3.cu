@@ -16,9 +16,7 @@
 //          ring of fp16 tiles K0 V0 K1 V1 ...
 //   12     S_g = Q_g K^T          13  O_g += P_g V (P_g from TMEM over S_g)
 // TMEM: S_0, S_1, O_0, O_1.  While one group's softmax runs, the tensor core
-// works on the other group.  A softmax thread holds 64 of its row's 128 scores
-// at a time and reads the others twice: with all of them in registers the 128 that
-// 14 warps leave a thread do not suffice.
+// works on the other group.
 //
 // Work: the streams (sequence, kv head, pair of tiles) laid end to end in
 // 128-key tiles, as many as the pair's last row sees, and cut into equal
@@ -149,7 +147,7 @@ __device__ __noinline__ void nan_columns(const AttendParams& p, int b, int h, in
 
 // Ties 32 values of an asynchronous TMEM load to the wait in front of it, so
 // that nothing computed from them moves ahead of the wait.
-__device__ __forceinline__ void arrived(float* v) {
+__device__ __forceinline__ void arrived(float (&v)[32]) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(v[i]));
 }
@@ -354,33 +352,35 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     for (; at.left > 0; at.next(p), ++a) {
       const int32_t* trow = p.block_table + (int64_t)at.b * p.bt_stride;
       const int lk = at.x.s.lk;
-      // Table entries of 32 units (four tiles) from `unit` on, one a lane.
+      // Lane l finds unit `unit` + l of 32 units (four tiles): the table entry,
+      // and later its place in either cache.  An entry outside the pool is
+      // reported and read as page 0, as is what lies behind the last key.
       auto table = [&](int unit) {
         unit += lane;
         return unit * kPage < lk ? __ldg(trow + (unit >> p.page_shift)) : 0;
       };
-      const uint8_t* kbase = p.k_cache + (int64_t)at.h * p.k_sh + c * 16;
-      const uint8_t* vbase = p.v_cache + (int64_t)at.h * p.v_sh + c * 16;
-      // An entry outside the pool is reported and read as page 0.
-      auto checked = [&](int entry, int unit) {
-        if (entry >= 0 && entry < p.num_pages) return entry;
-        if (ct < 32) report(p.err, PA_DEVERR_PAGE_OOB, at.b, unit + lane);
-        return 0;
+      int64_t koff, voff;
+      auto place = [&](int entry, int unit) {
+        unit += lane;
+        if (entry < 0 || entry >= p.num_pages) {
+          if (ct < 32) report(p.err, PA_DEVERR_PAGE_OOB, at.b, unit);
+          entry = 0;
+        }
+        const int row = (unit & ((1 << p.page_shift) - 1)) * kPage;
+        koff = entry * p.k_sb + row * p.k_st;
+        voff = entry * p.v_sb + row * p.v_st;
       };
+      const uint8_t* kbase = p.k_cache + (int64_t)at.h * p.k_sh + c * 16 + (r0 & 15) * p.k_st;
+      const uint8_t* vbase = p.v_cache + (int64_t)at.h * p.v_sh + c * 16 + (r0 & 15) * p.v_st;
       // The thread's 16 bytes of each of its keys of tile t: loads without a
       // condition (rows behind the last key lie in its page or in page 0, and
-      // are cleared before they are stored), so that all are in flight at
-      // once.  `entries` holds the table from tile t0 + 4 j on.
-      auto load = [&](const uint8_t* base, int64_t sb, int64_t st, int t, int entries,
-                      uint4 (&x)[kLoads]) {
+      // are cleared before they are stored), so that all are in flight at once.
+      auto load = [&](const uint8_t* base, int64_t off, int t, uint4 (&x)[kLoads]) {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-          const int r = i * kRowsAt + r0;  // key of the tile
-          const int unit = t * kUnits + (r >> 4);
-          const int page =
-              __shfl_sync(0xffffffffu, entries, ((t - at.t0) & 3) * kUnits + (r >> 4));
-          const int row = (unit & ((1 << p.page_shift) - 1)) * kPage + (r & 15);
-          x[i] = __ldg(reinterpret_cast<const uint4*>(base + page * sb + (int64_t)row * st));
+          const int unit = ((t - at.t0) & 3) * kUnits + (i * kRowsAt + r0) / kPage;
+          x[i] = __ldg(reinterpret_cast<const uint4*>(
+              base + __shfl_sync(0xffffffffu, (long long)off, unit)));
         }
       };
       // Zeros at keys of tile t behind the last one.
@@ -390,10 +390,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         for (int i = 0; i < kLoads; ++i)
           if (t * kN + i * kRowsAt + r0 >= lk) x[i] = make_uint4(0, 0, 0, 0);
       };
-      int cur = checked(table(at.t0 * kUnits), at.t0 * kUnits);
+      place(table(at.t0 * kUnits), at.t0 * kUnits);
       int nxt = at.n > 4 ? table((at.t0 + 4) * kUnits) : 0;
       uint4 xk[kLoads], xv[kLoads];
-      load(kbase, p.k_sb, p.k_st, at.t0, cur, xk);
+      load(kbase, koff, at.t0, xk);
       // Q: 16 (8 for D = 64) lanes a row
       if (a >= 1) wait(q_empty, (uint32_t)((a - 1) & 1), 10);
       if (a >= 1) wait(f_empty, (uint32_t)((a - 1) & 1), 11);
@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       for (int t = at.t0; t < at.t0 + at.n; ++t) {
         // V of this tile and K of the next are on their way while K of this one
         // is converted
-        load(vbase, p.v_sb, p.v_st, t, cur, xv);
+        load(vbase, voff, t, xv);
         int s = k % L::kRing;
         wait(&empty[s], (uint32_t)(((k / L::kRing) & 1) ^ 1), 20);
         clear(t, xk);
@@ -490,10 +490,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         ++k;
         if (t + 1 < at.t0 + at.n) {
           if (((t + 1 - at.t0) & 3) == 0) {
-            cur = checked(nxt, (t + 1) * kUnits);
+            place(nxt, (t + 1) * kUnits);
             if (t + 5 < at.t0 + at.n) nxt = table((t + 5) * kUnits);
           }
-          load(kbase, p.k_sb, p.k_st, t + 1, cur, xk);
+          load(kbase, koff, t + 1, xk);
         }
         s = k % L::kRing;
         wait(&empty[s], (uint32_t)(((k / L::kRing) & 1) ^ 1), 21);
@@ -554,21 +554,39 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         const uint32_t ts = tS(g) + lane_off;
         const int lim = sees - t * kN;  // keys [0, lim) of the tile are seen
         const bool whole = lim >= kN;
-        // keys 64 .. 127 for the maximum alone, then 0 .. 63, which stay
-        float v[64], top8[8];
+        float x[32], y[32], top8[8], sum8[8];
+        // The row's scores twice, 32 at a time, the next 32 under way: once for
+        // the maximum, once for P.  Rolled loops: unrolled over the tile, this
+        // code is as large as the instruction cache and every warp streams it.
 #pragma unroll
-        for (int i = 0; i < 8; ++i) top8[i] = neg_inf();
+        for (int i = 0; i < 8; ++i) {
+          top8[i] = neg_inf();
+          sum8[i] = 0.f;
+        }
+        auto highest = [&](const float (&v)[32], int key0) {
+          if (whole) {
 #pragma unroll
-        for (int hf = 1; hf >= 0; --hf) {
-          tc::tmem_ld32(ts + hf * 64, v);
-          tc::tmem_ld32(ts + hf * 64 + 32, v + 32);
-          tc::tmem_wait_ld();
-          if (!whole) {
+            for (int i = 0; i < 32; ++i) top8[i & 7] = fmaxf(top8[i & 7], v[i]);
+          } else {
+            const int left = lim - key0;
 #pragma unroll
-            for (int i = 0; i < 64; ++i) v[i] = hf * 64 + i < lim ? v[i] : neg_inf();
+            for (int i = 0; i < 32; ++i)
+              top8[i & 7] = i < left ? fmaxf(top8[i & 7], v[i]) : top8[i & 7];
           }
-#pragma unroll
-          for (int i = 0; i < 64; ++i) top8[i & 7] = fmaxf(top8[i & 7], v[i]);
+        };
+        tc::tmem_ld32(ts, x);
+        tc::tmem_wait_ld();
+        arrived(x);
+#pragma unroll 1
+        for (int c = 0; c < kN; c += 64) {
+          tc::tmem_ld32(ts + c + 32, y);
+          highest(x, c);
+          tc::tmem_wait_ld();
+          arrived(y);
+          tc::tmem_ld32(ts + (c ^ 64), x);  // in the end the first 32 again
+          highest(y, c + 32);
+          tc::tmem_wait_ld();
+          arrived(x);
         }
         const float top = fmaxf(fmaxf(fmaxf(top8[0], top8[1]), fmaxf(top8[2], top8[3])),
                                 fmaxf(fmaxf(top8[4], top8[5]), fmaxf(top8[6], top8[7]))) *
@@ -581,39 +599,34 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           m = to;
         }
         const float neg_m = m == neg_inf() ? 0.f : -m;
-        float sum8[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum8[i] = 0.f;
-        // P of keys key0 .. key0 + 31 over the columns from key0 / 2 on: scores
-        // that are in registers or have been used
-        auto probabilities = [&](const float* x, int key0) {
+        // P of keys key0 .. key0 + 31 over the columns from key0 / 2 on, whose
+        // scores have been used
+        auto probabilities = [&](const float (&v)[32], int key0) {
+          const int left = lim - key0;
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const int key = key0 + 2 * e;
-            float e0 = ex2(fmaf(x[2 * e], f, neg_m));
-            float e1 = ex2(fmaf(x[2 * e + 1], f, neg_m));
+            float e0 = ex2(fmaf(v[2 * e], f, neg_m));
+            float e1 = ex2(fmaf(v[2 * e + 1], f, neg_m));
             if (!whole) {
-              e0 = key < lim ? e0 : 0.f;
-              e1 = key + 1 < lim ? e1 : 0.f;
+              e0 = 2 * e < left ? e0 : 0.f;
+              e1 = 2 * e + 1 < left ? e1 : 0.f;
             }
             sum8[e & 7] += e0 + e1;
             pk[e] = Elem<__half>::from_f2(e0, e1);
           }
           tc::tmem_st16u(ts + key0 / 2, pk);
         };
-        {
-          float w[32];
-          tc::tmem_ld32(ts + 64, w);
-          probabilities(v, 0);
-          probabilities(v + 32, 32);
+#pragma unroll 1
+        for (int c = 0; c < kN; c += 64) {
+          tc::tmem_ld32(ts + c + 32, y);
+          probabilities(x, c);
           tc::tmem_wait_ld();
-          arrived(w);
-          tc::tmem_ld32(ts + 96, v);
-          probabilities(w, 64);
+          arrived(y);
+          if (c == 0) tc::tmem_ld32(ts + 64, x);
+          probabilities(y, c + 32);
           tc::tmem_wait_ld();
-          arrived(v);
-          probabilities(v, 96);
+          arrived(x);
         }
         l += ((sum8[0] + sum8[1]) + (sum8[2] + sum8[3])) +
              ((sum8[4] + sum8[5]) + (sum8[6] + sum8[7]));
