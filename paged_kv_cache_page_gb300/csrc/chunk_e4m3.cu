@@ -14,7 +14,7 @@
 //          K and V tiles in turn -- 16 bytes a load from the pages, two fp16
 //          chunks a store into the 128-byte-swizzled operand tile -- into a
 //          ring of fp16 tiles K0 V0 K1 V1 ...
-//   12     S_g = Q_g K^T          13  O_g += P_g V (P_g from TMEM over S_g)
+//   12     issues O_g += P_g V (P_g from TMEM over S_g) and S_g = Q_g K^T
 // TMEM: S_0, S_1, O_0, O_1.  While one group's softmax runs, the tensor core
 // works on the other group.
 //
@@ -34,8 +34,8 @@ namespace {
 constexpr int kM = 128;          // rows of a query tile
 constexpr int kN = 128;          // keys of a tile
 constexpr int kUnits = kN / kPage;
-constexpr int kWarpConv = 8, kWarpQK = 12, kWarpPV = 13;
-constexpr int kThreads = 14 * 32;
+constexpr int kWarpConv = 8, kWarpMma = 12;
+constexpr int kThreads = 13 * 32;
 constexpr int kMinShare = 4;     // tiles
 
 template <int D>
@@ -145,6 +145,33 @@ __device__ __noinline__ void nan_columns(const AttendParams& p, int b, int h, in
   }
 }
 
+// Two fp32 values at a time.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t x;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a), "f"(b));
+  return x;
+}
+__device__ __forceinline__ float2 halves(uint64_t x) {
+  float2 y;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(y.x), "=f"(y.y) : "l"(x));
+  return y;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t x;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(x) : "l"(a), "l"(b), "l"(c));
+  return x;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t x;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(x) : "l"(a), "l"(b));
+  return x;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float x;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(x) : "f"(a), "f"(b), "f"(c));
+  return x;
+}
+
 // Ties 32 values of an asynchronous TMEM load to the wait in front of it, so
 // that nothing computed from them moves ahead of the wait.
 __device__ __forceinline__ void arrived(float (&v)[32]) {
@@ -249,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     at.n = (int)min((long long)(at.all - at.t0), at.left);
     at.begin = first - at.t0;
   }
-  if (warp == kWarpPV) {
+  if (warp == kWarpMma) {
     tc::tmem_alloc(tslot, 512);
     tc::tmem_relinquish();
   }
@@ -267,79 +294,75 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     }
   };
 
-  if (warp >= kWarpQK) {
-    if (warp == kWarpQK) {
-      // ======================= S = Q K^T =======================
-      const uint32_t id = tc::idesc_f16(kM, kN, false, false);
-      const uint64_t dQ0 = tc::smem_desc(smem_u32(sQ), 16, 1024);
-      const uint64_t dK0 = tc::smem_desc(smem_u32(sKV), 16, 1024);
-      int k = 0, a = 0, n0 = 0, n1 = 0;
-      for (; at.left > 0; at.next(p), ++a) {
-        const int end0 = at.group_end(p, 0), end1 = at.group_end(p, 1);
-        wait(q_full, (uint32_t)(a & 1), 40);
-        for (int t = at.t0; t < at.t0 + at.n; ++t, k += 2) {
-          const int s = k % L::kRing;
-          wait(&full[s], (uint32_t)((k / L::kRing) & 1), 41);
+  if (warp == kWarpMma) {
+    // ======================= MMA issuer =======================
+    // Per tile and group: O_g += P_g V, then S_g of the next tile.  One thread's
+    // MMAs run in the order it issues them, so S_g may follow the product that
+    // reads P_g from the same columns without a wait.
+    const uint32_t id_s = tc::idesc_f16(kM, kN, false, false);
+    const uint32_t id_o = tc::idesc_f16(kM, D, false, true);
+    const uint64_t dQ0 = tc::smem_desc(smem_u32(sQ), 16, 1024);
+    const uint64_t dK0 = tc::smem_desc(smem_u32(sKV), 16, 1024);
+    const uint64_t dV0 = tc::smem_desc(smem_u32(sKV), L::kSlab, 1024);
+    int k = 0, a = 0, n0 = 0, n1 = 0, m0 = 0, m1 = 0;
+    auto scores = [&](int g, int s) {
+      if (lane == 0) {
+        const uint64_t dQ = dQ0 + (uint32_t)((g * L::kTile) >> 4);
+        const uint64_t dK = dK0 + (uint32_t)((s * L::kTile) >> 4);
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            if (t >= (g ? end1 : end0)) continue;
-            int& n = g ? n1 : n0;
-            if (n >= 1) wait(&pv_done[g], (uint32_t)((n - 1) & 1), 42 + g);
-            tc::fence_after_sync();
-            if (lane == 0) {
-              const uint64_t dQ = dQ0 + (uint32_t)((g * L::kTile) >> 4);
-              const uint64_t dK = dK0 + (uint32_t)((s * L::kTile) >> 4);
-#pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = ((kk >> 2) * L::kSlab + (kk & 3) * 32) >> 4;
-                tc::mma_f16_ss(tS(g), dQ + off, dK + off, id, kk > 0);
-              }
-              tc::commit(&s_full[g]);
-            }
-            __syncwarp();
-            ++n;
-          }
-          if (lane == 0) tc::commit(&empty[s]);
-          __syncwarp();
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * L::kSlab + (kk & 3) * 32) >> 4;
+          tc::mma_f16_ss(tS(g), dQ + off, dK + off, id_s, kk > 0);
         }
-        if (lane == 0) tc::commit(q_empty);
-        __syncwarp();
+        tc::commit(&s_full[g]);
       }
-    } else if (warp == kWarpPV) {
-      // ======================= O += P V =======================
-      const uint32_t id = tc::idesc_f16(kM, D, false, true);
-      const uint64_t dV0 = tc::smem_desc(smem_u32(sKV), L::kSlab, 1024);
-      int k = 1, n0 = 0, n1 = 0, m0 = 0, m1 = 0;
-      for (; at.left > 0; at.next(p)) {
-        const int end0 = at.group_end(p, 0), end1 = at.group_end(p, 1);
-        for (int t = at.t0; t < at.t0 + at.n; ++t, k += 2) {
-          const int s = k % L::kRing;
-          wait(&full[s], (uint32_t)((k / L::kRing) & 1), 50);
+      __syncwarp();
+    };
+    auto release = [&](uint64_t* bar) {
+      if (lane == 0) tc::commit(bar);
+      __syncwarp();
+    };
+    for (; at.left > 0; at.next(p), ++a) {
+      const int end0 = at.group_end(p, 0), end1 = at.group_end(p, 1), end = at.t0 + at.n;
+      wait(q_full, (uint32_t)(a & 1), 40);
+      wait(&full[k % L::kRing], (uint32_t)((k / L::kRing) & 1), 41);
+      tc::fence_after_sync();
+      if (at.t0 < end0) scores(0, k % L::kRing);
+      if (at.t0 < end1) scores(1, k % L::kRing);
+      release(&empty[k % L::kRing]);
+      for (int t = at.t0; t < end; ++t, k += 2) {
+        const int v = k + 1, kn = k + 2;  // places of V of this tile and K of the next
+        const int sv = v % L::kRing, sk = kn % L::kRing;
+        wait(&full[sv], (uint32_t)((v / L::kRing) & 1), 50);
+        if (t + 1 < end) wait(&full[sk], (uint32_t)((kn / L::kRing) & 1), 41);
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            if (t >= (g ? end1 : end0)) continue;
+        for (int g = 0; g < 2; ++g) {
+          const int gend = g ? end1 : end0;
+          if (t < gend) {
             int& n = g ? n1 : n0;
             const int m = g ? m1 : m0;
             wait(&p_full[g], (uint32_t)(n & 1), 51 + g);
             if (t == at.t0 && m >= 1) wait(&o_free[g], (uint32_t)((m - 1) & 1), 53 + g);
             tc::fence_after_sync();
             if (lane == 0) {
-              const uint64_t dV = dV0 + (uint32_t)((s * L::kTile) >> 4);
+              const uint64_t dV = dV0 + (uint32_t)((sv * L::kTile) >> 4);
 #pragma unroll
               for (int kk = 0; kk < kN / 16; ++kk)
-                tc::mma_f16_ts(tO(g), tS(g) + kk * 8, dV + (kk * 2048 >> 4), id,
+                tc::mma_f16_ts(tO(g), tS(g) + kk * 8, dV + (kk * 2048 >> 4), id_o,
                                (t > at.t0 || kk > 0) ? 1u : 0u);
               tc::commit(&pv_done[g]);
             }
             __syncwarp();
             ++n;
+            if (t + 1 < gend) scores(g, sk);
           }
-          if (lane == 0) tc::commit(&empty[s]);
-          __syncwarp();
         }
-        if (end0 > at.t0) ++m0;
-        if (end1 > at.t0) ++m1;
+        release(&empty[sv]);
+        if (t + 1 < end) release(&empty[sk]);
       }
+      release(q_empty);
+      if (end0 > at.t0) ++m0;
+      if (end1 > at.t0) ++m1;
     }
   } else if (warp >= kWarpConv) {
     // ======================= converters =======================
@@ -554,19 +577,19 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         const uint32_t ts = tS(g) + lane_off;
         const int lim = sees - t * kN;  // keys [0, lim) of the tile are seen
         const bool whole = lim >= kN;
-        float x[32], y[32], top8[8], sum8[8];
+        float x[32], y[32], top8[8];
+        uint64_t sum2[4] = {0, 0, 0, 0};  // four pairs of sums
         // The row's scores twice, 32 at a time, the next 32 under way: once for
         // the maximum, once for P.  Rolled loops: unrolled over the tile, this
         // code is as large as the instruction cache and every warp streams it.
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          top8[i] = neg_inf();
-          sum8[i] = 0.f;
-        }
+        for (int i = 0; i < 8; ++i) top8[i] = neg_inf();
+        const bool all_whole = __all_sync(0xffffffffu, whole);
         auto highest = [&](const float (&v)[32], int key0) {
-          if (whole) {
+          if (all_whole) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) top8[i & 7] = fmaxf(top8[i & 7], v[i]);
+            for (int i = 0; i < 32; i += 2)
+              top8[(i >> 1) & 7] = max3(top8[(i >> 1) & 7], v[i], v[i + 1]);
           } else {
             const int left = lim - key0;
 #pragma unroll
@@ -599,21 +622,29 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           m = to;
         }
         const float neg_m = m == neg_inf() ? 0.f : -m;
+        const uint64_t f2 = pair(f, f), m2 = pair(neg_m, neg_m);
         // P of keys key0 .. key0 + 31 over the columns from key0 / 2 on, whose
         // scores have been used
         auto probabilities = [&](const float (&v)[32], int key0) {
-          const int left = lim - key0;
           uint32_t pk[16];
+          if (all_whole) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float e0 = ex2(fmaf(v[2 * e], f, neg_m));
-            float e1 = ex2(fmaf(v[2 * e + 1], f, neg_m));
-            if (!whole) {
+            for (int e = 0; e < 16; ++e) {
+              const float2 z = halves(fma2(pair(v[2 * e], v[2 * e + 1]), f2, m2));
+              const float e0 = ex2(z.x), e1 = ex2(z.y);
+              sum2[e & 3] = add2(sum2[e & 3], pair(e0, e1));
+              pk[e] = Elem<__half>::from_f2(e0, e1);
+            }
+          } else {
+            const int left = lim - key0;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float e0 = ex2(fmaf(v[2 * e], f, neg_m)), e1 = ex2(fmaf(v[2 * e + 1], f, neg_m));
               e0 = 2 * e < left ? e0 : 0.f;
               e1 = 2 * e + 1 < left ? e1 : 0.f;
+              sum2[e & 3] = add2(sum2[e & 3], pair(e0, e1));
+              pk[e] = Elem<__half>::from_f2(e0, e1);
             }
-            sum8[e & 7] += e0 + e1;
-            pk[e] = Elem<__half>::from_f2(e0, e1);
           }
           tc::tmem_st16u(ts + key0 / 2, pk);
         };
@@ -628,8 +659,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           tc::tmem_wait_ld();
           arrived(x);
         }
-        l += ((sum8[0] + sum8[1]) + (sum8[2] + sum8[3])) +
-             ((sum8[4] + sum8[5]) + (sum8[6] + sum8[7]));
+        const float2 sum = halves(add2(add2(sum2[0], sum2[1]), add2(sum2[2], sum2[3])));
+        l += sum.x + sum.y;
         if (t > at.t0 && __any_sync(0xffffffffu, alpha != 1.f)) {
           // O_g is still once P V of the group's previous tile is done
           wait(&pv_done[g], (uint32_t)((n - 1) & 1), 62 + g);
@@ -770,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  if (warp == kWarpPV) tc::tmem_dealloc(tbase, 512);
+  if (warp == kWarpMma) tc::tmem_dealloc(tbase, 512);
 }
 
 template <int D, typename T>
