@@ -10,11 +10,12 @@
 // Bound: the tensor cores and the exponentials, 4 D operations and one
 // exponential a visible (row, key) pair.  Warps:
 //   0-7    softmax: one thread a row, group g = warp / 4 takes tile g
-//   8-11   converters: the pair's Q (a bf16 row scaled by a power of two), then
-//          K and V tiles in turn -- 16 bytes a load from the pages, two fp16
-//          chunks a store into the 128-byte-swizzled operand tile -- into a
-//          ring of fp16 tiles K0 V0 K1 V1 ...
+//   8-11   converters: K and V tiles in turn -- 16 bytes a load from the pages,
+//          two fp16 chunks a store into the 128-byte-swizzled operand tile --
+//          into a ring of fp16 tiles K0 V0 K1 V1 ...
 //   12     issues O_g += P_g V (P_g from TMEM over S_g) and S_g = Q_g K^T
+//   13-14  Q of the next segment (a bf16 row scaled by a power of two), into the
+//          other of two buffers
 // TMEM: S_0, S_1, O_0, O_1.  While one group's softmax runs, the tensor core
 // works on the other group.
 //
@@ -35,7 +36,7 @@ constexpr int kM = 128;          // rows of a query tile
 constexpr int kN = 128;          // keys of a tile
 constexpr int kUnits = kN / kPage;
 constexpr int kWarpConv = 8, kWarpMma = 12;
-constexpr int kThreads = 13 * 32;
+constexpr int kThreads = 15 * 32;
 constexpr int kMinShare = 4;     // tiles
 
 template <int D>
@@ -43,14 +44,14 @@ struct Layout {
   static constexpr int kHalves = D / 64;          // 64-column slabs of a row
   static constexpr int kSlab = 128 * 128;         // 128 rows x 128 bytes
   static constexpr int kTile = kHalves * kSlab;   // a fp16 operand tile
-  static constexpr int kRing = D == 128 ? 4 : 8;  // K and V tiles in the ring
-  static constexpr int kOffQ = 0;                 // [2]
-  static constexpr int kOffKV = 2 * kTile;
+  static constexpr int kRing = D == 128 ? 3 : 8;  // K and V tiles in the ring
+  static constexpr int kOffQ = 0;                 // [2 buffers][2]
+  static constexpr int kOffKV = 4 * kTile;
   static constexpr int kOffF = kOffKV + kRing * kTile;      // float [256] factor of a row's scores
   static constexpr int kOffNan = kOffF + kChunkRows * 4;    // int [kRing][4]
   static constexpr int kOffBar = kOffNan + kRing * 16;
-  // q_full, q_empty, f_empty; full, empty [kRing]; s_full, p_full, pv_done, o_free [2]
-  static constexpr int kBars = 3 + 2 * kRing + 8;
+  // q_full, q_empty [2], f_empty; full, empty [kRing]; s_full, p_full, pv_done, o_free [2]
+  static constexpr int kBars = 5 + 2 * kRing + 8;
   static constexpr int kOffMisc = kOffBar + kBars * 8;      // TMEM base, merge flag
   static constexpr int kOffSums = kOffKV;                   // long long [kThreads + 16], prologue
   static constexpr int kBytes = kOffMisc + 16 + 1024;
@@ -126,6 +127,28 @@ struct Walk {
   }
 };
 
+// Scales the first `cols` columns of fp16 probabilities in TMEM by a power of
+// two a lane (0 where it is below fp16's range).
+__device__ __noinline__ void scale_p(uint32_t t, int cols, float by) {
+  const __half2 h = __float2half2_rn(by);
+  tc::tmem_wait_st();
+#pragma unroll 1
+  for (int c = 0; c < cols; c += 16) {
+    float v[16];
+    uint32_t w[16];
+    tc::tmem_ld16(t + c, v);
+    tc::tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t u = __float_as_uint(v[i]);
+      const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&u), h);
+      w[i] = *reinterpret_cast<const uint32_t*>(&x);
+    }
+    tc::tmem_st16u(t + c, w);
+  }
+  tc::tmem_wait_st();
+}
+
 // Adds the columns in which one of keys [key0, key1) of the sequence has a NaN
 // in V (one bit a column).
 template <int D>
@@ -143,6 +166,11 @@ __device__ __noinline__ void nan_columns(const AttendParams& p, int b, int h, in
         nans[i] |= ((((nan_bytes(__ldg(src + i * 8 + e)) >> 7) * 0x00204081u) >> 21) & 0xfu)
                    << (4 * e);
   }
+}
+
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n)
+               : "memory");
 }
 
 // Two fp32 values at a time.
@@ -192,10 +220,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   float* sF = reinterpret_cast<float*>(smem + L::kOffF);
   int* sNan = reinterpret_cast<int*>(smem + L::kOffNan);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
-  uint64_t* q_full = bars;
-  uint64_t* q_empty = bars + 1;
-  uint64_t* f_empty = bars + 2;
-  uint64_t* full = bars + 3;
+  uint64_t* q_full = bars;        // [2]
+  uint64_t* q_empty = bars + 2;   // [2]
+  uint64_t* f_empty = bars + 4;   // the score factors have been read
+  uint64_t* full = bars + 5;
   uint64_t* empty = full + L::kRing;
   uint64_t* s_full = empty + L::kRing;
   uint64_t* p_full = s_full + 2;
@@ -208,8 +236,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   griddep_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    mbar_init(q_full, 4);
-    mbar_init(q_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 8);
+      mbar_init(&q_empty[i], 1);
+    }
     mbar_init(f_empty, 8);
     for (int i = 0; i < L::kRing; ++i) {
       mbar_init(&full[i], 4);
@@ -294,6 +324,66 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     }
   };
 
+  // Q of the pair of segment `w` into buffer `buf`, by `threads` threads of
+  // whole warps: 16 (D = 64: 8) lanes a row, kBatch rows in flight a thread.
+  // A bf16 row is scaled by a power of two to a largest magnitude in [1, 2);
+  // a negative scale of K turns the signs, so that no score factor is negative.
+  auto stage_q = [&](const Walk& w, int buf, int i, int threads) {
+    constexpr int kLanes = D / 8, kBatch = 16;
+    const int qc = i % kLanes, step = threads / kLanes;
+    const uint32_t flip =
+        p.k_scale != nullptr && __ldg(p.k_scale + w.h) < 0.f ? 0x80008000u : 0u;
+    uint8_t* tile = sQ + buf * 2 * L::kTile + (qc >> 3) * L::kSlab;
+    const T* base = reinterpret_cast<const T*>(p.q) + (int64_t)w.x.s.q0 * p.q_st +
+                    (int64_t)(w.h * p.G) * p.q_sh + qc * 8;
+#pragma unroll 1
+    for (int r0 = i / kLanes; r0 < kChunkRows; r0 += step * kBatch) {
+      uint4 x[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        // (rows behind the last are read as the last and stored as zeros)
+        const int row = min(w.rows0() + r0 + j * step, w.x.rows - 1);
+        x[j] = __ldg(reinterpret_cast<const uint4*>(base + (int64_t)(row / p.G) * p.q_st +
+                                                    (int64_t)(row % p.G) * p.q_sh));
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int r = r0 + j * step;
+        if (r >= kChunkRows) break;  // (uniform in a row's lanes)
+        const bool live = w.rows0() + r < w.x.rows;
+        float f = 1.f;
+        uint32_t u[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+        if constexpr (!std::is_same<T, __half>::value) {
+          uint32_t top = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            top = max(top, max((u[e] & 0x7fffu) << 16, u[e] & 0x7fff0000u));
+#pragma unroll
+          for (int o = 1; o < kLanes; o <<= 1)
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+          const int ex = (int)(top >> 23);
+          const bool turn = ex > 0 && ex < 255;
+          const int by = min(ex, 253);
+          const float down = turn ? __uint_as_float((uint32_t)(254 - by) << 23) : 1.f;
+          if (turn) f = __uint_as_float((uint32_t)by << 23);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 y = E::to_f2(u[e]);
+            u[e] = Elem<__half>::from_f2(y.x * down, y.y * down);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[e] = live ? u[e] ^ flip : 0u;
+        const int rt = r & 127;
+        *reinterpret_cast<uint4*>(tile + (r >> 7) * L::kTile + rt * 128 +
+                                  (((qc & 7) ^ (rt & 7)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
+        if (qc == 0) sF[r] = f;
+      }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+  };
+
   if (warp == kWarpMma) {
     // ======================= MMA issuer =======================
     // Per tile and group: O_g += P_g V, then S_g of the next tile.  One thread's
@@ -307,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     int k = 0, a = 0, n0 = 0, n1 = 0, m0 = 0, m1 = 0;
     auto scores = [&](int g, int s) {
       if (lane == 0) {
-        const uint64_t dQ = dQ0 + (uint32_t)((g * L::kTile) >> 4);
+        const uint64_t dQ = dQ0 + (uint32_t)((((a & 1) * 2 + g) * L::kTile) >> 4);
         const uint64_t dK = dK0 + (uint32_t)((s * L::kTile) >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
@@ -324,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     };
     for (; at.left > 0; at.next(p), ++a) {
       const int end0 = at.group_end(p, 0), end1 = at.group_end(p, 1), end = at.t0 + at.n;
-      wait(q_full, (uint32_t)(a & 1), 40);
+      wait(&q_full[a & 1], (uint32_t)((a >> 1) & 1), 40);
       wait(&full[k % L::kRing], (uint32_t)((k / L::kRing) & 1), 41);
       tc::fence_after_sync();
       if (at.t0 < end0) scores(0, k % L::kRing);
@@ -360,10 +450,23 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         release(&empty[sv]);
         if (t + 1 < end) release(&empty[sk]);
       }
-      release(q_empty);
+      release(&q_empty[a & 1]);
       if (end0 > at.t0) ++m0;
       if (end1 > at.t0) ++m1;
     }
+  } else if (warp > kWarpMma) {
+    // ======================= Q of the segments behind the first ===============
+    // One segment ahead, into the buffer that the segment before has left.
+    int a = 0;
+    for (; at.left > 0; at.next(p), ++a) {
+      if (a == 0) continue;  // the softmax warps, which have nothing to do yet
+      if (a >= 2) wait(&q_empty[a & 1], (uint32_t)(((a >> 1) - 1) & 1), 10);
+      wait(f_empty, (uint32_t)((a - 1) & 1), 11);
+      stage_q(at, a & 1, tid - (kWarpMma + 1) * 32, 64);
+      if (lane == 0) mbar_arrive_n(&q_full[a & 1], 4);
+    }
+    // nothing in flight may outlive the CTA: the last reads of either buffer
+    for (int b = max(0, a - 2); b < a; ++b) wait(&q_empty[b & 1], (uint32_t)((b >> 1) & 1), 12);
   } else if (warp >= kWarpConv) {
     // ======================= converters =======================
     const int ct = tid - kWarpConv * 32;  // 0 .. 127
@@ -371,8 +474,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     constexpr int kRowsAt = 128 / kChunks;
     constexpr int kLoads = kN / kRowsAt;  // of a thread and tile
     const int c = ct % kChunks, r0 = ct / kChunks;
-    int k = 0, a = 0;
-    for (; at.left > 0; at.next(p), ++a) {
+    int k = 0;
+    for (; at.left > 0; at.next(p)) {
       const int32_t* trow = p.block_table + (int64_t)at.b * p.bt_stride;
       const int lk = at.x.s.lk;
       // Lane l finds unit `unit` + l of 32 units (four tiles): the table entry,
@@ -417,64 +520,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       int nxt = at.n > 4 ? table((at.t0 + 4) * kUnits) : 0;
       uint4 xk[kLoads], xv[kLoads];
       load(kbase, koff, at.t0, xk);
-      // Q: 16 (8 for D = 64) lanes a row
-      if (a >= 1) wait(q_empty, (uint32_t)((a - 1) & 1), 10);
-      if (a >= 1) wait(f_empty, (uint32_t)((a - 1) & 1), 11);
-      {
-        constexpr int kLanes = D / 8, kAt = 128 / kLanes;
-        // a negative scale of K turns Q's sign, so that the scores' factor is none
-        const uint32_t flip =
-            p.k_scale != nullptr && __ldg(p.k_scale + at.h) < 0.f ? 0x80008000u : 0u;
-        const int qc = ct % kLanes;
-#pragma unroll 1
-        for (int i0 = 0; i0 < kChunkRows / kAt; i0 += 4) {
-          uint4 x[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int row = at.rows0() + (i0 + i) * kAt + ct / kLanes;
-            x[i] = make_uint4(0, 0, 0, 0);
-            if (row < at.x.rows) {
-              const int qi = row / p.G, h = at.h * p.G + row % p.G;
-              x[i] = __ldg(reinterpret_cast<const uint4*>(
-                  reinterpret_cast<const T*>(p.q) + (int64_t)(at.x.s.q0 + qi) * p.q_st +
-                  (int64_t)h * p.q_sh + qc * 8));
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = (i0 + i) * kAt + ct / kLanes;  // of the pair's 256 rows
-            float f = 1.f;
-            uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-            if constexpr (!std::is_same<T, __half>::value) {
-              uint32_t top = 0;
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                top = max(top, max((w[e] & 0x7fffu) << 16, w[e] & 0x7fff0000u));
-#pragma unroll
-              for (int o = 1; o < kLanes; o <<= 1)
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-              const int ex = (int)(top >> 23);
-              const bool turn = ex > 0 && ex < 255;
-              const int by = min(ex, 253);
-              const float down = turn ? __uint_as_float((uint32_t)(254 - by) << 23) : 1.f;
-              if (turn) f = __uint_as_float((uint32_t)by << 23);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float2 y = E::to_f2(w[e]);
-                w[e] = Elem<__half>::from_f2(y.x * down, y.y * down);
-              }
-            }
-            const int rt = r & 127;
-            *reinterpret_cast<uint4*>(sQ + (r >> 7) * L::kTile + (qc >> 3) * L::kSlab + rt * 128 +
-                                      (((qc & 7) ^ (rt & 7)) << 4)) =
-                make_uint4(w[0] ^ flip, w[1] ^ flip, w[2] ^ flip, w[3] ^ flip);
-            if (qc == 0) sF[r] = f;
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_full);
-      }
       // the first row of the pair sees the least
       const int least = seen(p, at.x, at.rows0());
       auto store = [&](uint8_t* tile, const uint4 (&x)[kLoads]) {
@@ -544,8 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         ++k;
       }
     }
-    // nothing in flight may outlive the CTA: the last reads of Q and the ring
-    if (a >= 1) wait(q_empty, (uint32_t)((a - 1) & 1), 12);
+    // nothing in flight may outlive the CTA: the last reads of the ring
     for (int i = 0; i < L::kRing; ++i, ++k)
       wait(&empty[k % L::kRing], (uint32_t)(((k / L::kRing) & 1) ^ 1), 22);
   } else {
@@ -560,7 +604,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       const int qi = valid ? row / p.G : 0, h = at.h * p.G + (valid ? row % p.G : 0);
       const float ks = p.k_scale != nullptr ? __ldg(p.k_scale + at.h) : 1.f;
       const float vs = p.v_scale != nullptr ? __ldg(p.v_scale + at.h) : 1.f;
-      wait(q_full, (uint32_t)(a & 1), 59);
+      if (a == 0) {
+        stage_q(at, 0, tid, 256);
+        if (lane == 0) mbar_arrive(&q_full[0]);
+      }
+      wait(&q_full[a & 1], (uint32_t)((a >> 1) & 1), 59);
       const float f = sF[g * kM + r] * (fabsf(ks) * p.scale_log2);
       __syncwarp();
       if (lane == 0) mbar_arrive(f_empty);
@@ -577,88 +625,80 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         const uint32_t ts = tS(g) + lane_off;
         const int lim = sees - t * kN;  // keys [0, lim) of the tile are seen
         const bool whole = lim >= kN;
-        float x[32], y[32], top8[8];
+        // One pass over the row's scores, 32 at a time with the next 32 under
+        // way.  A rolled loop: unrolled over the tile, this code is as large as
+        // the instruction cache and every warp streams it.
+        float x[32], y[32];
         uint64_t sum2[4] = {0, 0, 0, 0};  // four pairs of sums
-        // The row's scores twice, 32 at a time, the next 32 under way: once for
-        // the maximum, once for P.  Rolled loops: unrolled over the tile, this
-        // code is as large as the instruction cache and every warp streams it.
-#pragma unroll
-        for (int i = 0; i < 8; ++i) top8[i] = neg_inf();
-        const bool all_whole = __all_sync(0xffffffffu, whole);
-        auto highest = [&](const float (&v)[32], int key0) {
-          if (all_whole) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 2)
-              top8[(i >> 1) & 7] = max3(top8[(i >> 1) & 7], v[i], v[i + 1]);
-          } else {
-            const int left = lim - key0;
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              top8[i & 7] = i < left ? fmaxf(top8[i & 7], v[i]) : top8[i & 7];
-          }
-        };
-        tc::tmem_ld32(ts, x);
-        tc::tmem_wait_ld();
-        arrived(x);
-#pragma unroll 1
-        for (int c = 0; c < kN; c += 64) {
-          tc::tmem_ld32(ts + c + 32, y);
-          highest(x, c);
-          tc::tmem_wait_ld();
-          arrived(y);
-          tc::tmem_ld32(ts + (c ^ 64), x);  // in the end the first 32 again
-          highest(y, c + 32);
-          tc::tmem_wait_ld();
-          arrived(x);
-        }
-        const float top = fmaxf(fmaxf(fmaxf(top8[0], top8[1]), fmaxf(top8[2], top8[3])),
-                                fmaxf(fmaxf(top8[4], top8[5]), fmaxf(top8[6], top8[7]))) *
-                          f;
         float alpha = 1.f;
-        if (top > m + (kE4m3Shift + kE4m3Slack)) {
-          const float to = top - kE4m3Shift;
-          if (m != neg_inf()) alpha = ex2(m - to);
-          l *= alpha;
-          m = to;
-        }
-        const float neg_m = m == neg_inf() ? 0.f : -m;
-        const uint64_t f2 = pair(f, f), m2 = pair(neg_m, neg_m);
-        // P of keys key0 .. key0 + 31 over the columns from key0 / 2 on, whose
-        // scores have been used
-        auto probabilities = [&](const float (&v)[32], int key0) {
-          uint32_t pk[16];
-          if (all_whole) {
+        auto probabilities = [&](auto masked, float (&v)[32], float (&coming)[32], int key0) {
+          const int left = lim - key0;
+          if constexpr (masked) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float2 z = halves(fma2(pair(v[2 * e], v[2 * e + 1]), f2, m2));
-              const float e0 = ex2(z.x), e1 = ex2(z.y);
-              sum2[e & 3] = add2(sum2[e & 3], pair(e0, e1));
-              pk[e] = Elem<__half>::from_f2(e0, e1);
+            for (int i = 0; i < 32; ++i) v[i] = i < left ? v[i] : neg_inf();
+          }
+          float top4[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) top4[(i >> 1) & 3] = max3(top4[(i >> 1) & 3], v[i], v[i + 1]);
+          const float top = max3(fmaxf(top4[0], top4[1]), top4[2], top4[3]) * f;
+          if (__any_sync(0xffffffffu, top > m + (kE4m3Shift + kE4m3Slack))) {
+            // References are whole numbers, so what is scaled here is scaled
+            // by powers of two: this tile's sums and probabilities so far, and
+            // after the loop O.
+            tc::tmem_wait_ld();
+            arrived(coming);
+            float by = 1.f;
+            if (top > m + (kE4m3Shift + kE4m3Slack)) {
+              const float to = ceilf(top) - kE4m3Shift;
+              if (m != neg_inf()) by = ex2(m - to);
+              m = to;
             }
-          } else {
-            const int left = lim - key0;
+            alpha *= by;
+            l *= by;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float e0 = ex2(fmaf(v[2 * e], f, neg_m)), e1 = ex2(fmaf(v[2 * e + 1], f, neg_m));
+            for (int i = 0; i < 4; ++i) {
+              const float2 z = halves(sum2[i]);
+              sum2[i] = pair(z.x * by, z.y * by);
+            }
+            scale_p(ts, key0 / 2, by);
+          }
+          const float neg_m = m == neg_inf() ? 0.f : -m;
+          const uint64_t f2 = pair(f, f), m2 = pair(neg_m, neg_m);
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 z = halves(fma2(pair(v[2 * e], v[2 * e + 1]), f2, m2));
+            float e0 = ex2(z.x), e1 = ex2(z.y);
+            if constexpr (masked) {  // (a factor of zero turns -inf into NaN)
               e0 = 2 * e < left ? e0 : 0.f;
               e1 = 2 * e + 1 < left ? e1 : 0.f;
-              sum2[e & 3] = add2(sum2[e & 3], pair(e0, e1));
-              pk[e] = Elem<__half>::from_f2(e0, e1);
             }
+            sum2[e & 3] = add2(sum2[e & 3], pair(e0, e1));
+            pk[e] = Elem<__half>::from_f2(e0, e1);
           }
+          // over the columns of scores that have been used
           tc::tmem_st16u(ts + key0 / 2, pk);
         };
-#pragma unroll 1
-        for (int c = 0; c < kN; c += 64) {
-          tc::tmem_ld32(ts + c + 32, y);
-          probabilities(x, c);
-          tc::tmem_wait_ld();
-          arrived(y);
-          if (c == 0) tc::tmem_ld32(ts + 64, x);
-          probabilities(y, c + 32);
+        auto row = [&](auto masked) {
+          tc::tmem_ld32(ts, x);
           tc::tmem_wait_ld();
           arrived(x);
-        }
+#pragma unroll 1
+          for (int c = 0; c < kN; c += 64) {
+            tc::tmem_ld32(ts + c + 32, y);
+            probabilities(masked, x, y, c);
+            tc::tmem_wait_ld();
+            arrived(y);
+            if (c == 0) tc::tmem_ld32(ts + 64, x);
+            probabilities(masked, y, x, c + 32);
+            tc::tmem_wait_ld();
+            arrived(x);
+          }
+        };
+        if (__all_sync(0xffffffffu, whole))
+          row(std::false_type{});
+        else
+          row(std::true_type{});
         const float2 sum = halves(add2(add2(sum2[0], sum2[1]), add2(sum2[2], sum2[3])));
         l += sum.x + sum.y;
         if (t > at.t0 && __any_sync(0xffffffffu, alpha != 1.f)) {
