@@ -173,6 +173,24 @@ __device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
                : "memory");
 }
 
+// Loads that stay where they are written: left to itself the compiler moves
+// them down to their uses to save registers, and they wait for one another.
+__device__ __forceinline__ uint4 load16(const void* src) {
+  uint4 x;
+  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+               : "l"(src));
+  return x;
+}
+__device__ __forceinline__ float4 load16_l2(const void* src) {  // past L1
+  float4 x;
+  asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+               : "l"(src)
+               : "memory");
+  return x;
+}
+
 // Two fp32 values at a time.
 __device__ __forceinline__ uint64_t pair(float a, float b) {
   uint64_t x;
@@ -325,35 +343,50 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   };
 
   // Q of the pair of segment `w` into buffer `buf`, by `threads` threads of
-  // whole warps: 16 (D = 64: 8) lanes a row, kBatch rows in flight a thread.
-  // A bf16 row is scaled by a power of two to a largest magnitude in [1, 2);
-  // a negative scale of K turns the signs, so that no score factor is negative.
+  // whole warps, 16 (D = 64: 8) lanes a row: copied to its place by cp.async,
+  // then turned in place where it is not yet as the MMAs read it -- a bf16 row
+  // is scaled by a power of two to a largest magnitude in [1, 2); a negative
+  // scale of K turns the signs, so that no score factor is negative.  Rolled
+  // loops: code that runs once a segment comes from far away, and unrolled this
+  // took 28000 cycles, nearly all of them waiting for instructions.
   auto stage_q = [&](const Walk& w, int buf, int i, int threads) {
-    constexpr int kLanes = D / 8, kBatch = 16;
+    constexpr int kLanes = D / 8;
     const int qc = i % kLanes, step = threads / kLanes;
     const uint32_t flip =
         p.k_scale != nullptr && __ldg(p.k_scale + w.h) < 0.f ? 0x80008000u : 0u;
     uint8_t* tile = sQ + buf * 2 * L::kTile + (qc >> 3) * L::kSlab;
+    auto place = [&](int r) {
+      const int rt = r & 127;
+      return tile + (r >> 7) * L::kTile + rt * 128 + (((qc & 7) ^ (rt & 7)) << 4);
+    };
     const T* base = reinterpret_cast<const T*>(p.q) + (int64_t)w.x.s.q0 * p.q_st +
                     (int64_t)(w.h * p.G) * p.q_sh + qc * 8;
+    // row = token * G + head: divided once, then carried on
+    int token = (w.rows0() + i / kLanes) / p.G, head = (w.rows0() + i / kLanes) % p.G;
+    const int step_t = step / p.G, step_h = step % p.G;
 #pragma unroll 1
-    for (int r0 = i / kLanes; r0 < kChunkRows; r0 += step * kBatch) {
-      uint4 x[kBatch];
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        // (rows behind the last are read as the last and stored as zeros)
-        const int row = min(w.rows0() + r0 + j * step, w.x.rows - 1);
-        x[j] = __ldg(reinterpret_cast<const uint4*>(base + (int64_t)(row / p.G) * p.q_st +
-                                                    (int64_t)(row % p.G) * p.q_sh));
+    for (int r = i / kLanes; r < kChunkRows; r += step) {
+      const bool live = w.rows0() + r < w.x.rows;
+      const T* src = live ? base + (int64_t)token * p.q_st + (int64_t)head * p.q_sh : base;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(place(r))),
+                   "l"(src), "r"(live ? 16 : 0)
+                   : "memory");
+      token += step_t;
+      head += step_h;
+      if (head >= p.G) {
+        head -= p.G;
+        ++token;
       }
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int r = r0 + j * step;
-        if (r >= kChunkRows) break;  // (uniform in a row's lanes)
-        const bool live = w.rows0() + r < w.x.rows;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    constexpr bool kTurn = !std::is_same<T, __half>::value;
+    if (kTurn || flip != 0) {
+#pragma unroll 2
+      for (int r = i / kLanes; r < kChunkRows; r += step) {
+        const uint4 x = *reinterpret_cast<const uint4*>(place(r));
+        uint32_t u[4] = {x.x, x.y, x.z, x.w};
         float f = 1.f;
-        uint32_t u[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-        if constexpr (!std::is_same<T, __half>::value) {
+        if constexpr (kTurn) {
           uint32_t top = 0;
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -372,13 +405,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             u[e] = Elem<__half>::from_f2(y.x * down, y.y * down);
           }
         }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) u[e] = live ? u[e] ^ flip : 0u;
-        const int rt = r & 127;
-        *reinterpret_cast<uint4*>(tile + (r >> 7) * L::kTile + rt * 128 +
-                                  (((qc & 7) ^ (rt & 7)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
+        *reinterpret_cast<uint4*>(place(r)) =
+            make_uint4(u[0] ^ flip, u[1] ^ flip, u[2] ^ flip, u[3] ^ flip);
         if (qc == 0) sF[r] = f;
       }
+    } else if (qc == 0) {
+      for (int r = i / kLanes; r < kChunkRows; r += step) sF[r] = 1.f;
     }
     fence_proxy_async_smem();
     __syncwarp();
@@ -505,8 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
           const int unit = ((t - at.t0) & 3) * kUnits + (i * kRowsAt + r0) / kPage;
-          x[i] = __ldg(reinterpret_cast<const uint4*>(
-              base + __shfl_sync(0xffffffffu, (long long)off, unit)));
+          x[i] = load16(base + __shfl_sync(0xffffffffu, (long long)off, unit));
         }
       };
       // Zeros at keys of tile t behind the last one.
@@ -747,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         wait(&pv_done[g], (uint32_t)((n - 1) & 1), 64 + g);
         tc::fence_after_sync();
         const float by = l == 0.f ? 0.f : vs / l;
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < D / 32; ++i) {
           float o[32];
           tc::tmem_ld32(tO(g) + lane_off + i * 32, o);
@@ -793,38 +824,58 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         named_barrier(1, 256);
         if (*sFlag) {
           __threadfence();
+          // the first row of the stream's split n, of this thread's group
+          auto from = [&](int cta) {
+            return ((int64_t)(2 * cta + (cta == cta0 ? 1 : 0)) * 2 + g) * kM;
+          };
           float ref = neg_inf(), sum = 0.f;
+          for (int cta = cta0; cta <= cta1; ++cta)
+            ref = fmaxf(ref, __ldcg(p.part_ml + from(cta) + r).x);
+          // a row's part of a split: 0 where the group had no tile (O unset)
+          auto weight = [&](float2 ml) {
+            return ml.x == neg_inf() ? 0.f : ml.x == ref ? 1.f : ex2(ml.x - ref);
+          };
           for (int cta = cta0; cta <= cta1; ++cta) {
-            const int64_t from = ((int64_t)(2 * cta + (cta == cta0 ? 1 : 0)) * 2 + g) * kM;
-            ref = fmaxf(ref, __ldcg(p.part_ml + from + r).x);
+            const float2 ml = __ldcg(p.part_ml + from(cta) + r);
+            sum = fmaf(weight(ml), ml.y, sum);
           }
-          float4 acc[D / 16];  // a quarter of the row at a time
+          const float by = sum == 0.f ? 0.f : vs / sum;
+          constexpr int kPart = D / 32;  // 16-byte chunks of an eighth of the row
 #pragma unroll 1
-          for (int part = 0; part < 4; ++part) {
+          for (int part = 0; part < 8; ++part) {
+            float4 acc[kPart];
 #pragma unroll
-            for (int e = 0; e < D / 16; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-            sum = 0.f;
-            for (int cta = cta0; cta <= cta1; ++cta) {
-              const int64_t from = ((int64_t)(2 * cta + (cta == cta0 ? 1 : 0)) * 2 + g) * kM;
-              const float2 ml = __ldcg(p.part_ml + from + r);
-              if (ml.y == 0.f && ml.x == neg_inf()) continue;  // no tile of the group's: O unset
-              const float w = ml.x == ref ? 1.f : ex2(ml.x - ref);
-              sum = fmaf(w, ml.y, sum);
+            for (int e = 0; e < kPart; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+            for (int cta = cta0; cta <= cta1; cta += 4) {  // four splits in flight
+              float4 y[4][kPart];
+              float w[4];
 #pragma unroll
-              for (int e = 0; e < D / 16; ++e) {
-                const float4 y = __ldcg(reinterpret_cast<const float4*>(
-                    p.part_o + (from * (D / 4) + (part * (D / 16) + e) * kM + r) * 4));
-                acc[e].x = fmaf(w, y.x, acc[e].x);
-                acc[e].y = fmaf(w, y.y, acc[e].y);
-                acc[e].z = fmaf(w, y.z, acc[e].z);
-                acc[e].w = fmaf(w, y.w, acc[e].w);
+              for (int j = 0; j < 4; ++j) {
+                const int64_t at_row = from(min(cta + j, cta1));
+                const float2 ml = __ldcg(p.part_ml + at_row + r);
+                w[j] = cta + j <= cta1 ? weight(ml) : 0.f;
+#pragma unroll
+                for (int e = 0; e < kPart; ++e)
+                  y[j][e] = load16_l2(p.part_o +
+                                      (at_row * (D / 4) + (part * kPart + e) * kM + r) * 4);
+              }
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                if (w[j] == 0.f) continue;  // (an unset O is not read)
+#pragma unroll
+                for (int e = 0; e < kPart; ++e) {
+                  acc[e].x = fmaf(w[j], y[j][e].x, acc[e].x);
+                  acc[e].y = fmaf(w[j], y[j][e].y, acc[e].y);
+                  acc[e].z = fmaf(w[j], y[j][e].z, acc[e].z);
+                  acc[e].w = fmaf(w[j], y[j][e].w, acc[e].w);
+                }
               }
             }
-            const float by = sum == 0.f ? 0.f : vs / sum;
             if (valid) {
 #pragma unroll
-              for (int e = 0; e < D / 16; e += 2)
-                *reinterpret_cast<uint4*>(out_row() + part * (D / 4) + e * 4) = make_uint4(
+              for (int e = 0; e < kPart; e += 2)
+                *reinterpret_cast<uint4*>(out_row() + part * (D / 8) + e * 4) = make_uint4(
                     E::from_f2(acc[e].x * by, acc[e].y * by), E::from_f2(acc[e].z * by, acc[e].w * by),
                     E::from_f2(acc[e + 1].x * by, acc[e + 1].y * by),
                     E::from_f2(acc[e + 1].z * by, acc[e + 1].w * by));
