@@ -368,8 +368,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           const uint4 x = *reinterpret_cast<const uint4*>(sk + slot_of<D>(key, hf * 4 + t));
           const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            mma16816(c[nt], qa[hf * 4 + e], f16x2_of(w[e] & 0xffffu), f16x2_of(w[e] >> 16));
+          for (int e = 0; e < 4; ++e) {
+            uint32_t b0, b1;
+            f16x4_of(w[e], b0, b1);
+            mma16816(c[nt], qa[hf * 4 + e], b0, b1);
+          }
         }
       }
       // softmax
@@ -475,10 +478,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         const uint32_t x1 = __byte_perm(v[2][w], v[3][w], 0x5140);
         const uint32_t y0 = __byte_perm(v[0][w], v[1][w], 0x7362);
         const uint32_t y1 = __byte_perm(v[2][w], v[3][w], 0x7362);
-        mma16816(o[4 * w], pa, f16x2_of(x0 & 0xffffu), f16x2_of(x1 & 0xffffu));
-        mma16816(o[4 * w + 1], pa, f16x2_of(x0 >> 16), f16x2_of(x1 >> 16));
-        mma16816(o[4 * w + 2], pa, f16x2_of(y0 & 0xffffu), f16x2_of(y1 & 0xffffu));
-        mma16816(o[4 * w + 3], pa, f16x2_of(y0 >> 16), f16x2_of(y1 >> 16));
+        uint32_t a0, a1, b0, b1;
+        f16x4_of(x0, a0, a1);
+        f16x4_of(x1, b0, b1);
+        mma16816(o[4 * w], pa, a0, b0);
+        mma16816(o[4 * w + 1], pa, a1, b1);
+        f16x4_of(y0, a0, a1);
+        f16x4_of(y1, b0, b1);
+        mma16816(o[4 * w + 2], pa, a0, b0);
+        mma16816(o[4 * w + 3], pa, a1, b1);
       }
     }
 

@@ -423,18 +423,26 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     // reads P_g from the same columns without a wait.
     const uint32_t id_s = tc::idesc_f16(kM, kN, false, false);
     const uint32_t id_o = tc::idesc_f16(kM, D, false, true);
-    const uint64_t dQ0 = tc::smem_desc(smem_u32(sQ), 16, 1024);
-    const uint64_t dK0 = tc::smem_desc(smem_u32(sKV), 16, 1024);
-    const uint64_t dV0 = tc::smem_desc(smem_u32(sKV), L::kSlab, 1024);
+    // Descriptors move in their low words alone (addresses stay below 2^18), and
+    // the high words are constants: the issuing thread's own instructions are
+    // what slows a stream of N = 128 MMAs.
+    const uint64_t d16 = tc::smem_desc(0, 16, 1024), dslab = tc::smem_desc(0, L::kSlab, 1024);
+    const uint32_t qlo = (uint32_t)d16 + (smem_u32(sQ) >> 4), klo = (uint32_t)d16 + (smem_u32(sKV) >> 4);
+    const uint32_t vlo = (uint32_t)dslab + (smem_u32(sKV) >> 4);
+    auto desc = [](uint64_t base, uint32_t lo) {
+      uint64_t d;
+      asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"((uint32_t)(base >> 32)));
+      return d;
+    };
     int k = 0, a = 0, n0 = 0, n1 = 0, m0 = 0, m1 = 0;
     auto scores = [&](int g, int s) {
       if (lane == 0) {
-        const uint64_t dQ = dQ0 + (uint32_t)((((a & 1) * 2 + g) * L::kTile) >> 4);
-        const uint64_t dK = dK0 + (uint32_t)((s * L::kTile) >> 4);
+        const uint32_t q0 = qlo + (uint32_t)((((a & 1) * 2 + g) * L::kTile) >> 4);
+        const uint32_t k0 = klo + (uint32_t)((s * L::kTile) >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = ((kk >> 2) * L::kSlab + (kk & 3) * 32) >> 4;
-          tc::mma_f16_ss(tS(g), dQ + off, dK + off, id_s, kk > 0);
+          tc::mma_f16_ss(tS(g), desc(d16, q0 + off), desc(d16, k0 + off), id_s, kk > 0);
         }
         tc::commit(&s_full[g]);
       }
@@ -457,25 +465,25 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         const int sv = v % L::kRing, sk = kn % L::kRing;
         wait(&full[sv], (uint32_t)((v / L::kRing) & 1), 50);
         if (t + 1 < end) wait(&full[sk], (uint32_t)((kn / L::kRing) & 1), 41);
-#pragma unroll
+#pragma unroll 1
         for (int g = 0; g < 2; ++g) {
           const int gend = g ? end1 : end0;
           if (t < gend) {
-            int& n = g ? n1 : n0;
-            const int m = g ? m1 : m0;
+            const int n = g ? n1 : n0, m = g ? m1 : m0;
             wait(&p_full[g], (uint32_t)(n & 1), 51 + g);
             if (t == at.t0 && m >= 1) wait(&o_free[g], (uint32_t)((m - 1) & 1), 53 + g);
             tc::fence_after_sync();
             if (lane == 0) {
-              const uint64_t dV = dV0 + (uint32_t)((sv * L::kTile) >> 4);
+              const uint32_t v0 = vlo + (uint32_t)((sv * L::kTile) >> 4);
 #pragma unroll
               for (int kk = 0; kk < kN / 16; ++kk)
-                tc::mma_f16_ts(tO(g), tS(g) + kk * 8, dV + (kk * 2048 >> 4), id_o,
+                tc::mma_f16_ts(tO(g), tS(g) + kk * 8, desc(dslab, v0 + (kk * 2048 >> 4)), id_o,
                                (t > at.t0 || kk > 0) ? 1u : 0u);
               tc::commit(&pv_done[g]);
             }
             __syncwarp();
-            ++n;
+            if (g) ++n1;
+            else ++n0;
             if (t + 1 < gend) scores(g, sk);
           }
         }
@@ -505,7 +513,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     constexpr int kChunks = D / 16;       // 16-byte chunks of a key
     constexpr int kRowsAt = 128 / kChunks;
     constexpr int kLoads = kN / kRowsAt;  // of a thread and tile
-    const int c = ct % kChunks, r0 = ct / kChunks;
+    // Chunk and key: eight lanes take four chunks of two neighbouring keys, whose
+    // swizzled places cover every bank once.
+    const int c = D == 128 ? (ct & 3) | ((ct >> 1) & 4) : ct & 3;
+    const int r0 = D == 128 ? ((ct >> 2) & 1) | ((ct >> 4) << 1) : ct >> 2;
     int k = 0;
     for (; at.left > 0; at.next(p)) {
       const int32_t* trow = p.block_table + (int64_t)at.b * p.bt_stride;
@@ -554,22 +565,19 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       // the first row of the pair sees the least
       const int least = seen(p, at.x, at.rows0());
       auto store = [&](uint8_t* tile, const uint4 (&x)[kLoads]) {
-        // Eight lanes store a row of D = 128: those of the two slabs would meet
-        // in the same banks, so they store their two chunks in opposite order.
-        const int odd = D == 128 ? (c >> 2) : 0;
         uint8_t* slab = tile + (c >> 2) * L::kSlab;
+        const int c0 = 2 * (c & 3);
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
           const int r = i * kRowsAt + r0;
-          const uint32_t w0 = odd ? x[i].z : x[i].x, w1 = odd ? x[i].w : x[i].y;
-          const uint32_t w2 = odd ? x[i].x : x[i].z, w3 = odd ? x[i].y : x[i].w;
-          const int c0 = 2 * (c & 3) + odd, c1 = 2 * (c & 3) + 1 - odd;
+          const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          uint32_t h[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) f16x4_of(w[e], h[2 * e], h[2 * e + 1]);
           *reinterpret_cast<uint4*>(slab + r * 128 + ((c0 ^ (r & 7)) << 4)) =
-              make_uint4(f16x2_of(w0 & 0xffffu), f16x2_of(w0 >> 16), f16x2_of(w1 & 0xffffu),
-                         f16x2_of(w1 >> 16));
-          *reinterpret_cast<uint4*>(slab + r * 128 + ((c1 ^ (r & 7)) << 4)) =
-              make_uint4(f16x2_of(w2 & 0xffffu), f16x2_of(w2 >> 16), f16x2_of(w3 & 0xffffu),
-                         f16x2_of(w3 >> 16));
+              make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(slab + r * 128 + (((c0 + 1) ^ (r & 7)) << 4)) =
+              make_uint4(h[4], h[5], h[6], h[7]);
         }
       };
       auto done = [&](int s) {
@@ -656,13 +664,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         const uint32_t ts = tS(g) + lane_off;
         const int lim = sees - t * kN;  // keys [0, lim) of the tile are seen
         const bool whole = lim >= kN;
-        // One pass over the row's scores, 32 at a time with the next 32 under
-        // way.  A rolled loop: unrolled over the tile, this code is as large as
-        // the instruction cache and every warp streams it.
-        float x[32], y[32];
+        // One pass over the row's scores, 32 at a time in a rolled loop: the
+        // loads take 40 cycles, but unrolled over the tile the code of the
+        // roles passes what the instruction caches hold, and every warp waits
+        // for instructions.
+        float v[32];
         uint64_t sum2[4] = {0, 0, 0, 0};  // four pairs of sums
         float alpha = 1.f;
-        auto probabilities = [&](auto masked, float (&v)[32], float (&coming)[32], int key0) {
+        auto probabilities = [&](auto masked, int key0) {
           const int left = lim - key0;
           if constexpr (masked) {
 #pragma unroll
@@ -676,8 +685,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             // References are whole numbers, so what is scaled here is scaled
             // by powers of two: this tile's sums and probabilities so far, and
             // after the loop O.
-            tc::tmem_wait_ld();
-            arrived(coming);
             float by = 1.f;
             if (top > m + (kE4m3Shift + kE4m3Slack)) {
               const float to = ceilf(top) - kE4m3Shift;
@@ -711,19 +718,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           tc::tmem_st16u(ts + key0 / 2, pk);
         };
         auto row = [&](auto masked) {
-          tc::tmem_ld32(ts, x);
-          tc::tmem_wait_ld();
-          arrived(x);
 #pragma unroll 1
-          for (int c = 0; c < kN; c += 64) {
-            tc::tmem_ld32(ts + c + 32, y);
-            probabilities(masked, x, y, c);
+          for (int c = 0; c < kN; c += 32) {
+            tc::tmem_ld32(ts + c, v);
             tc::tmem_wait_ld();
-            arrived(y);
-            if (c == 0) tc::tmem_ld32(ts + 64, x);
-            probabilities(masked, y, x, c + 32);
-            tc::tmem_wait_ld();
-            arrived(x);
+            arrived(v);
+            probabilities(masked, c);
           }
         };
         if (__all_sync(0xffffffffu, whole))
