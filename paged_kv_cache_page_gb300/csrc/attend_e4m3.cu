@@ -49,7 +49,6 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRows = 16;       // query rows of a tile
 constexpr int kKeys = 16;       // keys of a unit
-constexpr int kStages = 5;      // units in a warp's ring
 constexpr int kMaxB = 4096;
 constexpr float kShift = kE4m3Shift, kSlack = kE4m3Slack;
 constexpr int kMinShare = 32;   // units
@@ -59,15 +58,17 @@ constexpr int kSmallRows = 64;
 
 template <int D>
 struct Layout {
+  static constexpr int kStages = D == 128 ? 6 : 12;        // units in a warp's ring
   static constexpr int kHalf = kKeys * D;                  // bytes of K (or V) in a stage
   static constexpr int kStage = 2 * kHalf;
   static constexpr int kRing = kStages * kStage;           // of a warp
-  static constexpr int kOffO = kWarps * kRing;             // float [kWarps][kRows][D]
-  static constexpr int kOffM = kOffO + kWarps * kRows * D * 4;
+  static constexpr int kOffO = kWarps * kRing;             // float [kWarps][8 rows][D]
+  static constexpr int kOffM = kOffO + kWarps * 8 * D * 4;
   static constexpr int kOffL = kOffM + kWarps * kRows * 4;
   static constexpr int kOffFlag = kOffL + kWarps * kRows * 4;
   static constexpr int kOffSums = kOffO;  // long long [kThreads + kWarps], before the first merge
   static constexpr int kBytes = kOffFlag + 16;
+  static_assert(kBytes <= 232448, "shared memory");
 };
 
 struct Seq {
@@ -86,6 +87,10 @@ __device__ __forceinline__ Seq load_seq(const AttendParams& p, int b, bool tell)
 
 __device__ __forceinline__ long long units_of(const AttendParams& p, const Seq& s) {
   return (long long)s.units * s.tiles * p.Hkv;
+}
+
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
 // A position in a CTA's share: one segment (units [u, u + len) of a stream).
@@ -158,6 +163,22 @@ __device__ __forceinline__ int key_of(int n, int j, int t) {
   return D == 128 ? 8 * n + t + 4 * j : 8 * n + 2 * t + j;
 }
 
+// Columns (bit hf D / 8 + e of x and y: column (2 t + hf) D / 8 + e) in which V
+// has a NaN at one of the unit's first end0 (x), end1 (y) keys.
+template <int D>
+__device__ __noinline__ uint2 nan_columns(const uint8_t* sv, int t, int end0, int end1) {
+  uint2 hit = make_uint2(0, 0);
+  for (int i = 0; i < D / 4; ++i) {
+    const int col = t * (D / 4) + i;
+    for (int key = 0; key < kKeys; ++key) {
+      if ((sv[slot_of<D>(key, col >> 4) + (col & 15)] & 0x7f) != 0x7f) continue;
+      if (key < end0) hit.x |= 1u << i;
+      if (key < end1) hit.y |= 1u << i;
+    }
+  }
+  return hit;
+}
+
 template <int D, typename T>
 __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_constant__
                                                                  AttendParams p) {
@@ -198,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   }
   sSums[tid] = incl;
   __syncthreads();
-  long long share = (total + gridDim.x - 1) / gridDim.x;
+  long long share = quotient(total + gridDim.x - 1, gridDim.x);
   share = max((share + kWarps - 1) / kWarps * kWarps, (long long)kMinShare);
   const long long first = share * blockIdx.x;
   if (first >= total) {
@@ -217,8 +238,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       off -= units_of(p, at.s);
       at.s = load_seq(p, ++at.b, false);
     }
-    at.h = (int)(off / ((long long)at.s.units * at.s.tiles));
-    const int rest = (int)(off % ((long long)at.s.units * at.s.tiles));
+    const long long head = (long long)at.s.units * at.s.tiles;
+    at.h = (int)quotient(off, head);
+    const int rest = (int)(off - at.h * head);
     at.tile = rest / at.s.units;
     at.u = rest % at.s.units;
     at.left = min(share, total - first);
@@ -228,18 +250,27 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   __syncthreads();  // sSums lies where the segments' results go
 
   // ---- the warp's copies: unit i of a segment, i = warp, warp + 8, ...
+  constexpr int kChunks = D / 16, kRowsAt = 32 / kChunks;  // keys a warp copies at a time
+  const int my_c = lane % kChunks, my_r = lane / kChunks;
   const uint32_t ring = smem_u32(smem) + warp * L::kRing;
+  const int64_t k_lane = (int64_t)my_r * p.k_st + my_c * 16, v_lane = (int64_t)my_r * p.v_st + my_c * 16;
+  const int64_t k_next = (int64_t)kRowsAt * p.k_st, v_next = (int64_t)kRowsAt * p.v_st;
   Cursor ahead = at;
   int a_i = warp, a_seen = ahead.seen(p), entry = 0;
+  const uint8_t *k_head = p.k_cache + ahead.h * p.k_sh + k_lane,
+                *v_head = p.v_cache + ahead.h * p.v_sh + v_lane;
+  const int32_t* a_row = p.block_table + (int64_t)ahead.b * p.bt_stride;
   auto find = [&]() {  // moves to the warp's next unit and reads its table entry
     while (ahead.left > 0 && a_i >= a_seen) {
       ahead.next(p);
+      if (ahead.left <= 0) return;
       a_i = warp;
-      a_seen = ahead.left > 0 ? ahead.seen(p) : 0;
+      a_seen = ahead.seen(p);
+      k_head = p.k_cache + ahead.h * p.k_sh + k_lane;
+      v_head = p.v_cache + ahead.h * p.v_sh + v_lane;
+      a_row = p.block_table + (int64_t)ahead.b * p.bt_stride;
     }
-    if (ahead.left > 0)
-      entry = __ldg(p.block_table + (int64_t)ahead.b * p.bt_stride +
-                    ((ahead.u + a_i) >> p.page_shift));
+    if (ahead.left > 0) entry = __ldg(a_row + ((ahead.u + a_i) >> p.page_shift));
   };
   auto copy = [&](int stage) {
     if (ahead.left > 0) {
@@ -251,20 +282,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       }
       const int row0 = (unit & ((1 << p.page_shift) - 1)) * kKeys;
       const uint32_t dst = ring + stage * L::kStage;
-      constexpr int kChunks = D / 16, kRowsAt = 32 / kChunks;
-      const int c = lane % kChunks, r0 = lane / kChunks;
-      const uint8_t* ks = p.k_cache + page * p.k_sb + ahead.h * p.k_sh + (row0 + r0) * p.k_st + c * 16;
-      const uint8_t* vs = p.v_cache + page * p.v_sb + ahead.h * p.v_sh + (row0 + r0) * p.v_st + c * 16;
+      const uint8_t* ks = k_head + ((int64_t)page * p.k_sb + (int64_t)row0 * p.k_st);
+      const uint8_t* vs = v_head + ((int64_t)page * p.v_sb + (int64_t)row0 * p.v_st);
       const int valid = ahead.s.lk - unit * kKeys;  // rows of the unit that hold a key
 #pragma unroll
       for (int i = 0; i < kKeys / kRowsAt; ++i) {
-        const int r = r0 + i * kRowsAt;
-        cp_async16(dst + slot_of<D>(r, c), ks + (int64_t)(i * kRowsAt) * p.k_st, r < valid);
-      }
-#pragma unroll
-      for (int i = 0; i < kKeys / kRowsAt; ++i) {
-        const int r = r0 + i * kRowsAt;
-        cp_async16(dst + L::kHalf + slot_of<D>(r, c), vs + (int64_t)(i * kRowsAt) * p.v_st, r < valid);
+        const int r = my_r + i * kRowsAt;
+        const uint32_t to = dst + slot_of<D>(r, my_c);
+        cp_async16(to, ks, r < valid);
+        cp_async16(to + L::kHalf, vs, r < valid);
+        ks += k_next;
+        vs += v_next;
       }
       a_i += kWarps;
       find();
@@ -272,8 +300,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     cp_commit();  // an empty group where nothing is left keeps the count
   };
   find();
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) copy(i);
+#pragma unroll 1
+  for (int i = 0; i < L::kStages; ++i) copy(i);
   int stage = 0;
 
   // ---- segments
@@ -348,47 +376,65 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     float m[2] = {neg_inf(), neg_inf()}, l[2] = {0.f, 0.f};  // m: the reference less kShift
 
     const int n = at.seen(p);
-    for (int i = warp; i < n; i += kWarps) {
-      cp_wait<kStages - 2>();
-      __syncwarp();  // every lane's copies of the unit; and the last unit's stage is free
-      copy(stage == 0 ? kStages - 1 : stage - 1);
-      const uint8_t* sk = smem + warp * L::kRing + stage * L::kStage;
-      const uint8_t* sv = sk + L::kHalf;
-      stage = stage + 1 == kStages ? 0 : stage + 1;
-      // S
-      float c[2][4];
+    // N of the warp's units at a time (two where there are two: twice the
+    // independent work for the same waits): i, i + 8.
+    auto step = [&](auto units, int i) {
+      constexpr int N = decltype(units)::value;
+      cp_wait<L::kStages - N>();
+      __syncwarp();  // every lane's copies of the units
+      const uint8_t* sk[N];
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
+      for (int u = 0; u < N; ++u) {
+        int at_stage = stage + u;
+        if (at_stage >= L::kStages) at_stage -= L::kStages;
+        sk[u] = smem + warp * L::kRing + at_stage * L::kStage;
+      }
+      // S: c[2 u + nt] is key tile nt of unit u
+      float c[2 * N][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) c[nt][e] = 0.f;
-        // column g of the tile: the inverse of key_of
-        const int key = D == 128 ? 8 * nt + (g >> 1) + 4 * (g & 1) : 8 * nt + g;
+      for (int x = 0; x < 2 * N; ++x)
 #pragma unroll
-        for (int hf = 0; hf < D / 64; ++hf) {
-          const uint4 x = *reinterpret_cast<const uint4*>(sk + slot_of<D>(key, hf * 4 + t));
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        for (int e = 0; e < 4; ++e) c[x][e] = 0.f;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
+      for (int hf = 0; hf < D / 64; ++hf) {
+        uint4 x[2 * N];
+#pragma unroll
+        for (int y = 0; y < 2 * N; ++y) {
+          // column g of the tile: the inverse of key_of
+          const int key = D == 128 ? 8 * (y & 1) + (g >> 1) + 4 * (g & 1) : 8 * (y & 1) + g;
+          x[y] = *reinterpret_cast<const uint4*>(sk[y >> 1] + slot_of<D>(key, hf * 4 + t));
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int y = 0; y < 2 * N; ++y) {
+            const uint32_t w[4] = {x[y].x, x[y].y, x[y].z, x[y].w};
             uint32_t b0, b1;
             f16x4_of(w[e], b0, b1);
-            mma16816(c[nt], qa[hf * 4 + e], b0, b1);
+            mma16816(c[y], qa[hf * 4 + e], b0, b1);
           }
-        }
       }
       // softmax
-      const int key0 = (at.u + i) * kKeys;
-      const bool part = key0 + kKeys > all;  // some row does not see all of the unit
+      const int key0 = (at.u + i) * kKeys;  // unit u: key0 + 128 u
+      const bool part = key0 + (N - 1) * kWarps * kKeys + kKeys > all;  // not seen whole by every row
       if (part) {
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
+        for (int y = 0; y < 2 * N; ++y)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (key0 + key_of<D>(nt, e & 1, t) >= lim[e >> 1]) c[nt][e] = neg_inf();
+            if (key0 + (y >> 1) * kWarps * kKeys + key_of<D>(y & 1, e & 1, t) >= lim[e >> 1])
+              c[y][e] = neg_inf();
       }
-      const float top0 = fmaxf(fmaxf(c[0][0], c[0][1]), fmaxf(c[1][0], c[1][1])) * f[0];
-      const float top1 = fmaxf(fmaxf(c[0][2], c[0][3]), fmaxf(c[1][2], c[1][3])) * f[1];
-      if (__any_sync(0xffffffffu, top0 > m[0] + (kShift + kSlack) || top1 > m[1] + (kShift + kSlack))) {
-        float top[2] = {top0, top1};
+      float top[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        top[j] = fmaxf(c[0][2 * j], c[0][2 * j + 1]);
+#pragma unroll
+        for (int y = 1; y < 2 * N; ++y) top[j] = max3(top[j], c[y][2 * j], c[y][2 * j + 1]);
+        top[j] *= f[j];
+      }
+      if (__any_sync(0xffffffffu,
+                     top[0] > m[0] + (kShift + kSlack) || top[1] > m[1] + (kShift + kSlack))) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], 1));
@@ -407,116 +453,117 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       // a row that has seen no key yet has the reference -inf: 0 stands in
       const float m0 = m[0] == neg_inf() ? 0.f : m[0], m1 = m[1] == neg_inf() ? 0.f : m[1];
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        c[nt][0] = ex2(fmaf(c[nt][0], f[0], -m0));
-        c[nt][1] = ex2(fmaf(c[nt][1], f[0], -m0));
-        c[nt][2] = ex2(fmaf(c[nt][2], f[1], -m1));
-        c[nt][3] = ex2(fmaf(c[nt][3], f[1], -m1));
+      for (int y = 0; y < 2 * N; ++y) {
+        c[y][0] = ex2(fmaf(c[y][0], f[0], -m0));
+        c[y][1] = ex2(fmaf(c[y][1], f[0], -m0));
+        c[y][2] = ex2(fmaf(c[y][2], f[1], -m1));
+        c[y][3] = ex2(fmaf(c[y][3], f[1], -m1));
       }
       if (part) {  // (a factor of zero turns -inf into NaN)
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
+        for (int y = 0; y < 2 * N; ++y)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (key0 + key_of<D>(nt, e & 1, t) >= lim[e >> 1]) c[nt][e] = 0.f;
+            if (key0 + (y >> 1) * kWarps * kKeys + key_of<D>(y & 1, e & 1, t) >= lim[e >> 1])
+              c[y][e] = 0.f;
       }
-      l[0] += (c[0][0] + c[0][1]) + (c[1][0] + c[1][1]);
-      l[1] += (c[0][2] + c[0][3]) + (c[1][2] + c[1][3]);
-      const uint32_t pa[4] = {Elem<__half>::from_f2(c[0][0], c[0][1]),
-                              Elem<__half>::from_f2(c[0][2], c[0][3]),
-                              Elem<__half>::from_f2(c[1][0], c[1][1]),
-                              Elem<__half>::from_f2(c[1][2], c[1][3])};
+      uint32_t pa[N][4];
+#pragma unroll
+      for (int u = 0; u < N; ++u) {
+        const float(&x)[4] = c[2 * u];
+        const float(&y)[4] = c[2 * u + 1];
+        l[0] += (x[0] + x[1]) + (y[0] + y[1]);
+        l[1] += (x[2] + x[3]) + (y[2] + y[3]);
+        pa[u][0] = Elem<__half>::from_f2(x[0], x[1]);
+        pa[u][1] = Elem<__half>::from_f2(x[2], x[3]);
+        pa[u][2] = Elem<__half>::from_f2(y[0], y[1]);
+        pa[u][3] = Elem<__half>::from_f2(y[2], y[3]);
+      }
       // O
-      constexpr int kWords = kO / 4;
-      uint32_t v[4][kWords];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int key = key_of<D>(e >> 1, e & 1, t);
-        if constexpr (D == 128) {
-          const uint4 x = *reinterpret_cast<const uint4*>(sv + slot_of<D>(key, g));
-          v[e][0] = x.x; v[e][1] = x.y; v[e][2] = x.z; v[e][3] = x.w;
-        } else {
-          const uint2 x = *reinterpret_cast<const uint2*>(sv + slot_of<D>(key, g >> 1) + (g & 1) * 8);
-          v[e][0] = x.x; v[e][1] = x.y;
+      for (int u = 0; u < N; ++u) {
+        const uint8_t* sv = sk[u] + L::kHalf;
+        constexpr int kWords = kO / 4;
+        uint32_t v[4][kWords];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int key = key_of<D>(e >> 1, e & 1, t);
+          if constexpr (D == 128) {
+            const uint4 x = *reinterpret_cast<const uint4*>(sv + slot_of<D>(key, g));
+            v[e][0] = x.x; v[e][1] = x.y; v[e][2] = x.z; v[e][3] = x.w;
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(sv + slot_of<D>(key, g >> 1) + (g & 1) * 8);
+            v[e][0] = x.x; v[e][1] = x.y;
+          }
         }
-      }
-      if (part) {
-        // A NaN in V at a key that only some rows see must not reach the
-        // others through 0 x NaN: it is taken out of the product here and put
-        // into the accumulators of the rows that do see it.
-        uint32_t bad = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-#pragma unroll
-          for (int w = 0; w < kWords; ++w)
-            bad |= nan_bytes(v[e][w]);
-        if (__any_sync(0xffffffffu, bad != 0)) {
+        if (part) {
+          // A NaN in V at a key that only some rows see must not reach the
+          // others through 0 x NaN: it is taken out of the product here and
+          // put into the accumulators of the rows that do see it.
+          uint32_t bad = 0;
 #pragma unroll
           for (int e = 0; e < 4; ++e)
 #pragma unroll
-            for (int w = 0; w < kWords; ++w) {
-              v[e][w] &= ~((nan_bytes(v[e][w]) >> 7) * 0xffu);
-            }
-          const int end0 = min(lim[0] - key0, kKeys), end1 = min(lim[1] - key0, kKeys);
+            for (int w = 0; w < kWords; ++w) bad |= nan_bytes(v[e][w]);
+          if (__any_sync(0xffffffffu, bad != 0)) {
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf)  // the lane's two runs of columns
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+              for (int w = 0; w < kWords; ++w) v[e][w] &= ~((nan_bytes(v[e][w]) >> 7) * 0xffu);
+            const int k0 = key0 + u * kWarps * kKeys;
+            const uint2 hit = nan_columns<D>(sv, t, min(lim[0] - k0, kKeys), min(lim[1] - k0, kKeys));
 #pragma unroll
             for (int e = 0; e < kO; ++e) {
-              const int col = (2 * t + hf) * kO + e;
-              for (int key = 0; key < kKeys; ++key) {
-                const uint8_t x = sv[slot_of<D>(key, col >> 4) + (col & 15)];
-                if ((x & 0x7f) != 0x7f) continue;
-                if (key < end0) o[e][hf] = __int_as_float(0x7fffffff);
-                if (key < end1) o[e][2 + hf] = __int_as_float(0x7fffffff);
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf) {
+                if ((hit.x >> (hf * kO + e)) & 1) o[e][hf] = __int_as_float(0x7fffffff);
+                if ((hit.y >> (hf * kO + e)) & 1) o[e][2 + hf] = __int_as_float(0x7fffffff);
               }
             }
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) {
+          const uint32_t x0 = __byte_perm(v[0][w], v[1][w], 0x5140);
+          const uint32_t x1 = __byte_perm(v[2][w], v[3][w], 0x5140);
+          const uint32_t y0 = __byte_perm(v[0][w], v[1][w], 0x7362);
+          const uint32_t y1 = __byte_perm(v[2][w], v[3][w], 0x7362);
+          uint32_t a0, a1, b0, b1;
+          f16x4_of(x0, a0, a1);
+          f16x4_of(x1, b0, b1);
+          mma16816(o[4 * w], pa[u], a0, b0);
+          mma16816(o[4 * w + 1], pa[u], a1, b1);
+          f16x4_of(y0, a0, a1);
+          f16x4_of(y1, b0, b1);
+          mma16816(o[4 * w + 2], pa[u], a0, b0);
+          mma16816(o[4 * w + 3], pa[u], a1, b1);
         }
       }
-#pragma unroll
-      for (int w = 0; w < kWords; ++w) {
-        const uint32_t x0 = __byte_perm(v[0][w], v[1][w], 0x5140);
-        const uint32_t x1 = __byte_perm(v[2][w], v[3][w], 0x5140);
-        const uint32_t y0 = __byte_perm(v[0][w], v[1][w], 0x7362);
-        const uint32_t y1 = __byte_perm(v[2][w], v[3][w], 0x7362);
-        uint32_t a0, a1, b0, b1;
-        f16x4_of(x0, a0, a1);
-        f16x4_of(x1, b0, b1);
-        mma16816(o[4 * w], pa, a0, b0);
-        mma16816(o[4 * w + 1], pa, a1, b1);
-        f16x4_of(y0, a0, a1);
-        f16x4_of(y1, b0, b1);
-        mma16816(o[4 * w + 2], pa, a0, b0);
-        mma16816(o[4 * w + 3], pa, a1, b1);
+      __syncwarp();  // the stages have been read
+#pragma unroll 1
+      for (int u = 0; u < N; ++u) {
+        copy(stage);
+        stage = stage + 1 == L::kStages ? 0 : stage + 1;
       }
-    }
+    };
+    int i = warp;
+#pragma unroll 1
+    for (; i + kWarps < n; i += 2 * kWarps) step(std::integral_constant<int, 2>{}, i);
+    if (i < n) step(std::integral_constant<int, 1>{}, i);
 
-    // ---- the warps' results: (m, l, O) of each, merged by column
+    // ---- the warps' results: (m, l, O) of each, merged by column, eight rows
+    // at a time
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       l[j] += __shfl_xor_sync(0xffffffffu, l[j], 1);
       l[j] += __shfl_xor_sync(0xffffffffu, l[j], 2);
-      const int r = g + 8 * j;
       if (t == 0) {
-        sM[warp * kRows + r] = m[j];
-        sL[warp * kRows + r] = l[j];
-      }
-      if (r < R) {
-        float* dst = sO + (warp * kRows + r) * D;
-#pragma unroll
-        for (int q4 = 0; q4 < kO / 2; ++q4) {  // 16-byte chunks of the lane's 2 kO columns
-          const int hf = q4 / (kO / 4), e = (q4 % (kO / 4)) * 4;
-          const int c = t * (kO / 2) + q4;
-          const int to = c ^ ((r & 1) | ((t << 1) & (D / 32 * 2 - 1)));
-          *reinterpret_cast<float4*>(dst + to * 4) =
-              make_float4(o[e][2 * j + hf], o[e + 1][2 * j + hf], o[e + 2][2 * j + hf],
-                          o[e + 3][2 * j + hf]);
-        }
+        sM[warp * kRows + g + 8 * j] = m[j];
+        sL[warp * kRows + g + 8 * j] = l[j];
       }
     }
-    __syncthreads();
     const bool whole = at.u == 0 && at.len == at.s.units;
     const long long stream1 = stream0 + at.s.units;
-    const int cta0 = (int)(stream0 / share), cta1 = (int)((stream1 - 1) / share);
     const int slot = 2 * blockIdx.x + (at.u == 0 ? 1 : 0);
     const float vs = p.v_scale != nullptr ? __ldg(p.v_scale + at.h) : 1.f;
     constexpr int kChunksO = D / 4;
@@ -533,33 +580,55 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         p.lse[(int64_t)h * p.total_q + at.s.q0 + i] =
             sum == 0.f ? neg_inf() : (ref + log2f(sum)) * kLn2;
     };
-    for (int x = tid; x < R * kChunksO; x += kThreads) {
-      const int r = x / kChunksO, c = x % kChunksO;
-      const int from = c ^ ((r & 1) | (((c / (kO / 2)) << 1) & (D / 32 * 2 - 1)));
-      float ref = neg_inf();
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) ref = fmaxf(ref, sM[w * kRows + r]);
-      float sum = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j = 0; j < 2; ++j) {
+      if (8 * j >= R) break;
+      if (j > 0) __syncthreads();  // the first eight rows have been read
+      if (g + 8 * j < R) {
+        float* dst = sO + (warp * 8 + g) * D;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float mw = sM[w * kRows + r];
-        const float by = mw == ref ? 1.f : ex2(mw - ref);
-        const float4 y = *reinterpret_cast<const float4*>(sO + (w * kRows + r) * D + from * 4);
-        sum = fmaf(by, sL[w * kRows + r], sum);
-        acc.x = fmaf(by, y.x, acc.x);
-        acc.y = fmaf(by, y.y, acc.y);
-        acc.z = fmaf(by, y.z, acc.z);
-        acc.w = fmaf(by, y.w, acc.w);
+        for (int q4 = 0; q4 < kO / 2; ++q4) {  // 16-byte chunks of the lane's 2 kO columns
+          const int hf = q4 / (kO / 4), e = (q4 % (kO / 4)) * 4;
+          const int c = t * (kO / 2) + q4;
+          const int to = c ^ ((g & 1) | ((t << 1) & (D / 32 * 2 - 1)));
+          *reinterpret_cast<float4*>(dst + to * 4) =
+              make_float4(o[e][2 * j + hf], o[e + 1][2 * j + hf], o[e + 2][2 * j + hf],
+                          o[e + 3][2 * j + hf]);
+        }
       }
-      if (whole) {
-        write_row(r, c, acc, ref, sum);
-      } else {
-        *reinterpret_cast<float4*>(p.part_o + ((int64_t)slot * kRows + r) * D + c * 4) = acc;
-        if (c == 0) p.part_ml[slot * kRows + r] = make_float2(ref, sum);
+      __syncthreads();
+#pragma unroll 1
+      for (int x = tid; x < min(R - 8 * j, 8) * kChunksO; x += kThreads) {
+        const int r = x / kChunksO, c = x % kChunksO;
+        const int from = c ^ ((r & 1) | (((c / (kO / 2)) << 1) & (D / 32 * 2 - 1)));
+        const float* ms = sM + r + 8 * j;
+        const float* ls = sL + r + 8 * j;
+        float ref = neg_inf();
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) ref = fmaxf(ref, ms[w * kRows]);
+        float sum = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float mw = ms[w * kRows];
+          const float by = mw == ref ? 1.f : ex2(mw - ref);
+          const float4 y = *reinterpret_cast<const float4*>(sO + (w * 8 + r) * D + from * 4);
+          sum = fmaf(by, ls[w * kRows], sum);
+          acc.x = fmaf(by, y.x, acc.x);
+          acc.y = fmaf(by, y.y, acc.y);
+          acc.z = fmaf(by, y.z, acc.z);
+          acc.w = fmaf(by, y.w, acc.w);
+        }
+        if (whole) {
+          write_row(r + 8 * j, c, acc, ref, sum);
+        } else {
+          *reinterpret_cast<float4*>(p.part_o + ((int64_t)slot * kRows + r + 8 * j) * D + c * 4) = acc;
+          if (c == 0) p.part_ml[slot * kRows + r + 8 * j] = make_float2(ref, sum);
+        }
       }
     }
     if (!whole) {
+      const int cta0 = (int)quotient(stream0, share), cta1 = (int)quotient(stream1 - 1, share);
       __threadfence();
       __syncthreads();
       if (tid == 0) *sFlag = arrive_last(p.words + cta0, launch_tag(), cta1 - cta0 + 1) ? 1 : 0;

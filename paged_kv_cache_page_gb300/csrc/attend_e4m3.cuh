@@ -44,8 +44,11 @@ __device__ __forceinline__ SeqRows seq_rows(const AttendParams& p, int b, bool t
   const int c0 = __ldg(p.cu_seqlens_q + b), c1 = __ldg(p.cu_seqlens_q + b + 1);
   s.q0 = min(max(c0, 0), p.total_q);
   s.qlen = min(max(c1, s.q0), p.total_q) - s.q0;
-  if (s.qlen == 0) return s;
-  s.lk = __ldg(p.seqlens_k + b);
+  s.lk = __ldg(p.seqlens_k + b);  // (not behind the offsets: one latency, not two)
+  if (s.qlen == 0) {
+    s.lk = 0;
+    return s;
+  }
   const long long cap = (long long)p.max_pages * (kPage << p.page_shift);
   if (s.lk < 0 || s.lk > p.max_seqlen_k || s.lk > cap) {
     if (tell) report(p.err, PA_DEVERR_LENGTH, b, s.lk);
@@ -68,6 +71,11 @@ __device__ __forceinline__ void f16x4_of(uint32_t w, uint32_t& lo, uint32_t& hi)
       "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
       : "=r"(lo), "=r"(hi)
       : "r"(w));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float x;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(x) : "f"(a), "f"(b), "f"(c));
+  return x;
 }
 // The sign bits (moved to bit 7) of the NaN bytes among four e4m3 values.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {

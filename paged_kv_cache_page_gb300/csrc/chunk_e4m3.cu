@@ -212,11 +212,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(x) : "l"(a), "l"(b));
   return x;
 }
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float x;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(x) : "f"(a), "f"(b), "f"(c));
-  return x;
-}
 
 // Ties 32 values of an asynchronous TMEM load to the wait in front of it, so
 // that nothing computed from them moves ahead of the wait.
