@@ -52,6 +52,9 @@ constexpr int kKeys = 16;       // keys of a unit
 constexpr int kMaxB = 4096;
 constexpr float kShift = kE4m3Shift, kSlack = kE4m3Slack;
 constexpr int kMinShare = 32;   // units
+// Side by side go twice as many heads while a CTA's share holds this many units
+// of each.
+constexpr int kMaxSide = 3, kSideUnits = 128;
 // Rows per kv head up to which a sequence runs here; longer query blocks fill
 // the 128-row tiles of the tcgen05 kernel.
 constexpr int kSmallRows = 64;
@@ -85,8 +88,9 @@ __device__ __forceinline__ Seq load_seq(const AttendParams& p, int b, bool tell)
   return s;
 }
 
-__device__ __forceinline__ long long units_of(const AttendParams& p, const Seq& s) {
-  return (long long)s.units * s.tiles * p.Hkv;
+// Units of one kv head, or of one group of them, of the sequence.
+__device__ __forceinline__ long long units_of(const Seq& s) {
+  return (long long)s.units * s.tiles;
 }
 
 __device__ __forceinline__ long long quotient(long long a, long long b) {
@@ -95,8 +99,9 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
 
 // A position in a CTA's share: one segment (units [u, u + len) of a stream).
 struct Cursor {
-  int b, h, tile, u, len;
-  long long left;  // units of the share from u on
+  int b, h, tile, u, len;  // h: group of neighbouring kv heads
+  long long left;          // units of the share from u on
+  int groups;
   Seq s;
 
   // Units of the segment that hold a key some row of the tile sees.
@@ -112,7 +117,7 @@ struct Cursor {
     if (left <= 0) return;
     if (++tile == s.tiles) {
       tile = 0;
-      if (++h == p.Hkv) {
+      if (++h == groups) {
         h = 0;
         do {
           if (++b >= p.B) {  // (lengths that change under the launch)
@@ -200,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   long long mine = 0;
   for (int i = 0; i < per; ++i) {
     const int b = tid * per + i;
-    if (b < p.B) mine += units_of(p, load_seq(p, b, blockIdx.x == 0));
+    if (b < p.B) mine += units_of(load_seq(p, b, blockIdx.x == 0));
   }
   long long incl = mine;
 #pragma unroll
@@ -219,8 +224,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   }
   sSums[tid] = incl;
   __syncthreads();
+  // Neighbouring kv heads side by side: 2^hw_log2 of them, each with 8 >> hw_log2
+  // of the warps.
+  int hw_log2 = 0;
+  while (hw_log2 < kMaxSide && (p.Hkv >> hw_log2) % 2 == 0 &&
+         total * p.Hkv >= ((long long)kSideUnits << hw_log2) * gridDim.x)
+    ++hw_log2;
+  const int hw = 1 << hw_log2, step_u = kWarps >> hw_log2;
+  const int my_u = warp & (step_u - 1), my_hh = warp >> (3 - hw_log2);
+  const int groups = p.Hkv >> hw_log2;
+  total *= groups;
   long long share = quotient(total + gridDim.x - 1, gridDim.x);
-  share = max((share + kWarps - 1) / kWarps * kWarps, (long long)kMinShare);
+  share = max((share + step_u - 1) & ~(long long)(step_u - 1), (long long)kMinShare);
   const long long first = share * blockIdx.x;
   if (first >= total) {
     griddep_wait();
@@ -230,15 +245,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   {
     int lo = 0;  // the first thread whose sum passes `first`
     for (int step = kThreads / 2; step > 0; step >>= 1)
-      if (sSums[lo + step - 1] <= first) lo += step;
-    long long off = first - (lo > 0 ? sSums[lo - 1] : 0);
+      if (sSums[lo + step - 1] * groups <= first) lo += step;
+    long long off = first - (lo > 0 ? sSums[lo - 1] * groups : 0);
+    at.groups = groups;
     at.b = lo * per;
     at.s = load_seq(p, at.b, false);
-    while (off >= units_of(p, at.s) && at.b + 1 < p.B) {
-      off -= units_of(p, at.s);
+    while (off >= units_of(at.s) * groups && at.b + 1 < p.B) {
+      off -= units_of(at.s) * groups;
       at.s = load_seq(p, ++at.b, false);
     }
-    const long long head = (long long)at.s.units * at.s.tiles;
+    const long long head = units_of(at.s);
     at.h = (int)quotient(off, head);
     const int rest = (int)(off - at.h * head);
     at.tile = rest / at.s.units;
@@ -249,25 +265,25 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
 
   __syncthreads();  // sSums lies where the segments' results go
 
-  // ---- the warp's copies: unit i of a segment, i = warp, warp + 8, ...
+  // ---- the warp's copies: units my_u, my_u + step_u, ... of a segment
   constexpr int kChunks = D / 16, kRowsAt = 32 / kChunks;  // keys a warp copies at a time
   const int my_c = lane % kChunks, my_r = lane / kChunks;
   const uint32_t ring = smem_u32(smem) + warp * L::kRing;
   const int64_t k_lane = (int64_t)my_r * p.k_st + my_c * 16, v_lane = (int64_t)my_r * p.v_st + my_c * 16;
   const int64_t k_next = (int64_t)kRowsAt * p.k_st, v_next = (int64_t)kRowsAt * p.v_st;
   Cursor ahead = at;
-  int a_i = warp, a_seen = ahead.seen(p), entry = 0;
-  const uint8_t *k_head = p.k_cache + ahead.h * p.k_sh + k_lane,
-                *v_head = p.v_cache + ahead.h * p.v_sh + v_lane;
+  int a_i = my_u, a_seen = ahead.seen(p), entry = 0;
+  const uint8_t *k_head = p.k_cache + (ahead.h * hw + my_hh) * p.k_sh + k_lane,
+                *v_head = p.v_cache + (ahead.h * hw + my_hh) * p.v_sh + v_lane;
   const int32_t* a_row = p.block_table + (int64_t)ahead.b * p.bt_stride;
   auto find = [&]() {  // moves to the warp's next unit and reads its table entry
     while (ahead.left > 0 && a_i >= a_seen) {
       ahead.next(p);
       if (ahead.left <= 0) return;
-      a_i = warp;
+      a_i = my_u;
       a_seen = ahead.seen(p);
-      k_head = p.k_cache + ahead.h * p.k_sh + k_lane;
-      v_head = p.v_cache + ahead.h * p.v_sh + v_lane;
+      k_head = p.k_cache + (ahead.h * hw + my_hh) * p.k_sh + k_lane;
+      v_head = p.v_cache + (ahead.h * hw + my_hh) * p.v_sh + v_lane;
       a_row = p.block_table + (int64_t)ahead.b * p.bt_stride;
     }
     if (ahead.left > 0) entry = __ldg(a_row + ((ahead.u + a_i) >> p.page_shift));
@@ -294,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         ks += k_next;
         vs += v_next;
       }
-      a_i += kWarps;
+      a_i += step_u;
       find();
     }
     cp_commit();  // an empty group where nothing is left keeps the count
@@ -308,7 +324,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   long long stream0 = first - at.u;  // first unit of the segment's stream
   for (;;) {
     const int R = min(kRows, at.s.qlen * p.G - at.tile * kRows);
-    const float ks = p.k_scale != nullptr ? __ldg(p.k_scale + at.h) : 1.f;
+    const int head = at.h * hw + my_hh;
+    const float ks = p.k_scale != nullptr ? __ldg(p.k_scale + head) : 1.f;
     uint32_t qa[kQ][4];
     float f[2];  // score factor of rows g, g + 8 (log2 domain)
     int lim[2];  // keys they see
@@ -317,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       const int r = g + 8 * j;
       const int row = at.tile * kRows + r;
       const bool live = r < R;
-      const int i = row / p.G, h = at.h * p.G + row % p.G;
+      const int i = row / p.G, h = head * p.G + row % p.G;
       lim[j] = p.causal && live ? min(at.s.lk, i + at.s.lk - at.s.qlen + 1) : at.s.lk;
       const T* src = reinterpret_cast<const T*>(p.q) + (int64_t)(at.s.q0 + (live ? i : 0)) * p.q_st +
                      (int64_t)(live ? h : 0) * p.q_sh;
@@ -377,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
 
     const int n = at.seen(p);
     // N of the warp's units at a time (two where there are two: twice the
-    // independent work for the same waits): i, i + 8.
+    // independent work for the same waits): i, i + step_u.
     auto step = [&](auto units, int i) {
       constexpr int N = decltype(units)::value;
       cp_wait<L::kStages - N>();
@@ -415,14 +432,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           }
       }
       // softmax
-      const int key0 = (at.u + i) * kKeys;  // unit u: key0 + 128 u
-      const bool part = key0 + (N - 1) * kWarps * kKeys + kKeys > all;  // not seen whole by every row
+      const int key0 = (at.u + i) * kKeys, key_step = step_u * kKeys;  // unit u: key0 + u key_step
+      const bool part = key0 + (N - 1) * key_step + kKeys > all;  // not seen whole by every row
       if (part) {
 #pragma unroll
         for (int y = 0; y < 2 * N; ++y)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (key0 + (y >> 1) * kWarps * kKeys + key_of<D>(y & 1, e & 1, t) >= lim[e >> 1])
+            if (key0 + (y >> 1) * key_step + key_of<D>(y & 1, e & 1, t) >= lim[e >> 1])
               c[y][e] = neg_inf();
       }
       float top[2];
@@ -464,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         for (int y = 0; y < 2 * N; ++y)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (key0 + (y >> 1) * kWarps * kKeys + key_of<D>(y & 1, e & 1, t) >= lim[e >> 1])
+            if (key0 + (y >> 1) * key_step + key_of<D>(y & 1, e & 1, t) >= lim[e >> 1])
               c[y][e] = 0.f;
       }
       uint32_t pa[N][4];
@@ -510,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             for (int e = 0; e < 4; ++e)
 #pragma unroll
               for (int w = 0; w < kWords; ++w) v[e][w] &= ~((nan_bytes(v[e][w]) >> 7) * 0xffu);
-            const int k0 = key0 + u * kWarps * kKeys;
+            const int k0 = key0 + u * key_step;
             const uint2 hit = nan_columns<D>(sv, t, min(lim[0] - k0, kKeys), min(lim[1] - k0, kKeys));
 #pragma unroll
             for (int e = 0; e < kO; ++e) {
@@ -546,9 +563,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         stage = stage + 1 == L::kStages ? 0 : stage + 1;
       }
     };
-    int i = warp;
+    int i = my_u;
 #pragma unroll 1
-    for (; i + kWarps < n; i += 2 * kWarps) step(std::integral_constant<int, 2>{}, i);
+    for (; i + step_u < n; i += 2 * step_u) step(std::integral_constant<int, 2>{}, i);
     if (i < n) step(std::integral_constant<int, 1>{}, i);
 
     // ---- the warps' results: (m, l, O) of each, merged by column, eight rows
@@ -565,11 +582,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     const bool whole = at.u == 0 && at.len == at.s.units;
     const long long stream1 = stream0 + at.s.units;
     const int slot = 2 * blockIdx.x + (at.u == 0 ? 1 : 0);
-    const float vs = p.v_scale != nullptr ? __ldg(p.v_scale + at.h) : 1.f;
     constexpr int kChunksO = D / 4;
-    auto write_row = [&](int r, int c, float4 x, float ref, float sum) {
+    auto write_row = [&](int hh, int r, int c, float4 x, float ref, float sum) {
       const int row = at.tile * kRows + r;
-      const int i = row / p.G, h = at.h * p.G + row % p.G;
+      const int i = row / p.G, h = (at.h * hw + hh) * p.G + row % p.G;
+      const float vs = p.v_scale != nullptr ? __ldg(p.v_scale + at.h * hw + hh) : 1.f;
       const float by = sum == 0.f ? 0.f : vs / sum;  // NaN sums stay NaN
       T* dst = reinterpret_cast<T*>(p.out) + ((int64_t)(at.s.q0 + i) * p.Hq + h) * D + c * 4;
       uint2 y;
@@ -597,22 +614,24 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         }
       }
       __syncthreads();
+      const int rows = min(R - 8 * j, 8);
 #pragma unroll 1
-      for (int x = tid; x < min(R - 8 * j, 8) * kChunksO; x += kThreads) {
-        const int r = x / kChunksO, c = x % kChunksO;
+      for (int x = tid; x < hw * rows * kChunksO; x += kThreads) {
+        const int hr = x / kChunksO, c = x % kChunksO;
+        const int hh = hr / rows, r = hr % rows, w0 = hh * step_u;  // the head's first warp
         const int from = c ^ ((r & 1) | (((c / (kO / 2)) << 1) & (D / 32 * 2 - 1)));
-        const float* ms = sM + r + 8 * j;
-        const float* ls = sL + r + 8 * j;
+        const float* ms = sM + w0 * kRows + r + 8 * j;
+        const float* ls = sL + w0 * kRows + r + 8 * j;
+        const float* os = sO + (w0 * 8 + r) * D + from * 4;
         float ref = neg_inf();
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) ref = fmaxf(ref, ms[w * kRows]);
+        for (int w = 0; w < step_u; ++w) ref = fmaxf(ref, ms[w * kRows]);
         float sum = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
+#pragma unroll 2
+        for (int w = 0; w < step_u; ++w) {
           const float mw = ms[w * kRows];
           const float by = mw == ref ? 1.f : ex2(mw - ref);
-          const float4 y = *reinterpret_cast<const float4*>(sO + (w * 8 + r) * D + from * 4);
+          const float4 y = *reinterpret_cast<const float4*>(os + w * 8 * D);
           sum = fmaf(by, ls[w * kRows], sum);
           acc.x = fmaf(by, y.x, acc.x);
           acc.y = fmaf(by, y.y, acc.y);
@@ -620,10 +639,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           acc.w = fmaf(by, y.w, acc.w);
         }
         if (whole) {
-          write_row(r + 8 * j, c, acc, ref, sum);
+          write_row(hh, r + 8 * j, c, acc, ref, sum);
         } else {
-          *reinterpret_cast<float4*>(p.part_o + ((int64_t)slot * kRows + r + 8 * j) * D + c * 4) = acc;
-          if (c == 0) p.part_ml[slot * kRows + r + 8 * j] = make_float2(ref, sum);
+          const int64_t to = ((int64_t)slot * kWarps + hh) * kRows + r + 8 * j;
+          *reinterpret_cast<float4*>(p.part_o + to * D + c * 4) = acc;
+          if (c == 0) p.part_ml[to] = make_float2(ref, sum);
         }
       }
     }
@@ -635,15 +655,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       __syncthreads();
       if (*sFlag) {
         __threadfence();
-        for (int x = tid; x < R * kChunksO; x += kThreads) {
-          const int r = x / kChunksO, c = x % kChunksO;
+#pragma unroll 1
+        for (int x = tid; x < hw * R * kChunksO; x += kThreads) {
+          const int hr = x / kChunksO, c = x % kChunksO;
+          const int hh = hr / R, r = hr % R;
           float ref = neg_inf(), sum = 0.f;
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
           for (int cta = cta0; cta <= cta1; ++cta) {
-            const int from = 2 * cta + (cta == cta0 ? 1 : 0);
-            const float2 ml = __ldcg(p.part_ml + from * kRows + r);
-            const float4 y = __ldcg(reinterpret_cast<const float4*>(
-                p.part_o + ((int64_t)from * kRows + r) * D + c * 4));
+            const int64_t from =
+                ((int64_t)(2 * cta + (cta == cta0 ? 1 : 0)) * kWarps + hh) * kRows + r;
+            const float2 ml = __ldcg(p.part_ml + from);
+            const float4 y = __ldcg(reinterpret_cast<const float4*>(p.part_o + from * D + c * 4));
             const float to = fmaxf(ref, ml.x);
             const float b0 = ref == to ? 1.f : ex2(ref - to), b1 = ml.x == to ? 1.f : ex2(ml.x - to);
             ref = to;
@@ -653,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             acc.z = fmaf(b1, y.z, acc.z * b0);
             acc.w = fmaf(b1, y.w, acc.w * b0);
           }
-          write_row(r, c, acc, ref, sum);
+          write_row(hh, r, c, acc, ref, sum);
         }
       }
     }
@@ -678,8 +701,8 @@ Workspace workspace_of(int D, bool chunks) {
   const size_t ctas = (size_t)num_sms();
   Workspace w{};
   w.ml = align256(ctas * 8);
-  w.o = w.ml + align256(ctas * 2 * kRows * 8);
-  w.total = w.o + align256(ctas * 2 * kRows * D * 4);
+  w.o = w.ml + align256(ctas * 2 * kWarps * kRows * 8);
+  w.total = w.o + align256(ctas * 2 * kWarps * kRows * D * 4);
   if (chunks) {
     w.chunk_words = w.total;
     w.chunk_ml = w.chunk_words + align256(ctas * 8);
