@@ -52,6 +52,7 @@ constexpr int kKeys = 16;       // keys of a unit
 constexpr int kMaxB = 4096;
 constexpr float kShift = kE4m3Shift, kSlack = kE4m3Slack;
 constexpr int kMinShare = 32;   // units
+constexpr int kWholeUnits = 64;  // streams of at most this many units are not split
 // Side by side go twice as many heads while a CTA's share holds this many units
 // of each.
 constexpr int kMaxSide = 3, kSideUnits = 128;
@@ -76,22 +77,22 @@ struct Layout {
 
 struct Seq {
   int q0, qlen, lk, units, tiles;  // tiles: 16-row tiles of a kv head
+  int cost;                        // of one tile's stream: its units, or 1 where none is split
 };
 
-__device__ __forceinline__ Seq load_seq(const AttendParams& p, int b, bool tell) {
+__device__ __forceinline__ Seq load_seq(const AttendParams& p, int b, bool whole, bool tell) {
   const SeqRows r = seq_rows(p, b, tell);
-  Seq s{r.q0, r.qlen, r.lk, 0, 0};
+  Seq s{r.q0, r.qlen, r.lk, 0, 0, 0};
   if ((long long)s.qlen * p.G > p.small_rows) s.qlen = 0;  // not this kernel's
   if (s.qlen == 0) return s;
   s.units = max(1, (s.lk + kKeys - 1) / kKeys);
+  s.cost = whole ? 1 : s.units;
   s.tiles = (s.qlen * p.G + kRows - 1) / kRows;
   return s;
 }
 
-// Units of one kv head, or of one group of them, of the sequence.
-__device__ __forceinline__ long long units_of(const Seq& s) {
-  return (long long)s.units * s.tiles;
-}
+// Cost of one kv head, or of one group of them, of the sequence.
+__device__ __forceinline__ long long cost_of(const Seq& s) { return (long long)s.cost * s.tiles; }
 
 __device__ __forceinline__ long long quotient(long long a, long long b) {
   return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
@@ -100,8 +101,9 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
 // A position in a CTA's share: one segment (units [u, u + len) of a stream).
 struct Cursor {
   int b, h, tile, u, len;  // h: group of neighbouring kv heads
-  long long left;          // units of the share from u on
+  long long left;          // cost of the share from u on
   int groups;
+  bool whole;              // streams are not split: each costs 1
   Seq s;
 
   // Units of the segment that hold a key some row of the tile sees.
@@ -112,7 +114,7 @@ struct Cursor {
     return min(len, max(0, (end + kKeys - 1) / kKeys - u));
   }
   __device__ __forceinline__ void next(const AttendParams& p) {
-    left -= len;
+    left -= whole ? 1 : len;
     u = len = 0;
     if (left <= 0) return;
     if (++tile == s.tiles) {
@@ -124,11 +126,11 @@ struct Cursor {
             left = 0;
             return;
           }
-          s = load_seq(p, b, false);
+          s = load_seq(p, b, whole, false);
         } while (s.units == 0);
       }
     }
-    len = (int)min((long long)s.units, left);
+    len = whole ? s.units : (int)min((long long)s.units, left);
   }
 };
 
@@ -201,12 +203,21 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   const int g = lane >> 2, t = lane & 3;
 
   // ---- the CTA's share
+  // Where the longest stream is short, none is split: the sums then count
+  // streams, otherwise units.
   const int per = (p.B + kThreads - 1) / kThreads;
   long long mine = 0;
+  int tiles = 0, longest = 0;
   for (int i = 0; i < per; ++i) {
     const int b = tid * per + i;
-    if (b < p.B) mine += units_of(load_seq(p, b, blockIdx.x == 0));
+    if (b >= p.B) break;
+    const Seq s = load_seq(p, b, false, blockIdx.x == 0);
+    mine += cost_of(s);
+    tiles += s.tiles;
+    longest = max(longest, s.units);
   }
+  const bool whole = __syncthreads_and(longest <= kWholeUnits) != 0;
+  if (whole) mine = tiles;
   long long incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -227,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   // Neighbouring kv heads side by side: 2^hw_log2 of them, each with 8 >> hw_log2
   // of the warps.
   int hw_log2 = 0;
-  while (hw_log2 < kMaxSide && (p.Hkv >> hw_log2) % 2 == 0 &&
+  while (!whole && hw_log2 < kMaxSide && (p.Hkv >> hw_log2) % 2 == 0 &&
          total * p.Hkv >= ((long long)kSideUnits << hw_log2) * gridDim.x)
     ++hw_log2;
   const int hw = 1 << hw_log2, step_u = kWarps >> hw_log2;
@@ -235,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   const int groups = p.Hkv >> hw_log2;
   total *= groups;
   long long share = quotient(total + gridDim.x - 1, gridDim.x);
-  share = max((share + step_u - 1) & ~(long long)(step_u - 1), (long long)kMinShare);
+  if (!whole) share = max((share + step_u - 1) & ~(long long)(step_u - 1), (long long)kMinShare);
   const long long first = share * blockIdx.x;
   if (first >= total) {
     griddep_wait();
@@ -248,19 +259,20 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       if (sSums[lo + step - 1] * groups <= first) lo += step;
     long long off = first - (lo > 0 ? sSums[lo - 1] * groups : 0);
     at.groups = groups;
+    at.whole = whole;
     at.b = lo * per;
-    at.s = load_seq(p, at.b, false);
-    while (off >= units_of(at.s) * groups && at.b + 1 < p.B) {
-      off -= units_of(at.s) * groups;
-      at.s = load_seq(p, ++at.b, false);
+    at.s = load_seq(p, at.b, whole, false);
+    while (off >= cost_of(at.s) * groups && at.b + 1 < p.B) {
+      off -= cost_of(at.s) * groups;
+      at.s = load_seq(p, ++at.b, whole, false);
     }
-    const long long head = units_of(at.s);
+    const long long head = cost_of(at.s);
     at.h = (int)quotient(off, head);
     const int rest = (int)(off - at.h * head);
-    at.tile = rest / at.s.units;
-    at.u = rest % at.s.units;
+    at.tile = rest / at.s.cost;
+    at.u = rest % at.s.cost;
     at.left = min(share, total - first);
-    at.len = (int)min((long long)(at.s.units - at.u), at.left);
+    at.len = whole ? at.s.units : (int)min((long long)(at.s.units - at.u), at.left);
   }
 
   __syncthreads();  // sSums lies where the segments' results go
@@ -272,26 +284,38 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   const int64_t k_lane = (int64_t)my_r * p.k_st + my_c * 16, v_lane = (int64_t)my_r * p.v_st + my_c * 16;
   const int64_t k_next = (int64_t)kRowsAt * p.k_st, v_next = (int64_t)kRowsAt * p.v_st;
   Cursor ahead = at;
-  int a_i = my_u, a_seen = ahead.seen(p), entry = 0;
+  int a_i = my_u, a_seen = ahead.seen(p);
+  // Table entries of the warp's next 32 units of the segment, one a lane, from
+  // unit e_from on: one latency for all of them.
+  int entries = 0, e_from = 0;
   const uint8_t *k_head = p.k_cache + (ahead.h * hw + my_hh) * p.k_sh + k_lane,
                 *v_head = p.v_cache + (ahead.h * hw + my_hh) * p.v_sh + v_lane;
   const int32_t* a_row = p.block_table + (int64_t)ahead.b * p.bt_stride;
-  auto find = [&]() {  // moves to the warp's next unit and reads its table entry
+  auto read_entries = [&]() {
+    e_from = a_i;
+    const int i = a_i + lane * step_u;
+    if (ahead.left > 0 && i < a_seen) entries = __ldg(a_row + ((ahead.u + i) >> p.page_shift));
+  };
+  auto find = [&]() {  // moves to the warp's next unit
+    if (a_i < a_seen) {
+      if (a_i == e_from + 32 * step_u) read_entries();
+      return;
+    }
     while (ahead.left > 0 && a_i >= a_seen) {
       ahead.next(p);
       if (ahead.left <= 0) return;
       a_i = my_u;
       a_seen = ahead.seen(p);
-      k_head = p.k_cache + (ahead.h * hw + my_hh) * p.k_sh + k_lane;
-      v_head = p.v_cache + (ahead.h * hw + my_hh) * p.v_sh + v_lane;
-      a_row = p.block_table + (int64_t)ahead.b * p.bt_stride;
     }
-    if (ahead.left > 0) entry = __ldg(a_row + ((ahead.u + a_i) >> p.page_shift));
+    k_head = p.k_cache + (ahead.h * hw + my_hh) * p.k_sh + k_lane;
+    v_head = p.v_cache + (ahead.h * hw + my_hh) * p.v_sh + v_lane;
+    a_row = p.block_table + (int64_t)ahead.b * p.bt_stride;
+    read_entries();
   };
   auto copy = [&](int stage) {
     if (ahead.left > 0) {
       const int unit = ahead.u + a_i;
-      int page = entry;
+      int page = __shfl_sync(0xffffffffu, entries, (a_i - e_from) >> (3 - hw_log2));
       if (page < 0 || page >= p.num_pages) {
         if (lane == 0 && unit * kKeys < ahead.s.lk) report(p.err, PA_DEVERR_PAGE_OOB, ahead.b, unit);
         page = 0;
@@ -315,7 +339,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     }
     cp_commit();  // an empty group where nothing is left keeps the count
   };
-  find();
+  if (a_i < a_seen)
+    read_entries();
+  else
+    find();
 #pragma unroll 1
   for (int i = 0; i < L::kStages; ++i) copy(i);
   int stage = 0;
@@ -579,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         sL[warp * kRows + g + 8 * j] = l[j];
       }
     }
-    const bool whole = at.u == 0 && at.len == at.s.units;
+    const bool done = at.u == 0 && at.len == at.s.units;  // not split
     const long long stream1 = stream0 + at.s.units;
     const int slot = 2 * blockIdx.x + (at.u == 0 ? 1 : 0);
     constexpr int kChunksO = D / 4;
@@ -638,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           acc.z = fmaf(by, y.z, acc.z);
           acc.w = fmaf(by, y.w, acc.w);
         }
-        if (whole) {
+        if (done) {
           write_row(hh, r + 8 * j, c, acc, ref, sum);
         } else {
           const int64_t to = ((int64_t)slot * kWarps + hh) * kRows + r + 8 * j;
@@ -647,37 +674,75 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         }
       }
     }
-    if (!whole) {
+    if (!done) {
       const int cta0 = (int)quotient(stream0, share), cta1 = (int)quotient(stream1 - 1, share);
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) *sFlag = arrive_last(p.words + cta0, launch_tag(), cta1 - cta0 + 1) ? 1 : 0;
+      __syncthreads();  // the partial rows of the CTA before its arrival
+      if (tid == 0) {
+        __threadfence();
+        *sFlag = arrive_last(p.words + cta0, launch_tag(), cta1 - cta0 + 1) ? 1 : 0;
+        __threadfence();
+      }
       __syncthreads();
       if (*sFlag) {
-        __threadfence();
+        // A chunks of rows and C splits in flight a thread
+        auto join = [&](auto rows_at_once, auto splits_at_once) {
+          constexpr int A = decltype(rows_at_once)::value, C = decltype(splits_at_once)::value;
 #pragma unroll 1
-        for (int x = tid; x < hw * R * kChunksO; x += kThreads) {
-          const int hr = x / kChunksO, c = x % kChunksO;
-          const int hh = hr / R, r = hr % R;
-          float ref = neg_inf(), sum = 0.f;
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-          for (int cta = cta0; cta <= cta1; ++cta) {
-            const int64_t from =
-                ((int64_t)(2 * cta + (cta == cta0 ? 1 : 0)) * kWarps + hh) * kRows + r;
-            const float2 ml = __ldcg(p.part_ml + from);
-            const float4 y = __ldcg(reinterpret_cast<const float4*>(p.part_o + from * D + c * 4));
-            const float to = fmaxf(ref, ml.x);
-            const float b0 = ref == to ? 1.f : ex2(ref - to), b1 = ml.x == to ? 1.f : ex2(ml.x - to);
-            ref = to;
-            sum = fmaf(b1, ml.y, sum * b0);
-            acc.x = fmaf(b1, y.x, acc.x * b0);
-            acc.y = fmaf(b1, y.y, acc.y * b0);
-            acc.z = fmaf(b1, y.z, acc.z * b0);
-            acc.w = fmaf(b1, y.w, acc.w * b0);
+          for (int x0 = tid; x0 < hw * R * kChunksO; x0 += A * kThreads) {
+            float ref[A], sum[A];
+            float4 acc[A];
+            int row[A];  // of a split's rows
+            const int c = x0 % kChunksO;
+#pragma unroll
+            for (int k = 0; k < A; ++k) {
+              const int hr = min((x0 + k * kThreads) / kChunksO, hw * R - 1);
+              row[k] = (hr / R) * kRows + hr % R;
+              ref[k] = neg_inf();
+              sum[k] = 0.f;
+              acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll 1
+            for (int cta = cta0; cta <= cta1; cta += C) {
+              float2 ml[C][A];
+              float4 y[C][A];
+#pragma unroll
+              for (int j = 0; j < C; ++j) {
+                const int s = min(cta + j, cta1);
+                const int64_t from = (int64_t)(2 * s + (s == cta0 ? 1 : 0)) * kWarps * kRows;
+#pragma unroll
+                for (int k = 0; k < A; ++k) {
+                  ml[j][k] = __ldcg(p.part_ml + from + row[k]);
+                  y[j][k] = __ldcg(reinterpret_cast<const float4*>(p.part_o + (from + row[k]) * D + c * 4));
+                }
+              }
+#pragma unroll
+              for (int j = 0; j < C; ++j) {
+                if (cta + j > cta1) break;
+#pragma unroll
+                for (int k = 0; k < A; ++k) {
+                  const float to = fmaxf(ref[k], ml[j][k].x);
+                  const float b0 = ref[k] == to ? 1.f : ex2(ref[k] - to);
+                  const float b1 = ml[j][k].x == to ? 1.f : ex2(ml[j][k].x - to);
+                  ref[k] = to;
+                  sum[k] = fmaf(b1, ml[j][k].y, sum[k] * b0);
+                  acc[k].x = fmaf(b1, y[j][k].x, acc[k].x * b0);
+                  acc[k].y = fmaf(b1, y[j][k].y, acc[k].y * b0);
+                  acc[k].z = fmaf(b1, y[j][k].z, acc[k].z * b0);
+                  acc[k].w = fmaf(b1, y[j][k].w, acc[k].w * b0);
+                }
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < A; ++k) {
+              const int hr = (x0 + k * kThreads) / kChunksO;
+              if (hr < hw * R) write_row(hr / R, hr % R, c, acc[k], ref[k], sum[k]);
+            }
           }
-          write_row(hh, r, c, acc, ref, sum);
-        }
+        };
+        if (hw * R * kChunksO <= kThreads)
+          join(std::integral_constant<int, 1>{}, std::integral_constant<int, 4>{});
+        else
+          join(std::integral_constant<int, 4>{}, std::integral_constant<int, 1>{});
       }
     }
     at.next(p);
