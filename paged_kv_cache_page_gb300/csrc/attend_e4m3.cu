@@ -53,9 +53,10 @@ constexpr int kMaxB = 4096;
 constexpr float kShift = kE4m3Shift, kSlack = kE4m3Slack;
 constexpr int kMinShare = 32;   // units
 constexpr int kWholeUnits = 64;  // streams of at most this many units are not split
+constexpr int kSegment = 64;     // units (of one head) that a CTA's further segment costs
 // Side by side go twice as many heads while a CTA's share holds this many units
 // of each.
-constexpr int kMaxSide = 3, kSideUnits = 128;
+constexpr int kMaxSide = 2, kSideUnits = 128;
 // Rows per kv head up to which a sequence runs here; longer query blocks fill
 // the 128-row tiles of the tcgen05 kernel.
 constexpr int kSmallRows = 64;
@@ -77,16 +78,22 @@ struct Layout {
 
 struct Seq {
   int q0, qlen, lk, units, tiles;  // tiles: 16-row tiles of a kv head
-  int cost;                        // of one tile's stream: its units, or 1 where none is split
+  int cost;                        // of one tile's stream: its units, or the slots it is cut into
+  int chunk;                       // units of a slot (all of them where the cost counts units)
 };
 
-__device__ __forceinline__ Seq load_seq(const AttendParams& p, int b, bool whole, bool tell) {
+// `slot` > 0: streams are cut into slots of at most that many units.
+__device__ __forceinline__ Seq load_seq(const AttendParams& p, int b, int slot, bool tell) {
   const SeqRows r = seq_rows(p, b, tell);
-  Seq s{r.q0, r.qlen, r.lk, 0, 0, 0};
+  Seq s{r.q0, r.qlen, r.lk, 0, 0, 0, 0};
   if ((long long)s.qlen * p.G > p.small_rows) s.qlen = 0;  // not this kernel's
   if (s.qlen == 0) return s;
   s.units = max(1, (s.lk + kKeys - 1) / kKeys);
-  s.cost = whole ? 1 : s.units;
+  s.cost = s.chunk = s.units;
+  if (slot > 0) {
+    s.cost = (s.units - 1) / slot + 1;
+    s.chunk = (s.units - 1) / s.cost + 1;
+  }
   s.tiles = (s.qlen * p.G + kRows - 1) / kRows;
   return s;
 }
@@ -103,7 +110,7 @@ struct Cursor {
   int b, h, tile, u, len;  // h: group of neighbouring kv heads
   long long left;          // cost of the share from u on
   int groups;
-  bool whole;              // streams are not split: each costs 1
+  int slot;                // load_seq's
   Seq s;
 
   // Units of the segment that hold a key some row of the tile sees.
@@ -114,9 +121,15 @@ struct Cursor {
     return min(len, max(0, (end + kKeys - 1) / kKeys - u));
   }
   __device__ __forceinline__ void next(const AttendParams& p) {
-    left -= whole ? 1 : len;
-    u = len = 0;
+    left -= slot > 0 ? 1 : len;
+    u = slot > 0 ? u + len : s.units;
+    len = 0;
     if (left <= 0) return;
+    if (u < s.units) {
+      len = min(s.chunk, s.units - u);
+      return;
+    }
+    u = 0;
     if (++tile == s.tiles) {
       tile = 0;
       if (++h == groups) {
@@ -126,11 +139,11 @@ struct Cursor {
             left = 0;
             return;
           }
-          s = load_seq(p, b, whole, false);
+          s = load_seq(p, b, slot, false);
         } while (s.units == 0);
       }
     }
-    len = whole ? s.units : (int)min((long long)s.units, left);
+    len = slot > 0 ? s.chunk : (int)min((long long)s.units, left);
   }
 };
 
@@ -203,28 +216,78 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   const int g = lane >> 2, t = lane & 3;
 
   // ---- the CTA's share
-  // Where the longest stream is short, none is split: the sums then count
-  // streams, otherwise units.
+  // Sums over the batch, for one kv head: units, tiles, and the longest stream.
   const int per = (p.B + kThreads - 1) / kThreads;
+  auto block_sum = [&](long long x, int row) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    if (lane == 0) sSums[row * kWarps + warp] = x;
+    __syncthreads();
+    long long y = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) y += sSums[row * kWarps + w];
+    return y;
+  };
   long long mine = 0;
   int tiles = 0, longest = 0;
   for (int i = 0; i < per; ++i) {
     const int b = tid * per + i;
     if (b >= p.B) break;
-    const Seq s = load_seq(p, b, false, blockIdx.x == 0);
+    const Seq s = load_seq(p, b, 0, blockIdx.x == 0);
     mine += cost_of(s);
     tiles += s.tiles;
     longest = max(longest, s.units);
   }
-  const bool whole = __syncthreads_and(longest <= kWholeUnits) != 0;
-  if (whole) mine = tiles;
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  if (lane == 0) sM[warp] = __int_as_float(longest);
+  const long long units = block_sum(mine, 0);
+  long long streams = block_sum(tiles, 1);
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) longest = max(longest, __float_as_int(sM[w]));
+  // Neighbouring kv heads side by side: 2^hw_log2 of them, each with 8 >> hw_log2
+  // of the warps, while a share stays long.
+  int hw_log2 = 0;
+  while (longest > kWholeUnits && hw_log2 < kMaxSide && (p.Hkv >> hw_log2) % 2 == 0 &&
+         units * p.Hkv >= ((long long)kSideUnits << hw_log2) * gridDim.x)
+    ++hw_log2;
+  const int hw = 1 << hw_log2, step_u = kWarps >> hw_log2;
+  const int my_u = warp & (step_u - 1), my_hh = warp >> (3 - hw_log2);
+  const int groups = p.Hkv >> hw_log2;
+  streams *= groups;
+  // How the streams are dealt.  Short ones whole.  A few long ones in slots, one
+  // a CTA: of a length that half a slot a stream less fills the CTAs with, where
+  // that suffices, or one that always does.  Otherwise equal shares that cut
+  // streams anywhere -- every CTA is as long, but a segment more costs it what
+  // kSegment units do.
+  int slot = 0;
+  const int ctas = (int)gridDim.x;
+  if (longest <= kWholeUnits) {
+    slot = kWholeUnits;
+  } else if (streams < ctas) {
+    const float all = (float)(units * groups);
+    slot = (int)(all / (ctas - 0.5f * (int)streams)) + 2;
+    int count = 0;  // slots
+    for (int i = 0; i < per; ++i) {
+      const int b = tid * per + i;
+      if (b < p.B) count += (int)cost_of(load_seq(p, b, slot, false));
+    }
+    if (block_sum(count, 2) * groups > ctas) slot = (int)(all / (ctas - (int)streams)) + 2;
+    if (slot > all / ctas + (kSegment >> hw_log2)) slot = 0;
+  }
+  if (slot > 0) {
+    mine = 0;
+    for (int i = 0; i < per; ++i) {
+      const int b = tid * per + i;
+      if (b < p.B) mine += cost_of(load_seq(p, b, slot, false));
+    }
+  }
   long long incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long y = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += y;
   }
-  if (lane == 31) sSums[kThreads + warp] = incl;
+  if (lane == 31) sSums[kThreads + warp] = incl;  // (behind the rows of block_sum)
   __syncthreads();
   long long total = 0;
 #pragma unroll
@@ -235,44 +298,39 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   }
   sSums[tid] = incl;
   __syncthreads();
-  // Neighbouring kv heads side by side: 2^hw_log2 of them, each with 8 >> hw_log2
-  // of the warps.
-  int hw_log2 = 0;
-  while (!whole && hw_log2 < kMaxSide && (p.Hkv >> hw_log2) % 2 == 0 &&
-         total * p.Hkv >= ((long long)kSideUnits << hw_log2) * gridDim.x)
-    ++hw_log2;
-  const int hw = 1 << hw_log2, step_u = kWarps >> hw_log2;
-  const int my_u = warp & (step_u - 1), my_hh = warp >> (3 - hw_log2);
-  const int groups = p.Hkv >> hw_log2;
   total *= groups;
   long long share = quotient(total + gridDim.x - 1, gridDim.x);
-  if (!whole) share = max((share + step_u - 1) & ~(long long)(step_u - 1), (long long)kMinShare);
+  if (slot == 0) share = max((share + step_u - 1) & ~(long long)(step_u - 1), (long long)kMinShare);
   const long long first = share * blockIdx.x;
   if (first >= total) {
     griddep_wait();
     return;
   }
   Cursor at{};
+  long long stream0;  // cost of the streams in front of the segment's
   {
     int lo = 0;  // the first thread whose sum passes `first`
     for (int step = kThreads / 2; step > 0; step >>= 1)
       if (sSums[lo + step - 1] * groups <= first) lo += step;
     long long off = first - (lo > 0 ? sSums[lo - 1] * groups : 0);
     at.groups = groups;
-    at.whole = whole;
+    at.slot = slot;
     at.b = lo * per;
-    at.s = load_seq(p, at.b, whole, false);
+    at.s = load_seq(p, at.b, slot, false);
     while (off >= cost_of(at.s) * groups && at.b + 1 < p.B) {
       off -= cost_of(at.s) * groups;
-      at.s = load_seq(p, ++at.b, whole, false);
+      at.s = load_seq(p, ++at.b, slot, false);
     }
     const long long head = cost_of(at.s);
     at.h = (int)quotient(off, head);
     const int rest = (int)(off - at.h * head);
     at.tile = rest / at.s.cost;
-    at.u = rest % at.s.cost;
+    at.u = rest % at.s.cost;  // units, or slots, of the stream in front
+    stream0 = first - at.u;
+    if (slot > 0) at.u *= at.s.chunk;
     at.left = min(share, total - first);
-    at.len = whole ? at.s.units : (int)min((long long)(at.s.units - at.u), at.left);
+    at.len = slot > 0 ? min(at.s.chunk, at.s.units - at.u)
+                      : (int)min((long long)(at.s.units - at.u), at.left);
   }
 
   __syncthreads();  // sSums lies where the segments' results go
@@ -339,6 +397,33 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     }
     cp_commit();  // an empty group where nothing is left keeps the count
   };
+  // The raw query rows g and g + 8 of a segment's tile: read before the copies
+  // of the first segment, or they wait behind all of them.
+  // With them the head's scale.
+  uint32_t raw[2][D / 64][8];
+  float raw_scale = 1.f;
+  auto read_rows = [&](const Cursor& w) {
+    const int head = w.h * hw + my_hh, R = min(kRows, w.s.qlen * p.G - w.tile * kRows);
+    if (p.k_scale != nullptr)
+      asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(raw_scale) : "l"(p.k_scale + head));
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      // (rows behind the last are read as the tile's first, and cleared when used)
+      const int row = w.tile * kRows + (g + 8 * j < R ? g + 8 * j : 0);
+      const int i = row / p.G, h = head * p.G + row % p.G;
+      const T* src = reinterpret_cast<const T*>(p.q) + (int64_t)(w.s.q0 + i) * p.q_st +
+                     (int64_t)h * p.q_sh + t * 16;
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint4 x = load16(src + c * 64 + e * 8);
+          raw[j][c][4 * e] = x.x; raw[j][c][4 * e + 1] = x.y;
+          raw[j][c][4 * e + 2] = x.z; raw[j][c][4 * e + 3] = x.w;
+        }
+    }
+  };
+  read_rows(at);
   if (a_i < a_seen)
     read_entries();
   else
@@ -348,11 +433,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   int stage = 0;
 
   // ---- segments
-  long long stream0 = first - at.u;  // first unit of the segment's stream
   for (;;) {
     const int R = min(kRows, at.s.qlen * p.G - at.tile * kRows);
-    const int head = at.h * hw + my_hh;
-    const float ks = p.k_scale != nullptr ? __ldg(p.k_scale + head) : 1.f;
+    const float ks = raw_scale;
     uint32_t qa[kQ][4];
     float f[2];  // score factor of rows g, g + 8 (log2 domain)
     int lim[2];  // keys they see
@@ -361,19 +444,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       const int r = g + 8 * j;
       const int row = at.tile * kRows + r;
       const bool live = r < R;
-      const int i = row / p.G, h = head * p.G + row % p.G;
-      lim[j] = p.causal && live ? min(at.s.lk, i + at.s.lk - at.s.qlen + 1) : at.s.lk;
-      const T* src = reinterpret_cast<const T*>(p.q) + (int64_t)(at.s.q0 + (live ? i : 0)) * p.q_st +
-                     (int64_t)(live ? h : 0) * p.q_sh;
+      lim[j] = p.causal && live ? min(at.s.lk, row / p.G + at.s.lk - at.s.qlen + 1) : at.s.lk;
       uint32_t w[D / 64][8];
 #pragma unroll
       for (int c = 0; c < D / 64; ++c)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (live) x = __ldg(reinterpret_cast<const uint4*>(src + c * 64 + t * 16) + e);
-          w[c][4 * e] = x.x; w[c][4 * e + 1] = x.y; w[c][4 * e + 2] = x.z; w[c][4 * e + 3] = x.w;
-        }
+        for (int e = 0; e < 8; ++e) w[c][e] = live ? raw[j][c][e] : 0u;
       f[j] = fabsf(ks) * p.scale_log2;
       if constexpr (sizeof(T) == 2 && !std::is_same<T, __half>::value) {
         uint32_t top = 0;  // bits of the largest magnitude
@@ -607,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       }
     }
     const bool done = at.u == 0 && at.len == at.s.units;  // not split
-    const long long stream1 = stream0 + at.s.units;
+    const long long stream1 = stream0 + at.s.cost;
     const int slot = 2 * blockIdx.x + (at.u == 0 ? 1 : 0);
     constexpr int kChunksO = D / 4;
     auto write_row = [&](int hh, int r, int c, float4 x, float ref, float sum) {
@@ -747,7 +823,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     }
     at.next(p);
     if (at.left <= 0) break;
-    stream0 = stream1;
+    read_rows(at);
+    if (at.u == 0) stream0 = stream1;
     __syncthreads();  // the merge has read what the next segment's overwrites
   }
   cp_wait<0>();

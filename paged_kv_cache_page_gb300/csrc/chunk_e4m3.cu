@@ -173,16 +173,8 @@ __device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
                : "memory");
 }
 
-// Loads that stay where they are written: left to itself the compiler moves
-// them down to their uses to save registers, and they wait for one another.
-__device__ __forceinline__ uint4 load16(const void* src) {
-  uint4 x;
-  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-               : "l"(src));
-  return x;
-}
-__device__ __forceinline__ float4 load16_l2(const void* src) {  // past L1
+// As load16, past L1: what another CTA has written.
+__device__ __forceinline__ float4 load16_l2(const void* src) {
   float4 x;
   asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];"
                : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
