@@ -1,6 +1,7 @@
 """Paged KV-cache attention for GB300 (sm_103a): Python binding.
 
-Thin ctypes layer over ``libpagedattn.so`` (``include/pagedattn.h``).  The
+Thin layer over ``libpagedattn.so`` (``include/pagedattn.h``): ctypes, and for
+the calls of a serving step a native module.  The
 functions keep the C names and only marshal arguments (pointers, strides,
 sizes, the current CUDA stream); every step of the computation runs in the
 library's CUDA kernels.  PyTorch is used for device memory and streams: the
@@ -13,12 +14,14 @@ call raises.
 """
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import math
 import os
 
 import torch
 
-from .build import lib_path
+from .build import BINDING_LIB, lib_path
 
 PA_OK = 0
 PA_ERR_INVALID_ARG = -1
@@ -330,33 +333,26 @@ def pa_split_combine(o_partial, lse_partial, out, lse=None, splits_per_seq=None)
 
 
 # ---------------------------------------------------------------- a step over a paged cache
-def _addr(t):
-    return None if t is None else t.data_ptr()
+# These calls are made for every token that is served, so their arguments are checked and packed
+# by a native module (csrc/binding.cpp) instead of ctypes.
+_native = None
 
 
-def _want(name, t, dtype, dim, device, shape=None):
-    """The argument's checks: on the call's CUDA device, of this type, number of axes (and shape),
-    with a contiguous last axis."""
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be on the call's CUDA device")
-    if t.dtype is not dtype or t.dim() != dim or (shape is not None and tuple(t.shape) != shape):
-        want = f"{dim}-d" if shape is None else str(shape)
-        raise ValueError(f"{name} must be a {dtype} tensor, {want} (got {t.dtype}, {tuple(t.shape)})")
-    if t.numel() > 1 and t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError(f"{name}: the last axis must be contiguous")
-    return t.data_ptr()
-
-
-def _run(fn, device, *args):
-    """The library call on the tensors' device and its current stream."""
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if device.index == torch.cuda.current_device():
-        rc = fn(*args, stream)
-    else:
-        with torch.cuda.device(device):
-            rc = fn(*args, stream)
-    if rc != PA_OK:
-        _check(rc)
+def _load_native():
+    global _native
+    lib = load_library()
+    path = lib_path(BINDING_LIB)
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is missing: build it with python -m paged_kv_cache_page_gb300.build")
+    loader = importlib.machinery.ExtensionFileLoader("_binding", path)
+    spec = importlib.util.spec_from_file_location("_binding", path, loader=loader)
+    native = importlib.util.module_from_spec(spec)
+    loader.exec_module(native)
+    native.bind(*[ctypes.cast(fn, _vp).value for fn in (
+        lib.pa_plan_step, lib.pa_release_pages, lib.pa_rotary_append_varlen,
+        lib.pa_fwd_varlen_e4m3, lib.pa_fwd_varlen_e4m3_workspace_size)])
+    _native = native
+    return native
 
 
 def pa_plan_step(cache_seqlens, q_lens, block_table, free_pages, free_count, page_size,
@@ -371,37 +367,25 @@ def pa_plan_step(cache_seqlens, q_lens, block_table, free_pages, free_count, pag
     Outputs that are not given are allocated; ``slot_mapping`` (int64) and ``positions`` (int32)
     then hold ``token_capacity`` rows.
     """
-    fn = (_lib or load_library()).pa_plan_step
     device = cache_seqlens.device
-    i32 = torch.int32
-    B = cache_seqlens.numel()
     if slot_mapping is None:
         if token_capacity is None:
             raise ValueError("pa_plan_step: token_capacity or slot_mapping must be given")
         slot_mapping = torch.empty(token_capacity, dtype=torch.int64, device=device)
-    tokens = slot_mapping.numel()
-    if token_capacity is not None and token_capacity != tokens:
+    elif token_capacity is not None and token_capacity != slot_mapping.numel():
         raise ValueError("pa_plan_step: slot_mapping does not have token_capacity rows")
     if cu_seqlens_q is None:
-        cu_seqlens_q = torch.empty(B + 1, dtype=i32, device=device)
+        cu_seqlens_q = torch.empty(cache_seqlens.numel() + 1, dtype=torch.int32, device=device)
     if seqlens_k is None:
-        seqlens_k = torch.empty(B, dtype=i32, device=device)
+        seqlens_k = torch.empty(cache_seqlens.numel(), dtype=torch.int32, device=device)
     if positions is None:
-        positions = torch.empty(tokens, dtype=i32, device=device)
-    if free_count_out is None:
-        free_count_out = free_count
-    table = _want("block_table", block_table, i32, 2, device)
-    if block_table.shape[0] != B:
-        raise ValueError("block_table must have a row for each sequence")
-    _run(fn, device, _want("cache_seqlens", cache_seqlens, i32, 1, device),
-         _want("q_lens", q_lens, i32, 1, device, (B,)), B, table, block_table.stride(0),
-         block_table.shape[1], page_size, _want("free_pages", free_pages, i32, 1, device),
-         _want("free_count", free_count, i32, 1, device, (1,)), free_pages.numel(),
-         _want("cu_seqlens_q", cu_seqlens_q, i32, 1, device, (B + 1,)),
-         _want("seqlens_k", seqlens_k, i32, 1, device, (B,)),
-         _want("slot_mapping", slot_mapping, torch.int64, 1, device),
-         _want("positions", positions, i32, 1, device, (tokens,)), tokens,
-         _want("free_count_out", free_count_out, i32, 1, device, (1,)), _addr(err))
+        positions = torch.empty(slot_mapping.numel(), dtype=torch.int32, device=device)
+    rc = (_native or _load_native()).plan_step(
+        cache_seqlens, q_lens, block_table, free_pages, free_count, page_size, cu_seqlens_q,
+        seqlens_k, slot_mapping, positions,
+        free_count if free_count_out is None else free_count_out, err)
+    if rc:
+        _check(rc)
     return cu_seqlens_q, seqlens_k, slot_mapping, positions
 
 
@@ -410,31 +394,16 @@ def pa_release_pages(cache_seqlens, keep_lens, block_table, free_pages, free_cou
     """Gives the pages behind each sequence's first ``keep_lens[b]`` tokens back to the pool (0: the
     request has finished).  ``seqlens_out`` defaults to ``cache_seqlens`` itself, ``free_count_out``
     to ``free_count``; returns ``(seqlens_out, free_count_out)``."""
-    fn = (_lib or load_library()).pa_release_pages
-    device = cache_seqlens.device
-    i32 = torch.int32
-    B = cache_seqlens.numel()
     if seqlens_out is None:
         seqlens_out = cache_seqlens
     if free_count_out is None:
         free_count_out = free_count
-    table = _want("block_table", block_table, i32, 2, device)
-    if block_table.shape[0] != B:
-        raise ValueError("block_table must have a row for each sequence")
-    _run(fn, device, _want("cache_seqlens", cache_seqlens, i32, 1, device),
-         _want("keep_lens", keep_lens, i32, 1, device, (B,)), B, table, block_table.stride(0),
-         block_table.shape[1], page_size, _want("free_pages", free_pages, i32, 1, device),
-         _want("free_count", free_count, i32, 1, device, (1,)), free_pages.numel(),
-         _want("seqlens_out", seqlens_out, i32, 1, device, (B,)),
-         _want("free_count_out", free_count_out, i32, 1, device, (1,)), _addr(err))
+    rc = (_native or _load_native()).release_pages(cache_seqlens, keep_lens, block_table, free_pages,
+                                                   free_count, page_size, seqlens_out,
+                                                   free_count_out, err)
+    if rc:
+        _check(rc)
     return seqlens_out, free_count_out
-
-
-_CACHE_DTYPE = {torch.float16: PA_F16, torch.bfloat16: PA_BF16, torch.float8_e4m3fn: PA_E4M3}
-
-
-def _scale_addr(name, t, hkv, device):
-    return None if t is None else _want(name, t, torch.float32, 1, device, (hkv,))
 
 
 def pa_rotary_append_varlen(q, k, v, k_cache, v_cache, slot_mapping, positions=None,
@@ -450,64 +419,16 @@ def pa_rotary_append_varlen(q, k, v, k_cache, v_cache, slot_mapping, positions=N
     ``[rotary_len, rotary_dim / 2]`` in q's dtype or fp32; without them nothing is rotated.  ``q``
     may be ``None``; ``q_out`` may be ``q`` (in place).
     """
-    fn = (_lib or load_library()).pa_rotary_append_varlen
-    device = k.device
-    dt = k.dtype
-    if dt not in _DTYPE:
-        raise ValueError(f"unsupported dtype {dt}")
-    T, hkv, d = k.shape
-    kp = _want("k", k, dt, 3, device)
-    vp = _want("v", v, dt, 3, device, (T, hkv, d))
-    qp = qo = None
-    hq = q_st = q_sh = qo_st = qo_sh = 0
-    if q is not None:
-        hq = q.shape[1]
-        qp = _want("q", q, dt, 3, device, (T, hq, d))
-        if q_out is None:
-            q_out = torch.empty((T, hq, d), dtype=dt, device=device)
-        qo = _want("q_out", q_out, dt, 3, device, (T, hq, d))
-        q_st, q_sh, qo_st, qo_sh = q.stride(0), q.stride(1), q_out.stride(0), q_out.stride(1)
-    cdt = k_cache.dtype
-    if cdt not in _CACHE_DTYPE:
-        raise ValueError(f"unsupported cache dtype {cdt}")
-    _want("k_cache", k_cache, cdt, 4, device)
-    _want("v_cache", v_cache, cdt, 4, device, tuple(k_cache.shape))
-    if k_cache.shape[2:] != (hkv, d):
-        raise ValueError("the caches' heads and head_dim must be those of k")
-    if cdt is not torch.float8_e4m3fn and (k_scale is not None or v_scale is not None):
-        raise ValueError("k_scale and v_scale belong to e4m3 caches")
-    pos = cos = sin = axes = None
-    pos_stride = n_axes = rot_len = rot = rot_dt = 0
-    if rotary_cos is not None:
-        if positions is None or rotary_sin is None:
-            raise ValueError("a rotation needs positions, rotary_cos and rotary_sin")
-        many = positions.dim() == 2
-        pos = _want("positions", positions, torch.int32, 2 if many else 1, device)
-        if positions.shape[-1] != T:
-            raise ValueError("positions must have a column for each token")
-        n_axes, pos_stride = (positions.shape[0], positions.stride(0)) if many else (1, T)
-        if many and n_axes == 1:
-            pos_stride = T
-        tdt = rotary_cos.dtype
-        if tdt is not dt and tdt is not torch.float32:
-            raise ValueError("the rotary tables must be of q's dtype or fp32")
-        rot_dt = PA_F32 if tdt is torch.float32 else _DTYPE[dt]
-        if not (rotary_cos.is_contiguous() and rotary_sin.is_contiguous()):
-            raise ValueError("the rotary tables must be contiguous")
-        cos = _want("rotary_cos", rotary_cos, tdt, 2, device)
-        sin = _want("rotary_sin", rotary_sin, tdt, 2, device, tuple(rotary_cos.shape))
-        rot_len, rot = rotary_cos.shape[0], 2 * rotary_cos.shape[1]
-        if pair_axis is not None:
-            axes = bytes(pair_axis)
-            if len(axes) != rot // 2:
-                raise ValueError("pair_axis must name an axis for each of the rotated pairs")
-    _run(fn, device, qp, q_st, q_sh, kp, k.stride(0), k.stride(1), vp, v.stride(0), v.stride(1), qo,
-         qo_st, qo_sh, _t4(k_cache), _t4(v_cache), _scale_addr("k_scale", k_scale, hkv, device),
-         _scale_addr("v_scale", v_scale, hkv, device),
-         _want("slot_mapping", slot_mapping, torch.int64, 1, device, (T,)), k_cache.shape[1],
-         k_cache.shape[0], pos, pos_stride, n_axes, axes, cos, sin, rot_len, rot,
-         int(bool(rotary_interleaved)), rot_dt, T, hq, hkv, d, _DTYPE[dt], _CACHE_DTYPE[cdt],
-         _addr(err))
+    if q is None:
+        q_out = None
+    elif q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    rc = (_native or _load_native()).rotary_append_varlen(
+        q, k, v, k_cache, v_cache, slot_mapping, positions, rotary_cos, rotary_sin,
+        rotary_interleaved, None if pair_axis is None else bytes(pair_axis), k_scale, v_scale,
+        q_out, err)
+    if rc:
+        _check(rc)
     return q_out
 
 
@@ -524,43 +445,13 @@ def pa_fwd_varlen_e4m3(q, k_cache, v_cache, cu_seqlens_q, seqlens_k, block_table
     ``k_scale``/``v_scale`` fp32 ``[Hkv]`` (device): what a stored value stands for is itself times
     its kv head's scale.  The other arguments are pa_fwd_varlen_unified's.
     """
-    lib = _lib or load_library()
-    device = q.device
-    total_q, hq, d = q.shape
-    qp = _want("q", q, q.dtype, 3, device)
-    if q.dtype not in _DTYPE:
-        raise ValueError(f"unsupported dtype {q.dtype}")
-    _want("k_cache", k_cache, torch.float8_e4m3fn, 4, device)
-    _want("v_cache", v_cache, torch.float8_e4m3fn, 4, device, tuple(k_cache.shape))
-    num_pages, page_size, hkv = k_cache.shape[:3]
-    if k_cache.shape[3] != d:
-        raise ValueError("the caches' head_dim must be that of q")
-    B = seqlens_k.numel()
-    table = _want("block_table", block_table, torch.int32, 2, device)
-    if block_table.shape[0] != B:
-        raise ValueError("block_table must have a row for each sequence")
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty((total_q, hq, d), dtype=q.dtype, device=device)
-    elif not out.is_contiguous():
-        raise ValueError("out must be contiguous")
-    if lse is None:
-        if return_lse:
-            lse = torch.empty((hq, total_q), dtype=torch.float32, device=device)
-    elif not lse.is_contiguous():
-        raise ValueError("lse must be contiguous")
-    if workspace is None:
-        workspace = torch.empty(lib.pa_fwd_varlen_e4m3_workspace_size(
-            B, total_q, max_seqlen_q, hq, hkv, d, max_seqlen_k), dtype=torch.uint8, device=device)
-    _run(lib.pa_fwd_varlen_e4m3, device, qp, q.stride(0), q.stride(1), _t4(k_cache), _t4(v_cache),
-         _scale_addr("k_scale", k_scale, hkv, device), _scale_addr("v_scale", v_scale, hkv, device),
-         _want("cu_seqlens_q", cu_seqlens_q, torch.int32, 1, device, (B + 1,)),
-         _want("seqlens_k", seqlens_k, torch.int32, 1, device), table, block_table.stride(0),
-         block_table.shape[1], page_size, B, total_q, max_seqlen_q, max_seqlen_k, hq, hkv, d,
-         num_pages, scale, 1 if causal else 0,
-         _want("out", out, q.dtype, 3, device, (total_q, hq, d)),
-         None if lse is None else _want("lse", lse, torch.float32, 2, device, (hq, total_q)),
-         workspace.data_ptr(), workspace.numel() * workspace.element_size(), _addr(err),
-         _DTYPE[q.dtype])
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if lse is None and return_lse:
+        lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
+    rc = (_native or _load_native()).fwd_varlen_e4m3(
+        q, k_cache, v_cache, cu_seqlens_q, seqlens_k, block_table, max_seqlen_q, max_seqlen_k,
+        k_scale, v_scale, scale, causal, out, lse, workspace, err)
+    if rc:
+        _check(rc)
     return out, lse

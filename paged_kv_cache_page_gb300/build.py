@@ -1,5 +1,6 @@
 """Build libpagedattn.so (and the test-only libpa_selftest.so) in-tree with
-nvcc for sm_103a.
+nvcc for sm_103a, and the Python module _binding.so (torch tensors to the C
+ABI of the serving-step calls) with the host compiler.
 
 Each translation unit is compiled in parallel, then linked into a shared
 library with the CUDA runtime linked statically (no libcuda dependency at load
@@ -8,10 +9,12 @@ paged_kv_cache_page_gb300.build`` or call :func:`build`.
 """
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -26,6 +29,9 @@ SOURCES = ["api.cu", "append.cu", "decode.cu", "combine.cu", "noalloc.cu", "engi
 SELFTEST_LIB = "libpa_selftest.so"
 SELFTEST_SOURCES = ["selftest_tcgen05.cu", "selftest_tcgen05_t.cu",
                     "selftest_timeout.cu"]
+# Python module of the serving-step calls (host code against torch's headers).
+BINDING_LIB = "_binding.so"
+BINDING_SOURCE = "binding.cpp"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -55,6 +61,24 @@ def _compile(src, obj, extra, verbose):
     return r.stdout + r.stderr
 
 
+def _build_binding(lib, verbose):
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path())))
+    inc = [os.path.join(torch_dir, "include"),
+           os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    tmp = lib + ".tmp"
+    cmd = ([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-o", tmp,
+            os.path.join(CSRC, BINDING_SOURCE)] + [x for i in inc for x in ("-isystem", i)]
+           + ["-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+              "-lc10_cuda"])
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on {BINDING_SOURCE}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, lib)
+    return r.stdout + r.stderr if verbose else ""
+
+
 def _stale(target, deps):
     if not os.path.exists(target):
         return True
@@ -72,7 +96,8 @@ def _link(lib, objs):
 
 
 def build(force=False, verbose=False, extra=()):
-    """Compile (if needed) both libraries; return the path of libpagedattn.so."""
+    """Compile (if needed) the libraries and the Python module; return the path of
+    libpagedattn.so."""
     os.makedirs(OUT_DIR, exist_ok=True)
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
     headers.append(os.path.join(ROOT, "include", "pagedattn.h"))
@@ -86,9 +111,13 @@ def build(force=False, verbose=False, extra=()):
             if force or verbose or _stale(obj, [os.path.join(CSRC, src)] + headers):
                 jobs.append((src, obj))
     logs = []
-    if jobs:
-        with cf.ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
+    binding = lib_path(BINDING_LIB)
+    bind = force or _stale(binding, [os.path.join(CSRC, BINDING_SOURCE), headers[-1]])
+    if jobs or bind:
+        with cf.ThreadPoolExecutor(max_workers=min(len(jobs) + 1, os.cpu_count() or 4)) as ex:
             futs = [ex.submit(_compile, s, o, extra, verbose) for s, o in jobs]
+            if bind:
+                futs.append(ex.submit(_build_binding, binding, verbose))
             for f in futs:
                 logs.append(f.result())
     for lib, objs in objs_of.items():

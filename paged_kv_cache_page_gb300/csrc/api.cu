@@ -211,6 +211,17 @@ int num_sms() {
   return sms[dev];
 }
 
+cudaError_t allow_shared(const void* kernel, int bytes, std::atomic<uint64_t>* devices) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (devices->load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) devices->fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
 bool encode_map(CUtensorMap* map, const void* base, int dtype, int D, int H, int64_t dim2,
                 int64_t dim3, int64_t stride_h, int64_t stride_t, int64_t stride_b, int box_d,
                 int box_h, int box_rows, bool swz = true) {

@@ -857,8 +857,9 @@ Workspace workspace_of(int D, bool chunks) {
 template <int D, typename T>
 cudaError_t launch(const AttendParams& p, bool dependent, cudaStream_t st) {
   const int bytes = Layout<D>::kBytes;
-  cudaError_t e = cudaFuncSetAttribute(attend_kernel<D, T>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  static std::atomic<uint64_t> devices{0};
+  const cudaError_t e =
+      allow_shared(reinterpret_cast<const void*>(attend_kernel<D, T>), bytes, &devices);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)num_sms());

@@ -884,8 +884,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
 
 template <int D, typename T>
 cudaError_t launch(const AttendParams& p, cudaStream_t st) {
-  const cudaError_t e = cudaFuncSetAttribute(
-      chunk_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::kBytes);
+  static std::atomic<uint64_t> devices{0};
+  const cudaError_t e = allow_shared(reinterpret_cast<const void*>(chunk_kernel<D, T>),
+                                     Layout<D>::kBytes, &devices);
   if (e != cudaSuccess) return e;
   chunk_kernel<D, T><<<(unsigned)num_sms(), kThreads, Layout<D>::kBytes, st>>>(p);
   return cudaGetLastError();

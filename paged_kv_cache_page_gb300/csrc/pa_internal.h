@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/pagedattn.h"
 
 namespace pa {
@@ -117,6 +119,9 @@ constexpr int kDecodeMaxSchedB = 512;
 
 // Host helpers (api.cu).
 int num_sms();
+// Lets `kernel` use `bytes` of dynamic shared memory on the current device;
+// `devices` remembers (a bit each) where that has been done.
+cudaError_t allow_shared(const void* kernel, int bytes, std::atomic<uint64_t>* devices);
 bool encode_cache_map(CUtensorMap* map, const void* base, int dtype, int D, int Hkv, int64_t dim2,
                       int64_t dim3, int64_t stride_h, int64_t stride_t, int64_t stride_b,
                       int box_d, int box_rows, bool swizzle128);
