@@ -82,16 +82,6 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
   return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
 }
 
-// Loads that stay where they are written: left to itself the compiler moves
-// them down to their uses to save registers, and they wait for one another.
-__device__ __forceinline__ uint4 load16(const void* src) {
-  uint4 x;
-  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-               : "l"(src));
-  return x;
-}
-
 // The attention of sequences of more than small_rows rows per kv head
 // (chunk_e4m3.cu).
 cudaError_t launch_chunks_e4m3(const AttendParams& p, int D, int dtype, cudaStream_t st);

@@ -58,6 +58,17 @@ __device__ __forceinline__ float lg2(float x) {
 }
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
 
+// ---------------------------------------------------------------- loads
+// Loads that stay where they are written: left to itself the compiler moves
+// them down to their uses to save registers, and they wait for one another.
+__device__ __forceinline__ uint4 load16(const void* src) {
+  uint4 x;
+  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+               : "l"(src));
+  return x;
+}
+
 // ---------------------------------------------------------------- errors
 __device__ __forceinline__ void report(int32_t* err, int code, int b, int value) {
   if (err == nullptr) return;

@@ -14,9 +14,12 @@
 // sums in front of an admitted request are already its offsets into the pool
 // and into the packed rows.  One scan serves both.
 //
-// Both kernels are one launch of one cluster of up to 8 CTAs.  What bounds
+// Both kernels are one launch of one cluster of up to 16 CTAs.  What bounds
 // them is latency, not bytes (a step of 1024 requests moves 0.8 MB): a chain
-// of launch, length loads, scan, binary search, table load, store.  Every CTA
+// of launch, length loads, scan, binary search, table load, store -- and of
+// instruction fetches: code that runs once comes from far away, and unrolled
+// eight-fold, with eight searches side by side, the same steps took 6.6 instead
+// of 4.3 us for 64 requests and 16.5 instead of 10.3 us for 1024.  Every CTA
 // of the cluster repeats the scan of the whole batch (at most 4096 entries,
 // four a thread), which costs less than a second launch or a wait on another
 // CTA's sums; the rows and pages are then dealt over the cluster's threads.
@@ -24,6 +27,8 @@
 // (free_count_out = free_count, seqlens_k = cache_seqlens): the cluster's
 // barrier tells when every CTA has read them.
 #include <cooperative_groups.h>
+
+#include <atomic>
 
 #include "pa_common.cuh"
 #include "pa_internal.h"
@@ -38,7 +43,8 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kMaxB = 4096;
 constexpr int kPer = kMaxB / kThreads;  // consecutive entries of the batch a thread scans
-constexpr int kCluster = 8;             // the largest portable cluster
+constexpr int kAtOnce = 4;
+constexpr int kCluster = 16;             // CTAs of the cluster at most (8 where 16 do not fit)
 
 struct PlanParams {
   const int32_t* cache_seqlens;
@@ -71,6 +77,13 @@ struct ReleaseParams {
   int num_pages;
 };
 
+// A load that stays where it is written (see load16).
+__device__ __forceinline__ int load4(const int32_t* src) {
+  int x;
+  asm volatile("ld.global.s32 %0, [%1];" : "=r"(x) : "l"(src) : "memory");
+  return x;
+}
+
 // Inclusive sums over the CTA of one 64-bit value a thread; `warp_sums` holds
 // 32 values.
 __device__ __forceinline__ long long block_scan(long long x, long long* warp_sums) {
@@ -83,19 +96,31 @@ __device__ __forceinline__ long long block_scan(long long x, long long* warp_sum
   if (lane == 31) warp_sums[warp] = x;
   __syncthreads();
   // every warp sums the totals of the warps in front of it
-  long long before = lane < warp ? warp_sums[lane] : 0;
+  long long before = lane < warp ? warp_sums[lane] : 0;  // (warp < warps of the CTA)
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
   return x + before;
 }
 
-// The last b < n with first[b] <= k, for ascending first[0] = 0 (entries that
-// hold nothing share their successor's start, so the one found holds k).
-__device__ __forceinline__ int find_entry(const int* first, int n, int k) {
-  int lo = 0;
+// The last b < n, from `b` on, with first[b] <= k, for ascending first[0] = 0
+// (entries that hold nothing share their successor's start, so the one found
+// holds k).  Most steps stay in the entry they came from.
+__device__ __noinline__ int find_entry(const int* first, int n, int b, int k) {
+  if (b + 1 >= n || first[b + 1] > k) return b;
   for (int step = 1 << (31 - __clz(n)); step > 0; step >>= 1)
-    if (lo + step < n && first[lo + step] <= k) lo += step;
-  return lo;
+    if (b + step < n && first[b + step] <= k) b += step;
+  return b;
+}
+
+// The part of [0, n) that the warp handles: whole multiples of 32.
+struct Range {
+  int begin, end;
+};
+__device__ __forceinline__ Range warp_range(int n, int rank, int ranks) {
+  const int warps = (int)blockDim.x / 32 * ranks;
+  const int w = rank * ((int)blockDim.x / 32) + (int)threadIdx.x / 32;
+  const int each = (n + 32 * warps - 1) / (32 * warps) * 32;
+  return {min(n, w * each), min(n, (w + 1) * each)};
 }
 
 __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanParams p) {
@@ -119,7 +144,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanParams p) {
   if (tid < 2) s_total[tid] = 0;
 
   // the thread's entries and their sums
-  const int per = (p.B + kThreads - 1) / kThreads;
+  const int per = (p.B + (int)blockDim.x - 1) / (int)blockDim.x;
   int old[kPer], add[kPer], need[kPer];
   long long pages = 0, rows = 0;
 #pragma unroll
@@ -184,25 +209,29 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanParams p) {
       *p.free_count_out = free_now - N;
     }
   }
-  const int first = rank * kThreads + tid, stride = ranks * kThreads;
-  for (int k = first; k < N; k += stride) {
-    const int b = find_entry(s_page, p.B, k);
+  // A warp's pages and rows are neighbours, so its entries are found by a look
+  // at the next one, and its loads and stores are whole lines.
+  const int lane = tid & 31;
+  Range r = warp_range(N, rank, ranks);
+  for (int k = r.begin + lane, b = 0; k < r.end; k += 32) {
+    b = find_entry(s_page, p.B, b, k);
     const int page = p.free_pages[free_now - 1 - k];
     const int j = ((s_old[b] + ps - 1) >> p.page_log2) + k - s_page[b];
     if (page < 0 || page >= p.num_pages) report(p.err, PA_DEVERR_PAGE_OOB, b, j);
     p.block_table[(int64_t)b * p.bt_stride + j] = page;
   }
-  for (int t = first; t < p.token_capacity; t += stride) {
+  r = warp_range(p.token_capacity, rank, ranks);
+  for (int t = r.begin + lane, b = 0; t < r.end; t += 32) {
     int64_t slot = -1;
     int pos = 0;
     if (t < T) {
-      const int b = find_entry(s_row, p.B, t);
+      b = find_entry(s_row, p.B, b, t);
       const int c = s_old[b];
       pos = c + t - s_row[b];
       const int j = pos >> p.page_log2;
       const int fresh = j - ((c + ps - 1) >> p.page_log2);
-      const int page = fresh >= 0 ? p.free_pages[free_now - 1 - (s_page[b] + fresh)]
-                                  : p.block_table[(int64_t)b * p.bt_stride + j];
+      const int page = *(fresh >= 0 ? p.free_pages + (free_now - 1 - (s_page[b] + fresh))
+                                    : p.block_table + ((int64_t)b * p.bt_stride + j));
       if (page >= 0 && page < p.num_pages)
         slot = ((int64_t)page << p.page_log2) + (pos & (ps - 1));
       else
@@ -232,7 +261,7 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const ReleaseParams p
   }
   if (tid == 0) s_total = s_bad = 0;
 
-  const int per = (p.B + kThreads - 1) / kThreads;
+  const int per = (p.B + (int)blockDim.x - 1) / (int)blockDim.x;
   int len[kPer], keep[kPer], gone[kPer];
   long long sum = 0;
 #pragma unroll
@@ -280,16 +309,43 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const ReleaseParams p
     }
     if (tid == 0) *p.free_count_out = free_now + N;
   }
-  const int first = rank * kThreads + tid, stride = ranks * kThreads;
-  for (int k = first; k < N; k += stride) {
-    const int b = find_entry(s_at, p.B, k);
-    const int j = s_from[b] + k - s_at[b];
-    const int page = p.block_table[(int64_t)b * p.bt_stride + j];
+  const int lane = tid & 31;
+  const Range r = warp_range(N, rank, ranks);
+  auto give = [&](int b, int k, int page) {
     if (page < 0 || page >= p.num_pages) {
-      report(p.err, PA_DEVERR_PAGE_OOB, b, j);
+      report(p.err, PA_DEVERR_PAGE_OOB, b, s_from[b] + k - s_at[b]);
       s_bad = 1;
     }
     p.free_pages[free_now + k] = page;
+  };
+  auto entry_at = [&](int b) {  // the table entry of the request's released page 0, less its place
+    return p.block_table + ((int64_t)b * p.bt_stride + s_from[b] - s_at[b]);
+  };
+  if (N >= 64 * p.B) {
+    // Long runs: the warp copies one request's entries after another's, kAtOnce
+    // of them in flight a lane.  Found one by one, below, they cost 100
+    // instructions a line (179000 pages of 700 requests: 17.4 us, so 14.4 us),
+    // but runs of a page or two would leave the lanes idle.
+    for (int k0 = r.begin, b = 0; k0 < r.end;) {
+      b = find_entry(s_at, p.B, b, k0);
+      const int end = b + 1 < p.B ? min(r.end, s_at[b + 1]) : r.end;
+      const int32_t* src = entry_at(b);
+#pragma unroll 1
+      for (int k = k0 + lane; k < end; k += 32 * kAtOnce) {
+        int page[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) page[i] = load4(src + min(k + 32 * i, end - 1));
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i)
+          if (k + 32 * i < end) give(b, k + 32 * i, page[i]);
+      }
+      k0 = end;
+    }
+  } else {
+    for (int k = r.begin + lane, b = 0; k < r.end; k += 32) {
+      b = find_entry(s_at, p.B, b, k);
+      give(b, k, load4(entry_at(b) + k));
+    }
   }
   // A table entry outside the pool is not given back: CTA 0 closes the gaps.
   cluster.sync();  // the pages written, s_bad of every CTA
@@ -300,7 +356,7 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const ReleaseParams p
   if (rank != 0 || !bad) return;
   int32_t* list = p.free_pages + free_now;
   int kept = 0;
-  for (int k0 = 0; k0 < N; k0 += kThreads) {
+  for (int k0 = 0; k0 < N; k0 += (int)blockDim.x) {
     const int k = k0 + tid;
     const int page = k < N ? __ldcg(list + k) : -1;
     const bool ok = page >= 0 && page < p.num_pages;
@@ -309,17 +365,47 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const ReleaseParams p
     if (ok) list[to] = page;
     __syncthreads();
     long long all = 0;
-    for (int w = 0; w < 32; ++w) all += s_sums[w];
+    for (int w = 0; w < (int)blockDim.x / 32; ++w) all += s_sums[w];
     kept += (int)all;
   }
   if (tid == 0) *p.free_count_out = free_now + kept;
 }
 
+// Whether the device schedules clusters of more than 8 CTAs of the kernel
+// (sizes that are not portable); asked once a device.
+template <typename K>
+bool wide_clusters(K kernel, const cudaLaunchConfig_t& cfg, std::atomic<uint64_t>* asked,
+                   std::atomic<uint64_t>* wide) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return false;
+  const uint64_t bit = uint64_t(1) << dev;
+  if ((asked->load(std::memory_order_acquire) & bit) == 0) {
+    int n = 0;
+    const bool ok =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
+            cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0;
+    if (!ok) cudaGetLastError();  // (not an error of the call's)
+    if (ok) wide->fetch_or(bit, std::memory_order_relaxed);
+    asked->fetch_or(bit, std::memory_order_release);
+  }
+  return (wide->load(std::memory_order_relaxed) & bit) != 0;
+}
+
 template <typename P>
-cudaError_t launch_cluster(void (*kernel)(P), const P& p, int ctas, size_t smem, cudaStream_t st) {
+cudaError_t launch_cluster(void (*kernel)(P), const P& p, long long items, size_t smem,
+                           cudaStream_t st) {
+  static std::atomic<uint64_t> asked{0}, wide{0};  // (one pair a kernel: P tells them apart)
+  // For few entries and items one CTA of 256 threads, whose barriers are short;
+  // otherwise as many CTAs as leave each thread two items.  16 CTAs instead of 8:
+  // 1024 requests with 33000 new tokens 11.3 -> 8.9 us, 179000 pages of 700
+  // finished requests 14.4 -> 11.5 us.
+  const bool small = p.B <= 256 && items <= 512;
+  int ctas = 1;
+  while (ctas < kCluster && (long long)ctas * 2 * kThreads < items) ctas *= 2;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(small ? 256 : kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at{};
@@ -333,14 +419,11 @@ cudaError_t launch_cluster(void (*kernel)(P), const P& p, int ctas, size_t smem,
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
+  if (ctas > 8 && !wide_clusters(kernel, cfg, &asked, &wide)) {
+    cfg.gridDim = dim3(8);
+    at.val.clusterDim.x = 8;
+  }
   return cudaLaunchKernelEx(&cfg, kernel, p);
-}
-
-// CTAs of the cluster for `items` rows or pages: one more for each 2048.
-int cluster_ctas(long long items) {
-  int c = 1;
-  while (c < kCluster && (long long)c * 2 * kThreads < items) c *= 2;
-  return c;
 }
 
 int check_step(int B, int max_pages, int64_t bt_stride, int page_size, int64_t num_pages,
@@ -405,7 +488,7 @@ PA_API int pa_plan_step(const int32_t* cache_seqlens, const int32_t* q_lens, int
   p.max_pages = max_pages;
   p.token_capacity = token_capacity;
   p.num_pages = (int)num_pages;
-  const cudaError_t e = launch_cluster(plan_kernel, p, cluster_ctas(token_capacity),
+  const cudaError_t e = launch_cluster(plan_kernel, p, token_capacity,
                                        (size_t)B * 3 * sizeof(int),
                                        reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return set_error(PA_ERR_CUDA, "plan launch: %s", cudaGetErrorString(e));
@@ -440,7 +523,7 @@ PA_API int pa_release_pages(const int32_t* cache_seqlens, const int32_t* keep_le
   p.max_pages = max_pages;
   p.num_pages = (int)num_pages;
   const long long most = (long long)B * max_pages;
-  const cudaError_t e = launch_cluster(release_kernel, p, cluster_ctas(most < num_pages ? most : num_pages),
+  const cudaError_t e = launch_cluster(release_kernel, p, most < num_pages ? most : num_pages,
                                        (size_t)B * 2 * sizeof(int),
                                        reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return set_error(PA_ERR_CUDA, "release launch: %s", cudaGetErrorString(e));
