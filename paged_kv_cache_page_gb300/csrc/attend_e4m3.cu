@@ -101,10 +101,6 @@ __device__ __forceinline__ Seq load_seq(const AttendParams& p, int b, int slot, 
 // Cost of one kv head, or of one group of them, of the sequence.
 __device__ __forceinline__ long long cost_of(const Seq& s) { return (long long)s.cost * s.tiles; }
 
-__device__ __forceinline__ long long quotient(long long a, long long b) {
-  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
-}
-
 // A position in a CTA's share: one segment (units [u, u + len) of a stream).
 struct Cursor {
   int b, h, tile, u, len;  // h: group of neighbouring kv heads

@@ -33,6 +33,11 @@ struct AttendParams {
   int32_t* err;
 };
 
+// a / b of non-negative values, in 32 bits where they do.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 struct SeqRows {
   int q0, qlen, lk;
 };

@@ -20,9 +20,9 @@
 // works on the other group.
 //
 // Work: the streams (sequence, kv head, pair of tiles) laid end to end in
-// 128-key tiles, as many as the pair's last row sees, and cut into equal
-// shares, one a CTA, as in the warp-level kernel; split streams are joined by
-// the CTA that finishes last.
+// 128-key tiles, as many as the pair's last row sees, and dealt to the CTAs in
+// equal shares or in slots (below); split streams are joined by the CTA that
+// finishes last.
 #include <algorithm>
 #include <type_traits>
 
@@ -38,6 +38,7 @@ constexpr int kUnits = kN / kPage;
 constexpr int kWarpConv = 8, kWarpMma = 12;
 constexpr int kThreads = 15 * 32;
 constexpr int kMinShare = 4;     // tiles
+constexpr int kSnap = 4;         // tiles that a cut moves to an end of its stream
 
 template <int D>
 struct Layout {
@@ -53,7 +54,8 @@ struct Layout {
   // q_full, q_empty [2], f_empty; full, empty [kRing]; s_full, p_full, pv_done, o_free [2]
   static constexpr int kBars = 5 + 2 * kRing + 8;
   static constexpr int kOffMisc = kOffBar + kBars * 8;      // TMEM base, merge flag
-  static constexpr int kOffSums = kOffKV;                   // long long [kThreads + 16], prologue
+  static constexpr int kOffSums = kOffKV;                   // long long [kThreads + 16]; int [B] from
+                                                            // 16 kThreads on; prologue
   static constexpr int kBytes = kOffMisc + 16 + 1024;
   static_assert(kBytes <= 232448, "shared memory");
 };
@@ -86,17 +88,18 @@ __device__ __forceinline__ int tiles_of(const AttendParams& p, const Stream& x, 
 __device__ __forceinline__ int pair_tiles(const AttendParams& p, const Stream& x, int pair) {
   return max(1, tiles_of(p, x, pair * kChunkRows, kChunkRows));
 }
-__device__ __forceinline__ long long head_tiles(const AttendParams& p, const Stream& x) {
-  long long n = 0;
-  for (int i = 0; i < x.pairs; ++i) n += pair_tiles(p, x, i);
-  return n;
+// Cost of pair `i`: its tiles or, where streams are cut into slots of at most
+// `slot` tiles, the number of them.
+__device__ __forceinline__ int cost_of(int tiles, int slot) {
+  return slot > 0 ? (tiles - 1) / slot + 1 : tiles;
 }
 
 // A segment of a CTA's share: tiles [t0, t0 + n) of a stream.
 struct Walk {
   int b, h, pair, t0, n, all;  // all: tiles of the stream
-  long long left;              // tiles of the share from t0 on
-  long long begin;             // first tile of the stream, counted over all streams
+  int slot;
+  long long left;              // cost of the share from t0 on
+  long long begin;             // cost of the streams in front
   Stream x;
 
   __device__ __forceinline__ int rows0() const { return pair * kChunkRows; }
@@ -104,11 +107,10 @@ struct Walk {
   __device__ __forceinline__ int group_end(const AttendParams& p, int g) const {
     return min(t0 + n, tiles_of(p, x, rows0() + g * kM, kM));
   }
-  __device__ __forceinline__ void next(const AttendParams& p) {
-    left -= n;
-    begin += all;
-    t0 = n = 0;
-    if (left <= 0) return;
+  // The stream behind this one.
+  __device__ __forceinline__ void next_stream(const AttendParams& p) {
+    begin += cost_of(all, slot);
+    t0 = 0;
     if (++pair == x.pairs) {
       pair = 0;
       if (++h == p.Hkv) {
@@ -123,6 +125,12 @@ struct Walk {
       }
     }
     all = pair_tiles(p, x, pair);
+  }
+  __device__ __forceinline__ void next(const AttendParams& p) {
+    left -= slot > 0 ? 1 : n;
+    n = 0;
+    if (left <= 0) return;
+    next_stream(p);
     n = (int)min((long long)all, left);
   }
 };
@@ -237,6 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
   int* sFlag = reinterpret_cast<int*>(smem + L::kOffMisc) + 1;
   long long* sSums = reinterpret_cast<long long*>(smem + L::kOffSums);
+  int* sStreams = reinterpret_cast<int*>(smem + L::kOffF);  // [warps], prologue
 
   griddep_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -260,57 +269,130 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   }
 
   // ---- the CTA's share
-  const int per = (p.B + kThreads - 1) / kThreads;
-  long long incl = 0;
-  for (int i = 0; i < per; ++i) {
-    const int b = tid * per + i;
-    if (b < p.B) incl += head_tiles(p, load_stream(p, b, false)) * p.Hkv;
-  }
+  // A pass over the batch finds each sequence's cost, a warp a sequence, a lane a
+  // pair, and its running sums, a thread kPer sequences.  The first pass counts
+  // tiles.  Fewer streams than CTAs are then cut into slots, one a CTA, of a
+  // length that half a slot a stream less fills the CTAs with (second pass) or,
+  // where there are more of those than CTAs, that always does (third).
+  int* sCost = reinterpret_cast<int*>(smem + L::kOffSums) + 4 * kThreads;  // [B]
+  const int per = (p.B + kThreads - 1) / kThreads, ctas = (int)gridDim.x;
+  long long total = 0, tiles = 0;
+  int slot = 0, streams = 0;
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    int mine = 0;
+    for (int b = warp; b < p.B; b += kThreads / 32) {
+      const Stream x = load_stream(p, b, false);
+      int cost = 0;
+      for (int i = lane; i < x.pairs; i += 32) cost += cost_of(pair_tiles(p, x, i), slot);
+      cost = __reduce_add_sync(0xffffffffu, cost);
+      if (lane == 0) sCost[b] = cost;
+      mine += x.pairs;
+    }
+    if (lane == 0) sStreams[warp] = mine;
+    __syncthreads();
+    long long incl = 0;
+    for (int i = 0; i < per; ++i)
+      if (tid * per + i < p.B) incl += (long long)sCost[tid * per + i] * p.Hkv;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) sSums[kThreads + warp] = incl;
+    __syncthreads();
+    total = 0;
+    streams = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      const long long x = sSums[kThreads + w];
+      if (w < warp) incl += x;
+      total += x;
+      streams += sStreams[w];
+    }
+    sSums[tid] = incl;
+    __syncthreads();
+    const long long all_streams = (long long)streams * p.Hkv;
+    if (pass == 0) tiles = total;
+    if (all_streams >= ctas || (pass > 0 && total <= ctas)) break;
+    const float room = pass == 0 ? (float)ctas - 0.5f * (float)all_streams
+                                 : (float)ctas - (float)all_streams;
+    slot = (int)((float)tiles / room) + 2;
   }
-  if (lane == 31) sSums[kThreads + warp] = incl;
-  __syncthreads();
-  long long total = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    const long long x = sSums[kThreads + w];
-    if (w < warp) incl += x;
-    total += x;
-  }
-  sSums[tid] = incl;
-  __syncthreads();
-  const long long share = max((total + gridDim.x - 1) / gridDim.x, (long long)kMinShare);
-  const long long first = share * blockIdx.x;
-  if (first >= total) return;
+  // Otherwise equal shares of the tiles.  A cut at most kSnap tiles from an end of
+  // its stream moves there: a segment costs about as much as that many tiles.
+  const long long share =
+      slot > 0 ? 1 : max(quotient(total + ctas - 1, ctas), (long long)kMinShare);
+  if (share * blockIdx.x >= total) return;
   Walk at{};
-  {
+  at.slot = slot;
+  long long end = 0;
+#pragma unroll 1
+  for (int side = 1; side >= 0; --side) {  // the end of the share, then its begin
+    const long long cut = share * (blockIdx.x + side);
+    if (side == 1 && (slot > 0 || cut >= total)) {
+      end = min(cut, total);
+      continue;
+    }
     int lo = 0;
     for (int step = 256; step > 0; step >>= 1)
-      if (lo + step <= kThreads && sSums[lo + step - 1] <= first) lo += step;
-    long long off = first - (lo > 0 ? sSums[lo - 1] : 0);
+      if (lo + step <= kThreads && sSums[lo + step - 1] <= cut) lo += step;
+    at.begin = lo > 0 ? sSums[lo - 1] : 0;
     at.b = lo * per;
+    while (at.b + 1 < p.B && cut - at.begin >= (long long)sCost[at.b] * p.Hkv)
+      at.begin += (long long)sCost[at.b++] * p.Hkv;
     at.x = load_stream(p, at.b, false);
-    long long head = head_tiles(p, at.x);
-    while (off >= head * p.Hkv && at.b + 1 < p.B) {
-      off -= head * p.Hkv;
-      at.x = load_stream(p, ++at.b, false);
-      head = head_tiles(p, at.x);
+    const int head = max(sCost[at.b], 1);
+    const long long off = cut - at.begin;
+    at.h = (int)quotient(off, head);
+    at.begin += (long long)at.h * head;
+    int rest = (int)(off - (long long)at.h * head);
+    // the pair: 32 a step, by a scan over the lanes
+    at.pair = 0;
+#pragma unroll 1
+    for (int i0 = 0;; i0 += 32) {
+      const int i = i0 + lane;
+      const int cost = i < at.x.pairs ? cost_of(pair_tiles(p, at.x, i), slot) : 0;
+      int sum = cost;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += y;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, sum > rest);
+      if (past == 0 && i0 + 32 < at.x.pairs) {
+        const int step = __shfl_sync(0xffffffffu, sum, 31);
+        rest -= step;
+        at.begin += step;
+        continue;
+      }
+      const int l = past != 0 ? __ffs(past) - 1 : 0;
+      const int before = __shfl_sync(0xffffffffu, sum - cost, l);
+      rest -= before;
+      at.begin += before;
+      at.pair = i0 + l;
+      break;
     }
-    at.h = (int)(off / head);
-    off %= head;
-    at.all = pair_tiles(p, at.x, 0);
-    while (off >= at.all) {
-      off -= at.all;
-      at.all = pair_tiles(p, at.x, ++at.pair);
+    at.all = pair_tiles(p, at.x, at.pair);
+    at.t0 = rest;
+    if (slot > 0) {
+      const int chunk = (at.all - 1) / cost_of(at.all, slot) + 1;
+      at.t0 = rest * chunk;
+      at.n = min(chunk, at.all - at.t0);
+      at.left = 1;
+    } else {
+      if (blockIdx.x + side > 0) {
+        if (at.t0 <= kSnap) at.t0 = 0;
+        else if (at.all - at.t0 <= kSnap) at.next_stream(p);
+      }
+      if (side == 1) {
+        end = at.begin + at.t0;
+      } else {
+        at.left = end - (at.begin + at.t0);
+        at.n = (int)min((long long)(at.all - at.t0), at.left);
+      }
     }
-    at.t0 = (int)off;
-    at.left = min(share, total - first);
-    at.n = (int)min((long long)(at.all - at.t0), at.left);
-    at.begin = first - at.t0;
   }
+  if (at.left <= 0) return;
   if (warp == kWarpMma) {
     tc::tmem_alloc(tslot, 512);
     tc::tmem_relinquish();
@@ -803,14 +885,22 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         if (valid) put_lse(m, l);
       } else {
         p.part_ml[my_part + r] = make_float2(m, l);
-        const int cta0 = (int)(at.begin / share);
-        const int cta1 = (int)((at.begin + at.all - 1) / share);
-        __threadfence();
-        named_barrier(1, 256);
-        if (tid == 0) *sFlag = arrive_last(p.words + cta0, launch_tag(), cta1 - cta0 + 1) ? 1 : 0;
+        int cta0, cta1;
+        if (at.slot > 0) {
+          cta0 = (int)at.begin;
+          cta1 = cta0 + cost_of(at.all, at.slot) - 1;
+        } else {  // the cuts that were not moved to the stream's ends
+          cta0 = (int)quotient(at.begin + kSnap, share);
+          cta1 = (int)quotient(at.begin + at.all - kSnap - 1, share);
+        }
+        named_barrier(1, 256);  // the partial rows of the CTA before its arrival
+        if (tid == 0) {
+          __threadfence();
+          *sFlag = arrive_last(p.words + cta0, launch_tag(), cta1 - cta0 + 1) ? 1 : 0;
+          __threadfence();
+        }
         named_barrier(1, 256);
         if (*sFlag) {
-          __threadfence();
           // the first row of the stream's split n, of this thread's group
           auto from = [&](int cta) {
             return ((int64_t)(2 * cta + (cta == cta0 ? 1 : 0)) * 2 + g) * kM;
@@ -827,18 +917,18 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             sum = fmaf(weight(ml), ml.y, sum);
           }
           const float by = sum == 0.f ? 0.f : vs / sum;
-          constexpr int kPart = D / 32;  // 16-byte chunks of an eighth of the row
+          constexpr int kPart = D / 16, kSplits = 2;  // 16-byte chunks of a quarter of the row
 #pragma unroll 1
-          for (int part = 0; part < 8; ++part) {
+          for (int part = 0; part < 4; ++part) {
             float4 acc[kPart];
 #pragma unroll
             for (int e = 0; e < kPart; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-            for (int cta = cta0; cta <= cta1; cta += 4) {  // four splits in flight
-              float4 y[4][kPart];
-              float w[4];
+            for (int cta = cta0; cta <= cta1; cta += kSplits) {
+              float4 y[kSplits][kPart];
+              float w[kSplits];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
+              for (int j = 0; j < kSplits; ++j) {
                 const int64_t at_row = from(min(cta + j, cta1));
                 const float2 ml = __ldcg(p.part_ml + at_row + r);
                 w[j] = cta + j <= cta1 ? weight(ml) : 0.f;
@@ -848,7 +938,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                                       (at_row * (D / 4) + (part * kPart + e) * kM + r) * 4);
               }
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
+              for (int j = 0; j < kSplits; ++j) {
                 if (w[j] == 0.f) continue;  // (an unset O is not read)
 #pragma unroll
                 for (int e = 0; e < kPart; ++e) {
@@ -862,7 +952,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             if (valid) {
 #pragma unroll
               for (int e = 0; e < kPart; e += 2)
-                *reinterpret_cast<uint4*>(out_row() + part * (D / 8) + e * 4) = make_uint4(
+                *reinterpret_cast<uint4*>(out_row() + part * (D / 4) + e * 4) = make_uint4(
                     E::from_f2(acc[e].x * by, acc[e].y * by), E::from_f2(acc[e].z * by, acc[e].w * by),
                     E::from_f2(acc[e + 1].x * by, acc[e + 1].y * by),
                     E::from_f2(acc[e + 1].z * by, acc[e + 1].w * by));

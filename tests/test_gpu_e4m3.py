@@ -44,6 +44,47 @@ def test_long_chunks(heads, dtype):
     check(w, out, lse)
 
 
+@pytest.mark.parametrize("heads", [(32, 32, 64), (24, 24, 128), (7, 1, 64), (9, 3, 128), (96, 32, 128)])
+def test_chunks_of_many_heads(heads):
+    """More streams than CTAs (equal shares that cut streams), group sizes that divide no tile, rows
+    that end inside a tile, and a chunk longer than its keys."""
+    q_lens, k_lens = [300, 129, 1, 513, 200, 0], [700, 129, 50, 1300, 90, 0]
+    w = batch(q_lens, k_lens, *heads, "bf16", page=32, seed=sum(heads))
+    err = pa.new_err_word(DEV)
+    out, lse = call(w, err=err)
+    assert err.tolist() == [0] * 4
+    check(w, out, lse)
+    again, lse2 = call(w)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("heads,dtype", [((4, 1, 128), "f16"), ((8, 2, 64), "bf16"), ((1, 1, 128), "bf16")])
+@pytest.mark.parametrize("causal", [True, False])
+def test_a_chunk_over_a_long_prefix_is_split_and_joined(heads, dtype, causal):
+    w = batch([150], [9001], *heads, dtype, page=128, seed=17, peaky=4.0)
+    out, lse = call(w, causal=causal)
+    check(w, out, lse, causal=causal)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_chunks_with_shifting_maxima_and_odd_scales(d):
+    """Rising maxima inside a tile and from tile to tile (probabilities already written are scaled
+    again), a negative and a zero scale, rows of zeros and of large magnitude."""
+    w = batch([200, 90], [900, 400], 6, 3, d, "bf16", seed=18)
+    k = w["k_cache"]
+    for b in range(2):
+        for j, page in enumerate(w["block_table"][b].tolist()):
+            if page >= 0:
+                step = torch.arange(16, device=DEV)[:, None, None] * 0.3
+                k[page] = (k[page].float() * 0.01 + j * 3.0 + step).clamp(-448, 448).to(k.dtype)
+    w["q"] = w["q"].abs()
+    w["q"][7] = 0
+    w["q"][9] *= 64
+    check(w, *call(w))
+    w["k_scale"] = w["k_scale"] * torch.tensor([-1.0, 0.0, 1.0], device=DEV)
+    check(w, *call(w))
+
+
 @pytest.mark.parametrize("heads", [(1, 1, 128), (1, 1, 64), (64, 1, 128), (8, 8, 128)])
 @pytest.mark.parametrize("q_len", [1, 4])
 def test_one_long_sequence_is_split_and_joined(heads, q_len):
