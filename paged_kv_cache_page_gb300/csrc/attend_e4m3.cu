@@ -70,8 +70,7 @@ struct Layout {
   static constexpr int kOffO = kWarps * kRing;             // float [kWarps][8 rows][D]
   static constexpr int kOffM = kOffO + kWarps * 8 * D * 4;
   static constexpr int kOffL = kOffM + kWarps * kRows * 4;
-  static constexpr int kOffCursor = kOffL + kWarps * kRows * 4;  // Cursor [2][kWarps]
-  static constexpr int kOffFlag = kOffCursor + 2 * kWarps * 72;
+  static constexpr int kOffFlag = kOffL + kWarps * kRows * 4;
   static constexpr int kOffSums = kOffO;  // long long [kThreads + kWarps], before the first merge
   static constexpr int kBytes = kOffFlag + 16;
   static_assert(kBytes <= 232448, "shared memory");
@@ -144,8 +143,6 @@ struct Cursor {
   }
 };
 
-static_assert(sizeof(Cursor) <= 72, "kOffCursor");
-
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
   asm volatile(
@@ -215,92 +212,93 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   const int g = lane >> 2, t = lane & 3;
 
   // ---- the CTA's share
-  // Rolled loops: what runs once costs its instructions' way from L2, about a
-  // dozen cycles each.  A pass finds the running sums of the sequences' costs for
-  // one kv head.  The first counts units, and with them tiles, the longest
-  // stream and what the long query blocks of a mixed batch cost their kernel.
+  // Sums over the batch, for one kv head: units, tiles, and the longest stream.
   const int per = (p.B + kThreads - 1) / kThreads;
-  int ctas = (int)gridDim.x, slot = 0, hw_log2 = 0, groups = p.Hkv;
-  long long total = 0, units = 0;
-  float streams = 0.f;
-#pragma unroll 1
-  for (int pass = 0; pass < 3; ++pass) {
-    long long incl = 0;
-    int tiles = 0, longest = 0, others = 0;
-#pragma unroll 1
-    for (int i = 0; i < per; ++i) {
-      const int b = tid * per + i;
-      if (b >= p.B) break;
-      const Seq s = load_seq(p, b, slot, pass == 0 && blockIdx.x == 0);
-      incl += cost_of(s);
-      tiles += s.tiles;
-      longest = max(longest, s.units);
-      if (p.mixed && pass == 0 && s.tiles == 0) others += (int)long_block_tiles(p, seq_rows(p, b, false));
-    }
-#pragma unroll 1
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    tiles = __reduce_add_sync(0xffffffffu, tiles);
-    longest = __reduce_max_sync(0xffffffffu, longest);
-    others = __reduce_add_sync(0xffffffffu, others);
-    if (lane == 31) {
-      sSums[kThreads + warp] = incl;
-      reinterpret_cast<int4*>(sM)[warp] = make_int4(tiles, longest, others, 0);
-    }
+  auto block_sum = [&](long long x, int row) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    if (lane == 0) sSums[row * kWarps + warp] = x;
     __syncthreads();
-    total = 0;
-    tiles = longest = others = 0;
-#pragma unroll 1
-    for (int w = 0; w < kWarps; ++w) {
-      const long long x = sSums[kThreads + w];
-      if (w < warp) incl += x;
-      total += x;
-      const int4 y = reinterpret_cast<const int4*>(sM)[w];
-      tiles += y.x;
-      longest = max(longest, y.y);
-      others += y.z;
-    }
-    sSums[tid] = incl;
-    __syncthreads();
-    if (pass == 0) {
-      units = total;
-      if (p.mixed) ctas -= chunk_ctas((float)others, (float)units * p.Hkv * kUnitTiles, ctas);
-      if (ctas <= (int)blockIdx.x) break;
-      // Neighbouring kv heads side by side: 2^hw_log2 of them, each with 8 >>
-      // hw_log2 of the warps, while a share stays long.
-      while (longest > kWholeUnits && hw_log2 < kMaxSide && (p.Hkv >> hw_log2) % 2 == 0 &&
-             units * p.Hkv >= ((long long)kSideUnits << hw_log2) * ctas)
-        ++hw_log2;
-      groups = p.Hkv >> hw_log2;
-      streams = (float)tiles * groups;
-    }
-    // How the streams are dealt.  Short ones whole.  A few long ones in slots, one
-    // a CTA: of a length that half a slot a stream less fills the CTAs with, where
-    // that suffices, or one that always does.  Otherwise equal shares that cut
-    // streams anywhere -- every CTA is as long, but a segment more costs it what
-    // kSegment units do.
-    const float all = (float)(units * groups);
-    if (longest <= kWholeUnits) {
-      if (slot > 0) break;
-      slot = kWholeUnits;
-    } else {
-      if (streams >= ctas || (pass > 0 && (slot == 0 || total * groups <= ctas))) break;
-      slot = (int)(all / (ctas - (pass > 0 ? streams : 0.5f * streams))) + 2;
-      if (slot > all / ctas + (kSegment >> hw_log2)) {
-        slot = 0;
-        if (pass == 0) break;
-      }
-    }
+    long long y = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) y += sSums[row * kWarps + w];
+    return y;
+  };
+  long long mine = 0;
+  int tiles = 0, longest = 0;
+  for (int i = 0; i < per; ++i) {
+    const int b = tid * per + i;
+    if (b >= p.B) break;
+    const Seq s = load_seq(p, b, 0, blockIdx.x == 0);
+    mine += cost_of(s);
+    tiles += s.tiles;
+    longest = max(longest, s.units);
   }
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  if (lane == 0) sM[warp] = __int_as_float(longest);
+  const long long units = block_sum(mine, 0);
+  long long streams = block_sum(tiles, 1);
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) longest = max(longest, __float_as_int(sM[w]));
+  // Neighbouring kv heads side by side: 2^hw_log2 of them, each with 8 >> hw_log2
+  // of the warps, while a share stays long.
+  int hw_log2 = 0;
+  while (longest > kWholeUnits && hw_log2 < kMaxSide && (p.Hkv >> hw_log2) % 2 == 0 &&
+         units * p.Hkv >= ((long long)kSideUnits << hw_log2) * gridDim.x)
+    ++hw_log2;
   const int hw = 1 << hw_log2, step_u = kWarps >> hw_log2;
   const int my_u = warp & (step_u - 1), my_hh = warp >> (3 - hw_log2);
+  const int groups = p.Hkv >> hw_log2;
+  streams *= groups;
+  // How the streams are dealt.  Short ones whole.  A few long ones in slots, one
+  // a CTA: of a length that half a slot a stream less fills the CTAs with, where
+  // that suffices, or one that always does.  Otherwise equal shares that cut
+  // streams anywhere -- every CTA is as long, but a segment more costs it what
+  // kSegment units do.
+  int slot = 0;
+  const int ctas = (int)gridDim.x;
+  if (longest <= kWholeUnits) {
+    slot = kWholeUnits;
+  } else if (streams < ctas) {
+    const float all = (float)(units * groups);
+    slot = (int)(all / (ctas - 0.5f * (int)streams)) + 2;
+    int count = 0;  // slots
+    for (int i = 0; i < per; ++i) {
+      const int b = tid * per + i;
+      if (b < p.B) count += (int)cost_of(load_seq(p, b, slot, false));
+    }
+    if (block_sum(count, 2) * groups > ctas) slot = (int)(all / (ctas - (int)streams)) + 2;
+    if (slot > all / ctas + (kSegment >> hw_log2)) slot = 0;
+  }
+  if (slot > 0) {
+    mine = 0;
+    for (int i = 0; i < per; ++i) {
+      const int b = tid * per + i;
+      if (b < p.B) mine += cost_of(load_seq(p, b, slot, false));
+    }
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) sSums[kThreads + warp] = incl;  // (behind the rows of block_sum)
+  __syncthreads();
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const long long x = sSums[kThreads + w];
+    if (w < warp) incl += x;
+    total += x;
+  }
+  sSums[tid] = incl;
+  __syncthreads();
   total *= groups;
-  long long share = quotient(total + ctas - 1, ctas);
+  long long share = quotient(total + gridDim.x - 1, gridDim.x);
   if (slot == 0) share = max((share + step_u - 1) & ~(long long)(step_u - 1), (long long)kMinShare);
   const long long first = share * blockIdx.x;
-  if ((int)blockIdx.x >= ctas || first >= total) {
+  if (first >= total) {
     griddep_wait();
     return;
   }
@@ -308,7 +306,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   long long stream0;  // cost of the streams in front of the segment's
   {
     int lo = 0;  // the first thread whose sum passes `first`
-#pragma unroll 1
     for (int step = kThreads / 2; step > 0; step >>= 1)
       if (sSums[lo + step - 1] * groups <= first) lo += step;
     long long off = first - (lo > 0 ? sSums[lo - 1] * groups : 0);
@@ -340,57 +337,48 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   const uint32_t ring = smem_u32(smem) + warp * L::kRing;
   const int64_t k_lane = (int64_t)my_r * p.k_st + my_c * 16, v_lane = (int64_t)my_r * p.v_st + my_c * 16;
   const int64_t k_next = (int64_t)kRowsAt * p.k_st, v_next = (int64_t)kRowsAt * p.v_st;
-  // The position of the copies, and during a segment's loop that of the
-  // segment, wait in shared memory: the loop's registers are worth more.
-  Cursor* sAhead = reinterpret_cast<Cursor*>(smem + L::kOffCursor) + warp;
-  Cursor* sAt = sAhead + kWarps;
-  if (lane == 0) *sAhead = at;
-  __syncwarp();
-  // The warp's units a_i, a_i + step_u, ... below a_end of the sequence's; a_end
-  // 0: no more.  Their table entries 32 at a time, one a lane, from unit e_from
-  // on: one latency for all of them.
-  int a_i = at.u + my_u, a_end = at.u + at.seen(p), a_lk = at.s.lk, entries = 0, e_from = 0;
-  const uint8_t *k_head = p.k_cache + (at.h * hw + my_hh) * p.k_sh + k_lane,
-                *v_head = p.v_cache + (at.h * hw + my_hh) * p.v_sh + v_lane;
-  const int32_t* a_row = p.block_table + (int64_t)at.b * p.bt_stride;
+  Cursor ahead = at;
+  int a_i = my_u, a_seen = ahead.seen(p);
+  // Table entries of the warp's next 32 units of the segment, one a lane, from
+  // unit e_from on: one latency for all of them.
+  int entries = 0, e_from = 0;
+  const uint8_t *k_head = p.k_cache + (ahead.h * hw + my_hh) * p.k_sh + k_lane,
+                *v_head = p.v_cache + (ahead.h * hw + my_hh) * p.v_sh + v_lane;
+  const int32_t* a_row = p.block_table + (int64_t)ahead.b * p.bt_stride;
   auto read_entries = [&]() {
     e_from = a_i;
     const int i = a_i + lane * step_u;
-    if (i < a_end) entries = __ldg(a_row + (i >> p.page_shift));
+    if (ahead.left > 0 && i < a_seen) entries = __ldg(a_row + ((ahead.u + i) >> p.page_shift));
   };
-  auto next_segment = [&]() {
-    Cursor c = *sAhead;
-    __syncwarp();
-#pragma unroll 1
-    do {
-      c.next(p);
-      if (c.left <= 0) {
-        a_end = 0;
-        return;
-      }
-      a_i = c.u + my_u;
-      a_end = c.u + c.seen(p);
-    } while (a_i >= a_end);
-    if (lane == 0) *sAhead = c;
-    __syncwarp();
-    a_lk = c.s.lk;
-    k_head = p.k_cache + (c.h * hw + my_hh) * p.k_sh + k_lane;
-    v_head = p.v_cache + (c.h * hw + my_hh) * p.v_sh + v_lane;
-    a_row = p.block_table + (int64_t)c.b * p.bt_stride;
+  auto find = [&]() {  // moves to the warp's next unit
+    if (a_i < a_seen) {
+      if (a_i == e_from + 32 * step_u) read_entries();
+      return;
+    }
+    while (ahead.left > 0 && a_i >= a_seen) {
+      ahead.next(p);
+      if (ahead.left <= 0) return;
+      a_i = my_u;
+      a_seen = ahead.seen(p);
+    }
+    k_head = p.k_cache + (ahead.h * hw + my_hh) * p.k_sh + k_lane;
+    v_head = p.v_cache + (ahead.h * hw + my_hh) * p.v_sh + v_lane;
+    a_row = p.block_table + (int64_t)ahead.b * p.bt_stride;
     read_entries();
   };
   auto copy = [&](int stage) {
-    if (a_end > 0) {
+    if (ahead.left > 0) {
+      const int unit = ahead.u + a_i;
       int page = __shfl_sync(0xffffffffu, entries, (a_i - e_from) >> (3 - hw_log2));
       if (page < 0 || page >= p.num_pages) {
-        if (lane == 0 && a_i * kKeys < a_lk) report(p.err, PA_DEVERR_PAGE_OOB, sAhead->b, a_i);
+        if (lane == 0 && unit * kKeys < ahead.s.lk) report(p.err, PA_DEVERR_PAGE_OOB, ahead.b, unit);
         page = 0;
       }
-      const int row0 = (a_i & ((1 << p.page_shift) - 1)) * kKeys;
+      const int row0 = (unit & ((1 << p.page_shift) - 1)) * kKeys;
       const uint32_t dst = ring + stage * L::kStage;
       const uint8_t* ks = k_head + ((int64_t)page * p.k_sb + (int64_t)row0 * p.k_st);
       const uint8_t* vs = v_head + ((int64_t)page * p.v_sb + (int64_t)row0 * p.v_st);
-      const int valid = a_lk - a_i * kKeys;  // rows of the unit that hold a key
+      const int valid = ahead.s.lk - unit * kKeys;  // rows of the unit that hold a key
 #pragma unroll
       for (int i = 0; i < kKeys / kRowsAt; ++i) {
         const int r = my_r + i * kRowsAt;
@@ -401,8 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         vs += v_next;
       }
       a_i += step_u;
-      if (a_i >= a_end) next_segment();
-      else if (a_i == e_from + 32 * step_u) read_entries();
+      find();
     }
     cp_commit();  // an empty group where nothing is left keeps the count
   };
@@ -433,8 +420,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     }
   };
   read_rows(at);
-  if (a_i < a_end) read_entries();
-  else next_segment();
+  if (a_i < a_seen)
+    read_entries();
+  else
+    find();
 #pragma unroll 1
   for (int i = 0; i < L::kStages; ++i) copy(i);
   int stage = 0;
@@ -502,10 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       for (int i = 0; i < 4; ++i) o[e][i] = 0.f;
     float m[2] = {neg_inf(), neg_inf()}, l[2] = {0.f, 0.f};  // m: the reference less kShift
 
-    const int n = at.seen(p), u0 = at.u;
-    __syncwarp();
-    if (lane == 0) *sAt = at;
-    __syncwarp();
+    const int n = at.seen(p);
     // N of the warp's units at a time (two where there are two: twice the
     // independent work for the same waits): i, i + step_u.
     auto step = [&](auto units, int i) {
@@ -545,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           }
       }
       // softmax
-      const int key0 = (u0 + i) * kKeys, key_step = step_u * kKeys;  // unit u: key0 + u key_step
+      const int key0 = (at.u + i) * kKeys, key_step = step_u * kKeys;  // unit u: key0 + u key_step
       const bool part = key0 + (N - 1) * key_step + kKeys > all;  // not seen whole by every row
       if (part) {
 #pragma unroll
@@ -680,7 +666,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
 #pragma unroll 1
     for (; i + step_u < n; i += 2 * step_u) step(std::integral_constant<int, 2>{}, i);
     if (i < n) step(std::integral_constant<int, 1>{}, i);
-    at = *sAt;
 
     // ---- the warps' results: (m, l, O) of each, merged by column, eight rows
     // at a time
@@ -992,7 +977,6 @@ PA_API int pa_fwd_varlen_e4m3(const void* q, int64_t q_st, int64_t q_sh, pa_tens
   p.err = err_word;
   // sequences of more rows than max_seqlen_q said run on the warp-level kernel
   p.small_rows = chunks ? kSmallRows : 0x7fffffff;
-  p.mixed = chunks ? 1 : 0;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (chunks) {

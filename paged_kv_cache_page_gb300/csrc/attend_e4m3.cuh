@@ -21,7 +21,6 @@ struct AttendParams {
   const int32_t *cu_seqlens_q, *seqlens_k, *block_table;
   int64_t bt_stride, num_pages;
   int B, total_q, Hq, Hkv, G, max_pages, page_shift, max_seqlen_k, causal;
-  int mixed;       // both kernels run, each on a part of the CTAs
   int small_rows;  // sequences of at most this many rows per kv head run on the warp-level kernel
   float scale_log2;
   void* out;
@@ -38,9 +37,6 @@ struct AttendParams {
 __device__ __forceinline__ long long quotient(long long a, long long b) {
   return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
-
-constexpr int kChunkRows = 256;  // rows of its pair of query tiles: part_ml [2 CTAs][256],
-                                 // part_o [2 CTAs][2 tiles][D / 4][128][4]
 
 struct SeqRows {
   int q0, qlen, lk;
@@ -72,30 +68,6 @@ __device__ __forceinline__ uint32_t f16x2_of(uint32_t e4m3x2) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)e4m3x2));
   return h;
 }
-// In a batch of long and short query blocks both kernels run at once, each on a
-// part of the CTAs.  Costs are counted in the long blocks' 256 x 128 tiles: a
-// segment of theirs costs kSegmentTiles more, and a unit of 16 keys of the
-// short ones kUnitTiles (an SM reads about twice its share of the memory's rate
-// when fewer of them read).
-constexpr float kSegmentTiles = 6.f, kUnitTiles = 1.f / 48.f;
-
-__device__ __forceinline__ float short_block_tiles(const AttendParams& p, const SeqRows& r) {
-  if (r.qlen == 0) return 0.f;
-  return (float)((r.qlen * p.G + 15) / 16) * (float)max(1, (r.lk + 15) / 16) * p.Hkv * kUnitTiles;
-}
-__device__ __forceinline__ float long_block_tiles(const AttendParams& p, const SeqRows& r) {
-  if (r.qlen == 0) return 0.f;
-  const float keys = p.causal ? r.lk - 0.5f * r.qlen : (float)r.lk;
-  return (float)((r.qlen * p.G + kChunkRows - 1) / kChunkRows) * p.Hkv *
-         (fmaxf(keys, 0.f) / 128.f + 0.5f + kSegmentTiles);
-}
-// CTAs of `ctas` for the long blocks.
-__device__ __forceinline__ int chunk_ctas(float longs, float shorts, int ctas) {
-  if (longs <= 0.f) return 0;
-  if (shorts <= 0.f) return ctas;
-  return min(max((int)(ctas * longs / (longs + shorts) + 0.5f), 1), ctas - 1);
-}
-
 // Four e4m3 values (the low byte first) as two pairs of fp16 values.
 __device__ __forceinline__ void f16x4_of(uint32_t w, uint32_t& lo, uint32_t& hi) {
   asm("{\n\t.reg .b16 a, b;\n\t"
@@ -118,5 +90,7 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
 // The attention of sequences of more than small_rows rows per kv head
 // (chunk_e4m3.cu).
 cudaError_t launch_chunks_e4m3(const AttendParams& p, int D, int dtype, cudaStream_t st);
+constexpr int kChunkRows = 256;  // rows of its pair of query tiles: part_ml [2 CTAs][256],
+                                 // part_o [2 CTAs][2 tiles][D / 4][128][4]
 
 }  // namespace pa

@@ -245,23 +245,20 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
   int* sFlag = reinterpret_cast<int*>(smem + L::kOffMisc) + 1;
   long long* sSums = reinterpret_cast<long long*>(smem + L::kOffSums);
-  int4* sStreams = reinterpret_cast<int4*>(smem + L::kOffF);  // [warps], prologue
+  int* sStreams = reinterpret_cast<int*>(smem + L::kOffF);  // [warps], prologue
 
   griddep_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-#pragma unroll 1
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 8);
       mbar_init(&q_empty[i], 1);
     }
     mbar_init(f_empty, 8);
-#pragma unroll 1
     for (int i = 0; i < L::kRing; ++i) {
       mbar_init(&full[i], 4);
       mbar_init(&empty[i], 1);
     }
-#pragma unroll 1
     for (int g = 0; g < 2; ++g) {
       mbar_init(&s_full[g], 1);
       mbar_init(&p_full[g], 4);
@@ -271,45 +268,33 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     fence_mbar_init();
   }
 
-  // ---- the CTA's share.  Rolled loops: what runs once costs its instructions'
-  // way from L2, about a dozen cycles each.
+  // ---- the CTA's share
   // A pass over the batch finds each sequence's cost, a warp a sequence, a lane a
   // pair, and its running sums, a thread kPer sequences.  The first pass counts
   // tiles.  Fewer streams than CTAs are then cut into slots, one a CTA, of a
   // length that half a slot a stream less fills the CTAs with (second pass) or,
   // where there are more of those than CTAs, that always does (third).
   int* sCost = reinterpret_cast<int*>(smem + L::kOffSums) + 4 * kThreads;  // [B]
-  const int per = (p.B + kThreads - 1) / kThreads;
-  int ctas = (int)gridDim.x;
+  const int per = (p.B + kThreads - 1) / kThreads, ctas = (int)gridDim.x;
   long long total = 0, tiles = 0;
   int slot = 0, streams = 0;
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     int mine = 0;
-    int longs = 0, shorts = 0;  // what this kernel's sequences cost, and the other's, about
-#pragma unroll 1
     for (int b = warp; b < p.B; b += kThreads / 32) {
       const Stream x = load_stream(p, b, false);
-      if (pass == 0) {
-        if (x.rows > 0) longs += (int)long_block_tiles(p, x.s);
-        else shorts += (int)ceilf(short_block_tiles(p, x.s));
-      }
       int cost = 0;
-#pragma unroll 1
       for (int i = lane; i < x.pairs; i += 32) cost += cost_of(pair_tiles(p, x, i), slot);
       cost = __reduce_add_sync(0xffffffffu, cost);
       if (lane == 0) sCost[b] = cost;
       mine += x.pairs;
     }
-    if (lane == 0) {
-      sStreams[warp] = make_int4(mine, longs, shorts, 0);
-    }
+    if (lane == 0) sStreams[warp] = mine;
     __syncthreads();
     long long incl = 0;
-#pragma unroll 1
     for (int i = 0; i < per; ++i)
       if (tid * per + i < p.B) incl += (long long)sCost[tid * per + i] * p.Hkv;
-#pragma unroll 1
+#pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += y;
@@ -318,25 +303,16 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     __syncthreads();
     total = 0;
     streams = 0;
-    longs = shorts = 0;
-#pragma unroll 1
     for (int w = 0; w < kThreads / 32; ++w) {
-      const int4 z = sStreams[w];
-      streams += z.x;
-      longs += z.y;
-      shorts += z.z;
       const long long x = sSums[kThreads + w];
       if (w < warp) incl += x;
       total += x;
+      streams += sStreams[w];
     }
     sSums[tid] = incl;
     __syncthreads();
     const long long all_streams = (long long)streams * p.Hkv;
-    if (pass == 0) {
-      tiles = total;
-      if (tiles == 0) return;
-      ctas = chunk_ctas((float)longs, (float)shorts, ctas);
-    }
+    if (pass == 0) tiles = total;
     if (all_streams >= ctas || (pass > 0 && total <= ctas)) break;
     const float room = pass == 0 ? (float)ctas - 0.5f * (float)all_streams
                                  : (float)ctas - (float)all_streams;
@@ -346,19 +322,18 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   // its stream moves there: a segment costs about as much as that many tiles.
   const long long share =
       slot > 0 ? 1 : max(quotient(total + ctas - 1, ctas), (long long)kMinShare);
-  if ((int)blockIdx.x >= ctas || share * blockIdx.x >= total) return;
+  if (share * blockIdx.x >= total) return;
   Walk at{};
   at.slot = slot;
   long long end = 0;
 #pragma unroll 1
   for (int side = 1; side >= 0; --side) {  // the end of the share, then its begin
     const long long cut = share * (blockIdx.x + side);
-    if (side == 1 && (slot > 0 || cut >= total)) {  // (the last share ends with the streams)
+    if (side == 1 && (slot > 0 || cut >= total)) {
       end = min(cut, total);
       continue;
     }
     int lo = 0;
-#pragma unroll 1
     for (int step = 256; step > 0; step >>= 1)
       if (lo + step <= kThreads && sSums[lo + step - 1] <= cut) lo += step;
     at.begin = lo > 0 ? sSums[lo - 1] : 0;
@@ -378,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       const int i = i0 + lane;
       const int cost = i < at.x.pairs ? cost_of(pair_tiles(p, at.x, i), slot) : 0;
       int sum = cost;
-#pragma unroll 1
+#pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, sum, o);
         if (lane >= o) sum += y;
