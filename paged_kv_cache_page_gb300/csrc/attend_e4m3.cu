@@ -56,7 +56,7 @@ constexpr int kWholeUnits = 64;  // streams of at most this many units are not s
 constexpr int kSegment = 64;     // units (of one head) that a CTA's further segment costs
 // Side by side go twice as many heads while a CTA's share holds this many units
 // of each.
-constexpr int kMaxSide = 2, kSideUnits = 128;
+constexpr int kMaxSide = 3, kSideUnits = 128;
 // Rows per kv head up to which a sequence runs here; longer query blocks fill
 // the 128-row tiles of the tcgen05 kernel.
 constexpr int kSmallRows = 64;
@@ -71,7 +71,7 @@ struct Layout {
   static constexpr int kOffM = kOffO + kWarps * 8 * D * 4;
   static constexpr int kOffL = kOffM + kWarps * kRows * 4;
   static constexpr int kOffFlag = kOffL + kWarps * kRows * 4;
-  static constexpr int kOffSums = kOffO;  // long long [kThreads + kWarps], before the first merge
+  static constexpr int kOffSums = kOffO;  // long long [kThreads + 3 kWarps], before the first merge
   static constexpr int kBytes = kOffFlag + 16;
   static_assert(kBytes <= 232448, "shared memory");
 };
@@ -212,88 +212,104 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   const int g = lane >> 2, t = lane & 3;
 
   // ---- the CTA's share
-  // Sums over the batch, for one kv head: units, tiles, and the longest stream.
-  const int per = (p.B + kThreads - 1) / kThreads;
-  auto block_sum = [&](long long x, int row) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    if (lane == 0) sSums[row * kWarps + warp] = x;
+  // Rolled loops: what runs once costs its instructions' way from L2, about a
+  // dozen cycles each.  First the batch's running sums for one kv head, a thread
+  // `per` sequences: units, tiles, and the longest stream.
+  const int per = (p.B + kThreads - 1) / kThreads, ctas = (int)gridDim.x;
+  int slot = 0, hw_log2 = 0, groups = p.Hkv, tiles = 0;
+  long long total = 0, incl = 0;
+  {
+    int incl_t = 0, longest = 0;
+#pragma unroll 1
+    for (int i = 0; i < per; ++i) {
+      const int b = tid * per + i;
+      if (b >= p.B) break;
+      const Seq s = load_seq(p, b, 0, blockIdx.x == 0);
+      incl += cost_of(s);
+      incl_t += s.tiles;
+      longest = max(longest, s.units);
+    }
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+      const int z = __shfl_up_sync(0xffffffffu, incl_t, o);
+      if (lane >= o) {
+        incl += y;
+        incl_t += z;
+      }
+    }
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if (lane == 31) {
+      sSums[kThreads + warp] = incl;
+      reinterpret_cast<int2*>(sM)[warp] = make_int2(incl_t, longest);
+    }
     __syncthreads();
-    long long y = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) y += sSums[row * kWarps + w];
-    return y;
-  };
-  long long mine = 0;
-  int tiles = 0, longest = 0;
-  for (int i = 0; i < per; ++i) {
-    const int b = tid * per + i;
-    if (b >= p.B) break;
-    const Seq s = load_seq(p, b, 0, blockIdx.x == 0);
-    mine += cost_of(s);
-    tiles += s.tiles;
-    longest = max(longest, s.units);
+#pragma unroll 1
+    for (int w = 0; w < kWarps; ++w) {
+      const long long x = sSums[kThreads + w];
+      const int2 y = reinterpret_cast<const int2*>(sM)[w];
+      if (w < warp) {
+        incl += x;
+        incl_t += y.x;
+      }
+      total += x;
+      tiles += y.x;
+      longest = max(longest, y.y);
+    }
+    if (longest <= kWholeUnits) {  // each stream one slot
+      slot = kWholeUnits;
+      incl = incl_t;
+      total = tiles;
+    } else {
+      // Neighbouring kv heads side by side: 2^hw_log2 of them, each with 8 >>
+      // hw_log2 of the warps, while a share stays long.
+      while (hw_log2 < kMaxSide && (p.Hkv >> hw_log2) % 2 == 0 &&
+             total * p.Hkv >= ((long long)kSideUnits << hw_log2) * ctas)
+        ++hw_log2;
+      groups = p.Hkv >> hw_log2;
+    }
   }
-  longest = __reduce_max_sync(0xffffffffu, longest);
-  if (lane == 0) sM[warp] = __int_as_float(longest);
-  const long long units = block_sum(mine, 0);
-  long long streams = block_sum(tiles, 1);
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) longest = max(longest, __float_as_int(sM[w]));
-  // Neighbouring kv heads side by side: 2^hw_log2 of them, each with 8 >> hw_log2
-  // of the warps, while a share stays long.
-  int hw_log2 = 0;
-  while (longest > kWholeUnits && hw_log2 < kMaxSide && (p.Hkv >> hw_log2) % 2 == 0 &&
-         units * p.Hkv >= ((long long)kSideUnits << hw_log2) * gridDim.x)
-    ++hw_log2;
-  const int hw = 1 << hw_log2, step_u = kWarps >> hw_log2;
-  const int my_u = warp & (step_u - 1), my_hh = warp >> (3 - hw_log2);
-  const int groups = p.Hkv >> hw_log2;
-  streams *= groups;
   // How the streams are dealt.  Short ones whole.  A few long ones in slots, one
   // a CTA: of a length that half a slot a stream less fills the CTAs with, where
   // that suffices, or one that always does.  Otherwise equal shares that cut
   // streams anywhere -- every CTA is as long, but a segment more costs it what
   // kSegment units do.
-  int slot = 0;
-  const int ctas = (int)gridDim.x;
-  if (longest <= kWholeUnits) {
-    slot = kWholeUnits;
-  } else if (streams < ctas) {
-    const float all = (float)(units * groups);
-    slot = (int)(all / (ctas - 0.5f * (int)streams)) + 2;
-    int count = 0;  // slots
-    for (int i = 0; i < per; ++i) {
-      const int b = tid * per + i;
-      if (b < p.B) count += (int)cost_of(load_seq(p, b, slot, false));
+  if (slot == 0 && tiles * (float)groups < ctas) {
+    const float all = (float)(total * groups), streams = (float)(tiles * groups);
+    const int most = (int)(all / ctas) + (kSegment >> hw_log2);
+    int other = (int)(all / (ctas - streams)) + 2;  // always suffices
+    slot = (int)(all / (ctas - 0.5f * streams)) + 2;
+    if (slot > most) slot = 0;
+#pragma unroll 1
+    for (int pass = 1; slot > 0 || pass == 2; ++pass) {
+      incl = 0;
+#pragma unroll 1
+      for (int i = 0; i < per; ++i) {
+        const int b = tid * per + i;
+        if (b < p.B) incl += cost_of(load_seq(p, b, slot, false));
+      }
+#pragma unroll 1
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      if (lane == 31) sSums[kThreads + pass * kWarps + warp] = incl;
+      __syncthreads();
+      total = 0;
+#pragma unroll 1
+      for (int w = 0; w < kWarps; ++w) {
+        const long long x = sSums[kThreads + pass * kWarps + w];
+        if (w < warp) incl += x;
+        total += x;
+      }
+      if (pass == 2 || total * groups <= ctas) break;
+      slot = other > most ? 0 : other;
     }
-    if (block_sum(count, 2) * groups > ctas) slot = (int)(all / (ctas - (int)streams)) + 2;
-    if (slot > all / ctas + (kSegment >> hw_log2)) slot = 0;
-  }
-  if (slot > 0) {
-    mine = 0;
-    for (int i = 0; i < per; ++i) {
-      const int b = tid * per + i;
-      if (b < p.B) mine += cost_of(load_seq(p, b, slot, false));
-    }
-  }
-  long long incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
-  if (lane == 31) sSums[kThreads + warp] = incl;  // (behind the rows of block_sum)
-  __syncthreads();
-  long long total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const long long x = sSums[kThreads + w];
-    if (w < warp) incl += x;
-    total += x;
   }
   sSums[tid] = incl;
   __syncthreads();
+  const int hw = 1 << hw_log2, step_u = kWarps >> hw_log2;
+  const int my_u = warp & (step_u - 1), my_hh = warp >> (3 - hw_log2);
   total *= groups;
   long long share = quotient(total + gridDim.x - 1, gridDim.x);
   if (slot == 0) share = max((share + step_u - 1) & ~(long long)(step_u - 1), (long long)kMinShare);
