@@ -32,6 +32,38 @@
 namespace pa {
 namespace {
 
+// MMAs and commits under a predicate: a branch around them would take the warp's
+// operands out of the uniform registers.
+__device__ __forceinline__ void mma_ss_if(uint32_t on, uint32_t d, uint64_t a, uint64_t b,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(on)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_if(uint32_t on, uint32_t d, uint32_t a, uint64_t b,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(on)
+      : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t on, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_u32(bar)),
+      "r"(on)
+      : "memory");
+}
+
 constexpr int kM = 128;          // rows of a query tile
 constexpr int kN = 128;          // keys of a tile
 constexpr int kUnits = kN / kPage;
@@ -503,22 +535,31 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"((uint32_t)(base >> 32)));
       return d;
     };
+    // The warp issues as one, an elected thread's predicate on, and every operand
+    // is broadcast, which lets the compiler hold it in uniform registers: branching
+    // to lane 0, a tile's 32 MMAs took 125 cycles each to issue, so they take 78
+    // (64 is the tensor core's own rate); 16 k rows of 4096 keys 255 -> 229 us.
+    auto uni = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
+    uint32_t on;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(on));
+    const uint32_t tb = uni(tbase);
     int k = 0, a = 0, n0 = 0, n1 = 0, m0 = 0, m1 = 0;
     auto scores = [&](int g, int s) {
-      if (lane == 0) {
-        const uint32_t q0 = qlo + (uint32_t)((((a & 1) * 2 + g) * L::kTile) >> 4);
-        const uint32_t k0 = klo + (uint32_t)((s * L::kTile) >> 4);
+      const uint32_t q0 = uni(qlo + (uint32_t)((((a & 1) * 2 + g) * L::kTile) >> 4));
+      const uint32_t k0 = uni(klo + (uint32_t)((s * L::kTile) >> 4));
+      const uint32_t ts = uni(tb + g * 128);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = ((kk >> 2) * L::kSlab + (kk & 3) * 32) >> 4;
-          tc::mma_f16_ss(tS(g), desc(d16, q0 + off), desc(d16, k0 + off), id_s, kk > 0);
-        }
-        tc::commit(&s_full[g]);
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = ((kk >> 2) * L::kSlab + (kk & 3) * 32) >> 4;
+        mma_ss_if(on, ts, desc(d16, q0 + off), desc(d16, k0 + off), id_s, kk > 0);
       }
+      commit_if(on, &s_full[g]);
       __syncwarp();
     };
     auto release = [&](uint64_t* bar) {
-      if (lane == 0) tc::commit(bar);
+      commit_if(on, bar);
       __syncwarp();
     };
     for (; at.left > 0; at.next(p), ++a) {
@@ -533,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         const int v = k + 1, kn = k + 2;  // places of V of this tile and K of the next
         const int sv = v % L::kRing, sk = kn % L::kRing;
         wait(&full[sv], (uint32_t)((v / L::kRing) & 1), 50);
-        if (t + 1 < end) wait(&full[sk], (uint32_t)((kn / L::kRing) & 1), 41);
+        bool next_k = false;  // K of the next tile has been waited for
 #pragma unroll 1
         for (int g = 0; g < 2; ++g) {
           const int gend = g ? end1 : end0;
@@ -542,18 +583,25 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             wait(&p_full[g], (uint32_t)(n & 1), 51 + g);
             if (t == at.t0 && m >= 1) wait(&o_free[g], (uint32_t)((m - 1) & 1), 53 + g);
             tc::fence_after_sync();
-            if (lane == 0) {
-              const uint32_t v0 = vlo + (uint32_t)((sv * L::kTile) >> 4);
+            const uint32_t v0 = uni(vlo + (uint32_t)((sv * L::kTile) >> 4));
+            const uint32_t ts = uni(tb + g * 128), to = uni(tb + 256 + g * D);
+            const uint32_t more = uni(t > at.t0);
 #pragma unroll
-              for (int kk = 0; kk < kN / 16; ++kk)
-                tc::mma_f16_ts(tO(g), tS(g) + kk * 8, desc(dslab, v0 + (kk * 2048 >> 4)), id_o,
-                               (t > at.t0 || kk > 0) ? 1u : 0u);
-              tc::commit(&pv_done[g]);
-            }
+            for (int kk = 0; kk < kN / 16; ++kk)
+              mma_ts_if(on, to, ts + kk * 8, desc(dslab, v0 + (kk * 2048 >> 4)), id_o,
+                        kk > 0 ? 1u : more);
+            commit_if(on, &pv_done[g]);
             __syncwarp();
             if (g) ++n1;
             else ++n0;
-            if (t + 1 < gend) scores(g, sk);
+            if (t + 1 < gend) {
+              if (!next_k) {
+                wait(&full[sk], (uint32_t)((kn / L::kRing) & 1), 41);
+                tc::fence_after_sync();
+                next_k = true;
+              }
+              scores(g, sk);
+            }
           }
         }
         release(&empty[sv]);
