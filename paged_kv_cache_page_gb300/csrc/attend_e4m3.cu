@@ -16,8 +16,13 @@
 // maximum only when it is passed by 2^5, so that p stays below 2^15 and the
 // accumulators are hardly ever rescaled; l sums the unrounded values in fp32.
 //
-// Bound: HBM, 2 D bytes a key and kv head; half of a 16-bit cache's.  A warp
-// takes 16 keys at a time:
+// Bound: HBM, 2 D bytes a key and kv head; half of a 16-bit cache's.  256
+// streams of 4096 keys of 32 kv heads, D = 128, run in 1.28 ms, 6.7 TB/s; 64
+// streams of 4096 keys of 8 kv heads in 102 us, 5.3 TB/s; shorter calls are
+// bound by latency (8 streams of 1024 to 8192 keys: 24.9 us, 3.0 TB/s; 1 of
+// 4096: 15 us; 2 of 100: 6.3 us): launch, lengths, table, keys, join, and the way
+// of code that runs once.  A warp takes units of 16 keys, two at a time where
+// it has two -- twice the independent work for the same waits:
 //   copy     cp.async 16 bytes a lane into the warp's own ring of stages --
 //            no producer warp, no barrier: a warp waits for its own copies
 //   S        [16 rows][16 keys] = Q K^T, MMAs m16n8k16, Q in registers.  A
@@ -30,10 +35,12 @@
 // bank once.
 //
 // Work.  The streams (sequence, kv head, 16-row tile) are laid end to end in
-// units of 16 keys and cut into equal shares, one a CTA; the cut is made on
-// the GPU from the lengths.  A CTA has at most one stream that began earlier
-// and one that goes on, so two partial results a CTA hold every split, and the
-// CTA that finishes a split stream last merges it.
+// units of 16 keys and dealt to the CTAs -- whole, in slots or in equal shares,
+// below; the cut is made on the GPU from the lengths.  A CTA has at most one
+// stream that began earlier and one that goes on, so two partial results a CTA
+// hold every split, and the CTA that finishes a split stream last merges it.
+// The 128 bytes of a key of one kv head lie Hkv D apart, too short a run for
+// DRAM: a CTA therefore takes up to eight neighbouring kv heads side by side.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -51,11 +58,23 @@ constexpr int kRows = 16;       // query rows of a tile
 constexpr int kKeys = 16;       // keys of a unit
 constexpr int kMaxB = 4096;
 constexpr float kShift = kE4m3Shift, kSlack = kE4m3Slack;
-constexpr int kMinShare = 32;   // units
-constexpr int kWholeUnits = 64;  // streams of at most this many units are not split
-constexpr int kSegment = 64;     // units (of one head) that a CTA's further segment costs
-// Side by side go twice as many heads while a CTA's share holds this many units
-// of each.
+// The limits of the dealing, with both sides on 8 kv heads of D = 128 unless said
+// otherwise (us).
+// Least share, units: 64 streams of 2000 keys 59 with 32, 68 with 128; 8 is no
+// faster, and a share of one unit a warp is no work.
+constexpr int kMinShare = 32;
+// Streams of at most this many units are not split: 8 of 1000 keys 12.6 with 64,
+// 14.1 with 32; 64 of 1000 keys 39.5 and 42.2; 64 of 2000 keys 59.4 with 64, 61.5
+// with 128.
+constexpr int kWholeUnits = 64;
+// Units (of one head) that a CTA's further segment costs, up to which slots beat
+// equal shares: 8 streams of 1024 to 8192 keys 24.9 with 64, 30.4 with 0; 16 of 4096
+// keys of 32 kv heads 97 with 64, 104 with 256.
+constexpr int kSegment = 64;
+// Side by side go twice as many heads, up to 2^kMaxSide, while a CTA's share holds
+// kSideUnits units of each.  256 streams of 4096 keys of 32 kv heads: 1446 with one
+// head, 1319 two, 1307 four, 1286 eight.  8 streams of 1024 to 8192 keys 24.9 with
+// 128, 31.8 with 32; 64 of 2000 keys 59.4 with 128, 66.7 with 512.
 constexpr int kMaxSide = 3, kSideUnits = 128;
 // Rows per kv head up to which a sequence runs here; longer query blocks fill
 // the 128-row tiles of the tcgen05 kernel.  Both sides of the limit, on 4096

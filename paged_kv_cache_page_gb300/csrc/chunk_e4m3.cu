@@ -8,7 +8,13 @@
 // share every K and V tile and its conversion.
 //
 // Bound: the tensor cores and the exponentials, 4 D operations and one
-// exponential a visible (row, key) pair.  Warps:
+// exponential a visible (row, key) pair.  Two chunks of 2048 rows a head on 4096
+// keys (32 heads on 8, D = 128) run in 229 us, 900 TFLOP/s, 0.47 of the measured
+// library product.  Of the 4000 cycles of a tile (256 rows, 128 keys) the MMAs
+// are 2050; what fills the rest is the chain of one group -- scores, softmax (2900
+// cycles beside the other group's and the converters), both products -- and the
+// converters' loads.  A segment's end, where the softmax warps write results,
+// costs 9000 to 14000 cycles, a fifth of the time.  Warps:
 //   0-7    softmax: one thread a row, group g = warp / 4 takes tile g
 //   8-11   converters: K and V tiles in turn -- 16 bytes a load from the pages,
 //          two fp16 chunks a store into the 128-byte-swizzled operand tile --
@@ -69,6 +75,9 @@ constexpr int kN = 128;          // keys of a tile
 constexpr int kUnits = kN / kPage;
 constexpr int kWarpConv = 8, kWarpMma = 12;
 constexpr int kThreads = 15 * 32;
+// The limits of the dealing, with both sides (us): 24 whole prompts of 300 tokens
+// 145 with a least share of 4 tiles, 200 with 16 (and 145 with 1); 8 whole prompts
+// of 1000 tokens 226 with cuts moved over up to 4 tiles, 243 over none, 249 over 12.
 constexpr int kMinShare = 4;     // tiles
 constexpr int kSnap = 4;         // tiles that a cut moves to an end of its stream
 
@@ -82,7 +91,8 @@ struct Layout {
   static constexpr int kOffKV = 4 * kTile;
   static constexpr int kOffF = kOffKV + kRing * kTile;      // float [256] factor of a row's scores
   static constexpr int kOffNan = kOffF + kChunkRows * 4;    // int [kRing][4]
-  static constexpr int kOffBar = kOffNan + kRing * 16;
+  static constexpr int kOffWalk = kOffNan + kRing * 16;     // Walk [4], the converters'
+  static constexpr int kOffBar = kOffWalk + 4 * 72;
   // q_full, q_empty [2], f_empty; full, empty [kRing]; s_full, p_full, pv_done, o_free [2]
   static constexpr int kBars = 5 + 2 * kRing + 8;
   static constexpr int kOffMisc = kOffBar + kBars * 8;      // TMEM base, merge flag
@@ -169,6 +179,8 @@ struct Walk {
 
 // Scales the first `cols` columns of fp16 probabilities in TMEM by a power of
 // two a lane (0 where it is below fp16's range).
+static_assert(sizeof(Walk) <= 72 && sizeof(Walk) % 8 == 0, "kOffWalk");
+
 __device__ __noinline__ void scale_p(uint32_t t, int cols, float by) {
   const __half2 h = __float2half2_rn(by);
   tc::tmem_wait_st();
@@ -284,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 8);
-      mbar_init(&q_empty[i], 1);
+      mbar_init(&q_empty[i], 9);  // the MMAs' reads, and the results staged there
     }
     mbar_init(f_empty, 8);
     for (int i = 0; i < L::kRing; ++i) {
@@ -482,33 +494,53 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     asm volatile("cp.async.wait_all;" ::: "memory");
     constexpr bool kTurn = !std::is_same<T, __half>::value;
     if (kTurn || flip != 0) {
-#pragma unroll 2
-      for (int r = i / kLanes; r < kChunkRows; r += step) {
-        const uint4 x = *reinterpret_cast<const uint4*>(place(r));
-        uint32_t u[4] = {x.x, x.y, x.z, x.w};
-        float f = 1.f;
-        if constexpr (kTurn) {
-          uint32_t top = 0;
+      constexpr int kAtOnce = 4;  // rows: their loads and reductions side by side
+#pragma unroll 1
+      for (int r = i / kLanes; r < kChunkRows; r += kAtOnce * step) {
+        uint4 x[kAtOnce];
+        float f[kAtOnce];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            top = max(top, max((u[e] & 0x7fffu) << 16, u[e] & 0x7fff0000u));
+        for (int j = 0; j < kAtOnce; ++j) {
+          x[j] = *reinterpret_cast<const uint4*>(place(r + j * step));
+          f[j] = 1.f;
+        }
+        if constexpr (kTurn) {
+          uint32_t top[kAtOnce];
+#pragma unroll
+          for (int j = 0; j < kAtOnce; ++j) {
+            const uint32_t u[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+            top[j] = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              top[j] = max(top[j], max((u[e] & 0x7fffu) << 16, u[e] & 0x7fff0000u));
+          }
 #pragma unroll
           for (int o = 1; o < kLanes; o <<= 1)
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-          const int ex = (int)(top >> 23);
-          const bool turn = ex > 0 && ex < 255;
-          const int by = min(ex, 253);
-          const float down = turn ? __uint_as_float((uint32_t)(254 - by) << 23) : 1.f;
-          if (turn) f = __uint_as_float((uint32_t)by << 23);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 y = E::to_f2(u[e]);
-            u[e] = Elem<__half>::from_f2(y.x * down, y.y * down);
+            for (int j = 0; j < kAtOnce; ++j)
+              top[j] = max(top[j], __shfl_xor_sync(0xffffffffu, top[j], o));
+#pragma unroll
+          for (int j = 0; j < kAtOnce; ++j) {
+            const int ex = (int)(top[j] >> 23);
+            const bool turn = ex > 0 && ex < 255;
+            const int by = min(ex, 253);
+            const float down = turn ? __uint_as_float((uint32_t)(254 - by) << 23) : 1.f;
+            if (turn) f[j] = __uint_as_float((uint32_t)by << 23);
+            uint32_t u[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 y = E::to_f2(u[e]);
+              u[e] = Elem<__half>::from_f2(y.x * down, y.y * down);
+            }
+            x[j] = make_uint4(u[0], u[1], u[2], u[3]);
           }
         }
-        *reinterpret_cast<uint4*>(place(r)) =
-            make_uint4(u[0] ^ flip, u[1] ^ flip, u[2] ^ flip, u[3] ^ flip);
-        if (qc == 0) sF[r] = f;
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+          *reinterpret_cast<uint4*>(place(r + j * step)) =
+              make_uint4(x[j].x ^ flip, x[j].y ^ flip, x[j].z ^ flip, x[j].w ^ flip);
+          if (qc == 0) sF[r + j * step] = f[j];
+        }
       }
     } else if (qc == 0) {
       for (int r = i / kLanes; r < kChunkRows; r += step) sF[r] = 1.f;
@@ -635,7 +667,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     const int c = D == 128 ? (ct & 3) | ((ct >> 1) & 4) : ct & 3;
     const int r0 = D == 128 ? ((ct >> 2) & 1) | ((ct >> 4) << 1) : ct >> 2;
     int k = 0;
-    for (; at.left > 0; at.next(p)) {
+    // The position waits in shared memory: with it in registers the compiler
+    // spills bytes that are on their way, which waits for them.
+    Walk* parked = reinterpret_cast<Walk*>(smem + L::kOffWalk) + (warp - kWarpConv);
+    while (at.left > 0) {
+      const int t0 = at.t0, t1 = at.t0 + at.n;
+      const int least = seen(p, at.x, at.rows0());  // keys that the pair's first row sees
+      if (lane == 0) *parked = at;
+      __syncwarp();
       const int32_t* trow = p.block_table + (int64_t)at.b * p.bt_stride;
       const int lk = at.x.s.lk;
       // Lane l finds unit `unit` + l of 32 units (four tiles): the table entry,
@@ -649,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       auto place = [&](int entry, int unit) {
         unit += lane;
         if (entry < 0 || entry >= p.num_pages) {
-          if (ct < 32) report(p.err, PA_DEVERR_PAGE_OOB, at.b, unit);
+          if (ct < 32) report(p.err, PA_DEVERR_PAGE_OOB, parked->b, unit);
           entry = 0;
         }
         const int row = (unit & ((1 << p.page_shift) - 1)) * kPage;
@@ -664,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       auto load = [&](const uint8_t* base, int64_t off, int t, uint4 (&x)[kLoads]) {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-          const int unit = ((t - at.t0) & 3) * kUnits + (i * kRowsAt + r0) / kPage;
+          const int unit = ((t - t0) & 3) * kUnits + (i * kRowsAt + r0) / kPage;
           x[i] = load16(base + __shfl_sync(0xffffffffu, (long long)off, unit));
         }
       };
@@ -675,12 +714,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         for (int i = 0; i < kLoads; ++i)
           if (t * kN + i * kRowsAt + r0 >= lk) x[i] = make_uint4(0, 0, 0, 0);
       };
-      place(table(at.t0 * kUnits), at.t0 * kUnits);
-      int nxt = at.n > 4 ? table((at.t0 + 4) * kUnits) : 0;
+      place(table(t0 * kUnits), t0 * kUnits);
+      int nxt = t1 - t0 > 4 ? table((t0 + 4) * kUnits) : 0;
       uint4 xk[kLoads], xv[kLoads];
-      load(kbase, koff, at.t0, xk);
-      // the first row of the pair sees the least
-      const int least = seen(p, at.x, at.rows0());
+      load(kbase, koff, t0, xk);
       auto store = [&](uint8_t* tile, const uint4 (&x)[kLoads]) {
         uint8_t* slab = tile + (c >> 2) * L::kSlab;
         const int c0 = 2 * (c & 3);
@@ -702,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[s]);
       };
-      for (int t = at.t0; t < at.t0 + at.n; ++t) {
+      for (int t = t0; t < t1; ++t) {
         // V of this tile and K of the next are on their way while K of this one
         // is converted
         load(vbase, voff, t, xv);
@@ -712,10 +749,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         store(sKV + s * L::kTile, xk);
         done(s);
         ++k;
-        if (t + 1 < at.t0 + at.n) {
-          if (((t + 1 - at.t0) & 3) == 0) {
+        if (t + 1 < t1) {
+          if (((t + 1 - t0) & 3) == 0) {
             place(nxt, (t + 1) * kUnits);
-            if (t + 5 < at.t0 + at.n) nxt = table((t + 5) * kUnits);
+            if (t + 5 < t1) nxt = table((t + 5) * kUnits);
           }
           load(kbase, koff, t + 1, xk);
         }
@@ -744,6 +781,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         done(s);
         ++k;
       }
+      __syncwarp();
+      at = *parked;
+      __syncwarp();
+      at.next(p);
     }
     // nothing in flight may outlive the CTA: the last reads of the ring
     for (int i = 0; i < L::kRing; ++i, ++k)
@@ -794,16 +835,35 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = i < left ? v[i] : neg_inf();
           }
-          float top4[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
+          // The exponentials do not wait for the largest score: the chunk is done
+          // again where it passes the reference by more than the slack.
+          uint32_t pk[16];
+          uint64_t more[4];
+#pragma unroll 1
+          for (;;) {
+            const float neg_m = m == neg_inf() ? 0.f : -m;
+            const uint64_t f2 = pair(f, f), m2 = pair(neg_m, neg_m);
+            float top4[4];
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) top4[(i >> 1) & 3] = max3(top4[(i >> 1) & 3], v[i], v[i + 1]);
-          const float top = max3(fmaxf(top4[0], top4[1]), top4[2], top4[3]) * f;
-          if (__any_sync(0xffffffffu, top > m + (kE4m3Shift + kE4m3Slack))) {
+            for (int e = 0; e < 16; ++e) {
+              const float2 z = halves(fma2(pair(v[2 * e], v[2 * e + 1]), f2, m2));
+              float e0 = ex2(z.x), e1 = ex2(z.y);
+              if constexpr (masked) {  // (a factor of zero turns -inf into NaN)
+                e0 = 2 * e < left ? e0 : 0.f;
+                e1 = 2 * e + 1 < left ? e1 : 0.f;
+              }
+              more[e & 3] = e < 4 ? pair(e0, e1) : add2(more[e & 3], pair(e0, e1));
+              top4[e & 3] = e < 4 ? fmaxf(v[2 * e], v[2 * e + 1]) : max3(top4[e & 3], v[2 * e], v[2 * e + 1]);
+              pk[e] = Elem<__half>::from_f2(e0, e1);
+            }
+            const float top = max3(fmaxf(top4[0], top4[1]), top4[2], top4[3]) * f;
+            const bool far = top > m + (kE4m3Shift + kE4m3Slack);
+            if (!__any_sync(0xffffffffu, far)) break;
             // References are whole numbers, so what is scaled here is scaled
             // by powers of two: this tile's sums and probabilities so far, and
             // after the loop O.
             float by = 1.f;
-            if (top > m + (kE4m3Shift + kE4m3Slack)) {
+            if (far) {
               const float to = ceilf(top) - kE4m3Shift;
               if (m != neg_inf()) by = ex2(m - to);
               m = to;
@@ -817,20 +877,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             }
             scale_p(ts, key0 / 2, by);
           }
-          const float neg_m = m == neg_inf() ? 0.f : -m;
-          const uint64_t f2 = pair(f, f), m2 = pair(neg_m, neg_m);
-          uint32_t pk[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float2 z = halves(fma2(pair(v[2 * e], v[2 * e + 1]), f2, m2));
-            float e0 = ex2(z.x), e1 = ex2(z.y);
-            if constexpr (masked) {  // (a factor of zero turns -inf into NaN)
-              e0 = 2 * e < left ? e0 : 0.f;
-              e1 = 2 * e + 1 < left ? e1 : 0.f;
-            }
-            sum2[e & 3] = add2(sum2[e & 3], pair(e0, e1));
-            pk[e] = Elem<__half>::from_f2(e0, e1);
-          }
+          for (int i = 0; i < 4; ++i) sum2[i] = add2(sum2[i], more[i]);
           // over the columns of scores that have been used
           tc::tmem_st16u(ts + key0 / 2, pk);
         };
@@ -882,8 +930,25 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       const bool whole = at.n == at.all;
       const int slot = 2 * blockIdx.x + (at.t0 == 0 ? 1 : 0);
       const int64_t my_part = ((int64_t)slot * 2 + g) * kM;
-      auto out_row = [&]() {
-        return reinterpret_cast<T*>(p.out) + ((int64_t)(at.x.s.q0 + qi) * p.Hq + h) * D;
+      // Results leave by way of the segment's Q tile, which is not read any more:
+      // a thread holds a row, and 32 rows a store instruction cost 32 cycles of
+      // the memory pipe, two whole rows four.
+      uint8_t* staged = sQ + ((a & 1) * 2 + g) * L::kTile;
+      auto stage = [&](int c, uint4 x) {
+        *reinterpret_cast<uint4*>(staged + r * (2 * D) + ((c ^ (r & 7)) << 4)) = x;
+      };
+      auto write_rows = [&]() {
+        constexpr int kLanes = D / 8;
+        const long long my_row = valid ? (long long)(at.x.s.q0 + qi) * p.Hq + h : -1;
+        const int c = lane % kLanes;
+        __syncwarp();
+#pragma unroll 4
+        for (int i = lane / kLanes; i < 32; i += 32 / kLanes) {
+          const long long to = __shfl_sync(0xffffffffu, my_row, i);
+          const int rt = quarter * 32 + i;
+          const uint4 x = *reinterpret_cast<const uint4*>(staged + rt * (2 * D) + ((c ^ (rt & 7)) << 4));
+          if (to >= 0) *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.out) + to * D + c * 8) = x;
+        }
       };
       auto put_lse = [&](float ref, float sum) {
         if (p.lse != nullptr)
@@ -906,14 +971,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
               if ((nans[i] >> e) & 1) o[e] = nan;
           }
           if (whole) {
-            if (valid) {
 #pragma unroll
-              for (int e = 0; e < 32; e += 8)
-                *reinterpret_cast<uint4*>(out_row() + i * 32 + e) = make_uint4(
-                    E::from_f2(o[e] * by, o[e + 1] * by), E::from_f2(o[e + 2] * by, o[e + 3] * by),
-                    E::from_f2(o[e + 4] * by, o[e + 5] * by),
-                    E::from_f2(o[e + 6] * by, o[e + 7] * by));
-            }
+            for (int e = 0; e < 32; e += 8)
+              stage(i * 4 + e / 8,
+                    make_uint4(E::from_f2(o[e] * by, o[e + 1] * by),
+                               E::from_f2(o[e + 2] * by, o[e + 3] * by),
+                               E::from_f2(o[e + 4] * by, o[e + 5] * by),
+                               E::from_f2(o[e + 6] * by, o[e + 7] * by)));
           } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
@@ -924,12 +988,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&o_free[g]);
-      } else if (whole && valid) {
-#pragma unroll
-        for (int i = 0; i < D; i += 8)
-          *reinterpret_cast<uint4*>(out_row() + i) = make_uint4(0, 0, 0, 0);
+      } else if (whole) {
+#pragma unroll 1
+        for (int c = 0; c < D / 8; ++c) stage(c, make_uint4(0, 0, 0, 0));
       }
       if (whole) {
+        write_rows();
         if (valid) put_lse(m, l);
       } else {
         p.part_ml[my_part + r] = make_float2(m, l);
@@ -965,7 +1029,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             sum = fmaf(weight(ml), ml.y, sum);
           }
           const float by = sum == 0.f ? 0.f : vs / sum;
-          constexpr int kPart = D / 16, kSplits = 2;  // 16-byte chunks of a quarter of the row
+          constexpr int kPart = D / 16, kSplits = 1;  // 16-byte chunks of a quarter of the row
 #pragma unroll 1
           for (int part = 0; part < 4; ++part) {
             float4 acc[kPart];
@@ -997,18 +1061,20 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 }
               }
             }
-            if (valid) {
 #pragma unroll
-              for (int e = 0; e < kPart; e += 2)
-                *reinterpret_cast<uint4*>(out_row() + part * (D / 4) + e * 4) = make_uint4(
-                    E::from_f2(acc[e].x * by, acc[e].y * by), E::from_f2(acc[e].z * by, acc[e].w * by),
-                    E::from_f2(acc[e + 1].x * by, acc[e + 1].y * by),
-                    E::from_f2(acc[e + 1].z * by, acc[e + 1].w * by));
-            }
+            for (int e = 0; e < kPart; e += 2)
+              stage(part * (D / 32) + e / 2,
+                    make_uint4(E::from_f2(acc[e].x * by, acc[e].y * by),
+                               E::from_f2(acc[e].z * by, acc[e].w * by),
+                               E::from_f2(acc[e + 1].x * by, acc[e + 1].y * by),
+                               E::from_f2(acc[e + 1].z * by, acc[e + 1].w * by)));
           }
+          write_rows();
           if (valid) put_lse(ref, sum);
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_empty[a & 1]);
       k += 2 * at.n;
       at.next(p);
     }

@@ -3,10 +3,9 @@
 Tolerances, in 64 bits from each row's own values.  Let A = sum_t p_t |v_t| / l, the result for
 |V|, and S = max_t scale |q| . |k_t|, the largest possible score.
   scores          fp32 sums of D exact products in D / 16 MMAs, each of which may cut 2^-22 of the
-                  magnitudes it adds (17 sums for D = 128), and one fused operation: 2^-17 S; a bf16
-                  row of q also loses what lies 2^-25 below its largest value: covered by 2^-17 S,
-                  as max|q| sum|k| <= 2^7 sum|q||k| needs more, it is counted with Q = scale
-                  max|q| max_t sum|k_t|: 2^-24 Q
+                  magnitudes it adds (17 sums for D = 128), and one fused operation: 2^-17 S; each
+                  value of a bf16 row of q also loses what lies 2^-25 below the row's largest:
+                  2^-24 Q, with Q = scale max|q| max_t sum|k_t|
   probabilities   e^score (2^-21), rounded to fp16: 2^-11; relative
   products        fp32 sums over the keys in MMAs of 16: n / 16 cuts of 2^-22 A; merges 2^-20 A
   result          one rounding to the type: half a step of |O| (fp16: 2^-25 below its range)
