@@ -442,6 +442,7 @@ PA_API int pa_rotary_append_varlen(
  *                     head is multiplied by; NULL: 1.
  *   workspace         pa_fwd_varlen_e4m3_workspace_size bytes, 256-byte
  *                     aligned, always; its contents on entry do not matter.
+ *                     A size for some B and max_seqlen_q holds for smaller ones.
  *                     Calls that may overlap on the GPU need one each.
  * q and out are fp16 or bf16; both products are computed in fp16 with fp32
  * accumulation (e4m3 is exact in fp16; a bf16 row of q is scaled by a power of

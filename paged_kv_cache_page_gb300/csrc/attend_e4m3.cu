@@ -77,10 +77,16 @@ constexpr int kSegment = 64;
 // 128, 31.8 with 32; 64 of 2000 keys 59.4 with 128, 66.7 with 512.
 constexpr int kMaxSide = 3, kSideUnits = 128;
 // Rows per kv head up to which a sequence runs here; longer query blocks fill
-// the 128-row tiles of the tcgen05 kernel.  Both sides of the limit, on 4096
-// keys of 8 kv heads, D = 128, in us here / there: 64 rows, 4 sequences 37.3 /
-// 48.8, 64 sequences 363 / 383; 80 rows 50.9 / 49.4 and 447 / 386.
-constexpr int kSmallRows = 64;
+// the 128-row tiles of the tcgen05 kernel, which takes as long for few rows as
+// for 128 but is the slower to start and to join.  In us, here / there, on 4096
+// keys of 8 kv heads (32 query heads), D = 128:
+//   sequences   48 rows     64 rows     80 rows
+//    4           30 / 49     37 / 48     51 / 48
+//   16           97 / 103   115 / 102     - / 103
+//   64          285 / 320   363 / 317   447 / 320
+// and 64 sequences of 512 keys 88 / 77 with 48 rows, 109 / 75 with 64.
+constexpr int kSmallRows = 64, kSmallRowsMany = 48;
+constexpr int kManyStreams = 64;  // sequences x kv heads from which the second holds
 
 template <int D>
 struct Layout {
@@ -907,10 +913,14 @@ cudaError_t launch(const AttendParams& p, bool dependent, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, attend_kernel<D, T>, p);
 }
 
+int small_rows(int B, int Hkv) {
+  return (long long)B * Hkv >= kManyStreams ? kSmallRowsMany : kSmallRows;
+}
+
 // Whether a sequence of the call may have more rows per kv head than the
 // warp-level kernel takes.
-bool has_chunks(int max_seqlen_q, int Hq, int Hkv) {
-  return (long long)max_seqlen_q * (Hq / Hkv) > kSmallRows;
+bool has_chunks(int B, int max_seqlen_q, int Hq, int Hkv) {
+  return (long long)max_seqlen_q * (Hq / Hkv) > small_rows(B, Hkv);
 }
 
 bool aligned16(const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15u) == 0; }
@@ -936,7 +946,7 @@ PA_API size_t pa_fwd_varlen_e4m3_workspace_size(int B, int total_q, int max_seql
                                                 int Hkv, int D, int max_seqlen_k) {
   (void)max_seqlen_k;
   if (B <= 0 || total_q <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0) return 0;
-  return workspace_of(D, has_chunks(max_seqlen_q, Hq, Hkv)).total;
+  return workspace_of(D, has_chunks(B, max_seqlen_q, Hq, Hkv)).total;
 }
 
 PA_API int pa_fwd_varlen_e4m3(const void* q, int64_t q_st, int64_t q_sh, pa_tensor4 k_cache,
@@ -981,7 +991,7 @@ PA_API int pa_fwd_varlen_e4m3(const void* q, int64_t q_st, int64_t q_sh, pa_tens
     return set_error(PA_ERR_UNSUPPORTED, "page_size must be 16, 32, 64, 128 or 256");
   if ((long long)max_pages * page_size > 0x7fffffff)
     return set_error(PA_ERR_UNSUPPORTED, "a block table row must hold fewer than 2^31 tokens");
-  const bool chunks = has_chunks(max_seqlen_q, Hq, Hkv);
+  const bool chunks = has_chunks(B, max_seqlen_q, Hq, Hkv);
   const Workspace ws = workspace_of(D, chunks);
   if (workspace == nullptr || workspace_bytes < ws.total)
     return set_error(PA_ERR_WORKSPACE, "workspace of %zu bytes required (got %zu)", ws.total,
@@ -1013,7 +1023,7 @@ PA_API int pa_fwd_varlen_e4m3(const void* q, int64_t q_st, int64_t q_sh, pa_tens
   p.lse = lse;
   p.err = err_word;
   // sequences of more rows than max_seqlen_q said run on the warp-level kernel
-  p.small_rows = chunks ? kSmallRows : 0x7fffffff;
+  p.small_rows = chunks ? small_rows(B, Hkv) : 0x7fffffff;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (chunks) {

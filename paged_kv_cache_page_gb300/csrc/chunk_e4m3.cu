@@ -9,12 +9,14 @@
 //
 // Bound: the tensor cores and the exponentials, 4 D operations and one
 // exponential a visible (row, key) pair.  Two chunks of 2048 rows a head on 4096
-// keys (32 heads on 8, D = 128) run in 229 us, 900 TFLOP/s, 0.47 of the measured
-// library product.  Of the 4000 cycles of a tile (256 rows, 128 keys) the MMAs
-// are 2050; what fills the rest is the chain of one group -- scores, softmax (2900
-// cycles beside the other group's and the converters), both products -- and the
-// converters' loads.  A segment's end, where the softmax warps write results,
-// costs 9000 to 14000 cycles, a fifth of the time.  Warps:
+// keys (32 heads on 8, D = 128) run in 209 us, 985 TFLOP/s, 0.51 of the measured
+// library product.  Of the 3500 cycles of a tile (256 rows, 128 keys) the MMAs
+// are 2050; what fills the rest is the chain of one group -- scores, softmax (2500
+// cycles beside the other group's and the converters), both products.  A
+// segment's end, where the softmax warps write results, costs 7000 to 12000
+// cycles, an eighth of the time.  Registers are what most steps ran into: a
+// role that spills bytes on their way waits for them (converters, 17 rows a
+// sequence: 420 against 320 us).  Warps:
 //   0-7    softmax: one thread a row, group g = warp / 4 takes tile g
 //   8-11   converters: K and V tiles in turn -- 16 bytes a load from the pages,
 //          two fp16 chunks a store into the 128-byte-swizzled operand tile --
@@ -459,9 +461,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   // whole warps, 16 (D = 64: 8) lanes a row: copied to its place by cp.async,
   // then turned in place where it is not yet as the MMAs read it -- a bf16 row
   // is scaled by a power of two to a largest magnitude in [1, 2); a negative
-  // scale of K turns the signs, so that no score factor is negative.  Rolled
-  // loops: code that runs once a segment comes from far away, and unrolled this
-  // took 28000 cycles, nearly all of them waiting for instructions.
+  // scale of K turns the signs, so that no score factor is negative.  Four rows
+  // a step: one at a time, two warps needed 33000 cycles for a segment's rows,
+  // more than the tiles of a short prompt (24 of 300 tokens 144 us, 104 with
+  // four); unrolled whole, code that runs once comes from far away, and the
+  // first segment's rows took 28000 cycles, waiting for instructions.
   auto stage_q = [&](const Walk& w, int buf, int i, int threads) {
     constexpr int kLanes = D / 8;
     const int qc = i % kLanes, step = threads / kLanes;
@@ -477,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     // row = token * G + head: divided once, then carried on
     int token = (w.rows0() + i / kLanes) / p.G, head = (w.rows0() + i / kLanes) % p.G;
     const int step_t = step / p.G, step_h = step % p.G;
-#pragma unroll 1
+#pragma unroll 4
     for (int r = i / kLanes; r < kChunkRows; r += step) {
       const bool live = w.rows0() + r < w.x.rows;
       const T* src = live ? base + (int64_t)token * p.q_st + (int64_t)head * p.q_sh : base;
@@ -570,7 +574,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     // The warp issues as one, an elected thread's predicate on, and every operand
     // is broadcast, which lets the compiler hold it in uniform registers: branching
     // to lane 0, a tile's 32 MMAs took 125 cycles each to issue, so they take 78
-    // (64 is the tensor core's own rate); 16 k rows of 4096 keys 255 -> 229 us.
+    // (64 is the tensor core's own rate): two chunks of 2048 on 4096 keys 255 -> 229
+    // us.
     auto uni = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
     uint32_t on;
     asm volatile(

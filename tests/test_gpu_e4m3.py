@@ -58,6 +58,15 @@ def test_chunks_of_many_heads(heads):
     assert torch.equal(out, again) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("b,q_len", [(2, 16), (2, 17), (63, 16), (64, 12), (64, 13), (64, 16), (65, 1)])
+def test_around_the_limits_between_the_kernels(b, q_len):
+    """48 and 64 rows per kv head, with few and with many streams; single tokens beside them."""
+    q_lens = [q_len if i % 3 else 1 for i in range(b)]
+    w = batch(q_lens, [(37 * i) % 190 + 18 for i in range(b)], 4, 1, 64, "bf16", seed=b + q_len)
+    out, lse = call(w)
+    check(w, out, lse)
+
+
 @pytest.mark.parametrize("heads,dtype", [((4, 1, 128), "f16"), ((8, 2, 64), "bf16"), ((1, 1, 128), "bf16")])
 @pytest.mark.parametrize("causal", [True, False])
 def test_a_chunk_over_a_long_prefix_is_split_and_joined(heads, dtype, causal):
