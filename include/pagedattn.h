@@ -352,7 +352,8 @@ PA_API int pa_split_combine(const float* o_partial, const float* lse_partial,
  *   positions     int32 [token_capacity] out: the token's position in its
  *                 sequence; 0 behind the last row.
  *   free_count_out  int32 [1] out: free pages left; may be free_count.
- * At most 4096 requests (PA_ERR_UNSUPPORTED).  A *free_count outside
+ * At most 4096 requests, 2^31 - 4096 tokens a table row, and 2^31 - 2^16 pages
+ * and rows; more are refused.  A *free_count outside
  * [0, num_pages] is reported (PA_DEVERR_CAPACITY, index -1) and clamped.
  * err_word[1] is the request, [2] the offending value.  Pages belong to one
  * request each; two calls on the same pool must be ordered by the caller.
@@ -449,7 +450,8 @@ PA_API int pa_rotary_append_varlen(
  * two first), so the result is that of the dequantised cache up to the rounding
  * of the probabilities to fp16.  Keys that a row does not see have no effect on
  * it, whatever they hold.  Rows behind cu_seqlens_q[B] are not written.  At most
- * 4096 entries; more return PA_ERR_UNSUPPORTED.
+ * 4096 entries and 2^31 - 4096 tokens a table row, and at most 2^31 - 1 tiles of
+ * 256 rows per kv head by 128 keys; more return PA_ERR_UNSUPPORTED.
  */
 PA_API int pa_fwd_varlen_e4m3(const void* q, int64_t q_st, int64_t q_sh, pa_tensor4 k_cache,
                               pa_tensor4 v_cache, const float* k_scale, const float* v_scale,

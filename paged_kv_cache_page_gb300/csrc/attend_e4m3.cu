@@ -362,9 +362,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     }
     const long long head = cost_of(at.s);
     at.h = (int)quotient(off, head);
-    const int rest = (int)(off - at.h * head);
-    at.tile = rest / at.s.cost;
-    at.u = rest % at.s.cost;  // units, or slots, of the stream in front
+    const long long rest = off - at.h * head;
+    at.tile = (int)quotient(rest, at.s.cost);
+    at.u = (int)(rest - (long long)at.tile * at.s.cost);  // units, or slots, of the stream in front
     stream0 = first - at.u;
     if (slot > 0) at.u *= at.s.chunk;
     at.left = min(share, total - first);
@@ -989,9 +989,12 @@ PA_API int pa_fwd_varlen_e4m3(const void* q, int64_t q_st, int64_t q_sh, pa_tens
     if (page_size == kPage << s) p.page_shift = s;
   if (p.page_shift < 0)
     return set_error(PA_ERR_UNSUPPORTED, "page_size must be 16, 32, 64, 128 or 256");
-  if ((long long)max_pages * page_size > 0x7fffffff)
-    return set_error(PA_ERR_UNSUPPORTED, "a block table row must hold fewer than 2^31 tokens");
+  if ((long long)max_pages * page_size > kMaxRowTokens)
+    return set_error(PA_ERR_UNSUPPORTED, "a block table row must hold at most 2^31 - 4096 tokens");
   const bool chunks = has_chunks(B, max_seqlen_q, Hq, Hkv);
+  if (chunks && ((long long)total_q * (Hq / Hkv) / kChunkRows + B) * (max_seqlen_k / 128 + 1) >
+                    0x7fffffff)
+    return set_error(PA_ERR_UNSUPPORTED, "total_q * Hq / Hkv * max_seqlen_k is too large");
   const Workspace ws = workspace_of(D, chunks);
   if (workspace == nullptr || workspace_bytes < ws.total)
     return set_error(PA_ERR_WORKSPACE, "workspace of %zu bytes required (got %zu)", ws.total,

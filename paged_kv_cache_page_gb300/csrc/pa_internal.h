@@ -13,6 +13,9 @@
 namespace pa {
 
 constexpr int kPage = 16;  // tokens per page
+// Tokens that a block table row may stand for in the serving-step calls: places
+// up to a few tiles behind the last one still fit in 32 bits.
+constexpr int kMaxRowTokens = 0x7fffffff - 4095;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 

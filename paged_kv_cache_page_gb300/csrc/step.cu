@@ -44,6 +44,7 @@ constexpr int kThreads = 1024;
 constexpr int kMaxB = 4096;
 constexpr int kPer = kMaxB / kThreads;  // consecutive entries of the batch a thread scans
 constexpr int kAtOnce = 4;
+constexpr int kMaxItems = 0x7fffffff - 0xffff;  // pages, rows: dealt to warps in 32-bit places
 constexpr int kCluster = 16;             // CTAs of the cluster at most (8 where 16 do not fit)
 
 struct PlanParams {
@@ -433,13 +434,14 @@ int check_step(int B, int max_pages, int64_t bt_stride, int page_size, int64_t n
   if (max_pages < 1 || bt_stride < max_pages)
     return set_error(PA_ERR_INVALID_ARG,
                      "block table needs max_pages >= 1 and bt_stride >= max_pages");
-  if (num_pages < 1 || num_pages > 0x7fffffff)
-    return set_error(PA_ERR_INVALID_ARG, "num_pages must be in [1, 2^31)");
+  if (num_pages < 1 || num_pages > kMaxItems)
+    return set_error(PA_ERR_INVALID_ARG, "num_pages must be in [1, 2^31 - 2^16]");
   for (int s = 4; s <= 8; ++s)
     if (page_size == 1 << s) {
       *page_log2 = s;
-      if (((long long)max_pages << s) > 0x7fffffff)
-        return set_error(PA_ERR_UNSUPPORTED, "a block table row must hold fewer than 2^31 tokens");
+      if (((long long)max_pages << s) > kMaxRowTokens)
+        return set_error(PA_ERR_UNSUPPORTED,
+                         "a block table row must hold at most 2^31 - 4096 tokens");
       return PA_OK;
     }
   return set_error(PA_ERR_UNSUPPORTED, "page_size must be 16, 32, 64, 128 or 256");
@@ -462,6 +464,8 @@ PA_API int pa_plan_step(const int32_t* cache_seqlens, const int32_t* q_lens, int
   const int rc = check_step(B, max_pages, bt_stride, page_size, num_pages, &p.page_log2);
   if (rc) return rc;
   if (token_capacity < 0) return set_error(PA_ERR_INVALID_ARG, "negative token_capacity");
+  if (token_capacity > kMaxItems)
+    return set_error(PA_ERR_UNSUPPORTED, "token_capacity must be at most 2^31 - 2^16");
   if (cu_seqlens_q == nullptr || free_count == nullptr || free_count_out == nullptr ||
       free_pages == nullptr)
     return set_error(PA_ERR_INVALID_ARG,

@@ -48,8 +48,18 @@ def test_step_refusals(lib, call):
     assert lib.pa_last_error_string()
 
 
+@pytest.mark.parametrize("call", [plan, release])
+def test_step_sizes_near_2_31_are_refused(lib, call):
+    """Places behind the last token, page or row of the largest step must fit in 32 bits."""
+    pages = 1 << 27
+    assert call(lib, pages=pages, bt=pages) == pa.PA_ERR_UNSUPPORTED
+    assert call(lib, pages=pages - 255, bt=pages) == pa.PA_ERR_UNSUPPORTED
+    assert call(lib, pool=(1 << 31) - (1 << 16) + 1) == pa.PA_ERR_INVALID_ARG
+
+
 def test_plan_refusals(lib):
     assert plan(lib, cap=-1) == pa.PA_ERR_INVALID_ARG
+    assert plan(lib, cap=(1 << 31) - (1 << 16) + 1) == pa.PA_ERR_UNSUPPORTED
     for name in ("new", "cu", "slots", "pos"):
         assert plan(lib, **{name: None}) == pa.PA_ERR_INVALID_ARG, name
 
@@ -135,6 +145,21 @@ def test_attend_refusals(lib):
     assert attend(lib, ws=P + 16) == pa.PA_ERR_WORKSPACE
     assert lib.pa_fwd_varlen_e4m3_workspace_size(2, 5, 4, 4, 2, 64, 128) > 0
     assert lib.pa_fwd_varlen_e4m3_workspace_size(0, 0, 0, 4, 2, 64, 128) == 0
+
+
+def test_attend_sizes_near_2_31_are_refused(lib):
+    pages = (1 << 27) - 255
+    assert attend(lib, pages=pages, bt=pages) == pa.PA_ERR_UNSUPPORTED
+    assert attend(lib, total=1 << 28, mq=1 << 28, mk=1 << 20) == pa.PA_ERR_UNSUPPORTED
+
+
+def test_a_workspace_serves_smaller_batches(lib):
+    size = lambda b, mq: lib.pa_fwd_varlen_e4m3_workspace_size(b, b * mq, mq, 4, 2, 64, 128)  # noqa: E731
+    sizes = [[size(b, mq) for mq in (1, 24, 25, 32, 33, 500)] for b in (1, 31, 32, 4096)]
+    for row in sizes:
+        assert row == sorted(row)
+    for column in zip(*sizes):
+        assert list(column) == sorted(column)
 
 
 def test_bindings_refuse_cpu_tensors(lib):
