@@ -123,6 +123,18 @@ def test_many_short_and_empty_sequences():
     check(w, out, lse, seqs=set(range(0, 4096, 7)) | set(range(4080, 4096)))
 
 
+@pytest.mark.parametrize("d,every", [(64, 50), (128, 3)])
+def test_chunks_among_the_most_sequences(d, every):
+    """4096 entries of which some are chunks for the tcgen05 kernel, the last one among them."""
+    q = [40 if i % every == 0 or i == 4095 else i % 2 for i in range(4096)]
+    k = [90 if m == 40 and i % 4 else m + i % 30 for i, m in enumerate(q)]
+    w = batch(q, k, 2, 1, d, "f16" if d == 64 else "bf16", seed=d)
+    err = pa.new_err_word(DEV)
+    out, lse = call(w, err=err)
+    assert err.tolist() == [0] * 4
+    check(w, out, lse, seqs=set(range(0, 4096, 37)) | set(range(4090, 4096)))
+
+
 def test_rows_behind_the_last_sequence_stay():
     w = batch([2, 0, 3], [50, 0, 20], 4, 2, 128, "f16", seed=4)
     w["q"] = torch.cat([w["q"], torch.randn(6, 4, 128, device=DEV).half()])
