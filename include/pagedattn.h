@@ -405,8 +405,8 @@ PA_API int pa_release_pages(const int32_t* cache_seqlens, const int32_t* keep_le
  *   q_out         the rotated q, with its own strides; may be q.
  *   k_cache, v_cache  paged, of `dtype` or PA_E4M3 (cache_dtype); for PA_E4M3
  *                 strides are multiples of 16 elements.  Stored is
- *                 e4m3(x r), r the fp32 reciprocal of the kv head's scale:
- *                 nearest, saturating at +-448; NaN stays NaN.
+ *                 e4m3(x / s), s the kv head's scale: the fp32 quotient, to
+ *                 the nearest e4m3 value, saturating at +-448; NaN stays NaN.
  *   k_scale, v_scale  fp32 [Hkv] on the device (PA_E4M3 only); NULL: 1.
  *   slot_mapping  int64 [T]: page * page_size + place; negative: the token's k
  *                 and v are not stored.  A slot outside the pool is skipped
