@@ -179,12 +179,15 @@ struct Walk {
   }
 };
 
-// Scales the first `cols` columns of fp16 probabilities in TMEM by a power of
-// two a lane (0 where it is below fp16's range).
 static_assert(sizeof(Walk) <= 72 && sizeof(Walk) % 8 == 0, "kOffWalk");
 
+// Scales the first `cols` columns of fp16 probabilities in TMEM by a power of
+// two a lane: exactly, but for what leaves fp16's normal range (2^-24 of the
+// row's largest probability).  In two factors, for one below fp16's range would be
+// zero where the probability, up to 2^15, is not.
 __device__ __noinline__ void scale_p(uint32_t t, int cols, float by) {
-  const __half2 h = __float2half2_rn(by);
+  const float first = fmaxf(by, 0x1p-14f);
+  const __half2 h0 = __float2half2_rn(first), h1 = __float2half2_rn(fminf(by * 0x1p14f, 1.f));
   tc::tmem_wait_st();
 #pragma unroll 1
   for (int c = 0; c < cols; c += 16) {
@@ -195,7 +198,7 @@ __device__ __noinline__ void scale_p(uint32_t t, int cols, float by) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const uint32_t u = __float_as_uint(v[i]);
-      const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&u), h);
+      const __half2 x = __hmul2(__hmul2(*reinterpret_cast<const __half2*>(&u), h0), h1);
       w[i] = *reinterpret_cast<const uint32_t*>(&x);
     }
     tc::tmem_st16u(t + c, w);
