@@ -1037,36 +1037,29 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             sum = fmaf(weight(ml), ml.y, sum);
           }
           const float by = sum == 0.f ? 0.f : vs / sum;
-          constexpr int kPart = D / 16, kSplits = 1;  // 16-byte chunks of a quarter of the row
+          constexpr int kPart = D / 16;  // 16-byte chunks of a quarter of the row
 #pragma unroll 1
           for (int part = 0; part < 4; ++part) {
             float4 acc[kPart];
 #pragma unroll
             for (int e = 0; e < kPart; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-            for (int cta = cta0; cta <= cta1; cta += kSplits) {
-              float4 y[kSplits][kPart];
-              float w[kSplits];
+            for (int cta = cta0; cta <= cta1; ++cta) {
+              const int64_t at_row = from(cta);
+              float4 y[kPart];
+              const float2 ml = __ldcg(p.part_ml + at_row + r);
 #pragma unroll
-              for (int j = 0; j < kSplits; ++j) {
-                const int64_t at_row = from(min(cta + j, cta1));
-                const float2 ml = __ldcg(p.part_ml + at_row + r);
-                w[j] = cta + j <= cta1 ? weight(ml) : 0.f;
+              for (int e = 0; e < kPart; ++e)
+                y[e] = load16_l2(p.part_o + (at_row * (D / 4) + (part * kPart + e) * kM + r) * 4);
+              // (an unset O is not used; one whose weight is 0 is, for it may hold NaN)
+              if (ml.x == neg_inf()) continue;
+              const float w = weight(ml);
 #pragma unroll
-                for (int e = 0; e < kPart; ++e)
-                  y[j][e] = load16_l2(p.part_o +
-                                      (at_row * (D / 4) + (part * kPart + e) * kM + r) * 4);
-              }
-#pragma unroll
-              for (int j = 0; j < kSplits; ++j) {
-                if (w[j] == 0.f) continue;  // (an unset O is not read)
-#pragma unroll
-                for (int e = 0; e < kPart; ++e) {
-                  acc[e].x = fmaf(w[j], y[j][e].x, acc[e].x);
-                  acc[e].y = fmaf(w[j], y[j][e].y, acc[e].y);
-                  acc[e].z = fmaf(w[j], y[j][e].z, acc[e].z);
-                  acc[e].w = fmaf(w[j], y[j][e].w, acc[e].w);
-                }
+              for (int e = 0; e < kPart; ++e) {
+                acc[e].x = fmaf(w, y[e].x, acc[e].x);
+                acc[e].y = fmaf(w, y[e].y, acc[e].y);
+                acc[e].z = fmaf(w, y[e].z, acc[e].z);
+                acc[e].w = fmaf(w, y[e].w, acc[e].w);
               }
             }
 #pragma unroll

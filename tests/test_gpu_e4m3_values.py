@@ -1,4 +1,5 @@
-"""What reaches a result of pa_fwd_varlen_e4m3: small probabilities beside large ones in one tile."""
+"""What reaches a result of pa_fwd_varlen_e4m3: small probabilities beside large ones in one tile, NaN in
+values of keys that hardly count."""
 
 import math
 
@@ -39,3 +40,18 @@ def test_probabilities_of_a_tile_whose_maximum_rises(rows, top, d, dtype):
     w["v_cache"][ids] = v.view(-1, 16, 1, d).to(torch.float8_e4m3fn).to(DEV)
     out, lse = call(w, scale=math.log(2.0), causal=False)
     check(w, out, lse, scale=math.log(2.0), causal=False)
+
+
+@pytest.mark.parametrize("rows", [1, 150])
+@pytest.mark.parametrize("n", [200, 9001])
+def test_nan_of_a_key_that_hardly_counts(rows, n):
+    """A NaN in V at a visible key reaches the row however small the key's weight is, in one piece and
+    joined from splits."""
+    scores = [0.0] * (n - 7) + [208.0] * 7
+    w, ids = by_first_feature(scores, rows, 64, "f16")
+    w["v_cache"].view(torch.uint8)[ids[0], 2, 0, 3] = 0x7f
+    w["v_cache"][ids[0], 2, 0, 4] = torch.ones((), dtype=torch.float8_e4m3fn, device=DEV)
+    out, lse = call(w, scale=math.log(2.0), causal=False)
+    assert torch.isnan(out[:, 0, 3]).all()
+    rest = torch.arange(64, device=DEV) != 3
+    assert (out[:, 0, rest] == 0).all() and torch.isfinite(lse).all()
