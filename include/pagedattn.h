@@ -332,8 +332,8 @@ PA_API int pa_split_combine(const float* o_partial, const float* lse_partial,
  * token_capacity suffice; the first one that does not fit and every later one
  * get no rows in this step and keep their lengths (PA_DEVERR_CAPACITY with the
  * first one's index and its needed pages).  A request with a negative length,
- * or more tokens than its table row holds, is left out the same way
- * (PA_DEVERR_LENGTH) and does not stop those behind it.
+ * or more tokens than its table row holds, is left out the same way, its length
+ * kept as it is (PA_DEVERR_LENGTH), and does not stop those behind it.
  *
  *   cache_seqlens, q_lens  int32 [B].
  *   block_table   int32 [B, >= max_pages] rows of stride bt_stride; the new

@@ -22,11 +22,10 @@ def plan_step(cached, new, table, free, page_size, capacity, num_pages):
     cu, seqlens, slots, positions, refused, bad = [0], [], [], [], [], []
     open_ = True
     for b, (c, n) in enumerate(zip(cached, new)):
-        c_ok = 0 <= c <= width
-        if not c_ok or n < 0 or c + n > width:
+        if not 0 <= c <= width or n < 0 or c + n > width:
             bad.append(b)
             cu.append(cu[-1])
-            seqlens.append(c if c_ok else 0)
+            seqlens.append(c)
             continue
         need = pages_of(c + n, page_size) - pages_of(c, page_size)
         if n and open_ and (need > len(free) or len(slots) + n > capacity):

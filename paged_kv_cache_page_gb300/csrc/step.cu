@@ -157,9 +157,9 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanParams p) {
     const bool c_ok = c >= 0 && c <= cap;
     const bool ok = c_ok && n >= 0 && (long long)c + n <= cap;
     if (!ok && rank == 0) report(p.err, PA_DEVERR_LENGTH, b, c_ok ? n : c);
-    old[i] = c_ok ? c : 0;
+    old[i] = c;  // (kept as it is where it is malformed: the entry holds no page or row)
     add[i] = ok ? n : 0;
-    need[i] = ((old[i] + add[i] + ps - 1) >> p.page_log2) - ((old[i] + ps - 1) >> p.page_log2);
+    if (ok) need[i] = ((c + n + ps - 1) >> p.page_log2) - ((c + ps - 1) >> p.page_log2);
     pages += need[i];
     rows += add[i];
   }
