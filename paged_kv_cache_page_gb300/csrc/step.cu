@@ -393,10 +393,12 @@ bool wide_clusters(K kernel, const cudaLaunchConfig_t& cfg, std::atomic<uint64_t
   return (wide->load(std::memory_order_relaxed) & bit) != 0;
 }
 
+// `entry_bytes`: of shared memory for each entry of the batch.
 template <typename P>
-cudaError_t launch_cluster(void (*kernel)(P), const P& p, long long items, size_t smem,
+cudaError_t launch_cluster(void (*kernel)(P), const P& p, long long items, int entry_bytes,
                            cudaStream_t st) {
-  static std::atomic<uint64_t> asked{0}, wide{0};  // (one pair a kernel: P tells them apart)
+  // (one set a kernel: P tells them apart)
+  static std::atomic<uint64_t> asked{0}, wide{0}, allowed{0};
   // For few entries and items one CTA of 256 threads, whose barriers are short;
   // otherwise as many CTAs as leave each thread two items.  16 CTAs instead of 8:
   // 1024 requests with 33000 new tokens 11.3 -> 8.9 us, 179000 pages of 700
@@ -407,7 +409,7 @@ cudaError_t launch_cluster(void (*kernel)(P), const P& p, long long items, size_
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(small ? 256 : kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = (size_t)p.B * entry_bytes;
   cfg.stream = st;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeClusterDimension;
@@ -415,9 +417,10 @@ cudaError_t launch_cluster(void (*kernel)(P), const P& p, long long items, size_
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  if (smem > (40 << 10)) {  // with the static arrays more than the 48 KB of a plain launch
+  if (cfg.dynamicSmemBytes > (40 << 10)) {  // with the static arrays more than the 48 KB of a plain launch
+    // (the largest batch's: another thread's launch may be on its way)
     const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        allow_shared(reinterpret_cast<const void*>(kernel), kMaxB * entry_bytes, &allowed);
     if (e != cudaSuccess) return e;
   }
   if (ctas > 8 && !wide_clusters(kernel, cfg, &asked, &wide)) {
@@ -493,7 +496,7 @@ PA_API int pa_plan_step(const int32_t* cache_seqlens, const int32_t* q_lens, int
   p.token_capacity = token_capacity;
   p.num_pages = (int)num_pages;
   const cudaError_t e = launch_cluster(plan_kernel, p, token_capacity,
-                                       (size_t)B * 3 * sizeof(int),
+                                       3 * (int)sizeof(int),
                                        reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return set_error(PA_ERR_CUDA, "plan launch: %s", cudaGetErrorString(e));
   return PA_OK;
@@ -528,7 +531,7 @@ PA_API int pa_release_pages(const int32_t* cache_seqlens, const int32_t* keep_le
   p.num_pages = (int)num_pages;
   const long long most = (long long)B * max_pages;
   const cudaError_t e = launch_cluster(release_kernel, p, most < num_pages ? most : num_pages,
-                                       (size_t)B * 2 * sizeof(int),
+                                       2 * (int)sizeof(int),
                                        reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return set_error(PA_ERR_CUDA, "release launch: %s", cudaGetErrorString(e));
   return PA_OK;
