@@ -2,9 +2,10 @@
 // pa_release_pages, pa_rotary_append_varlen, pa_fwd_varlen_e4m3) from torch
 // tensors.  A decode step's kernels take 4 to 6 us, and checking a dozen tensors
 // and packing forty ctypes arguments from Python took 16 to 32 us a call on the
-// GB300's host cores; here that is 1 to 2 us.  The module holds no computation:
-// it checks types, shapes and devices, and calls the C ABI on the tensors'
-// device and its current stream.
+// GB300's host cores; here a call takes 3 to 5 us, its launch included.  The
+// module holds no computation: it checks types, shapes and devices, and calls
+// the C ABI on the tensors' device and its current stream, without the
+// interpreter's lock: a launch waits where the queue of launches is full.
 //
 // The entry points are given as addresses by bind(), so that the module works
 // with whichever libpagedattn.so has been loaded.  Each function returns the
@@ -137,6 +138,16 @@ PyObject* guarded(F&& f) {
   return nullptr;
 }
 
+// fn(args...) without the interpreter's lock, and its return code.  The caller's
+// references keep the tensors alive.
+template <typename F, typename... A>
+PyObject* unlocked(F fn, A... args) {
+  PyThreadState* const state = PyEval_SaveThread();
+  const int rc = fn(args...);
+  PyEval_RestoreThread(state);
+  return PyLong_FromLong(rc);
+}
+
 bool count_is(Py_ssize_t n, Py_ssize_t expected) {
   if (n == expected) return true;
   PyErr_Format(PyExc_TypeError, "expected %zd arguments, got %zd", expected, n);
@@ -170,7 +181,8 @@ PyObject* plan_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const auto& slots = want(a[8], "slot_mapping", at::kLong, device, {-1});
     const int64_t rows = slots.numel();
     const c10::cuda::CUDAGuard guard(device);
-    return PyLong_FromLong(g_entries.plan(
+    return unlocked(
+        g_entries.plan,
         ptr<int32_t>(want(a[0], "cache_seqlens", at::kInt, device, {B})),
         ptr<int32_t>(want(a[1], "q_lens", at::kInt, device, {B})), size_of(B, "the batch"),
         ptr<int32_t>(table), table.stride(0), size_of(table.size(1), "block_table"),
@@ -181,7 +193,7 @@ PyObject* plan_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
         ptr<int32_t>(want(a[9], "positions", at::kInt, device, {rows})),
         size_of(rows, "slot_mapping"),
         ptr<int32_t>(want(a[10], "free_count_out", at::kInt, device, {1})), err_of(a[11], device),
-        stream_of(device)));
+        stream_of(device));
   });
 }
 
@@ -196,7 +208,8 @@ PyObject* release_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const auto& table = want(a[2], "block_table", at::kInt, device, {B, -1});
     const auto& pool = want(a[3], "free_pages", at::kInt, device, {-1});
     const c10::cuda::CUDAGuard guard(device);
-    return PyLong_FromLong(g_entries.release(
+    return unlocked(
+        g_entries.release,
         ptr<int32_t>(want(a[0], "cache_seqlens", at::kInt, device, {B})),
         ptr<int32_t>(want(a[1], "keep_lens", at::kInt, device, {B})), size_of(B, "the batch"),
         ptr<int32_t>(table), table.stride(0), size_of(table.size(1), "block_table"),
@@ -204,7 +217,7 @@ PyObject* release_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
         ptr<int32_t>(want(a[4], "free_count", at::kInt, device, {1})), pool.numel(),
         ptr<int32_t>(want(a[6], "seqlens_out", at::kInt, device, {B})),
         ptr<int32_t>(want(a[7], "free_count_out", at::kInt, device, {1})), err_of(a[8], device),
-        stream_of(device)));
+        stream_of(device));
   });
 }
 
@@ -284,7 +297,8 @@ PyObject* rotary_append_varlen(PyObject*, PyObject* const* a, Py_ssize_t n) {
       }
     }
     const c10::cuda::CUDAGuard guard(device);
-    return PyLong_FromLong(g_entries.append(
+    return unlocked(
+        g_entries.append,
         qp, q_st, q_sh, k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0),
         v.stride(1), qo, qo_st, qo_sh, cache_view(kc), cache_view(vc),
         scale_of(a[11], "k_scale", hkv, device), scale_of(a[12], "v_scale", hkv, device),
@@ -292,7 +306,7 @@ PyObject* rotary_append_varlen(PyObject*, PyObject* const* a, Py_ssize_t n) {
         size_of(n_axes, "positions"), axes, cos, sin, size_of(rot_len, "rotary_cos"),
         size_of(rot, "rotary_cos"), truth(a[9]) ? 1 : 0, rot_type, size_of(T, "k"),
         size_of(hq, "q"), size_of(hkv, "k"), size_of(d, "k"), dtype, e4m3 ? PA_E4M3 : dtype,
-        err_of(a[14], device), stream_of(device)));
+        err_of(a[14], device), stream_of(device));
   });
 }
 
@@ -347,14 +361,15 @@ PyObject* fwd_varlen_e4m3(PyObject*, PyObject* const* a, Py_ssize_t n) {
       scratch = at::empty({(int64_t)ws_bytes}, q.options().dtype(at::kByte));
       ws = scratch.data_ptr();
     }
-    return PyLong_FromLong(g_entries.attend(
+    return unlocked(
+        g_entries.attend,
         q.data_ptr(), q.stride(0), q.stride(1), cache_view(kc), cache_view(vc),
         scale_of(a[8], "k_scale", hkv, device), scale_of(a[9], "v_scale", hkv, device),
         ptr<int32_t>(cu), ptr<int32_t>(lens), ptr<int32_t>(table), table.stride(0),
         size_of(table.size(1), "block_table"), size_of(page, "the page size"),
         size_of(B, "the batch"), size_of(rows, "q"), max_q, max_k, size_of(hq, "q"),
         size_of(hkv, "k_cache"), size_of(d, "q"), pages, (float)scale, truth(a[11]) ? 1 : 0,
-        out.data_ptr(), lse, ws, ws_bytes, err_of(a[15], device), dtype, stream_of(device)));
+        out.data_ptr(), lse, ws, ws_bytes, err_of(a[15], device), dtype, stream_of(device));
   });
 }
 

@@ -42,3 +42,30 @@ def test_batches_of_different_sizes_from_two_threads():
     for t in threads:
         t.join()
     assert all(c[0] == {pa.PA_OK} for c in codes.values()), codes
+
+
+def test_the_interpreter_lock_is_not_held_over_a_launch():
+    """In the place of the library's entry the interpreter's own question whether the calling thread
+    holds the lock."""
+    native = pa._native or pa._load_native()
+    lib = pa.load_library()
+    entries = [ctypes.cast(f, ctypes.c_void_p).value for f in (
+        lib.pa_plan_step, lib.pa_release_pages, lib.pa_rotary_append_varlen, lib.pa_fwd_varlen_e4m3,
+        lib.pa_fwd_varlen_e4m3_workspace_size)]
+    ask = ctypes.cast(ctypes.pythonapi.PyGILState_Check, ctypes.c_void_p).value
+    x = torch.zeros((3, 2, 64), dtype=torch.float16, device=DEV)
+    c = torch.zeros((4, 16, 2, 64), dtype=torch.float8_e4m3fn, device=DEV)
+    try:
+        native.bind(ask, ask, ask, ask, entries[4])
+        held = [
+            native.plan_step(i32([1]), i32([1]), i32([[0]]), i32([0]), i32([0]), 16, i32([0, 0]), i32([0]),
+                             torch.zeros(2, dtype=torch.int64, device=DEV), i32([0, 0]), i32([0]), None),
+            native.release_pages(i32([1]), i32([1]), i32([[0]]), i32([0]), i32([0]), 16, i32([0]), i32([0]),
+                                 None),
+            native.rotary_append_varlen(x, x, x, c, c, torch.zeros(3, dtype=torch.int64, device=DEV), None,
+                                        None, None, False, None, None, None, x, None),
+            native.fwd_varlen_e4m3(x, c, c, i32([0, 3]), i32([3]), i32([[0]]), 3, 3, None, None, None, True,
+                                   torch.empty_like(x), None, None, None)]
+    finally:
+        native.bind(*entries)
+    assert held == [0] * 4
