@@ -63,6 +63,16 @@ struct RotAppendParams {
   uint32_t unit_axes[kMaxPairs / 8];  // byte a: which of the unit's 8 pairs axis a turns
 };
 
+// As load16, without the promise that nothing writes there while the kernel
+// runs: q_out may be q.
+__device__ __forceinline__ uint4 load16_rw(const void* src) {
+  uint4 x;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+               : "l"(src));
+  return x;
+}
+
 template <typename T>
 __device__ __forceinline__ void unpack8(const uint4& u, float* x) {
   using E = Elem<T>;
@@ -262,16 +272,17 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rotary_append_kernel(
   const int first = part * kRows + lane / kPerRow, step = kRows * p.parts;
   // The head rows first, first + step, ... of one tensor, BATCH of them in
   // flight: loads without a condition (a row behind the last is read as the
-  // last), or they would wait for one another.  `put` stores row r.
+  // thread's own first of them: another's may be written already), or they would
+  // wait for one another.  `put` stores row r.
   auto rows = [&](const T* src, int64_t sh, int n, auto&& put) {
 #pragma unroll 1
     for (int r0 = first; r0 < n; r0 += step * BATCH) {
       uint4 x_lo[BATCH], x_hi[BATCH];
 #pragma unroll
       for (int i = 0; i < BATCH; ++i) {
-        const T* row = src + min(r0 + i * step, n - 1) * sh;
-        x_lo[i] = load16(row + lo);
-        x_hi[i] = load16(row + hi);
+        const T* row = src + (r0 + i * step < n ? r0 + i * step : r0) * sh;
+        x_lo[i] = load16_rw(row + lo);
+        x_hi[i] = load16_rw(row + hi);
       }
 #pragma unroll
       for (int i = 0; i < BATCH; ++i)
