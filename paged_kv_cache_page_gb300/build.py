@@ -15,6 +15,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -97,7 +98,8 @@ def _link(lib, objs):
 
 def build(force=False, verbose=False, extra=()):
     """Compile (if needed) the libraries and the Python module; return the path of
-    libpagedattn.so."""
+    libpagedattn.so.  The library needs neither Python's headers nor torch's: where the module
+    cannot be built that is a warning, and the calls that need it say that it is missing."""
     os.makedirs(OUT_DIR, exist_ok=True)
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
     headers.append(os.path.join(ROOT, "include", "pagedattn.h"))
@@ -116,10 +118,17 @@ def build(force=False, verbose=False, extra=()):
     if jobs or bind:
         with cf.ThreadPoolExecutor(max_workers=min(len(jobs) + 1, os.cpu_count() or 4)) as ex:
             futs = [ex.submit(_compile, s, o, extra, verbose) for s, o in jobs]
-            if bind:
-                futs.append(ex.submit(_build_binding, binding, verbose))
+            module = ex.submit(_build_binding, binding, verbose) if bind else None
             for f in futs:
                 logs.append(f.result())
+            if module is not None:
+                try:
+                    logs.append(module.result())
+                except (RuntimeError, OSError, AttributeError) as e:
+                    # (one of older sources may not fit the library)
+                    if os.path.exists(binding):
+                        os.remove(binding)
+                    warnings.warn(f"{BINDING_LIB} was not built: {e}", RuntimeWarning, stacklevel=2)
     for lib, objs in objs_of.items():
         if force or _stale(lib, objs):
             _link(lib, objs)
