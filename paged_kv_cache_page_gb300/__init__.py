@@ -425,8 +425,8 @@ def pa_rotary_append_varlen(q, k, v, k_cache, v_cache, slot_mapping, positions=N
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     rc = (_native or _load_native()).rotary_append_varlen(
         q, k, v, k_cache, v_cache, slot_mapping, positions, rotary_cos, rotary_sin,
-        rotary_interleaved, None if pair_axis is None else bytes(pair_axis), k_scale, v_scale,
-        q_out, err)
+        rotary_interleaved, None if pair_axis is None else bytes(list(pair_axis)), k_scale,
+        v_scale, q_out, err)
     if rc:
         _check(rc)
     return q_out
