@@ -39,8 +39,9 @@ constexpr int kMaxPairs = 64;
 constexpr int kThreads = 256;
 // Head rows a thread has in flight where it takes several of a tensor, and
 // resident blocks of an SM: 2 and 4 (64 registers) run 8192 tokens of 32/8 heads
-// in 36 us; 1 and 4 take 38, 4 and 2 take 45, 3 and 3 take 41, 2 and 5 spill and
-// take 42.  Rows by way of shared memory, four or six of them ahead, take 37.
+// in 37 us; 1 and 4 take 39, 4 and 2 take 46, 3 and 3 take 42, 2 and 5 spill and
+// take 46.  Rows by way of shared memory, four or six of them ahead, took 1.5 us
+// more than these.
 constexpr int kBatch = 2, kBlocks = 4;
 constexpr int kWarpsWanted = 152 * 64;  // two rounds of the GPU's warps
 
@@ -408,7 +409,7 @@ cudaError_t launch(RotAppendParams& p, cudaStream_t st) {
     return cudaGetLastError();
   }
   // Warps of a token: one where the tokens alone fill the GPU (the angles are
-  // then loaded once a token; two warps a token: 35 -> 42 us for 8192 tokens of
+  // then loaded once a token; two warps a token took 42 us instead of 35 for 8192 tokens of
   // 32/8 heads), for fewer tokens more of them, and where one round of the GPU's
   // warps holds them one for every set of rows of q, of k and of v (64 tokens:
   // 3.5 -> 2.5 us; 1601 tokens of 12/12 heads, two rounds: 5.4 -> 7.3 us).
@@ -418,8 +419,8 @@ cudaError_t launch(RotAppendParams& p, cudaStream_t st) {
   p.parts = (int)std::max<long long>(1, std::min<long long>(most, want / p.T));
   p.roles = p.parts == most && (long long)p.T * p.parts * 6 <= want ? 3 : 1;
   const long long blocks = ((long long)p.T * p.parts * p.roles * 32 + kThreads - 1) / kThreads;
-  // A thread that has one row of each tensor loads one at a time: 64 tokens 2.47 ->
-  // 2.29 us, 1601 tokens of 12/12 heads 5.6 -> 5.1 us.
+  // A thread that has one row of each tensor loads one at a time: 8 % less for 64
+  // tokens (now 2.4 us), 9 % less for 1601 tokens of 12/12 heads (5.2 us).
   if (p.parts == most)
     rotary_append_kernel<D, T, E4M3, 1><<<(unsigned)blocks, kThreads, 0, st>>>(p);
   else
