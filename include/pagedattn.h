@@ -80,7 +80,8 @@ enum {
   PA_DEVERR_PAGE_OOB = 1,    /* block_table entry < 0 or >= num_pages            */
   PA_DEVERR_LENGTH = 2,      /* length < 0, beyond the table, cache or max_seqlen_k */
   PA_DEVERR_TIMEOUT = 3,     /* a pipeline wait exceeded its time limit          */
-  PA_DEVERR_CAPACITY = 4     /* the page pool or the packed rows do not suffice  */
+  PA_DEVERR_CAPACITY = 4,    /* the page pool or the packed rows do not suffice  */
+  PA_DEVERR_VALUE = 5        /* a beam's logits or parent that stand for nothing */
 };
 
 /* A 4-D cache view.  Paged: [num_pages, page_size, Hkv, D] with stride_b =
@@ -465,6 +466,135 @@ PA_API int pa_fwd_varlen_e4m3(const void* q, int64_t q_st, int64_t q_sh, pa_tens
 
 PA_API size_t pa_fwd_varlen_e4m3_workspace_size(int B, int total_q, int max_seqlen_q, int Hq,
                                                 int Hkv, int D, int max_seqlen_k);
+
+/*
+ * pa_beam_select -- the best continuations of each request over its beams and
+ * the vocabulary (one launch): a beam search's step from logits to scores,
+ * parents and tokens.  pa_beam_reorder then moves the beams' pages.
+ *
+ * Beam k of request b has the score s = scores[b, k] and the logits x:
+ *   score(k, v) = s + (x[v] - ln sum_w exp(x[w])), in 64 bits,
+ * and the N largest are returned in descending order, the lowest k * V + v first
+ * among equal ones.
+ *
+ *   logits       [B, K, V] of `dtype` (PA_F16, PA_BF16 or PA_F32), element
+ *                strides stride_b, stride_k; any alignment of the rows.  -inf:
+ *                a token that may not be chosen.
+ *   scores       fp32 [B, K]; a beam whose score is not finite is dead: it has
+ *                no candidates and its logits are not read.
+ *   finished     uint8 [B, K] or NULL; not 0: the beam's only candidate is
+ *                end_token with its score as it is, and its logits are not read.
+ *   end_token    in [0, V), or negative for none (finished must be NULL then).
+ *   scores_out   fp32 [B, N]; parents, tokens int32 [B, N]: k and v.  Where there
+ *                are fewer candidates: -inf, -1 and -1 (pa_beam_reorder drops
+ *                such a beam, and the next call takes it for dead).
+ *   finished_out uint8 [B, N] or NULL: the parent was finished, or the token is
+ *                end_token.  None of the outputs may be an input.
+ * A beam whose logits hold a NaN or +inf has no candidates and is reported
+ * (PA_DEVERR_VALUE, b * K + k).  K <= 32, N <= 64, V <= 2^24, B <= 2^20.
+ */
+PA_API int pa_beam_select(const void* logits, int64_t stride_b, int64_t stride_k,
+                          const float* scores, const uint8_t* finished, int end_token, int B,
+                          int K, int V, int N, float* scores_out, int32_t* parents,
+                          int32_t* tokens, uint8_t* finished_out, int32_t* err_word, int dtype,
+                          pa_stream_t stream);
+
+/*
+ * pa_beam_reorder -- block tables, lengths and page pool after the beams of each
+ * request have been replaced by their continuations (one launch).  Beams share
+ * the pages of their common past: what is moved is table entries, and only a
+ * page that would be written by several beams is copied (pa_copy_pages).
+ *
+ * Row b * K + i of the tables becomes child i of request b: the tokens and
+ * pages of row b * K + parents[b, i].  Beams of a request share pages only at
+ * the same column of their tables, and other requests' rows share none with
+ * them but such as all of the request's beams hold.
+ *   - A page of a column that no child holds there goes back to the pool: pushed
+ *     onto free_pages behind the first *free_count, by request, column, beam.
+ *   - A child's last page that is partly filled will be written to.  Where an
+ *     earlier child holds it too, or another child holds it whole, the child
+ *     gets a fresh page and an entry in `copies`.  Fresh pages come from the top
+ *     of the pool as it stands after the pushes, by request, column, child.
+ * The step after a prompt has parents all 0: one row becomes K.  A request that
+ * ends has parents all -1: its pages go back, each once.
+ *
+ *   parents       int32 [B, K]: a beam of the request, or -1: the child has no
+ *                 tokens and holds no page.
+ *   seqlens       int32 [B * K]: tokens in the cache of each row, each beam its own.
+ *   block_table   int32 [B * K, >= max_pages], rows of stride bt_stride.
+ *   block_table_out  with its own stride bto_stride; may be block_table (with the
+ *                 same stride).  A child's entries up to its last page are written.
+ *   seqlens_out   int32 [B * K]; may be seqlens.
+ *   free_pages    int32 [num_pages], free_count, free_count_out as in
+ *                 pa_plan_step and pa_release_pages.
+ *   copies        int32 [B * K, 3]: for each child the page to be copied, the
+ *                 fresh page and the number of tokens; -1, -1, 0: none.
+ * Requests are taken in order while the pool holds their fresh pages; the first
+ * that does not fit and every later one stay as they are, without copies
+ * (PA_DEVERR_CAPACITY, the request and its fresh pages).  A request with a parent
+ * outside [-1, K) (PA_DEVERR_VALUE, the row, the parent), a length outside its
+ * table row (PA_DEVERR_LENGTH, the row, the length) or an entry outside the pool
+ * (PA_DEVERR_PAGE_OOB, the row, the column) stays as it is, too, and does not
+ * stop those behind it.  K <= 32 and B * K <= 4096; other limits as pa_plan_step.
+ */
+PA_API int pa_beam_reorder(const int32_t* parents, const int32_t* seqlens, int B, int K,
+                           const int32_t* block_table, int64_t bt_stride, int max_pages,
+                           int page_size, int32_t* free_pages, const int32_t* free_count,
+                           int64_t num_pages, int32_t* block_table_out, int64_t bto_stride,
+                           int32_t* seqlens_out, int32_t* copies, int32_t* free_count_out,
+                           int32_t* err_word, pa_stream_t stream);
+
+/*
+ * pa_copy_pages -- copies the first tokens of pages to other pages, in the
+ * caches of all layers (one launch per 256 caches): what pa_beam_reorder asks for.
+ *
+ *   copies     int32 [n, 3] on the device: source page, target page, tokens; an
+ *              entry with a negative source or target, or no tokens, is skipped.
+ *              A page outside the pool, or more tokens than a page has, is
+ *              skipped and reported (PA_DEVERR_PAGE_OOB, the entry, the page;
+ *              PA_DEVERR_LENGTH, the entry, the tokens).  No target may be
+ *              another entry's source or target.
+ *   caches     HOST array of n_caches device pointers, read before the call
+ *              returns: [num_pages, page_size, H, D] each, k and v alike, with the
+ *              same BYTE strides stride_b, stride_t, stride_h (multiples of 16) and
+ *              head_bytes = D * element size (a multiple of 16) contiguous bytes.
+ */
+PA_API int pa_copy_pages(const int32_t* copies, int n, void* const* caches, int n_caches,
+                         int64_t stride_b, int64_t stride_t, int64_t stride_h, int head_bytes,
+                         int H, int page_size, int64_t num_pages, int32_t* err_word,
+                         pa_stream_t stream);
+
+/*
+ * pa_fwd_cross -- attention of a ragged batch's rows to the keys of their entry,
+ * of another length (cross attention to an encoder's states): no mask by
+ * position, no cache and no pages.  All rows of an entry read one copy of its
+ * keys and values: the beams of a request, and several tokens of each, are
+ * rows of one entry.
+ *
+ *   q             [total_q, Hq, D], element strides q_st, q_sh (multiples of 8),
+ *                 packed by cu_seqlens_q int32 [B+1], as in pa_fwd_varlen_unified.
+ *   k, v          [total_k, Hkv, D], element strides *_st, *_sh (multiples of 8),
+ *                 16-byte aligned: slices of one projection will do.
+ *   cu_seqlens_k  int32 [B+1]: entry b's keys begin at row cu_seqlens_k[b] and end
+ *                 at cu_seqlens_k[b+1], or, with seqlens_k, after its first
+ *                 seqlens_k[b] rows (a padded batch).
+ *   seqlens_k     int32 [B] or NULL.
+ *   key_mask      uint8 [total_k] or NULL: 0: no row sees the key, whatever k and v
+ *                 hold there (NaN and infinities too).
+ *   max_seqlen_q, max_seqlen_k  host-known bounds of an entry's rows and keys.
+ *   out [total_q, Hq, D] contiguous; lse fp32 [Hq, total_q] or NULL.
+ * Rows without a key: O = 0, LSE = -inf.  Rows behind cu_seqlens_q[B] are not
+ * written.  An entry with rows or keys outside q and k, or more than the bounds,
+ * is reported (PA_DEVERR_LENGTH, the entry, the length): its rows that lie in q
+ * and within max_seqlen_q have no keys then.
+ */
+PA_API int pa_fwd_cross(const void* q, int64_t q_st, int64_t q_sh, const void* k, int64_t k_st,
+                        int64_t k_sh, const void* v, int64_t v_st, int64_t v_sh,
+                        const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
+                        const int32_t* seqlens_k, const uint8_t* key_mask, int B, int total_q,
+                        int total_k, int max_seqlen_q, int max_seqlen_k, int Hq, int Hkv, int D,
+                        float scale, void* out, float* lse, int32_t* err_word, int dtype,
+                        pa_stream_t stream);
 
 /* Human-readable text of the last non-OK return on the calling thread. */
 PA_API const char* pa_last_error_string(void);

@@ -36,6 +36,7 @@ PA_DEVERR_PAGE_OOB = 1
 PA_DEVERR_LENGTH = 2
 PA_DEVERR_TIMEOUT = 3
 PA_DEVERR_CAPACITY = 4
+PA_DEVERR_VALUE = 5
 PAGE_SIZE = 16
 PA_NOALLOC_SCRATCH_BYTES = 8 << 20  # fixed split scratch of pa_fwd_kvcache_noalloc
 
@@ -92,6 +93,15 @@ _SIGNATURES = {
                                   _i64, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i64,
                                   _f32, _i32, _vp, _vp, _vp, _sz, _vp, _i32, _vp]),
     "pa_fwd_varlen_e4m3_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i32, _i32, _i32]),
+    "pa_beam_select": (_i32, [_vp, _i64, _i64, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp,
+                              _vp, _vp, _i32, _vp]),
+    "pa_beam_reorder": (_i32, [_vp, _vp, _i32, _i32, _vp, _i64, _i32, _i32, _vp, _vp, _i64, _vp, _i64,
+                               _vp, _vp, _vp, _vp, _vp]),
+    "pa_copy_pages": (_i32, [_vp, _i32, _vp, _i32, _i64, _i64, _i64, _i32, _i32, _i32, _i64, _vp,
+                             _vp]),
+    "pa_fwd_cross": (_i32, [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _vp,
+                            _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _vp, _vp, _vp, _i32,
+                            _vp]),
     "pa_last_error_string": (ctypes.c_char_p, []),
     "pa_version": (_i32, []),
 }
@@ -350,7 +360,8 @@ def _load_native():
     loader.exec_module(native)
     native.bind(*[ctypes.cast(fn, _vp).value for fn in (
         lib.pa_plan_step, lib.pa_release_pages, lib.pa_rotary_append_varlen,
-        lib.pa_fwd_varlen_e4m3, lib.pa_fwd_varlen_e4m3_workspace_size)])
+        lib.pa_fwd_varlen_e4m3, lib.pa_fwd_varlen_e4m3_workspace_size, lib.pa_beam_select,
+        lib.pa_beam_reorder, lib.pa_copy_pages, lib.pa_fwd_cross)])
     _native = native
     return native
 
@@ -452,6 +463,94 @@ def pa_fwd_varlen_e4m3(q, k_cache, v_cache, cu_seqlens_q, seqlens_k, block_table
     rc = (_native or _load_native()).fwd_varlen_e4m3(
         q, k_cache, v_cache, cu_seqlens_q, seqlens_k, block_table, max_seqlen_q, max_seqlen_k,
         k_scale, v_scale, scale, causal, out, lse, workspace, err)
+    if rc:
+        _check(rc)
+    return out, lse
+
+
+# ---------------------------------------------------------------- beam search over a paged cache
+def pa_beam_select(logits, scores, num_out=None, finished=None, end_token=-1, scores_out=None,
+                   parents=None, tokens=None, finished_out=None, err=None):
+    """The ``num_out`` best continuations of each request over its beams and the vocabulary; returns
+    ``(scores_out, parents, tokens, finished_out)``, each ``[B, num_out]``.
+
+    ``logits`` ``[B, K, V]`` (fp16, bf16 or fp32), ``scores`` fp32 ``[B, K]`` (not finite: a dead
+    beam), ``finished`` bool ``[B, K]`` (its only continuation is ``end_token``, at its score).
+    ``num_out`` defaults to K.  ``finished_out`` is allocated where ``end_token`` is given, ``None``
+    otherwise.
+    """
+    if num_out is None:
+        num_out = logits.shape[1] if parents is None else parents.shape[1]
+    elif parents is not None and parents.shape[1] != num_out:
+        raise ValueError("pa_beam_select: parents does not have num_out columns")
+    shape = (logits.shape[0], num_out)
+    if scores_out is None:
+        scores_out = torch.empty(shape, dtype=torch.float32, device=logits.device)
+    if parents is None:
+        parents = torch.empty(shape, dtype=torch.int32, device=logits.device)
+    if tokens is None:
+        tokens = torch.empty(shape, dtype=torch.int32, device=logits.device)
+    if finished_out is None and end_token >= 0:
+        finished_out = torch.empty(shape, dtype=torch.bool, device=logits.device)
+    rc = (_native or _load_native()).beam_select(logits, scores, finished, end_token, scores_out,
+                                                 parents, tokens, finished_out, err)
+    if rc:
+        _check(rc)
+    return scores_out, parents, tokens, finished_out
+
+
+def pa_beam_reorder(parents, seqlens, block_table, free_pages, free_count, page_size,
+                    block_table_out=None, seqlens_out=None, copies=None, free_count_out=None,
+                    err=None):
+    """Block tables, lengths and page pool after each request's beams have been replaced by their
+    continuations: row ``b * K + i`` becomes row ``b * K + parents[b, i]`` (-1: dropped).  Returns
+    ``(block_table_out, seqlens_out, copies)``; ``pa_copy_pages`` then makes the ``copies``.
+
+    ``parents`` int32 ``[B, K]``; ``seqlens`` int32 ``[B * K]``; ``block_table`` int32
+    ``[B * K, max_pages]``; ``free_pages`` and ``free_count`` as in ``pa_plan_step``.  Outputs that
+    are not given: ``block_table_out``, ``seqlens_out`` and ``free_count_out`` replace their inputs,
+    ``copies`` (int32 ``[B * K, 3]``) is allocated.
+    """
+    if block_table_out is None:
+        block_table_out = block_table
+    if seqlens_out is None:
+        seqlens_out = seqlens
+    if copies is None:
+        copies = torch.empty((seqlens.numel(), 3), dtype=torch.int32, device=seqlens.device)
+    rc = (_native or _load_native()).beam_reorder(
+        parents, seqlens, block_table, free_pages, free_count, page_size, block_table_out,
+        seqlens_out, copies, free_count if free_count_out is None else free_count_out, err)
+    if rc:
+        _check(rc)
+    return block_table_out, seqlens_out, copies
+
+
+def pa_copy_pages(copies, caches, err=None):
+    """Copies the first ``copies[i, 2]`` tokens of page ``copies[i, 0]`` to page ``copies[i, 1]``
+    (negative: nothing) in each of ``caches``, a list of ``[num_pages, page_size, H, D]`` tensors of
+    one shape, type and strides: k and v of every layer."""
+    rc = (_native or _load_native()).copy_pages(copies, caches, err)
+    if rc:
+        _check(rc)
+
+
+def pa_fwd_cross(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, seqlens_k=None,
+                 key_mask=None, scale=None, out=None, lse=None, err=None, return_lse=True):
+    """Attention of a ragged batch's rows to the keys of their entry (cross attention to an encoder's
+    states); returns ``(out, lse)``.
+
+    ``q`` ``[total_q, Hq, D]`` packed by ``cu_seqlens_q [B+1]``; ``k``, ``v`` ``[total_k, Hkv, D]``
+    packed by ``cu_seqlens_k [B+1]``, of which the first ``seqlens_k[b]`` rows count where that is
+    given (a padded batch).  ``key_mask`` bool ``[total_k]``: false for a key that no row sees.  All
+    beams and tokens of a request are rows of one entry.
+    """
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if lse is None and return_lse:
+        lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
+    rc = (_native or _load_native()).fwd_cross(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
+                                               max_seqlen_k, seqlens_k, key_mask, scale, out, lse,
+                                               err)
     if rc:
         _check(rc)
     return out, lse

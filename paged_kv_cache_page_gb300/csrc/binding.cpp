@@ -1,6 +1,6 @@
 // Python module `_binding`: the serving-step calls (pa_plan_step,
-// pa_release_pages, pa_rotary_append_varlen, pa_fwd_varlen_e4m3) from torch
-// tensors.  A decode step's kernels take 4 to 6 us, and checking a dozen tensors
+// pa_release_pages, pa_rotary_append_varlen, pa_fwd_varlen_e4m3; pa_beam_select,
+// pa_beam_reorder, pa_copy_pages, pa_fwd_cross) from torch tensors.  A decode step's kernels take 4 to 6 us, and checking a dozen tensors
 // and packing forty ctypes arguments from Python took 16 to 32 us a call on the
 // GB300's host cores; here a call takes 3 to 5 us, its launch included.  The
 // module holds no computation: it checks types, shapes and devices, and calls
@@ -23,6 +23,7 @@
 #include <initializer_list>
 #include <stdexcept>
 #include <string>
+#include <vector>
 
 #include "../../include/pagedattn.h"
 
@@ -34,6 +35,10 @@ struct Entries {
   decltype(&pa_rotary_append_varlen) append = nullptr;
   decltype(&pa_fwd_varlen_e4m3) attend = nullptr;
   decltype(&pa_fwd_varlen_e4m3_workspace_size) attend_workspace = nullptr;
+  decltype(&pa_beam_select) select = nullptr;
+  decltype(&pa_beam_reorder) reorder = nullptr;
+  decltype(&pa_copy_pages) copy = nullptr;
+  decltype(&pa_fwd_cross) cross = nullptr;
 } g_entries;
 
 struct BadArgument : std::runtime_error {
@@ -154,9 +159,10 @@ bool count_is(Py_ssize_t n, Py_ssize_t expected) {
   return false;
 }
 
-// bind(plan, release, append, attend, attend_workspace): entry addresses
+// bind(plan, release, append, attend, attend_workspace, select, reorder, copy, cross): entry
+// addresses
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (!count_is(n, 5)) return nullptr;
+  if (!count_is(n, 9)) return nullptr;
   return guarded([&]() -> PyObject* {
     auto at = [&](int i) { return (uintptr_t)(unsigned long long)integer(a[i]); };
     g_entries.plan = reinterpret_cast<decltype(g_entries.plan)>(at(0));
@@ -164,6 +170,10 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     g_entries.append = reinterpret_cast<decltype(g_entries.append)>(at(2));
     g_entries.attend = reinterpret_cast<decltype(g_entries.attend)>(at(3));
     g_entries.attend_workspace = reinterpret_cast<decltype(g_entries.attend_workspace)>(at(4));
+    g_entries.select = reinterpret_cast<decltype(g_entries.select)>(at(5));
+    g_entries.reorder = reinterpret_cast<decltype(g_entries.reorder)>(at(6));
+    g_entries.copy = reinterpret_cast<decltype(g_entries.copy)>(at(7));
+    g_entries.cross = reinterpret_cast<decltype(g_entries.cross)>(at(8));
     Py_RETURN_NONE;
   });
 }
@@ -373,6 +383,164 @@ PyObject* fwd_varlen_e4m3(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// A contiguous tensor of flags, one byte each.
+uint8_t* flags_of(PyObject* o, const char* name, c10::Device device,
+                  std::initializer_list<int64_t> shape) {
+  if (o == Py_None) return nullptr;
+  const at::ScalarType type = tensor_of(o, name).scalar_type();
+  const auto& t = want(o, name, type == at::kByte ? at::kByte : at::kBool, device, shape);
+  if (!t.is_contiguous()) bad(name, "must be contiguous");
+  return ptr<uint8_t>(t);
+}
+template <typename T>
+T* dense(PyObject* o, const char* name, at::ScalarType type, c10::Device device,
+         std::initializer_list<int64_t> shape) {
+  const auto& t = want(o, name, type, device, shape);
+  if (!t.is_contiguous()) bad(name, "must be contiguous");
+  return ptr<T>(t);
+}
+
+// beam_select(logits, scores, finished, end_token, scores_out, parents, tokens, finished_out, err)
+PyObject* beam_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count_is(n, 9)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const at::Tensor& x = tensor_of(a[0], "logits");
+    const c10::Device device = device_of(x, "logits");
+    const at::ScalarType type = x.scalar_type();
+    const int dtype = type == at::kFloat ? PA_F32 : dtype_of(type);
+    if (dtype < 0 || x.dim() != 3) bad("logits", "must be a 3-d fp16, bf16 or fp32 tensor");
+    const int64_t B = x.size(0), K = x.size(1), V = x.size(2);
+    want(a[0], "logits", type, device, {B, K, V});
+    const auto& parents = want(a[5], "parents", at::kInt, device, {B, -1});
+    const int64_t N = parents.size(1);
+    const c10::cuda::CUDAGuard guard(device);
+    return unlocked(
+        g_entries.select, x.data_ptr(), x.stride(0), x.stride(1),
+        dense<float>(a[1], "scores", at::kFloat, device, {B, K}),
+        flags_of(a[2], "finished", device, {B, K}), int_of(a[3], "end_token"),
+        size_of(B, "the batch"), size_of(K, "the beams"), size_of(V, "the vocabulary"),
+        size_of(N, "parents"), dense<float>(a[4], "scores_out", at::kFloat, device, {B, N}),
+        dense<int32_t>(a[5], "parents", at::kInt, device, {B, N}),
+        dense<int32_t>(a[6], "tokens", at::kInt, device, {B, N}),
+        flags_of(a[7], "finished_out", device, {B, N}), err_of(a[8], device), dtype,
+        stream_of(device));
+  });
+}
+
+// beam_reorder(parents, seqlens, block_table, free_pages, free_count, page_size, block_table_out,
+//              seqlens_out, copies, free_count_out, err)
+PyObject* beam_reorder(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count_is(n, 11)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const at::Tensor& parents = tensor_of(a[0], "parents");
+    const c10::Device device = device_of(parents, "parents");
+    if (parents.dim() != 2) bad("parents", "must be a 2-d tensor");
+    const int64_t B = parents.size(0), K = parents.size(1), rows = B * K;
+    const auto& table = want(a[2], "block_table", at::kInt, device, {rows, -1});
+    const int64_t width = table.size(1);
+    const auto& out = want(a[6], "block_table_out", at::kInt, device, {rows, width});
+    const auto& pool = want(a[3], "free_pages", at::kInt, device, {-1});
+    // (a table of one row: its stride does not matter)
+    const int64_t bt = rows > 1 ? table.stride(0) : width, bto = rows > 1 ? out.stride(0) : width;
+    const c10::cuda::CUDAGuard guard(device);
+    return unlocked(
+        g_entries.reorder, dense<int32_t>(a[0], "parents", at::kInt, device, {B, K}),
+        dense<int32_t>(a[1], "seqlens", at::kInt, device, {rows}), size_of(B, "the batch"),
+        size_of(K, "the beams"), ptr<int32_t>(table), bt, size_of(width, "block_table"),
+        int_of(a[5], "page_size"), ptr<int32_t>(pool),
+        ptr<int32_t>(want(a[4], "free_count", at::kInt, device, {1})), pool.numel(),
+        ptr<int32_t>(out), bto, dense<int32_t>(a[7], "seqlens_out", at::kInt, device, {rows}),
+        dense<int32_t>(a[8], "copies", at::kInt, device, {rows, 3}),
+        ptr<int32_t>(want(a[9], "free_count_out", at::kInt, device, {1})), err_of(a[10], device),
+        stream_of(device));
+  });
+}
+
+// copy_pages(copies, caches, err): caches a list or tuple of tensors
+PyObject* copy_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count_is(n, 3)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const at::Tensor& copies = tensor_of(a[0], "copies");
+    const c10::Device device = device_of(copies, "copies");
+    int32_t* list = dense<int32_t>(a[0], "copies", at::kInt, device, {-1, 3});
+    const bool tuple = PyTuple_Check(a[1]);
+    if (!tuple && !PyList_Check(a[1])) bad("caches", "must be a list or tuple of tensors");
+    const Py_ssize_t count = tuple ? PyTuple_GET_SIZE(a[1]) : PyList_GET_SIZE(a[1]);
+    std::vector<void*> at((size_t)count);
+    int64_t st[3] = {16, 16, 16}, shape[4] = {1, 1, 1, 16}, size = 1;
+    for (Py_ssize_t i = 0; i < count; ++i) {
+      const at::Tensor& c =
+          tensor_of(tuple ? PyTuple_GET_ITEM(a[1], i) : PyList_GET_ITEM(a[1], i), "caches");
+      if (!c.is_cuda() || c.device() != device || c.dim() != 4 ||
+          (c.size(3) > 1 && c.stride(3) != 1))
+        bad("caches", "must be 4-d with a contiguous last axis, on the call's CUDA device");
+      if (i == 0) {
+        size = c.element_size();
+        for (int x = 0; x < 4; ++x) shape[x] = c.size(x);
+      }
+      bool alike = (int64_t)c.element_size() == size;
+      for (int x = 0; x < 4; ++x) alike = alike && c.size(x) == shape[x];
+      for (int x = 2; x >= 0; --x) {
+        // (the stride of an axis with one place does not matter)
+        const int64_t s =
+            shape[x] > 1 ? c.stride(x) * size : x == 2 ? shape[3] * size : st[x + 1] * shape[x + 1];
+        alike = alike && (i == 0 || s == st[x]);
+        st[x] = s;
+      }
+      if (!alike) bad("caches", "must have one shape, type and strides");
+      at[(size_t)i] = c.data_ptr();
+    }
+    const c10::cuda::CUDAGuard guard(device);
+    return unlocked(g_entries.copy, list, size_of(copies.size(0), "copies"), at.data(),
+                    size_of(count, "caches"), st[0], st[1], st[2],
+                    size_of(shape[3] * size, "the head size"), size_of(shape[2], "the heads"),
+                    size_of(shape[1], "the page size"), shape[0], err_of(a[2], device),
+                    stream_of(device));
+  });
+}
+
+// fwd_cross(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, seqlens_k, key_mask,
+//           scale, out, lse, err)
+PyObject* fwd_cross(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count_is(n, 13)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const at::Tensor& q = tensor_of(a[0], "q");
+    const c10::Device device = device_of(q, "q");
+    const at::ScalarType type = q.scalar_type();
+    const int dtype = dtype_of(type);
+    if (dtype < 0 || q.dim() != 3) bad("q", "must be a 3-d fp16 or bf16 tensor");
+    const int64_t rows = q.size(0), hq = q.size(1), d = q.size(2);
+    want(a[0], "q", type, device, {rows, hq, d});
+    const auto& k = want(a[1], "k", type, device, {-1, -1, d});
+    const int64_t keys = k.size(0), hkv = k.size(1);
+    const auto& v = want(a[2], "v", type, device, {keys, hkv, d});
+    const auto& cu_q = want(a[3], "cu_seqlens_q", at::kInt, device, {-1});
+    const int64_t B = cu_q.numel() - 1;
+    if (B < 0) bad("cu_seqlens_q", "must not be empty");
+    const auto& cu_k = want(a[4], "cu_seqlens_k", at::kInt, device, {B + 1});
+    const int32_t* lens =
+        a[7] == Py_None ? nullptr : ptr<int32_t>(want(a[7], "seqlens_k", at::kInt, device, {B}));
+    double scale = 0;
+    if (a[9] == Py_None) {
+      scale = 1.0 / std::sqrt((double)d);
+    } else {
+      scale = PyFloat_AsDouble(a[9]);
+      if (scale == -1.0 && PyErr_Occurred()) throw PythonError();
+    }
+    float* lse = a[11] == Py_None ? nullptr : dense<float>(a[11], "lse", at::kFloat, device, {hq, rows});
+    const auto& out = want(a[10], "out", type, device, {rows, hq, d});
+    if (!out.is_contiguous()) bad("out", "must be contiguous");
+    const c10::cuda::CUDAGuard guard(device);
+    return unlocked(
+        g_entries.cross, q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), k.stride(0),
+        k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), ptr<int32_t>(cu_q), ptr<int32_t>(cu_k),
+        lens, flags_of(a[8], "key_mask", device, {keys}), size_of(B, "the batch"),
+        size_of(rows, "q"), size_of(keys, "k"), int_of(a[5], "max_seqlen_q"),
+        int_of(a[6], "max_seqlen_k"), size_of(hq, "q"), size_of(hkv, "k"), size_of(d, "q"),
+        (float)scale, out.data_ptr(), lse, err_of(a[12], device), dtype, stream_of(device));
+  });
+}
+
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
 PyCFunction as_method() {
   return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(F));
@@ -384,6 +552,10 @@ PyMethodDef g_methods[] = {
     {"release_pages", as_method<release_pages>(), METH_FASTCALL, nullptr},
     {"rotary_append_varlen", as_method<rotary_append_varlen>(), METH_FASTCALL, nullptr},
     {"fwd_varlen_e4m3", as_method<fwd_varlen_e4m3>(), METH_FASTCALL, nullptr},
+    {"beam_select", as_method<beam_select>(), METH_FASTCALL, nullptr},
+    {"beam_reorder", as_method<beam_reorder>(), METH_FASTCALL, nullptr},
+    {"copy_pages", as_method<copy_pages>(), METH_FASTCALL, nullptr},
+    {"fwd_cross", as_method<fwd_cross>(), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};

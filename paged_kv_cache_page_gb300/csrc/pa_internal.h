@@ -125,6 +125,27 @@ int num_sms();
 // Lets `kernel` use `bytes` of dynamic shared memory on the current device;
 // `devices` remembers (a bit each) where that has been done.
 cudaError_t allow_shared(const void* kernel, int bytes, std::atomic<uint64_t>* devices);
+// Whether the device schedules clusters of more than 8 CTAs of the kernel
+// (sizes that are not portable); asked once a device.
+template <typename K>
+bool wide_clusters(K kernel, const cudaLaunchConfig_t& cfg, std::atomic<uint64_t>* asked,
+                   std::atomic<uint64_t>* wide) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return false;
+  const uint64_t bit = uint64_t(1) << dev;
+  if ((asked->load(std::memory_order_acquire) & bit) == 0) {
+    int n = 0;
+    const bool ok =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
+            cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0;
+    if (!ok) cudaGetLastError();  // (not an error of the call's)
+    if (ok) wide->fetch_or(bit, std::memory_order_relaxed);
+    asked->fetch_or(bit, std::memory_order_release);
+  }
+  return (wide->load(std::memory_order_relaxed) & bit) != 0;
+}
+
 bool encode_cache_map(CUtensorMap* map, const void* base, int dtype, int D, int Hkv, int64_t dim2,
                       int64_t dim3, int64_t stride_h, int64_t stride_t, int64_t stride_b,
                       int box_d, int box_rows, bool swizzle128);

@@ -372,27 +372,6 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const ReleaseParams p
   if (tid == 0) *p.free_count_out = free_now + kept;
 }
 
-// Whether the device schedules clusters of more than 8 CTAs of the kernel
-// (sizes that are not portable); asked once a device.
-template <typename K>
-bool wide_clusters(K kernel, const cudaLaunchConfig_t& cfg, std::atomic<uint64_t>* asked,
-                   std::atomic<uint64_t>* wide) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return false;
-  const uint64_t bit = uint64_t(1) << dev;
-  if ((asked->load(std::memory_order_acquire) & bit) == 0) {
-    int n = 0;
-    const bool ok =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
-            cudaSuccess &&
-        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0;
-    if (!ok) cudaGetLastError();  // (not an error of the call's)
-    if (ok) wide->fetch_or(bit, std::memory_order_relaxed);
-    asked->fetch_or(bit, std::memory_order_release);
-  }
-  return (wide->load(std::memory_order_relaxed) & bit) != 0;
-}
-
 // `entry_bytes`: of shared memory for each entry of the batch.
 template <typename P>
 cudaError_t launch_cluster(void (*kernel)(P), const P& p, long long items, int entry_bytes,
