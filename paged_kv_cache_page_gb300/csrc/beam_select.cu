@@ -7,14 +7,16 @@
 // k * V + v first among equal ones.  exp is taken as 2^(x log2(e) - n) against
 // a whole number n, so that sums under different references are brought
 // together by exact powers of two; log2(e) is a sum of two fp32 values, which
-// leaves one rounding of the exponent.  lse and the scores of the candidates
-// are in 64 bits: next to the border candidates of different beams lie so close
-// that 32 bits would often choose another one.
+// leaves one rounding of the exponent.  Next to the border candidates of
+// different beams lie so close that 32 bits would often choose another one: the
+// sums of a row's parts and its logarithm (ln f = 2 atanh((f - 1) / (f + 1)))
+// are in pairs of fp32 values, the candidates' scores in 64 bits.  (FP64 is slow
+// here: log() of a double took 5500 cycles, the pairs take 700.)
 //
-// One pass over the logits.  A lane reads its elements once, in registers: their
-// maximum, then their sum.  Only the maxima are kept (one in 64 or more
-// elements, in shared memory).  The N largest elements lie in blocks whose
-// maximum is among the N largest maxima, so a bound found from the maxima
+// One pass over the logits, 4 KB of a warp on their way while it computes with the
+// 4 KB before.  A lane finds the maximum of its elements, then their sum.  Only the
+// maxima are kept (one of 32 or more elements, in shared memory).  The N largest elements lie in blocks
+// whose maximum is among the N largest maxima, so a bound found from the maxima
 // leaves a few dozen blocks, whose elements are read once more (from L2) and
 // ranked.  Where more elements than fit pass the bound (many equal logits), the
 // N best are found one after the other.
@@ -38,15 +40,18 @@ int set_error(int code, const char* fmt, ...);
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kCtasPerSm = 2;
 constexpr int kVecs = 8;           // 16-byte vectors of a lane in a step
+constexpr int kStepVecs = 32 * kVecs;
 constexpr int kMaxBeams = 32;
 constexpr int kMaxOut = 64;
 constexpr int kParts = 64;         // of the block maxima: the N-th largest of their maxima is the bound
 constexpr int kMaxCandidates = 1024;
 constexpr int kMaxCluster = 16;
-constexpr int kMaxUnits = 320;     // of a CTA: 40 KB of block maxima
+constexpr int kMaxUnits = 64;      // of a CTA
+constexpr uint32_t kAll = 0xffffffffu;
 
 constexpr float kLog2eHi = 1.44269502163f;  // log2(e) to fp32, and what is missing
 constexpr float kLog2eLo = 1.92596299e-8f;
@@ -59,7 +64,7 @@ struct SelectParams {
   const uint8_t* finished;
   int end_token;
   int B, K, V, N;
-  int steps;      // steps of kVecs vectors in a unit
+  int steps;      // steps of kStepVecs vectors in a unit
   int row_units;  // units of a row
   float* scores_out;
   int32_t* parents;
@@ -99,11 +104,96 @@ struct Logits {
       }
     }
   }
-  static __device__ __forceinline__ float one(const T* p) {
-    if constexpr (std::is_same<T, float>::value) return __ldg(p);
-    else return (float)*p;
+  // The largest of a lane's vectors (NaN does not count).
+  static __device__ __forceinline__ float largest(const uint4 (&v)[kVecs]) {
+    if constexpr (std::is_same<T, float>::value) {
+      float m = neg_inf();
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j)
+        m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(v[j].x), __uint_as_float(v[j].y)),
+                           fmaxf(__uint_as_float(v[j].z), __uint_as_float(v[j].w))));
+      return m;
+    } else {
+      using T2 = typename Elem<T>::T2;
+      auto as = [](uint32_t u) { return *reinterpret_cast<T2*>(&u); };
+      T2 m = as(v[0].x);
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j)
+        m = __hmax2(m, __hmax2(__hmax2(as(v[j].x), as(v[j].y)), __hmax2(as(v[j].z), as(v[j].w))));
+      const float2 f = Elem<T>::to_f2(*reinterpret_cast<uint32_t*>(&m));
+      return fmaxf(f.x, f.y);
+    }
+  }
+  static __device__ __forceinline__ float one(const T* p) { return (float)*p; }
+  // A first word whose first value is *p, the others -inf.
+  static __device__ __forceinline__ uint32_t alone(const T* p) {
+    if constexpr (std::is_same<T, float>::value) return __float_as_uint(*p);
+    else return (none().x & 0xffff0000u) | *reinterpret_cast<const uint16_t*>(p);
   }
 };
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)),
+        "l"(reinterpret_cast<uint64_t&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return d;
+}
+
+// A sum in a pair of fp32 values (the second is what the first lacks), times
+// 2^n.
+struct Sum {
+  float n, hi, lo;
+};
+constexpr float kNothing = -3e38f;  // the reference where there is nothing but -inf
+// 2^d for a whole d <= 0 (0 below the normal range).
+__device__ __forceinline__ float pow2_whole(float d) {
+  return d < -126.f ? 0.f : __int_as_float((127 + (int)d) << 23);
+}
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll 1
+  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(kAll, x, o));
+  return x;
+}
+// Over the warp, the same in every lane (x + y and what it lacks do not depend
+// on their order).
+__device__ __noinline__ Sum warp_total(Sum s) {
+  const float n = warp_max(s.n), f = pow2_whole(s.n - n);
+  float hi = s.hi * f, lo = s.lo * f;
+#pragma unroll 1
+  for (int o = 16; o > 0; o >>= 1) {
+    const float y = __shfl_xor_sync(kAll, hi, o), z = __shfl_xor_sync(kAll, lo, o);
+    const float t = hi + y, u = t - hi;
+    const float e = ((hi - (t - u)) + (y - u)) + (lo + z);
+    hi = t + e;
+    lo = e - (hi - t);
+  }
+  return {n, hi, lo};
+}
+// ln(s), s positive and finite.
+__device__ __forceinline__ double ln_of(const Sum& s) {
+  // s = 2^e f with f in [0.7, 1.42)
+  const int bits = __float_as_int(s.hi);
+  const int e = (bits - 0x3f350000) >> 23;
+  const float down = __int_as_float((127 - e) << 23);
+  const float f = s.hi * down, g = s.lo * down;
+  const float num = f - 1.f, den = f + 1.f;  // num is exact
+  const float den_lo = (1.f - (den - f)) + g;
+  const float q = __fdividef(num, den);  // (what it lacks is in r)
+  const float r = __fdividef(fmaf(-q, den, num) + (g - q * den_lo), den);
+  const float z = q * q;
+  const float t = fmaf(fmaf(fmaf(fmaf(z, 1.f / 11, 1.f / 9), z, 1.f / 7), z, 1.f / 5), z, 1.f / 3);
+  return ((double)s.n + e) * kLn2d + (2.0 * (double)q + (double)(2.f * (r + q * z * t)));
+}
 
 // Larger is better; a score's order as a whole number (+0 and -0 alike).
 __device__ __forceinline__ long long order_of(double s) {
@@ -113,59 +203,85 @@ __device__ __forceinline__ long long order_of(double s) {
 __device__ __forceinline__ double score_of(long long k) {
   return __longlong_as_double(k ^ ((k >> 63) & 0x7fffffffffffffffll));
 }
-struct Candidate {
+struct __align__(16) Candidate {
   long long key;
-  int flat;  // k * V + v; < 0: none
-  int pad;
+  int flat, k;  // k * V + v, and k
 };
-__device__ __forceinline__ bool better(long long ka, int fa, long long kb, int fb) {
-  return ka > kb || (ka == kb && fa < fb);
+constexpr long long kNoKey = -0x7fffffffffffffffll - 1;  // (behind every score's)
+__device__ __forceinline__ bool better(const Candidate& a, const Candidate& b) {
+  return a.key > b.key || (a.key == b.key && a.flat < b.flat);
+}
+// How many of list[0 .. n) are better than c; four neighbouring lanes share a
+// candidate.
+__device__ __noinline__ int rank_of(const Candidate c, const Candidate* list, int n) {
+  int above = 0;
+#pragma unroll 2
+  for (int j = threadIdx.x & 3; j < n; j += 4) above += better(list[j], c);
+  above += __shfl_xor_sync(kAll, above, 1);
+  return above + __shfl_xor_sync(kAll, above, 2);
 }
 
-// 2^d for a whole d <= 0 (0 below the normal range).
-__device__ __forceinline__ float pow2_whole(float d) {
-  return d < -126.f ? 0.f : __int_as_float((127 + (int)d) << 23);
-}
-
-// The shape of row k in vectors: `head` elements in front of the first whole
-// vector, `vecs` whole ones, `tail` elements behind them.
+// A living row in vectors: `head` elements in front of the first whole vector,
+// `vecs` whole ones, `tail` elements behind them.
 template <typename T>
 struct Row {
   const T* p;
-  int head, vecs, tail;
-  __device__ __forceinline__ Row(const SelectParams& a, int b, int k) {
+  int k, head, vecs, tail;
+  __device__ __forceinline__ Row(const SelectParams& a, int b, int k) : k(k) {
     p = reinterpret_cast<const T*>(a.logits) + b * a.stride_b + k * a.stride_k;
     const int off = (int)((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
     constexpr int per = Logits<T>::kPer;
-    head = min((per - off) % per, a.V);
+    head = min((per - off) & (per - 1), a.V);
     vecs = (a.V - head) / per;
     tail = a.V - head - vecs * per;
+  }
+  __device__ __forceinline__ const uint4* vec() const {
+    return reinterpret_cast<const uint4*>(p + head);
   }
   // element number of the lane's extra element (lanes 0 .. head + tail - 1 of
   // the row's first unit have one), or -1
   __device__ __forceinline__ int extra(int lane) const {
-    return lane < head ? lane : lane < head + tail ? head + vecs * Logits<T>::kPer + lane - head : -1;
+    return lane < head ? lane : lane < head + tail ? vecs * Logits<T>::kPer + lane : -1;
   }
 };
 
+struct SelectShared {
+  uint8_t row[kMaxBeams * 32];                // Row of each living beam
+  float max[kMaxUnits * 32];                  // block maxima
+  float unit_n[kMaxUnits], unit_s[kMaxUnits];
+  int unit_at[kMaxUnits];                     // a unit's first vector
+  uint8_t unit_r[kMaxUnits];                  // and its row
+  float4 rows[kMaxCluster][kMaxBeams];        // every CTA's sums of every row
+  double base[kMaxBeams];
+  float base32[kMaxBeams];
+  int parts[kParts / 32][kMaxBeams][32];      // maxima of the even and the odd units of every row
+  Candidate cand[kMaxCandidates];
+  Candidate lists[kMaxCluster * kMaxOut];     // of every CTA, in order (CTA 0's are used)
+  int list_count[kMaxCluster];
+  Candidate warp_best[kWarps];
+  uint16_t list[kMaxUnits * 32];              // blocks that pass the bound
+  int blocks, count;
+};
+static_assert(kCtasPerSm * (sizeof(SelectShared) + 1024) <= 228 << 10, "resident together");
+
+// An fp32 value's order as a whole number.
+__device__ __forceinline__ int order32(float x) {
+  const int i = __float_as_int(x);
+  return i ^ ((i >> 31) & 0x7fffffff);
+}
+
+__device__ __forceinline__ float value32(int i) {
+  return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) select_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) select_kernel(const SelectParams p) {
   using L = Logits<T>;
   constexpr int per = L::kPer;
-  extern __shared__ float s_max[];  // [units of the CTA][32] block maxima
-  __shared__ float s_unit_n[kMaxUnits], s_unit_s[kMaxUnits];
-  __shared__ float s_row_n[kMaxCluster][kMaxBeams];   // every CTA's sums of every row
-  __shared__ double s_row_s[kMaxCluster][kMaxBeams];
-  __shared__ double s_base[kMaxBeams];
-  __shared__ float s_base32[kMaxBeams];
-  __shared__ int s_live[kMaxBeams];
-  __shared__ float s_part[kParts];
-  __shared__ float s_bound;
-  __shared__ int s_blocks, s_count;
-  __shared__ uint16_t s_list[kMaxUnits * 32];  // blocks that pass the bound
-  __shared__ Candidate s_cand[kMaxCandidates + kMaxBeams];
-  __shared__ Candidate s_best[kMaxOut];
-  __shared__ Candidate s_warp[kWarps];
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  SelectShared& sm = *reinterpret_cast<SelectShared*>(smem_raw);
+  Row<T>* const rows = reinterpret_cast<Row<T>*>(sm.row);
+  static_assert(sizeof(Row<T>) <= 32, "a row's place");
 
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
@@ -180,294 +296,354 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const SelectParams 
     done = p.finished != nullptr && p.finished[(int64_t)b * p.K + lane] != 0;
   }
   const bool scored = isfinite(cum);
-  const uint32_t live_mask = __ballot_sync(0xffffffffu, scored && !done);
-  const uint32_t done_mask = __ballot_sync(0xffffffffu, scored && done);
+  const uint32_t live_mask = __ballot_sync(kAll, scored && !done);
+  const uint32_t done_mask = __ballot_sync(kAll, scored && done);
   const int live = __popc(live_mask);
-  if (warp == 0 && scored && !done) s_live[__popc(live_mask & ((1u << lane) - 1))] = lane;
-  if (tid == 0) s_blocks = s_count = 0;
+  if (warp == 0) {
+    if (scored && !done) rows[__popc(live_mask & ((1u << lane) - 1))] = Row<T>(p, b, lane);
+    if (lane == 0) sm.blocks = sm.count = 0;
+  }
+  for (int r = warp; r < p.K; r += kWarps)
+    sm.parts[0][r][lane] = sm.parts[1][r][lane] = order32(neg_inf());
   __syncthreads();
   cluster_arrive();  // (the others' shared memory is written once they have started)
 
-  // units [u0, u1) of every row are this CTA's: unit i * live + r is number
-  // u0 + i of living row r
+  // units [u0, u1) of every row are this CTA's: its unit i * live + r is number
+  // u0 + i of living row r; a warp takes every kWarps-th, a step at a time
   const int u0 = (int)((int64_t)p.row_units * rank / ranks);
   const int u1 = (int)((int64_t)p.row_units * (rank + 1) / ranks);
   const int units = (u1 - u0) * live;
-  const int unit_vecs = p.steps * kVecs * 32;
-
-  for (int u = warp; u < units; u += kWarps) {
-    const int i = u / live, r = u - i * live;
-    const Row<T> row(p, b, s_live[r]);
-    const uint4* vec = reinterpret_cast<const uint4*>(row.p + row.head);
-    float top = neg_inf(), n = 0.f, sum = 0.f;
-    for (int s = 0; s < p.steps; ++s) {
-      const int at = (u0 + i) * unit_vecs + s * kVecs * 32 + lane;
-      uint4 v[kVecs];
+  struct Place {  // of a step: unit, row, unit in the row, first vector of the step, step in the unit
+    int u, r, i, at, s;
+  };
+  const int row_step = p.steps * kStepVecs;
+  auto settle = [&](Place& x) {  // a row behind the last one: the next unit of an earlier one
+    while (x.r >= live) {
+      x.r -= live;
+      x.at += row_step;
+      ++x.i;
+    }
+  };
+  auto advance = [&](Place& x) {
+    x.at += kStepVecs;
+    if (++x.s < p.steps) return;
+    x.s = 0;
+    x.at -= row_step;
+    x.u += kWarps;
+    x.r += kWarps;
+    settle(x);
+  };
+  Place now = {warp, warp, 0, u0 * row_step, 0};
+  if (units > 0) settle(now);
+  Place next = now;
+  // the next step's vectors are on their way while a step is computed
+  auto load = [&](uint4 (&v)[kVecs]) {
+    if (next.u >= units) return;
+    const Row<T>& row = rows[next.r];
+    const uint4* from = row.vec() + next.at + lane;
+    const int left = row.vecs - next.at - lane;
+    if (left + lane >= kStepVecs) {
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j) v[j] = load16(from + j * 32);
+    } else {
 #pragma unroll
       for (int j = 0; j < kVecs; ++j) {
         v[j] = L::none();
-        if (at + j * 32 < row.vecs) v[j] = load16(vec + at + j * 32);
+        if (j * 32 < left) v[j] = load16(from + j * 32);
       }
-      float x_extra = neg_inf();
-      if (s == 0 && u0 + i == 0) {
-        const int e = row.extra(lane);
-        if (e >= 0) x_extra = L::one(row.p + e);
-      }
-      float m = x_extra;
-#pragma unroll
-      for (int j = 0; j < kVecs; ++j) {
-        float f[per];
-        L::expand(v[j], f);
-#pragma unroll
-        for (int c = 0; c < per; ++c) m = fmaxf(m, f[c]);
-      }
-      const float was = top;
-      top = fmaxf(top, m);
-      const float ref = top == neg_inf() ? 0.f : rintf(top * kLog2eHi);
-      if (was != neg_inf()) sum *= pow2_whole(n - ref);
-      n = ref;
-      auto add = [&](float x) { sum += ex2(fmaf(x, kLog2eLo, fmaf(x, kLog2eHi, -n))); };
-#pragma unroll
-      for (int j = 0; j < kVecs; ++j) {
-        float f[per];
-        L::expand(v[j], f);
-#pragma unroll
-        for (int c = 0; c < per; ++c) add(f[c]);
-      }
-      add(x_extra);
     }
-    s_max[u * 32 + lane] = top;
-    // the unit's sum, under the largest of the lanes' references (a lane that
-    // holds nothing but -inf has a sum of zero or NaN)
-    float un = top == neg_inf() ? neg_inf() : n;
+    advance(next);
+  };
+  float top = neg_inf(), n = kNothing, sum = 0.f;
+  auto compute = [&](const uint4 (&v)[kVecs]) {
+    float x_extra = neg_inf();
+    if (now.at == 0) {
+      const int e = rows[now.r].extra(lane);
+      if (e >= 0) x_extra = L::one(rows[now.r].p + e);
+    }
+    top = fmaxf(top, fmaxf(L::largest(v), x_extra));
+    const float ref = fmaxf(rintf(top * kLog2eHi), kNothing);
+    sum *= pow2_whole(n - ref);
+    n = ref;
+    const float2 hi = make_float2(kLog2eHi, kLog2eHi), lo = make_float2(kLog2eLo, kLog2eLo);
+    const float2 minus = make_float2(-n, -n);
+    float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) un = fmaxf(un, __shfl_xor_sync(0xffffffffu, un, o));
-    if (un != neg_inf() && top != neg_inf()) sum *= pow2_whole(n - un);
+    for (int j = 0; j < kVecs; ++j) {
+      float f[per];
+      L::expand(v[j], f);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      for (int c = 0; c < per; c += 2) {
+        const float2 x = make_float2(f[c], f[c + 1]);
+        const float2 t = fma2(x, lo, fma2(x, hi, minus));
+        acc[c / 2 & 1] = add2(acc[c / 2 & 1], make_float2(ex2(t.x), ex2(t.y)));
+      }
+    }
+    const float2 both = add2(acc[0], acc[1]);
+    sum += both.x + both.y;
+    if (now.at == 0) sum += ex2(fmaf(x_extra, kLog2eLo, fmaf(x_extra, kLog2eHi, -n)));
+    const int u = now.u, r = now.r, odd = now.i & 1, at = now.at - now.s * kStepVecs;
+    advance(now);
+    if (now.u == u) return;
+    // the unit's maxima, and its sum under the largest of the lanes' references
+    sm.max[u * 32 + lane] = top;
+    atomicMax(&sm.parts[odd][r][lane], order32(top));
+    const float un = warp_max(n);
+    sum *= pow2_whole(n - un);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
     if (lane == 0) {
-      s_unit_n[u] = un;
-      s_unit_s[u] = sum;
+      sm.unit_n[u] = un;
+      sm.unit_s[u] = sum;
+      sm.unit_at[u] = at;
+      sm.unit_r[u] = (uint8_t)r;
+    }
+    top = neg_inf();
+    n = kNothing;
+    sum = 0.f;
+  };
+  {
+    uint4 v[kVecs], w[kVecs];
+    load(v);
+#pragma unroll 1
+    while (now.u < units) {
+      load(w);
+      compute(v);
+      if (now.u >= units) break;
+      load(v);
+      compute(w);
     }
   }
   __syncthreads();
 
   // rows: this CTA's sums, given to every CTA of the cluster
   cluster_wait();
+#pragma unroll 1
   for (int r = warp; r < live; r += kWarps) {
-    float rn = neg_inf();
-    for (int i = lane; i < u1 - u0; i += 32) rn = fmaxf(rn, s_unit_n[i * live + r]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) rn = fmaxf(rn, __shfl_xor_sync(0xffffffffu, rn, o));
-    double rs = 0;
-    for (int i = lane; i < u1 - u0; i += 32) {
-      const float un = s_unit_n[i * live + r];
-      const float f = un == neg_inf() ? 1.f : pow2_whole(un - rn);
-      rs += (double)(s_unit_s[i * live + r] * f);
+    Sum s = {kNothing, 0.f, 0.f};
+    // (at most two units a lane)
+#pragma unroll 1
+    for (int u = lane * live + r; u < units; u += 32 * live) {
+      const float n = sm.unit_n[u], m = fmaxf(n, s.n);
+      const float x = s.hi * pow2_whole(s.n - m), y = sm.unit_s[u] * pow2_whole(n - m);
+      const float t = x + y;
+      s = {m, t, (x - (t - (t - x))) + (y - (t - x))};
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) rs += __shfl_xor_sync(0xffffffffu, rs, o);
-    if (lane < ranks) {
-      *cluster.map_shared_rank(&s_row_n[rank][r], lane) = rn;
-      *cluster.map_shared_rank(&s_row_s[rank][r], lane) = rs;
-    }
+    s = warp_total(s);
+    if (lane < ranks)
+      *cluster.map_shared_rank(&sm.rows[rank][r], lane) = make_float4(s.n, s.hi, s.lo, 0.f);
   }
   cluster.sync();
-  if (warp == 0 && lane < live) {
-    float rn = neg_inf();
-    for (int c = 0; c < ranks; ++c) rn = fmaxf(rn, s_row_n[c][lane]);
-    double rs = 0;
-    for (int c = 0; c < ranks; ++c) {
-      const float cn = s_row_n[c][lane];
-      rs += s_row_s[c][lane] * (double)(cn == neg_inf() ? 1.f : pow2_whole(cn - rn));
+#pragma unroll 1
+  for (int r = warp; r < live; r += kWarps) {
+    Sum s = {kNothing, 0.f, 0.f};
+    if (lane < ranks) {
+      const float4 f = sm.rows[lane][r];
+      s = {f.x, f.y, f.z};
     }
-    const int k = s_live[lane];
-    // a row without a distribution (NaN or +inf in it, or nothing but -inf) has no candidates
-    double base = -INFINITY;
-    if (rs > 0 && isfinite(rs) && isfinite(rn))
-      base = (double)p.scores[(int64_t)b * p.K + k] - ((double)rn * kLn2d + log(rs));
-    else if (rank == 0 && (rn != neg_inf() || rs != 0))
-      report(p.err, PA_DEVERR_VALUE, b * p.K + k, 0);
-    s_base[lane] = base;
-    s_base32[lane] = (float)base;
+    s = warp_total(s);
+    const float row_cum = __shfl_sync(kAll, cum, rows[r].k);
+    if (lane == 0) {
+      // a row without a distribution (NaN or +inf in it, or nothing but -inf) has no candidates
+      double base = -INFINITY;
+      if (s.hi > 0.f && isfinite(s.hi) && isfinite(s.n)) base = (double)row_cum - ln_of(s);
+      else if (rank == 0 && s.hi != 0.f) report(p.err, PA_DEVERR_VALUE, b * p.K + rows[r].k, 0);
+      sm.base[r] = base;
+      sm.base32[r] = (float)base;
+    }
   }
   __syncthreads();
 
-  // the bound: N-th largest of the maxima of kParts parts of the blocks
-  const int blocks = units * 32;
-  auto block_score = [&](int blk) {
-    const int u = blk >> 5;
-    return s_base32[u - u / live * live] + s_max[blk];
-  };
+  // The bound: the N-th largest of the maxima of kParts parts of the blocks.  A
+  // part has blocks of every row (the best beam may be far ahead of the others).
+  float bound = neg_inf();
   {
-    float m = neg_inf();
-    for (int i = tid; i < blocks; i += kThreads) {
-      const float s = block_score(i);
-      m = fmaxf(m, s);
+    float size = 0.f, part[2] = {neg_inf(), neg_inf()};
+#pragma unroll 1
+    for (int r = 0; r < live; ++r) {
+      const float base = sm.base32[r];
+      if (base == neg_inf()) continue;
+      size = fmaxf(size, fabsf(base));
+      part[0] = fmaxf(part[0], base + value32(sm.parts[0][r][lane]));
+      part[1] = fmaxf(part[1], base + value32(sm.parts[1][r][lane]));
     }
-    constexpr int each = kThreads / kParts;
-#pragma unroll
-    for (int o = each / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (tid % each == 0) s_part[tid / each] = m;
-  }
-  __syncthreads();
-  if (tid < kParts) {
-    const float m = s_part[tid];
-    int above = 0;
-    for (int i = 0; i < kParts; ++i) above += s_part[i] > m || (s_part[i] == m && i < tid);
-    if (above == p.N - 1) {
-      // fp32 scores are off by 2^-24 of the base and of the sum; the N-th best
-      // element and the blocks that bound it each once
-      float size = fabsf(m);
-      for (int r = 0; r < live; ++r)
-        if (s_base32[r] > neg_inf()) size = fmaxf(size, fabsf(s_base32[r]));
-      s_bound = m - size * 0x1p-21f;
+    int even = order32(part[0]), odd = order32(part[1]), top = order32(neg_inf());
+    // the largest ones, one value after the other, until N parts have gone
+#pragma unroll 1
+    for (int gone = 0; gone < p.N;) {
+      top = __reduce_max_sync(kAll, max(even, odd));
+      if (top <= order32(neg_inf())) break;
+      gone += __popc(__ballot_sync(kAll, even == top)) + __popc(__ballot_sync(kAll, odd == top));
+      if (even == top) even = order32(neg_inf());
+      if (odd == top) odd = order32(neg_inf());
     }
+    bound = value32(top);
+    // fp32 scores are off by 2^-24 of the base and of the sum; the N-th best
+    // element and the blocks that bound it each once
+    bound -= fmaxf(size, fabsf(bound)) * 0x1p-21f;
   }
-  __syncthreads();
-  const float bound = s_bound;
   // (a score of -inf: nothing to choose, or a row without a distribution)
   auto passes = [&](float s) { return s > neg_inf() && s >= bound; };
-  for (int i = tid; i < blocks; i += kThreads)
-    if (passes(block_score(i))) s_list[atomicAdd(&s_blocks, 1)] = (uint16_t)i;
+#pragma unroll 1
+  for (int u = warp; u < units; u += kWarps)
+    if (passes(sm.base32[sm.unit_r[u]] + sm.max[u * 32 + lane]))
+      sm.list[atomicAdd(&sm.blocks, 1)] = (uint16_t)(u * 32 + lane);
   __syncthreads();
 
-  // elements of these blocks, one vector a thread
+  // elements of these blocks: eight lanes a block, one vector each at a time
   const int per_block = p.steps * kVecs + 1;
-  auto take = [&](int r, float x, int e) {
-    if (!passes(s_base32[r] + x)) return;
-    const int at = atomicAdd(&s_count, 1);
-    if (at < kMaxCandidates)
-      s_cand[at] = {order_of(s_base[r] + (double)x), s_live[r] * p.V + e, 0};
-  };
-  // every element of vector j (the last one: the extra element) of a block
-  auto each_of = [&](int blk, int j, auto&& f) {
-    const int u = blk >> 5, l = blk & 31, i = u / live, r = u - i * live;
-    const Row<T> row(p, b, s_live[r]);
-    if (j == per_block - 1) {
-      const int e = u0 + i == 0 ? row.extra(l) : -1;
-      if (e >= 0) f(r, L::one(row.p + e), e);
-      return;
-    }
-    const int at = (u0 + i) * unit_vecs + j * 32 + l;
-    if (at >= row.vecs) return;
-    const uint4 v = load16(reinterpret_cast<const uint4*>(row.p + row.head) + at);
-    float x[per];
-    L::expand(v, x);
+  auto each_element = [&](auto&& f) {  // f(row, element, logit)
+#pragma unroll 1
+    for (int i = tid >> 3; i < sm.blocks; i += kThreads / 8) {
+      const int blk = sm.list[i], u = blk >> 5, l = blk & 31, r = sm.unit_r[u], at = sm.unit_at[u];
+      const Row<T>& row = rows[r];
+      const float base = sm.base32[r];
+#pragma unroll 1
+      for (int j = tid & 7; j < per_block; j += 8) {
+        uint4 v = L::none();
+        int e = row.head + (at + j * 32 + l) * per;
+        if (j == per_block - 1) {  // the extra element
+          e = at == 0 ? row.extra(l) : -1;
+          if (e >= 0) v.x = L::alone(row.p + e);
+        } else if (at + j * 32 + l < row.vecs) {
+          v = load16(row.vec() + at + j * 32 + l);
+        }
+        float x[per];
+        L::expand(v, x);
+        uint32_t in = 0;
 #pragma unroll
-    for (int c = 0; c < per; ++c) f(r, x[c], row.head + at * per + c);
+        for (int c = 0; c < per; ++c) in |= passes(base + x[c]) ? 1u << c : 0u;
+        for (; in != 0; in &= in - 1) {
+          const int c = __ffs((int)in) - 1;
+          f(r, e + c, L::one(row.p + e + c));
+        }
+      }
+    }
   };
-  for (int w = tid; w < s_blocks * per_block; w += kThreads)
-    each_of(s_list[w / per_block], w % per_block, take);
+  auto candidate = [&](int r, int e, float x) {
+    return Candidate{order_of(sm.base[r] + (double)x), rows[r].k * p.V + e, rows[r].k};
+  };
+  each_element([&](int r, int e, float x) {
+    const int at = atomicAdd(&sm.count, 1);
+    if (at < kMaxCandidates) sm.cand[at] = candidate(r, e, x);
+  });
   __syncthreads();
 
-  int count = s_count;
+  // the CTA's best, in order, to CTA 0
+  Candidate* const lists = cluster.map_shared_rank(sm.lists, 0) + rank * p.N;
+  const int count = sm.count;
   if (count <= kMaxCandidates) {
-    if (tid < p.N) s_best[tid] = {0, -1, 0};
-    __syncthreads();
-    for (int i = tid; i < count; i += kThreads) {
-      const Candidate c = s_cand[i];
-      int above = 0;
-      for (int j = 0; j < count && above < p.N; ++j)
-        above += better(s_cand[j].key, s_cand[j].flat, c.key, c.flat);
-      if (above < p.N) s_best[above] = c;
+#pragma unroll 1
+    for (int i0 = 0; i0 < count; i0 += kThreads / 4) {
+      const int i = i0 + tid / 4;
+      const Candidate c = sm.cand[min(i, count - 1)];
+      const int above = rank_of(c, sm.cand, count);
+      if (i < count && above < p.N && (tid & 3) == 0) lists[above] = c;
     }
   } else {
     // too many: the best one behind the last one found, N times
     Candidate last = {0x7fffffffffffffffll, -1, 0};
     for (int out = 0; out < p.N; ++out) {
-      Candidate best = {0, -1, 0};
-      auto look = [&](int r, float x, int e) {
-        if (!passes(s_base32[r] + x)) return;
-        const long long key = order_of(s_base[r] + (double)x);
-        const int flat = s_live[r] * p.V + e;
-        if (!better(last.key, last.flat, key, flat)) return;
-        if (best.flat < 0 || better(key, flat, best.key, best.flat)) best = {key, flat, 0};
-      };
-      for (int w = tid; w < s_blocks * per_block; w += kThreads)
-        each_of(s_list[w / per_block], w % per_block, look);
+      Candidate best = {kNoKey, 0x7fffffff, 0};
+      each_element([&](int r, int e, float x) {
+        const Candidate c = candidate(r, e, x);
+        if (better(last, c) && better(c, best)) best = c;
+      });
       auto fold = [&](int o) {
-        const long long key = __shfl_xor_sync(0xffffffffu, best.key, o);
-        const int flat = __shfl_xor_sync(0xffffffffu, best.flat, o);
-        if (flat >= 0 && (best.flat < 0 || better(key, flat, best.key, best.flat)))
-          best = {key, flat, 0};
+        const Candidate c = {__shfl_xor_sync(kAll, best.key, o), __shfl_xor_sync(kAll, best.flat, o),
+                             __shfl_xor_sync(kAll, best.k, o)};
+        if (better(c, best)) best = c;
       };
-#pragma unroll
       for (int o = 16; o > 0; o >>= 1) fold(o);
-      if (lane == 0) s_warp[warp] = best;
+      if (lane == 0) sm.warp_best[warp] = best;
       __syncthreads();
-      best = lane < kWarps ? s_warp[lane] : Candidate{0, -1, 0};
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) fold(o);
-      if (tid == 0) s_best[out] = best;
-      last = best;
+      best = sm.warp_best[lane % kWarps];
+      for (int o = kWarps / 2; o > 0; o >>= 1) fold(o);
+      if (tid == 0) lists[out] = best;
+      last = best;  // (more than kMaxCandidates pass, so there is one)
       __syncthreads();
-      if (best.flat < 0) {  // (uniform) nothing is left
-        for (int i = out + 1 + tid; i < p.N; i += kThreads) s_best[i] = best;
-        break;
-      }
     }
   }
-  cluster.sync();  // every CTA's best; and the candidates of CTA 0 are no longer read
-
-  if (rank == 0) {
-    // the lists of all CTAs, and one candidate of each finished beam
-    const int all = ranks * p.N;
-    for (int i = tid; i < all; i += kThreads)
-      s_cand[i] = cluster.map_shared_rank(s_best, i / p.N)[i % p.N];
-    if (tid < kMaxBeams) {
-      Candidate c = {0, -1, 0};
-      if (tid < p.K && (done_mask >> tid & 1))
-        c = {order_of((double)cum), tid * p.V + p.end_token, 0};
-      s_cand[all + tid] = c;
-    }
-  }
-  cluster.sync();  // (no CTA leaves while its list is read)
+  if (tid == 0) *cluster.map_shared_rank(&sm.list_count[rank], 0) = min(count, p.N);
+  cluster_arrive();
   if (rank != 0) return;
-  const int all = ranks * p.N + kMaxBeams;
+  cluster_wait();
+
+  // One warp joins the lists: lane c has the first candidate left of CTA c's, and
+  // that of beam c if it is finished; the best of all, N times.
+  if (warp != 0) return;
   const int64_t out0 = (int64_t)b * p.N;
-  int here = 0;
-  for (int i = tid; i < all; i += kThreads) {
-    const Candidate c = s_cand[i];
-    if (c.flat < 0) continue;
-    ++here;
-    int above = 0;
-    for (int j = 0; j < all && above < p.N; ++j)
-      above += s_cand[j].flat >= 0 && better(s_cand[j].key, s_cand[j].flat, c.key, c.flat);
-    if (above >= p.N) continue;
-    const int k = c.flat / p.V, v = c.flat - k * p.V;
-    p.scores_out[out0 + above] = (float)score_of(c.key);
-    p.parents[out0 + above] = k;
-    p.tokens[out0 + above] = v;
-    if (p.finished_out != nullptr)
-      p.finished_out[out0 + above] = v == p.end_token || (done_mask >> k & 1);
+  const Candidate none = {kNoKey, 0x7fffffff, 0};
+  const Candidate* head = sm.lists + lane * p.N;
+  int left = lane < ranks ? sm.list_count[lane] : 0;
+  Candidate a = left > 0 ? *head : none;
+  Candidate f = none;
+  if (done_mask >> lane & 1) f = {order_of((double)cum), lane * p.V + p.end_token, lane};
+#pragma unroll 1
+  for (int out = 0; out < p.N; ++out) {
+    const bool end = better(f, a);
+    const Candidate c = end ? f : a;
+    // the largest key, its high word first, then the lowest place
+    const int hi = (int)(c.key >> 32), top = __reduce_max_sync(kAll, hi);
+    const uint32_t lo = hi == top ? (uint32_t)c.key : 0u, low = __reduce_max_sync(kAll, lo);
+    const int at = hi == top && lo == low ? c.flat : 0x7fffffff;
+    if (at == __reduce_min_sync(kAll, at) && hi == top && lo == low && c.key != kNoKey) {
+      const int v = c.flat - c.k * p.V;
+      p.scores_out[out0 + out] = (float)score_of(c.key);
+      p.parents[out0 + out] = c.k;
+      p.tokens[out0 + out] = v;
+      if (p.finished_out != nullptr)
+        p.finished_out[out0 + out] = v == p.end_token || (done_mask >> c.k & 1);
+      if (end) {
+        f = none;
+      } else {
+        ++head;
+        a = --left > 0 ? *head : none;
+      }
+    } else if (top == (int)(kNoKey >> 32) && low == 0 && lane == 0) {  // nothing is left
+      p.scores_out[out0 + out] = neg_inf();
+      p.parents[out0 + out] = p.tokens[out0 + out] = -1;
+      if (p.finished_out != nullptr) p.finished_out[out0 + out] = 0;
+    }
   }
-  // places without a candidate
-  here = __reduce_add_sync(0xffffffffu, here);
-  if (tid == 0) s_count = 0;
-  __syncthreads();
-  if (lane == 0) atomicAdd(&s_count, here);
-  __syncthreads();
-  for (int i = s_count + tid; i < p.N; i += kThreads) {
-    p.scores_out[out0 + i] = neg_inf();
-    p.parents[out0 + i] = p.tokens[out0 + i] = -1;
-    if (p.finished_out != nullptr) p.finished_out[out0 + i] = 0;
+}
+
+// How many clusters of the configuration's size the device holds at a time; asked
+// once a device and size.
+template <typename K>
+int resident_clusters(K kernel, const cudaLaunchConfig_t& cfg, int size,
+                      std::atomic<int> (*known)[kMaxCluster + 1]) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return size <= 8 ? num_sms() / size : 0;
+  int n = known[dev][size].load(std::memory_order_relaxed);
+  if (n == 0) {
+    // (sizes above 8 are not portable)
+    const bool ok = (size <= 8 || cudaFuncSetAttribute(
+                                      kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
+                                      cudaSuccess) &&
+                    cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess;
+    if (!ok) {
+      cudaGetLastError();  // (not an error of the call's)
+      n = 0;
+    }
+    if (n <= 0) n = -1;
+    known[dev][size].store(n, std::memory_order_relaxed);
   }
+  return n;
 }
 
 template <typename T>
 cudaError_t launch_select(SelectParams p, cudaStream_t st) {
-  static std::atomic<uint64_t> asked{0}, wide{0}, allowed{0};
+  static std::atomic<uint64_t> allowed{0};
+  static std::atomic<int> resident[64][kMaxCluster + 1];  // by device and size; 0: not known
   constexpr int per = 16 / (int)sizeof(T);
   const int vecs = p.V / per + 1;
-  // CTAs of a request: as many as are resident together (two an SM), with a step
-  // of a row for each
-  int ctas = 1;
-  while (ctas < kMaxCluster && (int64_t)p.B * ctas * 2 <= 2 * num_sms() &&
-         (vecs + kVecs * 32 - 1) / (kVecs * 32) >= 2 * ctas)
-    ctas *= 2;
+  const int steps = (vecs + kStepVecs - 1) / kStepVecs;  // of a row
+  // CTAs of a request: as many as let all requests be resident together, with a
+  // step of a row for each.  (Where they are not, one each.)
   cudaLaunchConfig_t cfg{};
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = sizeof(SelectShared);
   cfg.stream = st;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeClusterDimension;
@@ -475,22 +651,24 @@ cudaError_t launch_select(SelectParams p, cudaStream_t st) {
   cfg.attrs = &at;
   cfg.numAttrs = 1;
   const cudaError_t e = allow_shared(reinterpret_cast<const void*>(select_kernel<T>),
-                                     kMaxUnits * 32 * (int)sizeof(float), &allowed);
+                                     (int)sizeof(SelectShared), &allowed);
   if (e != cudaSuccess) return e;
-  for (;;) {
-    // a unit has as few steps as let the CTA's maxima fit
-    p.steps = 1;
-    for (;;) {
-      p.row_units = (vecs + p.steps * kVecs * 32 - 1) / (p.steps * kVecs * 32);
-      if ((int64_t)((p.row_units + ctas - 1) / ctas) * p.K <= kMaxUnits) break;
-      ++p.steps;
-    }
-    cfg.dynamicSmemBytes = (size_t)((p.row_units + ctas - 1) / ctas) * p.K * 32 * sizeof(float);
-    cfg.gridDim = dim3((unsigned)(p.B * ctas));
+  int ctas = steps < kMaxCluster ? steps : kMaxCluster;
+  while (ctas > 1) {
+    cfg.gridDim = dim3((unsigned)ctas);
     at.val.clusterDim.x = (unsigned)ctas;
-    if (ctas <= 8 || wide_clusters(select_kernel<T>, cfg, &asked, &wide)) break;
-    ctas = 8;
+    if (p.B <= resident_clusters(select_kernel<T>, cfg, ctas, resident)) break;
+    --ctas;
   }
+  // a unit has as few steps as let the CTA's maxima fit
+  p.steps = 1;
+  for (;;) {
+    p.row_units = (vecs + p.steps * kStepVecs - 1) / (p.steps * kStepVecs);
+    if ((int64_t)((p.row_units + ctas - 1) / ctas) * p.K <= kMaxUnits) break;
+    ++p.steps;
+  }
+  cfg.gridDim = dim3((unsigned)(p.B * ctas));
+  at.val.clusterDim.x = (unsigned)ctas;
   return cudaLaunchKernelEx(&cfg, select_kernel<T>, p);
 }
 
