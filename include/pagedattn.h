@@ -583,6 +583,9 @@ PA_API int pa_copy_pages(const int32_t* copies, int n, void* const* caches, int 
  *                 hold there (NaN and infinities too).
  *   max_seqlen_q, max_seqlen_k  host-known bounds of an entry's rows and keys.
  *   out [total_q, Hq, D] contiguous; lse fp32 [Hq, total_q] or NULL.
+ *   workspace     pa_fwd_cross_workspace_size bytes, 256-byte aligned (NULL where
+ *                 that is 0); its contents on entry do not matter.  Calls that may
+ *                 overlap on the GPU need one each.
  * Rows without a key: O = 0, LSE = -inf.  Rows behind cu_seqlens_q[B] are not
  * written.  An entry with rows or keys outside q and k, or more than the bounds,
  * is reported (PA_DEVERR_LENGTH, the entry, the length): its rows that lie in q
@@ -593,8 +596,10 @@ PA_API int pa_fwd_cross(const void* q, int64_t q_st, int64_t q_sh, const void* k
                         const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
                         const int32_t* seqlens_k, const uint8_t* key_mask, int B, int total_q,
                         int total_k, int max_seqlen_q, int max_seqlen_k, int Hq, int Hkv, int D,
-                        float scale, void* out, float* lse, int32_t* err_word, int dtype,
-                        pa_stream_t stream);
+                        float scale, void* out, float* lse, void* workspace,
+                        size_t workspace_bytes, int32_t* err_word, int dtype, pa_stream_t stream);
+
+PA_API size_t pa_fwd_cross_workspace_size(int total_q, int max_seqlen_q, int Hq, int Hkv, int D);
 
 /* Human-readable text of the last non-OK return on the calling thread. */
 PA_API const char* pa_last_error_string(void);

@@ -100,8 +100,9 @@ _SIGNATURES = {
     "pa_copy_pages": (_i32, [_vp, _i32, _vp, _i32, _i64, _i64, _i64, _i32, _i32, _i32, _i64, _vp,
                              _vp]),
     "pa_fwd_cross": (_i32, [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _vp,
-                            _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _vp, _vp, _vp, _i32,
-                            _vp]),
+                            _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _vp, _vp, _vp, _sz,
+                            _vp, _i32, _vp]),
+    "pa_fwd_cross_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i32]),
     "pa_last_error_string": (ctypes.c_char_p, []),
     "pa_version": (_i32, []),
 }
@@ -361,7 +362,8 @@ def _load_native():
     native.bind(*[ctypes.cast(fn, _vp).value for fn in (
         lib.pa_plan_step, lib.pa_release_pages, lib.pa_rotary_append_varlen,
         lib.pa_fwd_varlen_e4m3, lib.pa_fwd_varlen_e4m3_workspace_size, lib.pa_beam_select,
-        lib.pa_beam_reorder, lib.pa_copy_pages, lib.pa_fwd_cross)])
+        lib.pa_beam_reorder, lib.pa_copy_pages, lib.pa_fwd_cross,
+        lib.pa_fwd_cross_workspace_size)])
     _native = native
     return native
 
@@ -534,8 +536,13 @@ def pa_copy_pages(copies, caches, err=None):
         _check(rc)
 
 
+def fwd_cross_workspace_size(total_q, max_seqlen_q, Hq, Hkv, D):
+    return load_library().pa_fwd_cross_workspace_size(total_q, max_seqlen_q, Hq, Hkv, D)
+
+
 def pa_fwd_cross(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, seqlens_k=None,
-                 key_mask=None, scale=None, out=None, lse=None, err=None, return_lse=True):
+                 key_mask=None, scale=None, out=None, lse=None, workspace=None, err=None,
+                 return_lse=True):
     """Attention of a ragged batch's rows to the keys of their entry (cross attention to an encoder's
     states); returns ``(out, lse)``.
 
@@ -550,7 +557,7 @@ def pa_fwd_cross(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k
         lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
     rc = (_native or _load_native()).fwd_cross(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
                                                max_seqlen_k, seqlens_k, key_mask, scale, out, lse,
-                                               err)
+                                               workspace, err)
     if rc:
         _check(rc)
     return out, lse

@@ -24,7 +24,8 @@ OUT_DIR = os.path.join(PKG, "_lib")
 LIB_NAME = "libpagedattn.so"
 SOURCES = ["api.cu", "append.cu", "decode.cu", "combine.cu", "noalloc.cu", "engine.cu",
            "rotary.cu", "prefill.cu", "step.cu", "rotary_append.cu", "attend_e4m3.cu",
-           "chunk_e4m3.cu", "beam_select.cu", "beam_pages.cu", "cross.cu"]
+           "chunk_e4m3.cu", "beam_select.cu", "beam_pages.cu", "cross.cu",
+           "cross_wide.cu"]
 # Encoding self-test of the tensor-core operand layouts: test infrastructure,
 # kept out of the product library.
 SELFTEST_LIB = "libpa_selftest.so"

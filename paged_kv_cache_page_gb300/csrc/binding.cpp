@@ -39,6 +39,7 @@ struct Entries {
   decltype(&pa_beam_reorder) reorder = nullptr;
   decltype(&pa_copy_pages) copy = nullptr;
   decltype(&pa_fwd_cross) cross = nullptr;
+  decltype(&pa_fwd_cross_workspace_size) cross_workspace = nullptr;
 } g_entries;
 
 struct BadArgument : std::runtime_error {
@@ -159,10 +160,10 @@ bool count_is(Py_ssize_t n, Py_ssize_t expected) {
   return false;
 }
 
-// bind(plan, release, append, attend, attend_workspace, select, reorder, copy, cross): entry
-// addresses
+// bind(plan, release, append, attend, attend_workspace, select, reorder, copy, cross,
+//      cross_workspace): entry addresses
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (!count_is(n, 9)) return nullptr;
+  if (!count_is(n, 10)) return nullptr;
   return guarded([&]() -> PyObject* {
     auto at = [&](int i) { return (uintptr_t)(unsigned long long)integer(a[i]); };
     g_entries.plan = reinterpret_cast<decltype(g_entries.plan)>(at(0));
@@ -174,6 +175,7 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     g_entries.reorder = reinterpret_cast<decltype(g_entries.reorder)>(at(6));
     g_entries.copy = reinterpret_cast<decltype(g_entries.copy)>(at(7));
     g_entries.cross = reinterpret_cast<decltype(g_entries.cross)>(at(8));
+    g_entries.cross_workspace = reinterpret_cast<decltype(g_entries.cross_workspace)>(at(9));
     Py_RETURN_NONE;
   });
 }
@@ -500,9 +502,9 @@ PyObject* copy_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // fwd_cross(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, seqlens_k, key_mask,
-//           scale, out, lse, err)
+//           scale, out, lse, workspace, err)
 PyObject* fwd_cross(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (!count_is(n, 13)) return nullptr;
+  if (!count_is(n, 14)) return nullptr;
   return guarded([&]() -> PyObject* {
     const at::Tensor& q = tensor_of(a[0], "q");
     const c10::Device device = device_of(q, "q");
@@ -531,13 +533,31 @@ PyObject* fwd_cross(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const auto& out = want(a[10], "out", type, device, {rows, hq, d});
     if (!out.is_contiguous()) bad("out", "must be contiguous");
     const c10::cuda::CUDAGuard guard(device);
+    const int max_q = int_of(a[5], "max_seqlen_q");
+    at::Tensor scratch;
+    void* ws = nullptr;
+    size_t ws_bytes = 0;
+    if (a[12] != Py_None) {
+      const at::Tensor& w = tensor_of(a[12], "workspace");
+      if (!w.is_cuda() || w.device() != device || !w.is_contiguous())
+        bad("workspace", "must be contiguous, on the call's CUDA device");
+      ws = w.data_ptr();
+      ws_bytes = (size_t)w.numel() * w.element_size();
+    } else {
+      ws_bytes = g_entries.cross_workspace(size_of(rows, "q"), max_q, size_of(hq, "q"),
+                                           size_of(hkv, "k"), size_of(d, "q"));
+      if (ws_bytes > 0) {
+        scratch = at::empty({(int64_t)ws_bytes}, q.options().dtype(at::kByte));
+        ws = scratch.data_ptr();
+      }
+    }
     return unlocked(
         g_entries.cross, q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), k.stride(0),
         k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), ptr<int32_t>(cu_q), ptr<int32_t>(cu_k),
         lens, flags_of(a[8], "key_mask", device, {keys}), size_of(B, "the batch"),
-        size_of(rows, "q"), size_of(keys, "k"), int_of(a[5], "max_seqlen_q"),
+        size_of(rows, "q"), size_of(keys, "k"), max_q,
         int_of(a[6], "max_seqlen_k"), size_of(hq, "q"), size_of(hkv, "k"), size_of(d, "q"),
-        (float)scale, out.data_ptr(), lse, err_of(a[12], device), dtype, stream_of(device));
+        (float)scale, out.data_ptr(), lse, ws, ws_bytes, err_of(a[13], device), dtype, stream_of(device));
   });
 }
 

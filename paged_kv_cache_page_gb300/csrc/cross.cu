@@ -323,17 +323,19 @@ __global__ void __launch_bounds__(kThreads, 2)
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int i = 0; i < parts; ++i) {
       const float* f = from(i);
-      const float mi = f[MT * 16 * D + 2 * r];
-      if (mi == neg_inf()) continue;
-      const float x = ex2(mi - top);
-      sum += x * f[MT * 16 * D + 2 * r + 1];
+      const float mi = f[MT * 16 * D + 2 * r], li = f[MT * 16 * D + 2 * r + 1];
+      // (a part without a seen key counts for nothing; a NaN in one without any
+      // number reaches the result)
+      if (li == 0.f) continue;
+      const float x = mi == top ? 1.f : ex2(mi - top);
+      sum += x * li;
       const float4 y = *reinterpret_cast<const float4*>(f + r * D + 4 * c);
       acc.x += x * y.x;
       acc.y += x * y.y;
       acc.z += x * y.z;
       acc.w += x * y.w;
     }
-    const float inv = top == neg_inf() ? 0.f : 1.f / sum;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const int at = (row0 + r) / p.G, g = (row0 + r) - at * p.G;
     const int head = (h - warp % hs + hh) * p.G + g;
     uint2 u;
@@ -343,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     *reinterpret_cast<uint2*>(dst) = u;
     if (c == 0 && p.lse != nullptr)
       p.lse[(int64_t)head * p.total_q + e.q0 + at] =
-          top == neg_inf() ? neg_inf() : (top + log2f(sum)) * kLn2;
+          sum == 0.f ? neg_inf() : (top + log2f(sum)) * kLn2;
   }
   cluster.sync();  // no CTA leaves while its parts are read
 }
@@ -419,7 +421,22 @@ bool fix_strides(int64_t* st, int64_t* sh, int64_t rows, int heads, int D) {
   return *st > 0 && *sh > 0 && *st % 8 == 0 && *sh % 8 == 0;
 }
 
+// More rows of a kv head than this run on tcgen05, whose tiles hold 128.
+constexpr int kNarrowRows = 64;
+bool is_wide(int total_q, int max_seqlen_q, int G) {
+  const long long rows = (long long)(max_seqlen_q < total_q ? max_seqlen_q : total_q) * G;
+  return rows > kNarrowRows && G <= 128;
+}
+
 }  // namespace
+
+extern "C" PA_API size_t pa_fwd_cross_workspace_size(int total_q, int max_seqlen_q, int Hq, int Hkv,
+                                                     int D) {
+  if (total_q <= 0 || max_seqlen_q <= 0 || Hkv <= 0 || Hq <= 0 || Hq % Hkv != 0 ||
+      (D != 64 && D != 128))
+    return 0;
+  return is_wide(total_q, max_seqlen_q, Hq / Hkv) ? cross_wide_workspace(D) : 0;
+}
 
 extern "C" PA_API int pa_fwd_cross(const void* q, int64_t q_st, int64_t q_sh, const void* k,
                                    int64_t k_st, int64_t k_sh, const void* v, int64_t v_st,
@@ -427,8 +444,9 @@ extern "C" PA_API int pa_fwd_cross(const void* q, int64_t q_st, int64_t q_sh, co
                                    const int32_t* cu_seqlens_k, const int32_t* seqlens_k,
                                    const uint8_t* key_mask, int B, int total_q, int total_k,
                                    int max_seqlen_q, int max_seqlen_k, int Hq, int Hkv, int D,
-                                   float scale, void* out, float* lse, int32_t* err_word,
-                                   int dtype, pa_stream_t stream) {
+                                   float scale, void* out, float* lse, void* workspace,
+                                   size_t workspace_bytes, int32_t* err_word, int dtype,
+                                   pa_stream_t stream) {
   if (dtype != PA_F16 && dtype != PA_BF16) return set_error(PA_ERR_UNSUPPORTED, "dtype %d", dtype);
   if (D != 64 && D != 128) return set_error(PA_ERR_UNSUPPORTED, "head_dim %d (64 or 128)", D);
   if (Hq < 1 || Hkv < 1) return set_error(PA_ERR_INVALID_ARG, "head counts must be >= 1");
@@ -457,6 +475,11 @@ extern "C" PA_API int pa_fwd_cross(const void* q, int64_t q_st, int64_t q_sh, co
   const long long tiles = ((long long)max_q * G + 15) / 16;
   if ((long long)B * Hkv * tiles > (1 << 26))
     return set_error(PA_ERR_UNSUPPORTED, "more than 2^26 tiles of 16 rows per kv head");
+  const bool wide = is_wide(total_q, max_seqlen_q, G);
+  if (wide && (workspace == nullptr || workspace_bytes < cross_wide_workspace(D) ||
+               (reinterpret_cast<uintptr_t>(workspace) & 255) != 0))
+    return set_error(PA_ERR_WORKSPACE, "workspace of %zu bytes, 256-byte aligned, is needed",
+                     cross_wide_workspace(D));
   CrossParams p{};
   p.q = q;
   p.q_st = q_st;
@@ -482,12 +505,14 @@ extern "C" PA_API int pa_fwd_cross(const void* q, int64_t q_st, int64_t q_sh, co
   const void* kb = total_k > 0 ? k : q;
   const void* vb = total_k > 0 ? v : q;
   const int64_t rows = total_k > 0 ? total_k : 1;
-  const int box = cross_narrow_box(D);
-  CUtensorMap tmk, tmv;
+  const int box = wide ? 128 : cross_narrow_box(D);
+  CUtensorMap tmq, tmk, tmv;
   if (!encode_map(&tmk, kb, dtype, D, Hkv, rows, 1, k_sh, k_st, k_st, 64, 1, box, true) ||
-      !encode_map(&tmv, vb, dtype, D, Hkv, rows, 1, v_sh, v_st, v_st, 64, 1, box, true))
-    return set_error(PA_ERR_CUDA, "the tensor maps of k and v could not be encoded");
-  const cudaError_t e = launch_cross_narrow(p, tmk, tmv, D, dtype, st);
+      !encode_map(&tmv, vb, dtype, D, Hkv, rows, 1, v_sh, v_st, v_st, 64, 1, box, true) ||
+      (wide && !encode_map(&tmq, q, dtype, D, Hq, total_q, 1, q_sh, q_st, q_st, 64, G, 128 / G, true)))
+    return set_error(PA_ERR_CUDA, "the tensor maps of q, k and v could not be encoded");
+  const cudaError_t e = wide ? launch_cross_wide(p, tmq, tmk, tmv, D, dtype, workspace, st)
+                             : launch_cross_narrow(p, tmk, tmv, D, dtype, st);
   if (e != cudaSuccess) return set_error(PA_ERR_CUDA, "cross launch: %s", cudaGetErrorString(e));
   return PA_OK;
 }

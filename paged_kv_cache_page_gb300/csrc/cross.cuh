@@ -19,6 +19,10 @@ struct CrossParams {
   void* out;
   float* lse;
   int32_t* err;
+  // the wide kernel's parts of cut streams
+  unsigned long long* words;
+  float2* part_ml;
+  float* part_o;
 };
 
 // Rows [q0, q0 + rows) of q and keys [k0, k0 + keys) of k and v.
@@ -48,6 +52,11 @@ __device__ __forceinline__ CrossEntry cross_entry(const CrossParams& p, int b, b
 // Few rows: warp-level MMAs, clusters over the keys.  Many rows: tcgen05.
 cudaError_t launch_cross_narrow(const CrossParams& p, const CUtensorMap& tmk,
                                 const CUtensorMap& tmv, int D, int dtype, cudaStream_t st);
+// tmq: q with boxes of 64 columns, G heads, 128 / G rows; tmk, tmv: 64 columns, 128 keys.
+cudaError_t launch_cross_wide(CrossParams p, const CUtensorMap& tmq, const CUtensorMap& tmk,
+                              const CUtensorMap& tmv, int D, int dtype, void* workspace,
+                              cudaStream_t st);
+size_t cross_wide_workspace(int D);
 constexpr int cross_narrow_box(int D) { return D == 64 ? 32 : 16; }  // keys of a box
 
 }  // namespace pa

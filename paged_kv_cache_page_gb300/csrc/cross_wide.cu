@@ -1,0 +1,810 @@
+// Attention of a ragged batch's rows to the keys of their entry (pa_fwd_cross)
+// on the 5th-generation tensor cores (sm_103a): many rows a kv head, as whole
+// target sequences have them.
+//
+// Mathematics as in cross.cu: softmax(scale Q K^T) V in one pass over the keys.
+// The rows of a tile are packed over the G heads of a kv head (row i G + g of an
+// entry; 128 / G whole tokens a tile), so that all rows of a CTA's two tiles share
+// every K and V tile.  A row's reference m is a whole number that follows the
+// largest score only where that passes it by more than the slack of P's type: P
+// and O are then scaled by exact powers of two, which is rare, and the exponentials
+// do not wait for the maximum.
+//
+// Bound: the tensor cores, 4 D operations a (row, key) pair, and next to them the
+// exponentials.  One persistent CTA an SM:
+//   warps 0-7  softmax: one thread a row, group g = warp / 4 takes tile g
+//   warp 8     K and Q tiles by TMA, warp 9 V tiles
+//   warp 10    issues O_g += P_g V (P_g from TMEM over S_g) and S_g = Q_g K^T
+//   warp 11    clears rows of V that no row sees (0 times what they hold may be NaN)
+// TMEM: S_0, S_1, O_0, O_1.  While one group's softmax runs, the tensor core works
+// on the other group.
+//
+// Work: the streams (entry, kv head, pair of tiles) laid end to end in 128-key
+// tiles and dealt to the CTAs in equal shares; a stream that is cut is joined by
+// the CTA that finishes last.  Whole streams dealt in turn would leave the last
+// round of a few hundred streams half empty.
+#include <type_traits>
+
+#include "cross.cuh"
+#include "pa_tcgen05.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kM = 128;  // rows of a query tile
+constexpr int kN = 128;  // keys of a tile
+constexpr int kSlab = 128 * 128;
+constexpr int kWarpK = 8, kWarpV = 9, kWarpMma = 10, kWarpFix = 11;
+constexpr int kThreads = 12 * 32;
+constexpr int kMinShare = 2;  // tiles
+
+template <int D>
+struct Layout {
+  static constexpr int kTile = D / 64 * kSlab;
+  static constexpr int kStages = D == 128 ? 2 : 3;  // of K and of V
+  static constexpr int kOffQ = 0;                   // [2]
+  static constexpr int kOffK = 2 * kTile;
+  static constexpr int kOffV = kOffK + kStages * kTile;
+  static constexpr int kOffOut = kOffV + kStages * kTile;  // [8 warps][32 rows][128 bytes]
+  static constexpr int kOffBar = kOffOut + 8 * 4096;
+  // q_full, q_empty; k_full, k_empty, v_full, v_ready, v_empty [kStages];
+  // s_full, p_full, pv_done, o_free [2]
+  static constexpr int kBars = 2 + 5 * kStages + 8;
+  static constexpr int kOffSums = kOffBar + kBars * 8;  // long long [16]
+  static constexpr int kOffMisc = kOffSums + 16 * 8;    // start; TMEM base, flag
+  static constexpr int kBytes = kOffMisc + 32 + 1024;
+  static_assert(kBytes <= 232448, "shared memory");
+};
+
+// P of the type: the largest score is brought to 2^shift at first, and may pass
+// that by 2^slack before the reference moves.
+template <typename T> struct Range;
+template <> struct Range<__half> {  // up to 2^15, and 2^-32 of the largest still counts
+  static constexpr float kShift = 8.f, kSlack = 7.f;
+};
+template <> struct Range<__nv_bfloat16> {
+  static constexpr float kShift = 0.f, kSlack = 40.f;
+};
+
+// MMAs and commits under a predicate: a branch around them would take the warp's
+// operands out of the uniform registers.
+__device__ __forceinline__ void mma_ss_if(uint32_t on, uint32_t d, uint64_t a, uint64_t b,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(on)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_if(uint32_t on, uint32_t d, uint32_t a, uint64_t b,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(on)
+      : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t on, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_u32(bar)),
+      "r"(on)
+      : "memory");
+}
+
+// Two fp32 values at a time.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t x;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a), "f"(b));
+  return x;
+}
+__device__ __forceinline__ float2 halves(uint64_t x) {
+  float2 y;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(y.x), "=f"(y.y) : "l"(x));
+  return y;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t x;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(x) : "l"(a), "l"(b), "l"(c));
+  return x;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t x;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(x) : "l"(a), "l"(b));
+  return x;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float x;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(x) : "f"(a), "f"(b), "f"(c));
+  return x;
+}
+// Ties the values of an asynchronous TMEM load to the wait in front of it.
+__device__ __forceinline__ void arrived(float (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(v[i]));
+}
+
+// Scales the first `cols` columns of 16-bit probabilities in TMEM by 2^-k a lane,
+// in two factors: one alone could lie below the type's range.
+template <typename T>
+__device__ __noinline__ void scale_p(uint32_t t, int cols, float by) {
+  using E = Elem<T>;
+  const float first = fmaxf(by, 0x1p-14f), second = fminf(by * 0x1p14f, 1.f);
+  tc::tmem_wait_st();
+#pragma unroll 1
+  for (int c = 0; c < cols; c += 16) {
+    float v[16];
+    uint32_t w[16];
+    tc::tmem_ld16(t + c, v);
+    tc::tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float2 x = E::to_f2(__float_as_uint(v[i]));
+      x.x = x.x * first * second;
+      x.y = x.y * first * second;
+      w[i] = E::from_f2(x.x, x.y);
+    }
+    tc::tmem_st16u(t + c, w);
+  }
+  tc::tmem_wait_st();
+}
+
+__device__ __forceinline__ float4 load16_l2(const void* src) {  // what another CTA has written
+  float4 x;
+  asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+               : "l"(src)
+               : "memory");
+  return x;
+}
+
+// Tokens of a tile, of a pair of tiles.
+__device__ __forceinline__ int pair_tokens(const CrossParams& p) { return 2 * (kM / p.G); }
+__device__ __forceinline__ int entry_pairs(const CrossParams& p, const CrossEntry& e) {
+  const int n = pair_tokens(p);
+  return (e.rows + n - 1) / n;
+}
+__device__ __forceinline__ int entry_tiles(const CrossEntry& e) {
+  return max(1, (e.keys + kN - 1) / kN);  // (without keys: one, to write the empty rows)
+}
+
+// A part of a CTA's share: tiles [t0, t0 + n) of a stream.
+struct Walk {
+  int b, h, pair, t0, n, all, pairs;  // all: tiles of the stream
+  long long left;                     // of the share from t0 on
+  long long begin;                    // tiles of the streams in front
+  CrossEntry e;
+
+  __device__ __forceinline__ void next(const CrossParams& p) {
+    left -= n;
+    n = 0;
+    if (left <= 0) return;
+    begin += all;
+    t0 = 0;
+    if (++pair == pairs) {
+      pair = 0;
+      if (++h == p.Hkv) {
+        h = 0;
+        do {
+          if (++b >= p.B) {  // (lengths that change under the launch)
+            left = 0;
+            return;
+          }
+          e = cross_entry(p, b, false);
+          pairs = entry_pairs(p, e);
+        } while (pairs == 0);
+        all = entry_tiles(e);
+      }
+    }
+    n = (int)min((long long)all, left);
+  }
+};
+
+template <int D, typename T>
+__global__ void __launch_bounds__(kThreads, 1)
+    wide_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ CUtensorMap tmq,
+                const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
+  using L = Layout<D>;
+  using E = Elem<T>;
+  using R = Range<T>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint8_t* sQ = smem + L::kOffQ;
+  uint8_t* sK = smem + L::kOffK;
+  uint8_t* sV = smem + L::kOffV;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
+  uint64_t* q_full = bars;
+  uint64_t* q_empty = bars + 1;
+  uint64_t* k_full = bars + 2;
+  uint64_t* k_empty = k_full + L::kStages;
+  uint64_t* v_full = k_empty + L::kStages;
+  uint64_t* v_ready = v_full + L::kStages;
+  uint64_t* v_empty = v_ready + L::kStages;
+  uint64_t* s_full = v_empty + L::kStages;
+  uint64_t* p_full = s_full + 2;
+  uint64_t* pv_done = p_full + 2;
+  uint64_t* o_free = pv_done + 2;
+  long long* sSums = reinterpret_cast<long long*>(smem + L::kOffSums);
+  long long* sStart = reinterpret_cast<long long*>(smem + L::kOffMisc);  // entry, tiles in front of it
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc + 16);
+  int* sFlag = reinterpret_cast<int*>(smem + L::kOffMisc + 20);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    for (int i = 0; i < L::kStages; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_ready[i], 1);
+      mbar_init(&v_empty[i], 1);
+    }
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(&s_full[g], 1);
+      mbar_init(&p_full[g], 4);
+      mbar_init(&pv_done[g], 1);
+      mbar_init(&o_free[g], 4);
+    }
+    fence_mbar_init();
+  }
+
+  // ---- the CTA's share: the tiles of all entries, then the entry it begins in
+  long long total = 0, share = 0, start = 0;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    long long before = 0;
+#pragma unroll 1
+    for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+      const int b = b0 + tid;
+      long long cost = 0;
+      if (b < p.B) {
+        const CrossEntry e = cross_entry(p, b, pass == 0 && blockIdx.x == 0);
+        cost = (long long)entry_pairs(p, e) * p.Hkv * entry_tiles(e);
+      }
+      long long x = cost;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      __syncthreads();  // (sSums of the pass before have been read)
+      if (lane == 31) sSums[warp] = x;
+      __syncthreads();
+      long long in_front = before, all = 0;
+      for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) in_front += sSums[w];
+        all += sSums[w];
+      }
+      x += in_front;  // up to and with entry b
+      if (pass == 1 && cost > 0 && start >= x - cost && start < x) {
+        sStart[0] = b;
+        sStart[1] = x - cost;
+      }
+      before += all;
+    }
+    if (pass == 0) {
+      total = before;
+      share = max((long long)kMinShare, (total + gridDim.x - 1) / gridDim.x);
+      start = share * blockIdx.x;
+      if (start >= total) return;  // (the whole CTA)
+    }
+  }
+  __syncthreads();
+  Walk at;
+  at.b = (int)sStart[0];
+  at.e = cross_entry(p, at.b, false);
+  at.pairs = entry_pairs(p, at.e);
+  at.all = entry_tiles(at.e);
+  at.left = min(share, total - start);
+  {
+    const long long off = start - sStart[1], stream = off / at.all;
+    at.begin = sStart[1] + stream * at.all;
+    at.t0 = (int)(off - stream * at.all);
+    at.h = (int)(stream / at.pairs);
+    at.pair = (int)(stream - (long long)at.h * at.pairs);
+    at.n = (int)min((long long)(at.all - at.t0), at.left);
+  }
+  const int tokens = kM / p.G, tile_rows = tokens * p.G;
+
+  // rows of a Q tile that no token fills stay zero
+  if (tile_rows < kM) {
+    for (int i = tid; i < 2 * L::kTile / 16; i += kThreads)
+      *reinterpret_cast<uint4*>(sQ + i * 16) = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+  }
+  if (warp == kWarpMma) {
+    tc::tmem_alloc(tslot, 512);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tbase = *tslot;
+  auto tS = [&](int g) { return tbase + (uint32_t)(g * 128); };
+  auto tO = [&](int g) { return tbase + 256u + (uint32_t)(g * D); };
+  // Whether group g has rows in the part, and tiles of keys are read for it.
+  auto has_rows = [&](const Walk& w, int g) { return (2 * w.pair + g) * tokens < w.e.rows; };
+
+  bool failed = false;
+  auto wait = [&](uint64_t* bar, uint32_t par, int where) {
+    if (!failed && !mbar_wait(bar, par)) {
+      report(p.err, PA_DEVERR_TIMEOUT, -1, where);
+      failed = true;
+    }
+  };
+
+  if (warp == kWarpK || warp == kWarpV) {
+    // ======================= K and Q, V =======================
+    const bool is_v = warp == kWarpV;
+    const uint64_t keep = l2_policy_evict_last(), once = l2_policy_evict_first();
+    uint64_t* full = is_v ? v_full : k_full;
+    uint64_t* empty = is_v ? v_empty : k_empty;
+    uint8_t* ring = is_v ? sV : sK;
+    const CUtensorMap* map = is_v ? &tmv : &tmk;
+    int k = 0, a = 0;
+    if (lane == 0) {
+      tma_prefetch_desc(map);
+      if (!is_v) tma_prefetch_desc(&tmq);
+      for (; at.left > 0; at.next(p)) {
+        if (at.e.keys == 0) continue;
+        for (int t = at.t0; t < at.t0 + at.n; ++t, ++k) {
+          const int s = k % L::kStages;
+          wait(&empty[s], (uint32_t)((k / L::kStages & 1) ^ 1), is_v ? 21 : 20);
+          if (failed) break;
+          mbar_arrive_expect_tx(&full[s], L::kTile);
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_4d(ring + s * L::kTile + c * kSlab, map, &full[s], c * 64, at.h,
+                        at.e.k0 + t * kN, 0, keep);
+          if (!is_v && t == at.t0) {
+            if (a >= 1) wait(q_empty, (uint32_t)((a - 1) & 1), 10);
+            if (failed) break;
+            mbar_arrive_expect_tx(q_full, (uint32_t)(2 * (D / 64) * tile_rows * 128));
+            for (int g = 0; g < 2; ++g)
+              for (int c = 0; c < D / 64; ++c)
+                tma_load_4d(sQ + g * L::kTile + c * kSlab, &tmq, q_full, c * 64, at.h * p.G,
+                            at.e.q0 + (2 * at.pair + g) * tokens, 0, once);
+          }
+        }
+        ++a;
+      }
+      // every copy must land before the CTA leaves
+      if (!failed)
+        for (int i = 0; i < L::kStages; ++i, ++k)
+          wait(&empty[k % L::kStages], (uint32_t)((k / L::kStages & 1) ^ 1), 30);
+      else
+        for (int i = max(0, k - L::kStages); i < k; ++i)
+          mbar_wait(&full[i % L::kStages], (uint32_t)(i / L::kStages & 1));
+    }
+    __syncwarp();
+  } else if (warp == kWarpFix) {
+    // ======================= rows of V that no row sees =======================
+    int k = 0;
+    for (; at.left > 0; at.next(p)) {
+      if (at.e.keys == 0) continue;
+      for (int t = at.t0; t < at.t0 + at.n; ++t, ++k) {
+        const int s = k % L::kStages;
+        const bool whole = p.key_mask == nullptr && (t + 1) * kN <= at.e.keys;
+        uint32_t drop[kN / 32];
+        if (!whole) {
+#pragma unroll
+          for (int c = 0; c < kN / 32; ++c) {
+            const int key = t * kN + c * 32 + lane;
+            drop[c] = __ballot_sync(
+                0xffffffffu, key >= at.e.keys || (p.key_mask != nullptr &&
+                                                  __ldg(p.key_mask + at.e.k0 + key) == 0));
+          }
+        }
+        wait(&v_full[s], (uint32_t)(k / L::kStages & 1), 25);
+        if (!whole) {
+          uint8_t* tile = sV + s * L::kTile;
+#pragma unroll 1
+          for (int c = 0; c < kN / 32; ++c) {
+            uint32_t w = drop[0];
+            if (c == 1) w = drop[1];
+            if (c == 2) w = drop[2];
+            if (c == 3) w = drop[3];
+            // eight lanes a row of 128 bytes, four rows at a time
+            for (int i = lane >> 3; i < 32; i += 4)
+              if (w >> i & 1)
+                for (int x = 0; x < D / 64; ++x)
+                  *reinterpret_cast<uint4*>(tile + x * kSlab + (c * 32 + i) * 128 + (lane & 7) * 16) =
+                      make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&v_ready[s]);
+      }
+    }
+  } else if (warp == kWarpMma) {
+    // ======================= MMA issuer =======================
+    // Per tile and group: O_g += P_g V, then S_g of the next tile.  One thread's
+    // MMAs run in the order it issues them, so S_g may follow the product that
+    // reads P_g from the same columns without a wait.  The warp issues as one, an
+    // elected thread's predicate on, with operands broadcast to uniform registers.
+    constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
+    const uint32_t id_s = tc::idesc_f16(kM, kN, bf, false);
+    const uint32_t id_o = tc::idesc_f16(kM, D, bf, true);
+    const uint64_t d16 = tc::smem_desc(0, 16, 1024), dslab = tc::smem_desc(0, kSlab, 1024);
+    const uint32_t qlo = (uint32_t)d16 + (smem_u32(sQ) >> 4), klo = (uint32_t)d16 + (smem_u32(sK) >> 4);
+    const uint32_t vlo = (uint32_t)dslab + (smem_u32(sV) >> 4);
+    auto desc = [](uint64_t base, uint32_t lo) {
+      uint64_t d;
+      asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"((uint32_t)(base >> 32)));
+      return d;
+    };
+    auto uni = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
+    uint32_t on;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(on));
+    const uint32_t tb = uni(tbase);
+    int k = 0, a = 0, n0 = 0, n1 = 0, m0 = 0, m1 = 0;
+    auto scores = [&](int g, int s) {
+      const uint32_t q0 = uni(qlo + (uint32_t)((g * L::kTile) >> 4));
+      const uint32_t k0 = uni(klo + (uint32_t)((s * L::kTile) >> 4));
+      const uint32_t ts = uni(tb + g * 128);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = ((kk >> 2) * kSlab + (kk & 3) * 32) >> 4;
+        mma_ss_if(on, ts, desc(d16, q0 + off), desc(d16, k0 + off), id_s, kk > 0);
+      }
+      commit_if(on, &s_full[g]);
+      __syncwarp();
+    };
+    auto release = [&](uint64_t* bar) {
+      commit_if(on, bar);
+      __syncwarp();
+    };
+    for (; at.left > 0; at.next(p)) {
+      if (at.e.keys == 0) continue;
+      const int groups = has_rows(at, 1) ? 2 : 1;
+      wait(q_full, (uint32_t)(a & 1), 40);
+      wait(&k_full[k % L::kStages], (uint32_t)(k / L::kStages & 1), 41);
+      tc::fence_after_sync();
+      for (int g = 0; g < groups; ++g) scores(g, k % L::kStages);
+      release(&k_empty[k % L::kStages]);
+      if (at.n == 1) release(q_empty);
+      for (int t = 0; t < at.n; ++t, ++k) {
+        const int s = k % L::kStages, sn = (k + 1) % L::kStages;
+        const bool more = t + 1 < at.n;
+        wait(&v_ready[s], (uint32_t)(k / L::kStages & 1), 50);
+#pragma unroll 1
+        for (int g = 0; g < groups; ++g) {
+          const int n = g ? n1 : n0, m = g ? m1 : m0;
+          wait(&p_full[g], (uint32_t)(n & 1), 51 + g);
+          if (t == 0 && m >= 1) wait(&o_free[g], (uint32_t)((m - 1) & 1), 53 + g);
+          tc::fence_after_sync();
+          const uint32_t v0 = uni(vlo + (uint32_t)((s * L::kTile) >> 4));
+          const uint32_t ts = uni(tb + g * 128), to = uni(tb + 256 + g * D);
+          const uint32_t add = uni(t > 0);
+#pragma unroll
+          for (int kk = 0; kk < kN / 16; ++kk)
+            mma_ts_if(on, to, ts + kk * 8, desc(dslab, v0 + (kk * 2048 >> 4)), id_o,
+                      kk > 0 ? 1u : add);
+          commit_if(on, &pv_done[g]);
+          __syncwarp();
+          if (g) ++n1;
+          else ++n0;
+          if (more) {
+            if (g == 0) {
+              wait(&k_full[sn], (uint32_t)((k + 1) / L::kStages & 1), 42);
+              tc::fence_after_sync();
+            }
+            scores(g, sn);
+          }
+        }
+        release(&v_empty[s]);
+        if (more) release(&k_empty[sn]);
+        if (t + 2 == at.n) release(q_empty);  // the part's last scores
+      }
+      ++a;
+      ++m0;
+      if (groups == 2) ++m1;
+    }
+  } else {
+    // ======================= softmax =======================
+    const int g = warp >> 2, quarter = warp & 3;
+    const int r = quarter * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    const float f = p.scale_log2;
+    uint8_t* staged = smem + L::kOffOut + warp * 4096;
+    int n = 0;
+    for (; at.left > 0; at.next(p)) {
+      if (!has_rows(at, g)) {
+        // (the barriers of a cut stream are both groups')
+        if (at.n == at.all) continue;
+      }
+      const int token = (2 * at.pair + g) * tokens + r / p.G, head = at.h * p.G + r % p.G;
+      const bool valid = r < tile_rows && token < at.e.rows;
+      const bool active = has_rows(at, g) && at.e.keys > 0;
+      float m = neg_inf(), l = 0.f;
+      for (int t = at.t0; active && t < at.t0 + at.n; ++t) {
+        const bool whole = p.key_mask == nullptr && (t + 1) * kN <= at.e.keys;
+        uint32_t seen[kN / 32];
+        if (!whole) {
+#pragma unroll
+          for (int c = 0; c < kN / 32; ++c) {
+            const int key = t * kN + c * 32 + lane;
+            seen[c] = __ballot_sync(
+                0xffffffffu, key < at.e.keys && (p.key_mask == nullptr ||
+                                                 __ldg(p.key_mask + at.e.k0 + key) != 0));
+          }
+        }
+        wait(&s_full[g], (uint32_t)(n & 1), 60 + g);
+        tc::fence_after_sync();
+        const uint32_t ts = tS(g) + lane_off;
+        uint64_t sum2[4] = {0, 0, 0, 0};  // four pairs of sums
+        float alpha = 1.f;
+        float v[32];
+        // 32 scores at a time, in a rolled loop (unrolled, the roles' code passes
+        // what the instruction caches hold)
+        auto probabilities = [&](auto masked, int key0, uint32_t bits) {
+          if constexpr (masked) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = bits >> i & 1 ? v[i] : neg_inf();
+          }
+          // The exponentials do not wait for the largest score: the chunk is done
+          // again where it passes the reference by more than the slack.
+          uint32_t pk[16];
+          uint64_t more[4];
+#pragma unroll 1
+          for (;;) {
+            const float neg_m = m == neg_inf() ? 0.f : -m;
+            const uint64_t f2 = pair(f, f), m2 = pair(neg_m, neg_m);
+            float top4[4];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float2 z = halves(fma2(pair(v[2 * e], v[2 * e + 1]), f2, m2));
+              const float e0 = ex2(z.x), e1 = ex2(z.y);
+              more[e & 3] = e < 4 ? pair(e0, e1) : add2(more[e & 3], pair(e0, e1));
+              top4[e & 3] = e < 4 ? fmaxf(v[2 * e], v[2 * e + 1])
+                                  : max3(top4[e & 3], v[2 * e], v[2 * e + 1]);
+              pk[e] = E::from_f2(e0, e1);
+            }
+            const float top = max3(fmaxf(top4[0], top4[1]), top4[2], top4[3]) * f;
+            const bool far = top > m + (R::kShift + R::kSlack);
+            if (!__any_sync(0xffffffffu, far)) break;
+            float by = 1.f;
+            if (far) {
+              const float to = ceilf(top) - R::kShift;
+              if (m != neg_inf()) by = ex2(m - to);
+              m = to;
+            }
+            alpha *= by;
+            l *= by;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 z = halves(sum2[i]);
+              sum2[i] = pair(z.x * by, z.y * by);
+            }
+            scale_p<T>(ts, key0 / 2, by);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sum2[i] = add2(sum2[i], more[i]);
+          tc::tmem_st16u(ts + key0 / 2, pk);  // over scores that have been used
+        };
+        auto row = [&](auto masked) {
+#pragma unroll 1
+          for (int c = 0; c < kN; c += 32) {
+            tc::tmem_ld32(ts + c, v);
+            uint32_t bits = 0;
+            if constexpr (masked) {
+              bits = seen[0];
+              if (c == 32) bits = seen[1];
+              if (c == 64) bits = seen[2];
+              if (c == 96) bits = seen[3];
+            }
+            tc::tmem_wait_ld();
+            arrived(v);
+            probabilities(masked, c, bits);
+          }
+        };
+        if (whole) row(std::false_type{});
+        else row(std::true_type{});
+        const float2 sum = halves(add2(add2(sum2[0], sum2[1]), add2(sum2[2], sum2[3])));
+        l += sum.x + sum.y;
+        if (t > at.t0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+          // O_g is still once P V of the group's previous tile is done
+          wait(&pv_done[g], (uint32_t)((n - 1) & 1), 62 + g);
+          tc::fence_after_sync();
+#pragma unroll 1
+          for (int i = 0; i < D / 32; ++i) {
+            float o[32];
+            tc::tmem_ld32(tO(g) + lane_off + i * 32, o);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= alpha;
+            tc::tmem_st32(tO(g) + lane_off + i * 32, o);
+          }
+        }
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[g]);
+        ++n;
+      }
+
+      // ---- the part's result
+      const bool whole = at.n == at.all;
+      const long long my_row = valid ? (long long)(at.e.q0 + token) * p.Hq + head : -1;
+      // 64 columns of the warp's rows by way of shared memory: a thread holds a row,
+      // and whole lines are written
+      auto stage = [&](int c, uint4 x) {
+        *reinterpret_cast<uint4*>(staged + lane * 128 + ((c ^ (lane & 7)) << 4)) = x;
+      };
+      auto write_rows = [&](int half) {
+        const int c = lane & 7;
+        __syncwarp();
+#pragma unroll
+        for (int i = lane >> 3; i < 32; i += 4) {
+          const long long to = __shfl_sync(0xffffffffu, my_row, i);
+          const uint4 x = *reinterpret_cast<const uint4*>(staged + i * 128 + ((c ^ (i & 7)) << 4));
+          if (to >= 0)
+            *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.out) + to * D + half * 64 + c * 8) = x;
+        }
+        __syncwarp();
+      };
+      auto put_lse = [&](float ref, float sum) {
+        if (valid && p.lse != nullptr)
+          p.lse[(int64_t)head * p.total_q + at.e.q0 + token] =
+              sum == 0.f ? neg_inf() : (ref + log2f(sum)) * kLn2;
+      };
+      const int slot = 2 * blockIdx.x + (at.t0 == 0 ? 1 : 0);
+      const int64_t my_part = ((int64_t)slot * 2 + g) * kM;
+      if (active) {
+        wait(&pv_done[g], (uint32_t)((n - 1) & 1), 64 + g);
+        tc::fence_after_sync();
+      }
+      const float by = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+      for (int i = 0; i < D / 32; ++i) {
+        float o[32];
+        if (active) {
+          tc::tmem_ld32(tO(g) + lane_off + i * 32, o);
+          tc::tmem_wait_ld();
+          arrived(o);
+        }
+        if (l == 0.f) {  // (no key, or none that is seen: O may hold nothing)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0.f;
+        }
+        if (whole) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8)
+            stage((i & 1) * 4 + e / 8, make_uint4(E::from_f2(o[e] * by, o[e + 1] * by),
+                                                  E::from_f2(o[e + 2] * by, o[e + 3] * by),
+                                                  E::from_f2(o[e + 4] * by, o[e + 5] * by),
+                                                  E::from_f2(o[e + 6] * by, o[e + 7] * by)));
+          if (i & 1) write_rows(i >> 1);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<float4*>(p.part_o + (my_part * (D / 4) + (i * 8 + e) * kM + r) * 4) =
+                make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        }
+      }
+      if (active) {
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&o_free[g]);
+      }
+      if (whole) {
+        put_lse(m, l);
+        continue;
+      }
+      p.part_ml[my_part + r] = make_float2(m, l);
+      const int cta0 = (int)(at.begin / share), cta1 = (int)((at.begin + at.all - 1) / share);
+      named_barrier(1, 256);  // the partial rows of the CTA before its arrival
+      if (tid == 0) {
+        __threadfence();
+        *sFlag = arrive_last(p.words + cta0, launch_tag(), cta1 - cta0 + 1) ? 1 : 0;
+        __threadfence();
+      }
+      named_barrier(1, 256);
+      const bool join = *sFlag != 0;
+      named_barrier(1, 256);  // the flag has been read
+      if (!join) continue;
+      // this thread's group's first row of part `cta`
+      auto from = [&](int cta) {
+        return ((int64_t)(2 * cta + (cta == cta0 ? 1 : 0)) * 2 + g) * kM;
+      };
+      float ref = neg_inf(), sum = 0.f;
+      for (int cta = cta0; cta <= cta1; ++cta)
+        ref = fmaxf(ref, __ldcg(p.part_ml + from(cta) + r).x);
+      // (a part without a seen key counts for nothing; a NaN in one without any
+      // number reaches the result)
+      auto weight = [&](float2 ml) {
+        return ml.y == 0.f ? 0.f : ml.x == ref ? 1.f : ex2(ml.x - ref);
+      };
+      for (int cta = cta0; cta <= cta1; ++cta) {
+        const float2 ml = __ldcg(p.part_ml + from(cta) + r);
+        sum = fmaf(weight(ml), ml.y, sum);
+      }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll 1
+      for (int i = 0; i < D / 32; ++i) {
+        float4 acc[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int cta = cta0; cta <= cta1; ++cta) {
+          float4 y[8];
+          const float2 ml = __ldcg(p.part_ml + from(cta) + r);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            y[e] = load16_l2(p.part_o + (from(cta) * (D / 4) + (i * 8 + e) * kM + r) * 4);
+          if (ml.y == 0.f) continue;
+          const float w = weight(ml);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            acc[e].x = fmaf(w, y[e].x, acc[e].x);
+            acc[e].y = fmaf(w, y[e].y, acc[e].y);
+            acc[e].z = fmaf(w, y[e].z, acc[e].z);
+            acc[e].w = fmaf(w, y[e].w, acc[e].w);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; e += 2)
+          stage((i & 1) * 4 + e / 2,
+                make_uint4(E::from_f2(acc[e].x * inv, acc[e].y * inv),
+                           E::from_f2(acc[e].z * inv, acc[e].w * inv),
+                           E::from_f2(acc[e + 1].x * inv, acc[e + 1].y * inv),
+                           E::from_f2(acc[e + 1].z * inv, acc[e + 1].w * inv)));
+        if (i & 1) write_rows(i >> 1);
+      }
+      put_lse(ref, sum);
+    }
+  }
+
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == kWarpMma) tc::tmem_dealloc(tbase, 512);
+}
+
+template <int D, typename T>
+cudaError_t launch(const CrossParams& p, const CUtensorMap& tmq, const CUtensorMap& tmk,
+                   const CUtensorMap& tmv, cudaStream_t st) {
+  static std::atomic<uint64_t> devices{0};
+  const cudaError_t e = allow_shared(reinterpret_cast<const void*>(wide_kernel<D, T>),
+                                     Layout<D>::kBytes, &devices);
+  if (e != cudaSuccess) return e;
+  wide_kernel<D, T><<<(unsigned)num_sms(), kThreads, Layout<D>::kBytes, st>>>(p, tmq, tmk, tmv);
+  return cudaGetLastError();
+}
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+}  // namespace
+
+// Of each CTA: an arrival word; m, l and O of two parts of two tiles.
+size_t cross_wide_workspace(int D) {
+  const size_t rows = (size_t)num_sms() * 2 * 2 * kM;
+  return align256((size_t)num_sms() * 8) + align256(rows * 8) + rows * D * 4;
+}
+
+cudaError_t launch_cross_wide(CrossParams p, const CUtensorMap& tmq, const CUtensorMap& tmk,
+                              const CUtensorMap& tmv, int D, int dtype, void* workspace,
+                              cudaStream_t st) {
+  const size_t rows = (size_t)num_sms() * 2 * 2 * kM;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.words = reinterpret_cast<unsigned long long*>(ws);
+  p.part_ml = reinterpret_cast<float2*>(ws + align256((size_t)num_sms() * 8));
+  p.part_o = reinterpret_cast<float*>(ws + align256((size_t)num_sms() * 8) + align256(rows * 8));
+  if (D == 64)
+    return dtype == PA_F16 ? launch<64, __half>(p, tmq, tmk, tmv, st)
+                           : launch<64, __nv_bfloat16>(p, tmq, tmk, tmv, st);
+  return dtype == PA_F16 ? launch<128, __half>(p, tmq, tmk, tmv, st)
+                         : launch<128, __nv_bfloat16>(p, tmq, tmk, tmv, st);
+}
+
+}  // namespace pa

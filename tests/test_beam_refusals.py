@@ -94,7 +94,7 @@ def test_copy_refusals(lib):
 def cross(lib, **kw):
     a = dict(q=P, q_st=256, q_sh=64, k=P, k_st=256, k_sh=64, v=P, v_st=256, v_sh=64, cu_q=P, cu_k=P,
              lens=None, mask=None, B=2, tq=5, tk=50, mq=4, mk=40, Hq=4, Hkv=2, D=64, scale=0.125, out=P,
-             lse=None, err=None, dtype=pa.PA_F16)
+             lse=None, ws=None, ws_bytes=0, err=None, dtype=pa.PA_F16)
     a.update(kw)
     return lib.pa_fwd_cross(*a.values(), None)
 
@@ -121,6 +121,12 @@ def test_cross_refusals(lib):
     assert cross(lib, tq=2 ** 31 - 1) == pa.PA_ERR_UNSUPPORTED
     assert cross(lib, tk=2 ** 31 - 1) == pa.PA_ERR_UNSUPPORTED
     assert cross(lib, B=1 << 20, tq=1 << 30, mq=1 << 20) == pa.PA_ERR_UNSUPPORTED
+    # many rows need a workspace
+    size = lib.pa_fwd_cross_workspace_size(500, 400, 4, 2, 64)
+    assert size > 0 and lib.pa_fwd_cross_workspace_size(5, 4, 4, 2, 64) == 0
+    many = dict(tq=500, mq=400, ws=P, ws_bytes=size)
+    for bad in (dict(ws=None), dict(ws=P + 16), dict(ws_bytes=size - 1)):
+        assert cross(lib, **{**many, **bad}) == pa.PA_ERR_WORKSPACE, bad
 
 
 def test_bindings_refuse_cpu_tensors():

@@ -87,6 +87,49 @@ def test_ragged(hq, hkv, d, dtype):
     check([5], [1000], hq, hkv, d, dtype, seed=1)
 
 
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("hq,hkv,d", HEADS + [(7, 1, 64), (20, 1, 128), (66, 2, 64), (130, 1, 64)])
+def test_ragged_with_many_rows(hq, hkv, d, dtype):
+    check([70, 1, 0, 37, 131], [300, 1, 33, 0, 129], hq, hkv, d, dtype, seed=hq + d, spare=3)
+
+
+@pytest.mark.parametrize("dtype,d", [("f16", 128), ("bf16", 64)])
+def test_long_streams_are_cut_and_joined(dtype, d):
+    check([90, 3], [9000, 130], 2, 2, d, dtype, seed=1)
+    # groups without rows in cut streams; a mask that leaves a whole part unseen
+    mask = torch.ones(9130, dtype=torch.bool, device=DEV)
+    mask[:4000] = False
+    mask[9000:] = False
+    check([90, 3], [9000, 130], 2, 2, d, dtype, seed=2, mask=mask)
+    check([300], [2000], 4, 1, d, dtype, seed=3)
+
+
+@pytest.mark.parametrize("rows", [1, 70])
+def test_many_entries(rows):
+    n = 1000
+    check([rows if i % 100 == 7 else i % 3 for i in range(n)], [i * 7 % 50 for i in range(n)], 2, 1, 64,
+          "f16", spare=1)
+
+
+@pytest.mark.parametrize("rows", [5, 80])
+def test_nan_in_seen_places_reaches_its_rows(rows):
+    q, k, v = inputs(9, [rows, rows], [300, 200], 4, 2, 64, "bf16")
+    q[2] = math.nan
+    k[310, 1] = math.nan
+    v[5, 0, 3] = math.nan
+    out, lse = pa.pa_fwd_cross(q, k, v, i32([0, rows, 2 * rows]), i32([0, 300, 500]), rows, 300)
+    bad = torch.isnan(out.float())
+    want = torch.zeros_like(bad)
+    want[2] = True
+    want[rows:, 2:] = True
+    want[:rows, :2, 3] = True
+    assert torch.equal(bad, want)
+    want = torch.zeros_like(lse, dtype=torch.bool)
+    want[:, 2] = True
+    want[2:, rows:] = True
+    assert torch.equal(torch.isnan(lse), want)
+
+
 @pytest.mark.parametrize("dtype,d", [("f16", 64), ("bf16", 64), ("f16", 128), ("bf16", 128)])
 @pytest.mark.parametrize("keys", [1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 511, 640])
 def test_key_counts(keys, dtype, d):
