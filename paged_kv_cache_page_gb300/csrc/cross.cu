@@ -40,6 +40,9 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 3;
 constexpr int kStageBytes = 8192;  // K and V of a tile of one head
+constexpr int kRows = 16;          // packed rows of an entry and kv head
+constexpr int kCtasPerSm = 2;
+constexpr int kFill = 2;
 constexpr int kMaxCluster = 16;
 constexpr float kRescale = 8.f;
 
@@ -70,11 +73,10 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// MT tiles of 16 packed rows a warp; a warp's heads are hs neighbouring ones.
-template <int D, typename T, int MT>
-__global__ void __launch_bounds__(kThreads, 2)
-    cross_kernel(const CrossParams p, const int hs, const int row_tiles,
-                 const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
+// A CTA's warps have hs neighbouring kv heads.
+template <int D, typename T>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+    cross_kernel(const __grid_constant__ CrossParams p, const int hs, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
   using E = Elem<T>;
   constexpr int TK = cross_narrow_box(D);  // keys of a tile
   constexpr int NT = TK / 8;               // its n-tiles
@@ -83,7 +85,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   constexpr int kSlab = TK * 128;          // 64 columns of K or V
   constexpr int kTensor = kSlab * (D / 64);
   static_assert(2 * kTensor == kStageBytes, "a stage holds K and V of a tile");
-  static_assert(MT * 16 * (D + 2) * 4 <= kStages * kStageBytes, "partial results fit in a ring");
+  static_assert(kRows * (D + 2) * 4 <= kStages * kStageBytes, "partial results fit in a ring");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ uint64_t s_full[kWarps][kStages];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -92,16 +94,13 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
-  // cluster -> entry, group of heads, tile of rows
-  int item = blockIdx.x / ranks;
-  const int rt = item % row_tiles;
-  item /= row_tiles;
+  // cluster -> entry, group of heads
+  const int item = blockIdx.x / ranks;
   const int groups = p.Hkv / hs;
   const int b = item / groups, h = (item - b * groups) * hs + warp % hs;
   const int slice = warp / hs, slices = kWarps / hs;
-  const CrossEntry e = cross_entry(p, b, tid == 0 && rank == 0 && rt == 0 && item % groups == 0);
-  const int row0 = rt * MT * 16;
-  const int rows = min(MT * 16, e.rows * p.G - row0);
+  const CrossEntry e = cross_entry(p, b, tid == 0 && rank == 0 && item % groups == 0);
+  const int rows = e.rows * p.G;
   if (rows <= 0) return;  // (the whole cluster)
 
   // this warp's tiles: `slices` warps take turns over the CTA's part
@@ -112,7 +111,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   uint8_t* ring = smem + warp * kStages * kStageBytes;
   uint64_t* full = s_full[warp];
-  const uint64_t policy = row_tiles > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
+  const uint64_t policy = l2_policy_evict_first();
   auto fill = [&](int i) {  // by one lane
     const int s = i % kStages, key = e.k0 + (t_begin + i * slices) * TK;
     mbar_arrive_expect_tx(&full[s], kStageBytes);
@@ -133,33 +132,28 @@ __global__ void __launch_bounds__(kThreads, 2)
   __syncwarp();
 
   // Q as the A operand; packed row r is query head h * G + r % G of row r / G
-  uint32_t qf[MT][KD][4];
+  uint32_t qf[KD][4];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int half = 0; half < 2; ++half) {
+    const int r = half * 8 + lane / 4;
+    const int at = r / p.G, g = r - at * p.G;
+    const T* src = reinterpret_cast<const T*>(p.q) + (int64_t)(e.q0 + at) * p.q_st +
+                   (int64_t)(h * p.G + g) * p.q_sh + 2 * (lane & 3);
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int r = m * 16 + half * 8 + lane / 4;
-      const int at = (row0 + r) / p.G, g = (row0 + r) - at * p.G;
-      const T* src = reinterpret_cast<const T*>(p.q) + (int64_t)(e.q0 + at) * p.q_st +
-                     (int64_t)(h * p.G + g) * p.q_sh + 2 * (lane & 3);
+    for (int k = 0; k < KD; ++k)
 #pragma unroll
-      for (int k = 0; k < KD; ++k)
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-          qf[m][k][2 * c + half] =
-              r < rows ? __ldg(reinterpret_cast<const uint32_t*>(src + k * 16 + c * 8)) : 0u;
-    }
-
-  float o[MT][ND][4], m_use[MT][2], l[MT][2];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-#pragma unroll
-    for (int i = 0; i < ND; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) o[m][i][j] = 0.f;
-    m_use[m][0] = m_use[m][1] = neg_inf();
-    l[m][0] = l[m][1] = 0.f;
+      for (int c = 0; c < 2; ++c)
+        qf[k][2 * c + half] =
+            r < rows ? __ldg(reinterpret_cast<const uint32_t*>(src + k * 16 + c * 8)) : 0u;
   }
+
+  float o[ND][4], m_use[2], l[2];
+#pragma unroll
+  for (int i = 0; i < ND; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
+  m_use[0] = m_use[1] = neg_inf();
+  l[0] = l[1] = 0.f;
   // the lane's key of tile i: whether it is seen
   auto seen = [&](int i) -> bool {
     const int key = (t_begin + i * slices) * TK + lane;
@@ -182,13 +176,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint32_t sk = smem_u32(ring + s * kStageBytes), sv = sk + kTensor;
 
     // S = Q K^T
-    float sc[MT][NT][4];
+    float sc[NT][4];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) sc[m][j][c] = 0.f;
+      for (int c = 0; c < 4; ++c) sc[j][c] = 0.f;
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -197,11 +189,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int key = j * 8 + (lane & 7), col = k * 2 + (lane >> 3);
         uint32_t r[4];
         ldsm4(r, sk + (col >> 3) * kSlab + key * 128 + (((col & 7) ^ (key & 7)) << 4));
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          mma<T>(sc[m][j], qf[m][k], r[0], r[1]);
-          mma<T>(sc[m][j], qf[m][k + 1], r[2], r[3]);
-        }
+        mma<T>(sc[j], qf[k], r[0], r[1]);
+        mma<T>(sc[j], qf[k + 1], r[2], r[3]);
       }
 
     // scores of unseen keys
@@ -210,46 +199,40 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int c = 0; c < 2; ++c)
-          if ((bits >> (j * 8 + 2 * (lane & 3) + c) & 1) == 0) {
-#pragma unroll
-            for (int m = 0; m < MT; ++m) sc[m][j][c] = sc[m][j][c + 2] = neg_inf();
-          }
+          if ((bits >> (j * 8 + 2 * (lane & 3) + c) & 1) == 0) sc[j][c] = sc[j][c + 2] = neg_inf();
     }
-    uint32_t pf[MT][NT / 2][4];
+    uint32_t pf[NT / 2][4];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int half = 0; half < 2; ++half) {
+      float top = neg_inf();
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        float top = neg_inf();
+      for (int j = 0; j < NT; ++j) top = fmaxf(top, fmaxf(sc[j][2 * half], sc[j][2 * half + 1]));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      top *= p.scale_log2;
+      float& mu = m_use[half];
+      const bool lift = top > mu + kRescale || (mu == neg_inf() && top != neg_inf());
+      if (__any_sync(0xffffffffu, lift)) {
+        const float f = lift ? ex2(mu - top) : 1.f;
+        if (lift) mu = top;
+        l[half] *= f;
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-          top = fmaxf(top, fmaxf(sc[m][j][2 * half], sc[m][j][2 * half + 1]));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        top *= p.scale_log2;
-        float& mu = m_use[m][half];
-        const bool lift = top > mu + kRescale || (mu == neg_inf() && top != neg_inf());
-        if (__any_sync(0xffffffffu, lift)) {
-          const float f = lift ? ex2(mu - top) : 1.f;
-          if (lift) mu = top;
-          l[m][half] *= f;
-#pragma unroll
-          for (int d = 0; d < ND; ++d) {
-            o[m][d][2 * half] *= f;
-            o[m][d][2 * half + 1] *= f;
-          }
+        for (int d = 0; d < ND; ++d) {
+          o[d][2 * half] *= f;
+          o[d][2 * half + 1] *= f;
         }
-        const float ref = mu == neg_inf() ? 0.f : -mu;
-        float sum = 0.f;
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const float a = ex2(fmaf(sc[m][j][2 * half], p.scale_log2, ref));
-          const float c = ex2(fmaf(sc[m][j][2 * half + 1], p.scale_log2, ref));
-          sum += a + c;
-          pf[m][j / 2][(j & 1) * 2 + half] = E::from_f2(a, c);
-        }
-        l[m][half] += sum;
       }
+      const float ref = mu == neg_inf() ? 0.f : -mu;
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const float a = ex2(fmaf(sc[j][2 * half], p.scale_log2, ref));
+        const float c = ex2(fmaf(sc[j][2 * half + 1], p.scale_log2, ref));
+        sum += a + c;
+        pf[j / 2][(j & 1) * 2 + half] = E::from_f2(a, c);
+      }
+      l[half] += sum;
+    }
 
     // O += P V
 #pragma unroll
@@ -270,11 +253,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             r[x + 2] &= keep;
           }
         }
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          mma<T>(o[m][d], pf[m][k], r[0], r[1]);
-          mma<T>(o[m][d + 1], pf[m][k], r[2], r[3]);
-        }
+        mma<T>(o[d], pf[k], r[0], r[1]);
+        mma<T>(o[d + 1], pf[k], r[2], r[3]);
       }
     __syncwarp();  // the stage has been read by every lane
     if (lane == 0 && ok && i + kStages < n) fill(i + kStages);
@@ -285,24 +265,22 @@ __global__ void __launch_bounds__(kThreads, 2)
       mbar_wait(&full[j % kStages], (uint32_t)(j / kStages & 1));
 
   // ---- the warp's partial result, over its own ring
-  float* part = reinterpret_cast<float*>(ring);  // [MT * 16][D], then m and l of each row
+  float* part = reinterpret_cast<float*>(ring);  // [kRows][D], then m and l of each row
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int half = 0; half < 2; ++half) {
+    float sum = l[half];
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    const int r = half * 8 + lane / 4;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      float sum = l[m][half];
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      const int r = m * 16 + half * 8 + lane / 4;
-#pragma unroll
-      for (int d = 0; d < ND; ++d)
-        *reinterpret_cast<float2*>(part + r * D + d * 8 + 2 * (lane & 3)) =
-            make_float2(o[m][d][2 * half], o[m][d][2 * half + 1]);
-      if ((lane & 3) == 0) {
-        part[MT * 16 * D + 2 * r] = m_use[m][half];
-        part[MT * 16 * D + 2 * r + 1] = sum;
-      }
+    for (int d = 0; d < ND; ++d)
+      *reinterpret_cast<float2*>(part + r * D + d * 8 + 2 * (lane & 3)) =
+          make_float2(o[d][2 * half], o[d][2 * half + 1]);
+    if ((lane & 3) == 0) {
+      part[kRows * D + 2 * r] = m_use[half];
+      part[kRows * D + 2 * r + 1] = sum;
     }
+  }
   cluster.sync();
 
   // ---- join: the CTAs share the rows of all heads
@@ -318,12 +296,12 @@ __global__ void __launch_bounds__(kThreads, 2)
                                      cta);
     };
     float top = neg_inf();
-    for (int i = 0; i < parts; ++i) top = fmaxf(top, from(i)[MT * 16 * D + 2 * r]);
+    for (int i = 0; i < parts; ++i) top = fmaxf(top, from(i)[kRows * D + 2 * r]);
     float sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int i = 0; i < parts; ++i) {
       const float* f = from(i);
-      const float mi = f[MT * 16 * D + 2 * r], li = f[MT * 16 * D + 2 * r + 1];
+      const float mi = f[kRows * D + 2 * r], li = f[kRows * D + 2 * r + 1];
       // (a part without a seen key counts for nothing; a NaN in one without any
       // number reaches the result)
       if (li == 0.f) continue;
@@ -336,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       acc.w += x * y.w;
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const int at = (row0 + r) / p.G, g = (row0 + r) - at * p.G;
+    const int at = r / p.G, g = r - at * p.G;
     const int head = (h - warp % hs + hh) * p.G + g;
     uint2 u;
     u.x = E::from_f2(acc.x * inv, acc.y * inv);
@@ -350,24 +328,22 @@ __global__ void __launch_bounds__(kThreads, 2)
   cluster.sync();  // no CTA leaves while its parts are read
 }
 
-template <int D, typename T, int MT>
+template <int D, typename T>
 cudaError_t launch_t(const CrossParams& p, const CUtensorMap& tmk, const CUtensorMap& tmv,
                      cudaStream_t st) {
   static std::atomic<uint64_t> asked{0}, wide{0}, allowed{0};
   constexpr int smem = kWarps * kStages * kStageBytes + 1024;
   const cudaError_t e =
-      allow_shared(reinterpret_cast<const void*>(cross_kernel<D, T, MT>), smem, &allowed);
+      allow_shared(reinterpret_cast<const void*>(cross_kernel<D, T>), smem, &allowed);
   if (e != cudaSuccess) return e;
   int hs = kWarps;
   while (p.Hkv % hs != 0) hs /= 2;
-  const long long most = (long long)p.max_q * p.G;
-  const int row_tiles = (int)((most + MT * 16 - 1) / (MT * 16));
-  const long long items = (long long)p.B * (p.Hkv / hs) * row_tiles;
+  const long long items = (long long)p.B * (p.Hkv / hs);
   if (items > 0x7fffffffll / kMaxCluster) return cudaErrorInvalidValue;
-  // as many CTAs as are resident (two an SM), with two tiles a warp at least
+  // as many CTAs as are resident, with two tiles a warp at least
   const int tiles = (p.max_k + cross_narrow_box(D) - 1) / cross_narrow_box(D);
   int ctas = 1;
-  while (ctas < kMaxCluster && items * ctas * 2 <= 2 * num_sms() &&
+  while (ctas < kMaxCluster && items * ctas * 2 <= kFill * num_sms() &&
          tiles >= ctas * 2 * 2 * (kWarps / hs))
     ctas *= 2;
   cudaLaunchConfig_t cfg{};
@@ -382,17 +358,10 @@ cudaError_t launch_t(const CrossParams& p, const CUtensorMap& tmk, const CUtenso
   for (;;) {
     cfg.gridDim = dim3((unsigned)(items * ctas));
     at.val.clusterDim.x = (unsigned)ctas;
-    if (ctas <= 8 || wide_clusters(cross_kernel<D, T, MT>, cfg, &asked, &wide)) break;
+    if (ctas <= 8 || wide_clusters(cross_kernel<D, T>, cfg, &asked, &wide)) break;
     ctas = 8;
   }
-  return cudaLaunchKernelEx(&cfg, cross_kernel<D, T, MT>, p, hs, row_tiles, tmk, tmv);
-}
-
-template <int D, typename T>
-cudaError_t launch_d(const CrossParams& p, const CUtensorMap& tmk, const CUtensorMap& tmv,
-                     cudaStream_t st) {
-  return (long long)p.max_q * p.G <= 16 ? launch_t<D, T, 1>(p, tmk, tmv, st)
-                                        : launch_t<D, T, 2>(p, tmk, tmv, st);
+  return cudaLaunchKernelEx(&cfg, cross_kernel<D, T>, p, hs, tmk, tmv);
 }
 
 }  // namespace
@@ -400,10 +369,10 @@ cudaError_t launch_d(const CrossParams& p, const CUtensorMap& tmk, const CUtenso
 cudaError_t launch_cross_narrow(const CrossParams& p, const CUtensorMap& tmk,
                                 const CUtensorMap& tmv, int D, int dtype, cudaStream_t st) {
   if (D == 64)
-    return dtype == PA_F16 ? launch_d<64, __half>(p, tmk, tmv, st)
-                           : launch_d<64, __nv_bfloat16>(p, tmk, tmv, st);
-  return dtype == PA_F16 ? launch_d<128, __half>(p, tmk, tmv, st)
-                         : launch_d<128, __nv_bfloat16>(p, tmk, tmv, st);
+    return dtype == PA_F16 ? launch_t<64, __half>(p, tmk, tmv, st)
+                           : launch_t<64, __nv_bfloat16>(p, tmk, tmv, st);
+  return dtype == PA_F16 ? launch_t<128, __half>(p, tmk, tmv, st)
+                         : launch_t<128, __nv_bfloat16>(p, tmk, tmv, st);
 }
 
 }  // namespace pa
@@ -422,10 +391,10 @@ bool fix_strides(int64_t* st, int64_t* sh, int64_t rows, int heads, int D) {
 }
 
 // More rows of a kv head than this run on tcgen05, whose tiles hold 128.
-constexpr int kNarrowRows = 64;
+constexpr int kNarrowRows = 16;
 bool is_wide(int total_q, int max_seqlen_q, int G) {
   const long long rows = (long long)(max_seqlen_q < total_q ? max_seqlen_q : total_q) * G;
-  return rows > kNarrowRows && G <= 128;
+  return rows > kNarrowRows;
 }
 
 }  // namespace
@@ -476,6 +445,9 @@ extern "C" PA_API int pa_fwd_cross(const void* q, int64_t q_st, int64_t q_sh, co
   if ((long long)B * Hkv * tiles > (1 << 26))
     return set_error(PA_ERR_UNSUPPORTED, "more than 2^26 tiles of 16 rows per kv head");
   const bool wide = is_wide(total_q, max_seqlen_q, G);
+  // (the most heads that fit in a tile of 128 rows and divide G)
+  int heads = G < 128 ? G : 128;
+  while (wide && G % heads != 0) --heads;
   if (wide && (workspace == nullptr || workspace_bytes < cross_wide_workspace(D) ||
                (reinterpret_cast<uintptr_t>(workspace) & 255) != 0))
     return set_error(PA_ERR_WORKSPACE, "workspace of %zu bytes, 256-byte aligned, is needed",
@@ -494,8 +466,9 @@ extern "C" PA_API int pa_fwd_cross(const void* q, int64_t q_st, int64_t q_sh, co
   p.max_q = max_q;
   p.max_k = max_k;
   p.Hq = Hq;
-  p.Hkv = Hkv;
-  p.G = G;
+  p.kv_split = wide ? G / heads : 1;
+  p.Hkv = Hkv * p.kv_split;
+  p.G = G / p.kv_split;
   p.scale_log2 = scale * kLog2e;
   p.out = out;
   p.lse = lse;
@@ -509,7 +482,7 @@ extern "C" PA_API int pa_fwd_cross(const void* q, int64_t q_st, int64_t q_sh, co
   CUtensorMap tmq, tmk, tmv;
   if (!encode_map(&tmk, kb, dtype, D, Hkv, rows, 1, k_sh, k_st, k_st, 64, 1, box, true) ||
       !encode_map(&tmv, vb, dtype, D, Hkv, rows, 1, v_sh, v_st, v_st, 64, 1, box, true) ||
-      (wide && !encode_map(&tmq, q, dtype, D, Hq, total_q, 1, q_sh, q_st, q_st, 64, G, 128 / G, true)))
+      (wide && !encode_map(&tmq, q, dtype, D, Hq, total_q, 1, q_sh, q_st, q_st, 64, p.G, 128 / p.G, true)))
     return set_error(PA_ERR_CUDA, "the tensor maps of q, k and v could not be encoded");
   const cudaError_t e = wide ? launch_cross_wide(p, tmq, tmk, tmv, D, dtype, workspace, st)
                              : launch_cross_narrow(p, tmk, tmv, D, dtype, st);

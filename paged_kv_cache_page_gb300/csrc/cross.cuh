@@ -19,7 +19,9 @@ struct CrossParams {
   void* out;
   float* lse;
   int32_t* err;
-  // the wide kernel's parts of cut streams
+  // The wide kernel takes at most 128 heads at a time: a kv head with more counts as
+  // kv_split of them (Hkv and G above are then those).  Its parts of cut streams:
+  int kv_split;
   unsigned long long* words;
   float2* part_ml;
   float* part_o;

@@ -17,12 +17,14 @@
 //   warp 10    issues O_g += P_g V (P_g from TMEM over S_g) and S_g = Q_g K^T
 //   warp 11    clears rows of V that no row sees (0 times what they hold may be NaN)
 // TMEM: S_0, S_1, O_0, O_1.  While one group's softmax runs, the tensor core works
-// on the other group.
+// on the other group.  Where a pair has rows for one tile only, the groups take
+// its tiles of keys in turn and their results are brought together at the end.
 //
 // Work: the streams (entry, kv head, pair of tiles) laid end to end in 128-key
-// tiles and dealt to the CTAs in equal shares; a stream that is cut is joined by
-// the CTA that finishes last.  Whole streams dealt in turn would leave the last
-// round of a few hundred streams half empty.
+// tiles and dealt to the CTAs in equal shares, with cuts near an end of a stream
+// moved there; a stream that is cut is joined by the CTA that finishes last.
+// Whole streams dealt in turn would leave the last round of a few hundred streams
+// half empty.
 #include <type_traits>
 
 #include "cross.cuh"
@@ -37,6 +39,7 @@ constexpr int kSlab = 128 * 128;
 constexpr int kWarpK = 8, kWarpV = 9, kWarpMma = 10, kWarpFix = 11;
 constexpr int kThreads = 12 * 32;
 constexpr int kMinShare = 2;  // tiles
+constexpr int kSnap = 4;      // tiles that a cut moves to an end of its stream
 
 template <int D>
 struct Layout {
@@ -51,7 +54,8 @@ struct Layout {
   // s_full, p_full, pv_done, o_free [2]
   static constexpr int kBars = 2 + 5 * kStages + 8;
   static constexpr int kOffSums = kOffBar + kBars * 8;  // long long [16]
-  static constexpr int kOffMisc = kOffSums + 16 * 8;    // start; TMEM base, flag
+  static constexpr int kOffSeen = kOffSums + 16 * 8;    // uint32 [kStages][4] keys of a tile
+  static constexpr int kOffMisc = kOffSeen + kStages * 16;  // start; TMEM base, flag
   static constexpr int kBytes = kOffMisc + 32 + 1024;
   static_assert(kBytes <= 232448, "shared memory");
 };
@@ -155,6 +159,10 @@ __device__ __noinline__ void scale_p(uint32_t t, int cols, float by) {
   tc::tmem_wait_st();
 }
 
+__device__ __forceinline__ void mbar_arrive_2(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], 2;" ::"r"(smem_u32(bar)) : "memory");
+}
+
 __device__ __forceinline__ float4 load16_l2(const void* src) {  // what another CTA has written
   float4 x;
   asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -174,17 +182,28 @@ __device__ __forceinline__ int entry_tiles(const CrossEntry& e) {
   return max(1, (e.keys + kN - 1) / kN);  // (without keys: one, to write the empty rows)
 }
 
-// A part of a CTA's share: tiles [t0, t0 + n) of a stream.
+// A part of a CTA's share: tiles [t0, t0 + n) of a stream.  The cuts are at whole
+// multiples of `share`; one that lies at most kSnap tiles behind a stream's begin
+// counts as there, else one that lies at most kSnap in front of its end as there.
 struct Walk {
-  int b, h, pair, t0, n, all, pairs;  // all: tiles of the stream
-  long long left;                     // of the share from t0 on
+  int b, h, pair, t0, n, all, pairs;  // all: tiles of the stream; n = 0: no more
   long long begin;                    // tiles of the streams in front
+  long long stop;                     // the cut behind the share; -1: none
   CrossEntry e;
 
+  __device__ __forceinline__ void take() {
+    const long long d = stop - begin;
+    n = stop < 0 || d >= all ? all - t0 : d <= kSnap ? 0 : d >= all - kSnap ? all - t0 : (int)d - t0;
+  }
   __device__ __forceinline__ void next(const CrossParams& p) {
-    left -= n;
+    if (t0 + n < all) {  // (cut)
+      n = 0;
+      return;
+    }
+    next_stream(p);
+  }
+  __device__ __forceinline__ void next_stream(const CrossParams& p) {
     n = 0;
-    if (left <= 0) return;
     begin += all;
     t0 = 0;
     if (++pair == pairs) {
@@ -192,17 +211,14 @@ struct Walk {
       if (++h == p.Hkv) {
         h = 0;
         do {
-          if (++b >= p.B) {  // (lengths that change under the launch)
-            left = 0;
-            return;
-          }
+          if (++b >= p.B) return;
           e = cross_entry(p, b, false);
           pairs = entry_pairs(p, e);
         } while (pairs == 0);
         all = entry_tiles(e);
       }
     }
-    n = (int)min((long long)all, left);
+    take();
   }
 };
 
@@ -235,6 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   long long* sStart = reinterpret_cast<long long*>(smem + L::kOffMisc);  // entry, tiles in front of it
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc + 16);
   int* sFlag = reinterpret_cast<int*>(smem + L::kOffMisc + 20);
+  uint32_t* sSeen = reinterpret_cast<uint32_t*>(smem + L::kOffSeen);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -251,50 +268,54 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&s_full[g], 1);
       mbar_init(&p_full[g], 4);
       mbar_init(&pv_done[g], 1);
-      mbar_init(&o_free[g], 4);
+      mbar_init(&o_free[g], 8);
     }
     fence_mbar_init();
   }
 
   // ---- the CTA's share: the tiles of all entries, then the entry it begins in
   long long total = 0, share = 0, start = 0;
+  {
+    long long cost = 0, x = 0;  // of entry b, and up to and with it
 #pragma unroll 1
-  for (int pass = 0; pass < 2; ++pass) {
-    long long before = 0;
+    for (int pass = 0; pass < 2; ++pass) {
+      long long before = 0;
 #pragma unroll 1
-    for (int b0 = 0; b0 < p.B; b0 += kThreads) {
-      const int b = b0 + tid;
-      long long cost = 0;
-      if (b < p.B) {
-        const CrossEntry e = cross_entry(p, b, pass == 0 && blockIdx.x == 0);
-        cost = (long long)entry_pairs(p, e) * p.Hkv * entry_tiles(e);
+      for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+        const int b = b0 + tid;
+        if (pass == 0 || p.B > kThreads) {
+          cost = 0;
+          if (b < p.B) {
+            const CrossEntry e = cross_entry(p, b, pass == 0 && blockIdx.x == 0);
+            cost = (long long)entry_pairs(p, e) * p.Hkv * entry_tiles(e);
+          }
+          x = cost;
+#pragma unroll 1
+          for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+          }
+          __syncthreads();  // (sSums have been read)
+          if (lane == 31) sSums[warp] = x;
+          __syncthreads();
+          x += before;
+#pragma unroll 1
+          for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) x += sSums[w];
+            before += sSums[w];
+          }
+        }
+        if (pass == 1 && cost > 0 && start >= x - cost && start < x) {
+          sStart[0] = b;
+          sStart[1] = x - cost;
+        }
       }
-      long long x = cost;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+      if (pass == 0) {
+        total = before;
+        share = max((long long)kMinShare, (total + gridDim.x - 1) / gridDim.x);
+        start = share * blockIdx.x;
+        if (start >= total) return;  // (the whole CTA)
       }
-      __syncthreads();  // (sSums of the pass before have been read)
-      if (lane == 31) sSums[warp] = x;
-      __syncthreads();
-      long long in_front = before, all = 0;
-      for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) in_front += sSums[w];
-        all += sSums[w];
-      }
-      x += in_front;  // up to and with entry b
-      if (pass == 1 && cost > 0 && start >= x - cost && start < x) {
-        sStart[0] = b;
-        sStart[1] = x - cost;
-      }
-      before += all;
-    }
-    if (pass == 0) {
-      total = before;
-      share = max((long long)kMinShare, (total + gridDim.x - 1) / gridDim.x);
-      start = share * blockIdx.x;
-      if (start >= total) return;  // (the whole CTA)
     }
   }
   __syncthreads();
@@ -303,14 +324,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   at.e = cross_entry(p, at.b, false);
   at.pairs = entry_pairs(p, at.e);
   at.all = entry_tiles(at.e);
-  at.left = min(share, total - start);
+  at.stop = start + share < total ? start + share : -1;
   {
     const long long off = start - sStart[1], stream = off / at.all;
     at.begin = sStart[1] + stream * at.all;
     at.t0 = (int)(off - stream * at.all);
     at.h = (int)(stream / at.pairs);
     at.pair = (int)(stream - (long long)at.h * at.pairs);
-    at.n = (int)min((long long)(at.all - at.t0), at.left);
+    if (at.t0 <= kSnap) at.t0 = 0;
+    if (at.t0 > 0 && at.t0 >= at.all - kSnap) at.next_stream(p);
+    else at.take();
   }
   const int tokens = kM / p.G, tile_rows = tokens * p.G;
 
@@ -330,8 +353,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tbase = *tslot;
   auto tS = [&](int g) { return tbase + (uint32_t)(g * 128); };
   auto tO = [&](int g) { return tbase + 256u + (uint32_t)(g * D); };
-  // Whether group g has rows in the part, and tiles of keys are read for it.
-  auto has_rows = [&](const Walk& w, int g) { return (2 * w.pair + g) * tokens < w.e.rows; };
+  // One tile of rows: the groups take its tiles of keys in turn.
+  auto solo = [&](const Walk& w) { return (2 * w.pair + 1) * tokens >= w.e.rows; };
 
   bool failed = false;
   auto wait = [&](uint64_t* bar, uint32_t par, int where) {
@@ -353,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       tma_prefetch_desc(map);
       if (!is_v) tma_prefetch_desc(&tmq);
-      for (; at.left > 0; at.next(p)) {
+      for (; at.n > 0; at.next(p)) {
         if (at.e.keys == 0) continue;
         for (int t = at.t0; t < at.t0 + at.n; ++t, ++k) {
           const int s = k % L::kStages;
@@ -361,13 +384,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (failed) break;
           mbar_arrive_expect_tx(&full[s], L::kTile);
           for (int c = 0; c < D / 64; ++c)
-            tma_load_4d(ring + s * L::kTile + c * kSlab, map, &full[s], c * 64, at.h,
+            tma_load_4d(ring + s * L::kTile + c * kSlab, map, &full[s], c * 64, at.h / p.kv_split,
                         at.e.k0 + t * kN, 0, keep);
           if (!is_v && t == at.t0) {
             if (a >= 1) wait(q_empty, (uint32_t)((a - 1) & 1), 10);
             if (failed) break;
-            mbar_arrive_expect_tx(q_full, (uint32_t)(2 * (D / 64) * tile_rows * 128));
-            for (int g = 0; g < 2; ++g)
+            const int q_tiles = solo(at) ? 1 : 2;
+            mbar_arrive_expect_tx(q_full, (uint32_t)(q_tiles * (D / 64) * tile_rows * 128));
+            for (int g = 0; g < q_tiles; ++g)
               for (int c = 0; c < D / 64; ++c)
                 tma_load_4d(sQ + g * L::kTile + c * kSlab, &tmq, q_full, c * 64, at.h * p.G,
                             at.e.q0 + (2 * at.pair + g) * tokens, 0, once);
@@ -387,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kWarpFix) {
     // ======================= rows of V that no row sees =======================
     int k = 0;
-    for (; at.left > 0; at.next(p)) {
+    for (; at.n > 0; at.next(p)) {
       if (at.e.keys == 0) continue;
       for (int t = at.t0; t < at.t0 + at.n; ++t, ++k) {
         const int s = k % L::kStages;
@@ -404,6 +428,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         wait(&v_full[s], (uint32_t)(k / L::kStages & 1), 25);
         if (!whole) {
+          if (lane < kN / 32)  // (the stage's words have been read: P V of its last tile is done)
+            sSeen[s * 4 + lane] = ~(lane == 0 ? drop[0] : lane == 1 ? drop[1] : lane == 2 ? drop[2] : drop[3]);
           uint8_t* tile = sV + s * L::kTile;
 #pragma unroll 1
           for (int c = 0; c < kN / 32; ++c) {
@@ -448,8 +474,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         : "=r"(on));
     const uint32_t tb = uni(tbase);
     int k = 0, a = 0, n0 = 0, n1 = 0, m0 = 0, m1 = 0;
-    auto scores = [&](int g, int s) {
-      const uint32_t q0 = uni(qlo + (uint32_t)((g * L::kTile) >> 4));
+    auto scores = [&](int g, int q_tile, int s) {
+      const uint32_t q0 = uni(qlo + (uint32_t)((q_tile * L::kTile) >> 4));
       const uint32_t k0 = uni(klo + (uint32_t)((s * L::kTile) >> 4));
       const uint32_t ts = uni(tb + g * 128);
 #pragma unroll
@@ -464,51 +490,52 @@ __global__ void __launch_bounds__(kThreads, 1)
       commit_if(on, bar);
       __syncwarp();
     };
-    for (; at.left > 0; at.next(p)) {
-      if (at.e.keys == 0) continue;
-      const int groups = has_rows(at, 1) ? 2 : 1;
-      wait(q_full, (uint32_t)(a & 1), 40);
-      wait(&k_full[k % L::kStages], (uint32_t)(k / L::kStages & 1), 41);
-      tc::fence_after_sync();
-      for (int g = 0; g < groups; ++g) scores(g, k % L::kStages);
-      release(&k_empty[k % L::kStages]);
-      if (at.n == 1) release(q_empty);
-      for (int t = 0; t < at.n; ++t, ++k) {
-        const int s = k % L::kStages, sn = (k + 1) % L::kStages;
-        const bool more = t + 1 < at.n;
-        wait(&v_ready[s], (uint32_t)(k / L::kStages & 1), 50);
-#pragma unroll 1
-        for (int g = 0; g < groups; ++g) {
-          const int n = g ? n1 : n0, m = g ? m1 : m0;
-          wait(&p_full[g], (uint32_t)(n & 1), 51 + g);
-          if (t == 0 && m >= 1) wait(&o_free[g], (uint32_t)((m - 1) & 1), 53 + g);
-          tc::fence_after_sync();
-          const uint32_t v0 = uni(vlo + (uint32_t)((s * L::kTile) >> 4));
-          const uint32_t ts = uni(tb + g * 128), to = uni(tb + 256 + g * D);
-          const uint32_t add = uni(t > 0);
+    auto values = [&](int g, int s, bool add) {  // O_g (+)= P_g V
+      const uint32_t v0 = uni(vlo + (uint32_t)((s * L::kTile) >> 4));
+      const uint32_t ts = uni(tb + g * 128), to = uni(tb + 256 + g * D);
+      const uint32_t more = uni(add);
 #pragma unroll
-          for (int kk = 0; kk < kN / 16; ++kk)
-            mma_ts_if(on, to, ts + kk * 8, desc(dslab, v0 + (kk * 2048 >> 4)), id_o,
-                      kk > 0 ? 1u : add);
-          commit_if(on, &pv_done[g]);
-          __syncwarp();
-          if (g) ++n1;
-          else ++n0;
-          if (more) {
-            if (g == 0) {
-              wait(&k_full[sn], (uint32_t)((k + 1) / L::kStages & 1), 42);
-              tc::fence_after_sync();
-            }
-            scores(g, sn);
-          }
-        }
-        release(&v_empty[s]);
-        if (more) release(&k_empty[sn]);
-        if (t + 2 == at.n) release(q_empty);  // the part's last scores
+      for (int kk = 0; kk < kN / 16; ++kk)
+        mma_ts_if(on, to, ts + kk * 8, desc(dslab, v0 + (kk * 2048 >> 4)), id_o, kk > 0 ? 1u : more);
+      commit_if(on, &pv_done[g]);
+      __syncwarp();
+    };
+    for (; at.n > 0; at.next(p)) {
+      if (at.e.keys == 0) continue;
+      // steps of the part: (tile, group), a tile's two groups or one of them
+      const bool one = solo(at);
+      wait(q_full, (uint32_t)(a & 1), 40);
+      auto first = [&](int g, int t, bool last_of_tile) {
+        const int s = (k + t) % L::kStages;
+        wait(&k_full[s], (uint32_t)((k + t) / L::kStages & 1), 41);
+        tc::fence_after_sync();
+        scores(g, one ? 0 : g, s);
+        if (last_of_tile) release(&k_empty[s]);
+        if (last_of_tile && t == at.n - 1) release(q_empty);  // the part's last scores
+      };
+      first(0, 0, one);
+      if (!one) first(1, 0, true);
+      else if (at.n > 1) first(1, 1, true);
+#pragma unroll 1
+      for (int i = 0; i < (one ? at.n : 2 * at.n); ++i) {
+        const int g = i & 1, t = one ? i : i >> 1, next_t = one ? i + 2 : t + 1;
+        const int s = (k + t) % L::kStages;
+        const int n = g ? n1 : n0, m = g ? m1 : m0;
+        const bool fresh = one ? i < 2 : t == 0;
+        if (one || g == 0) wait(&v_ready[s], (uint32_t)((k + t) / L::kStages & 1), 50);
+        wait(&p_full[g], (uint32_t)(n & 1), 51 + g);
+        if (fresh && m >= 1) wait(&o_free[g], (uint32_t)((m - 1) & 1), 53 + g);
+        tc::fence_after_sync();
+        values(g, s, !fresh);
+        if (g) ++n1;
+        else ++n0;
+        if (next_t < at.n) first(g, next_t, one || g == 1);
+        if (one || g == 1) release(&v_empty[s]);
       }
+      k += at.n;
       ++a;
       ++m0;
-      if (groups == 2) ++m1;
+      ++m1;
     }
   } else {
     // ======================= softmax =======================
@@ -517,29 +544,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const float f = p.scale_log2;
     uint8_t* staged = smem + L::kOffOut + warp * 4096;
-    int n = 0;
-    for (; at.left > 0; at.next(p)) {
-      if (!has_rows(at, g)) {
-        // (the barriers of a cut stream are both groups')
-        if (at.n == at.all) continue;
-      }
-      const int token = (2 * at.pair + g) * tokens + r / p.G, head = at.h * p.G + r % p.G;
+    int done[2] = {0, 0}, k = 0;  // tiles of either group, of the CTA
+    for (; at.n > 0; at.next(p)) {
+      const bool one = solo(at);
+      const int tile = one ? 0 : g;  // the group's rows
+      const int token = (2 * at.pair + tile) * tokens + r / p.G, head = at.h * p.G + r % p.G;
       const bool valid = r < tile_rows && token < at.e.rows;
-      const bool active = has_rows(at, g) && at.e.keys > 0;
       float m = neg_inf(), l = 0.f;
-      for (int t = at.t0; active && t < at.t0 + at.n; ++t) {
-        const bool whole = p.key_mask == nullptr && (t + 1) * kN <= at.e.keys;
-        uint32_t seen[kN / 32];
-        if (!whole) {
-#pragma unroll
-          for (int c = 0; c < kN / 32; ++c) {
-            const int key = t * kN + c * 32 + lane;
-            seen[c] = __ballot_sync(
-                0xffffffffu, key < at.e.keys && (p.key_mask == nullptr ||
-                                                 __ldg(p.key_mask + at.e.k0 + key) != 0));
-          }
-        }
+      int n = g ? done[1] : done[0];
+      for (int j = one ? g : 0; j < at.n && at.e.keys > 0; j += one ? 2 : 1) {
+        const bool whole = p.key_mask == nullptr && (at.t0 + j + 1) * kN <= at.e.keys;
+        const int stage = (k + j) % L::kStages;
         wait(&s_full[g], (uint32_t)(n & 1), 60 + g);
+        // (behind the scores, whose issue waited for the stage's tile before)
+        if (!whole) wait(&v_ready[stage], (uint32_t)((k + j) / L::kStages & 1), 66);
         tc::fence_after_sync();
         const uint32_t ts = tS(g) + lane_off;
         uint64_t sum2[4] = {0, 0, 0, 0};  // four pairs of sums
@@ -597,12 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < kN; c += 32) {
             tc::tmem_ld32(ts + c, v);
             uint32_t bits = 0;
-            if constexpr (masked) {
-              bits = seen[0];
-              if (c == 32) bits = seen[1];
-              if (c == 64) bits = seen[2];
-              if (c == 96) bits = seen[3];
-            }
+            if constexpr (masked) bits = sSeen[stage * 4 + c / 32];
             tc::tmem_wait_ld();
             arrived(v);
             probabilities(masked, c, bits);
@@ -612,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         else row(std::true_type{});
         const float2 sum = halves(add2(add2(sum2[0], sum2[1]), add2(sum2[2], sum2[3])));
         l += sum.x + sum.y;
-        if (t > at.t0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+        if (j >= (one ? 2 : 1) && __any_sync(0xffffffffu, alpha != 1.f)) {
           // O_g is still once P V of the group's previous tile is done
           wait(&pv_done[g], (uint32_t)((n - 1) & 1), 62 + g);
           tc::fence_after_sync();
@@ -633,76 +646,120 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++n;
       }
 
-      // ---- the part's result
-      const bool whole = at.n == at.all;
+      if (at.e.keys > 0) {
+        k += at.n;
+        done[0] += one ? (at.n + 1) / 2 : at.n;
+        done[1] += one ? at.n / 2 : at.n;
+      }
+
+      // ---- the part's result: the group's rows, or half of the columns of the one
+      // tile's rows, whose results are those of both groups
+      const bool whole = at.t0 == 0 && at.n == at.all;
+      const int col0 = one ? g * (D / 2) : 0, cols = one ? D / 2 : D;
       const long long my_row = valid ? (long long)(at.e.q0 + token) * p.Hq + head : -1;
-      // 64 columns of the warp's rows by way of shared memory: a thread holds a row,
-      // and whole lines are written
-      auto stage = [&](int c, uint4 x) {
-        *reinterpret_cast<uint4*>(staged + lane * 128 + ((c ^ (lane & 7)) << 4)) = x;
-      };
-      auto write_rows = [&](int half) {
-        const int c = lane & 7;
-        __syncwarp();
+      // 32 columns of the warp's rows by way of shared memory: a thread holds a row,
+      // and whole sectors of few rows are written at a time
+      auto write = [&](int col, const float (&x)[32], float by) {
+        uint8_t* buf = staged + (col >> 5 & 1) * 2048;
 #pragma unroll
-        for (int i = lane >> 3; i < 32; i += 4) {
+        for (int e = 0; e < 32; e += 8)
+          *reinterpret_cast<uint4*>(buf + lane * 64 + (((e >> 3) ^ (lane >> 1 & 3)) << 4)) =
+              make_uint4(E::from_f2(x[e] * by, x[e + 1] * by), E::from_f2(x[e + 2] * by, x[e + 3] * by),
+                         E::from_f2(x[e + 4] * by, x[e + 5] * by),
+                         E::from_f2(x[e + 6] * by, x[e + 7] * by));
+        __syncwarp();
+        const int c = lane & 3;
+#pragma unroll
+        for (int i = lane >> 2; i < 32; i += 8) {
           const long long to = __shfl_sync(0xffffffffu, my_row, i);
-          const uint4 x = *reinterpret_cast<const uint4*>(staged + i * 128 + ((c ^ (i & 7)) << 4));
+          const uint4 y = *reinterpret_cast<const uint4*>(buf + i * 64 + ((c ^ (i >> 1 & 3)) << 4));
           if (to >= 0)
-            *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.out) + to * D + half * 64 + c * 8) = x;
+            *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.out) + to * D + col + c * 8) = y;
         }
         __syncwarp();
       };
       auto put_lse = [&](float ref, float sum) {
-        if (valid && p.lse != nullptr)
+        if (valid && (!one || g == 0) && p.lse != nullptr)
           p.lse[(int64_t)head * p.total_q + at.e.q0 + token] =
               sum == 0.f ? neg_inf() : (ref + log2f(sum)) * kLn2;
       };
-      const int slot = 2 * blockIdx.x + (at.t0 == 0 ? 1 : 0);
-      const int64_t my_part = ((int64_t)slot * 2 + g) * kM;
-      if (active) {
-        wait(&pv_done[g], (uint32_t)((n - 1) & 1), 64 + g);
-        tc::fence_after_sync();
-      }
-      const float by = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll 1
-      for (int i = 0; i < D / 32; ++i) {
-        float o[32];
-        if (active) {
-          tc::tmem_ld32(tO(g) + lane_off + i * 32, o);
-          tc::tmem_wait_ld();
-          arrived(o);
-        }
-        if (l == 0.f) {  // (no key, or none that is seen: O may hold nothing)
+      if (at.e.keys == 0) {
+        float zero[32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0.f;
+        for (int e = 0; e < 32; ++e) zero[e] = 0.f;
+#pragma unroll 1
+        for (int col = col0; col < col0 + cols; col += 32) write(col, zero, 0.f);
+        put_lse(m, l);
+        continue;
+      }
+      // What O_0 and O_1 count for (a part without a seen key counts for nothing,
+      // and its O may hold nothing).
+      float2 half[2] = {make_float2(m, l), make_float2(m, l)};
+      if (one) {
+        // (by way of the warps' places for results)
+        reinterpret_cast<float2*>(staged)[lane] = half[0];
+        named_barrier(1, 256);
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          half[x] = reinterpret_cast<const float2*>(smem + L::kOffOut + (4 * x + quarter) * 4096)[lane];
+        named_barrier(1, 256);  // (read, before it is written again)
+        m = fmaxf(half[0].x, half[1].x);
+      }
+      auto weight = [](float2 x, float ref) {
+        return x.y == 0.f ? 0.f : x.x == ref ? 1.f : ex2(x.x - ref);
+      };
+      const float weight0 = weight(half[0], m), weight1 = weight(half[1], m);
+      if (one) l = fmaf(weight0, half[0].y, weight1 * half[1].y);
+      // P V of either group's last tile (the other group's softmax of it is done)
+      if (one || g == 0) wait(&pv_done[0], (uint32_t)((done[0] - 1) & 1), 64);
+      if (one ? at.n > 1 : g == 1) wait(&pv_done[1], (uint32_t)((done[1] - 1) & 1), 65);
+      tc::fence_after_sync();
+      const float by = l == 0.f ? 0.f : 1.f / l;
+      const int slot = 2 * blockIdx.x + (at.t0 == 0 ? 1 : 0);
+      const int64_t my_part = ((int64_t)slot * 2 + tile) * kM;
+#pragma unroll 1
+      for (int col = col0; col < col0 + cols; col += 32) {
+        float o[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = 0.f;
+#pragma unroll 1
+        for (int x = one ? 0 : g; x < (one ? min(at.n, 2) : g + 1); ++x) {
+          float y[32];
+          tc::tmem_ld32(tO(x) + lane_off + col, y);
+          tc::tmem_wait_ld();
+          arrived(y);
+          const float w = x ? weight1 : weight0;
+          if ((x ? half[1] : half[0]).y != 0.f) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = fmaf(w, y[e], o[e]);
+          }
         }
         if (whole) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 8)
-            stage((i & 1) * 4 + e / 8, make_uint4(E::from_f2(o[e] * by, o[e + 1] * by),
-                                                  E::from_f2(o[e + 2] * by, o[e + 3] * by),
-                                                  E::from_f2(o[e + 4] * by, o[e + 5] * by),
-                                                  E::from_f2(o[e + 6] * by, o[e + 7] * by)));
-          if (i & 1) write_rows(i >> 1);
-        } else {
+          write(col, o, by);
+        } else if (valid) {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            *reinterpret_cast<float4*>(p.part_o + (my_part * (D / 4) + (i * 8 + e) * kM + r) * 4) =
+            *reinterpret_cast<float4*>(p.part_o + (my_part * (D / 4) + (col / 4 + e) * kM + r) * 4) =
                 make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         }
       }
-      if (active) {
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&o_free[g]);
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        if (one) {
+          mbar_arrive(&o_free[0]);
+          mbar_arrive(&o_free[1]);
+        } else {
+          mbar_arrive_2(&o_free[g]);
+        }
       }
       if (whole) {
         put_lse(m, l);
         continue;
       }
-      p.part_ml[my_part + r] = make_float2(m, l);
-      const int cta0 = (int)(at.begin / share), cta1 = (int)((at.begin + at.all - 1) / share);
+      if (valid && (!one || g == 0)) p.part_ml[my_part + r] = make_float2(m, l);
+      const int cta0 = (int)((at.begin + min(kSnap, at.all - 1)) / share),
+                cta1 = max(cta0, (int)((at.begin + at.all - kSnap - 1) / share));
       named_barrier(1, 256);  // the partial rows of the CTA before its arrival
       if (tid == 0) {
         __threadfence();
@@ -713,53 +770,46 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool join = *sFlag != 0;
       named_barrier(1, 256);  // the flag has been read
       if (!join) continue;
-      // this thread's group's first row of part `cta`
+      // the row's place in part `cta`
       auto from = [&](int cta) {
-        return ((int64_t)(2 * cta + (cta == cta0 ? 1 : 0)) * 2 + g) * kM;
+        return ((int64_t)(2 * cta + (cta == cta0 ? 1 : 0)) * 2 + tile) * kM + r;
       };
       float ref = neg_inf(), sum = 0.f;
-      for (int cta = cta0; cta <= cta1; ++cta)
-        ref = fmaxf(ref, __ldcg(p.part_ml + from(cta) + r).x);
-      // (a part without a seen key counts for nothing; a NaN in one without any
-      // number reaches the result)
-      auto weight = [&](float2 ml) {
-        return ml.y == 0.f ? 0.f : ml.x == ref ? 1.f : ex2(ml.x - ref);
-      };
-      for (int cta = cta0; cta <= cta1; ++cta) {
-        const float2 ml = __ldcg(p.part_ml + from(cta) + r);
-        sum = fmaf(weight(ml), ml.y, sum);
+      if (valid) {
+        for (int cta = cta0; cta <= cta1; ++cta) ref = fmaxf(ref, __ldcg(p.part_ml + from(cta)).x);
+        for (int cta = cta0; cta <= cta1; ++cta) {
+          const float2 ml = __ldcg(p.part_ml + from(cta));
+          sum = fmaf(weight(ml, ref), ml.y, sum);
+        }
       }
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll 1
-      for (int i = 0; i < D / 32; ++i) {
-        float4 acc[8];
+      for (int col = col0; col < col0 + cols; col += 32) {
+        float o[32];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int e = 0; e < 32; ++e) o[e] = 0.f;
+        if (valid) {
 #pragma unroll 1
-        for (int cta = cta0; cta <= cta1; ++cta) {
-          float4 y[8];
-          const float2 ml = __ldcg(p.part_ml + from(cta) + r);
+          for (int cta = cta0; cta <= cta1; ++cta) {
+            float4 y[8];
+            const float2 ml = __ldcg(p.part_ml + from(cta));
+            const int64_t row = from(cta) - r;
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            y[e] = load16_l2(p.part_o + (from(cta) * (D / 4) + (i * 8 + e) * kM + r) * 4);
-          if (ml.y == 0.f) continue;
-          const float w = weight(ml);
+            for (int e = 0; e < 8; ++e)
+              y[e] = load16_l2(p.part_o + (row * (D / 4) + (col / 4 + e) * kM + r) * 4);
+            if (ml.y == 0.f) continue;
+            const float w = weight(ml, ref);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            acc[e].x = fmaf(w, y[e].x, acc[e].x);
-            acc[e].y = fmaf(w, y[e].y, acc[e].y);
-            acc[e].z = fmaf(w, y[e].z, acc[e].z);
-            acc[e].w = fmaf(w, y[e].w, acc[e].w);
+            for (int e = 0; e < 8; ++e) {
+              o[4 * e] = fmaf(w, y[e].x, o[4 * e]);
+              o[4 * e + 1] = fmaf(w, y[e].y, o[4 * e + 1]);
+              o[4 * e + 2] = fmaf(w, y[e].z, o[4 * e + 2]);
+              o[4 * e + 3] = fmaf(w, y[e].w, o[4 * e + 3]);
+            }
           }
         }
-#pragma unroll
-        for (int e = 0; e < 8; e += 2)
-          stage((i & 1) * 4 + e / 2,
-                make_uint4(E::from_f2(acc[e].x * inv, acc[e].y * inv),
-                           E::from_f2(acc[e].z * inv, acc[e].w * inv),
-                           E::from_f2(acc[e + 1].x * inv, acc[e + 1].y * inv),
-                           E::from_f2(acc[e + 1].z * inv, acc[e + 1].w * inv)));
-        if (i & 1) write_rows(i >> 1);
+        __syncwarp();
+        write(col, o, inv);
       }
       put_lse(ref, sum);
     }
