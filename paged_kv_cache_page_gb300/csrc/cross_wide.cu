@@ -50,14 +50,17 @@ struct Layout {
   static constexpr int kOffV = kOffK + kStages * kTile;
   static constexpr int kOffOut = kOffV + kStages * kTile;  // [8 warps][32 rows][128 bytes]
   static constexpr int kOffBar = kOffOut + 8 * 4096;
+  static constexpr int kLimits = kStages + 1;              // tiles whose limits are held
   // q_full, q_empty; k_full, k_empty, v_full, v_ready, v_empty [kStages];
-  // s_full, p_full, pv_done, o_free [2]
-  static constexpr int kBars = 2 + 5 * kStages + 8;
+  // s_full, p_full, pv_done, o_free [2]; l_full [kLimits]
+  static constexpr int kBars = 2 + 5 * kStages + 8 + kLimits;
   static constexpr int kOffSums = kOffBar + kBars * 8;  // long long [16]
-  static constexpr int kOffSeen = kOffSums + 16 * 8;    // uint32 [kStages][4] keys of a tile
-  static constexpr int kOffMisc = kOffSeen + kStages * 16;  // start; TMEM base, flag
+  static constexpr int kOffLimit = (kOffSums + 16 * 8 + 15) & ~15;  // float [kLimits][kN] of scores
+  static constexpr int kOffMisc = kOffLimit + kLimits * kN * 4;  // start; TMEM base, flag
   static constexpr int kBytes = kOffMisc + 32 + 1024;
   static_assert(kBytes <= 232448, "shared memory");
+  static_assert(kOffOut % 16 == 0 && kOffLimit % 16 == 0, "read 16 bytes at a time");
+  static_assert(kOffSums % 8 == 0 && kOffMisc % 8 == 0, "64-bit values");
 };
 
 // P of the type: the largest score is brought to 2^shift at first, and may pass
@@ -247,11 +250,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* p_full = s_full + 2;
   uint64_t* pv_done = p_full + 2;
   uint64_t* o_free = pv_done + 2;
+  uint64_t* l_full = o_free + 2;
   long long* sSums = reinterpret_cast<long long*>(smem + L::kOffSums);
   long long* sStart = reinterpret_cast<long long*>(smem + L::kOffMisc);  // entry, tiles in front of it
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc + 16);
   int* sFlag = reinterpret_cast<int*>(smem + L::kOffMisc + 20);
-  uint32_t* sSeen = reinterpret_cast<uint32_t*>(smem + L::kOffSeen);
+  float* sLimit = reinterpret_cast<float*>(smem + L::kOffLimit);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -270,6 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&pv_done[g], 1);
       mbar_init(&o_free[g], 8);
     }
+    for (int i = 0; i < L::kLimits; ++i) mbar_init(&l_full[i], 1);
     fence_mbar_init();
   }
 
@@ -409,40 +414,47 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp == kWarpFix) {
-    // ======================= rows of V that no row sees =======================
+    // ======================= limits of scores, rows of V that no row sees =====
     int k = 0;
     for (; at.n > 0; at.next(p)) {
       if (at.e.keys == 0) continue;
+      auto mask_bytes = [&](int t) -> uint32_t {  // of the lane's four keys of tile t
+        uint32_t x = 0;
+#pragma unroll
+        for (int c = 0; c < kN / 32; ++c) {
+          const int key = t * kN + c * 32 + lane;
+          if (key < at.e.keys && (p.key_mask == nullptr || __ldg(p.key_mask + at.e.k0 + key) != 0))
+            x |= 1u << c;
+        }
+        return x;
+      };
+      uint32_t next = mask_bytes(at.t0);
+#pragma unroll 1
       for (int t = at.t0; t < at.t0 + at.n; ++t, ++k) {
-        const int s = k % L::kStages;
+        const int s = k % L::kStages, place = k % L::kLimits;
         const bool whole = p.key_mask == nullptr && (t + 1) * kN <= at.e.keys;
-        uint32_t drop[kN / 32];
+        const uint32_t seen = next;
+        // (V of the tile before has arrived, so P V of the last tile with these
+        // limits is done)
         if (!whole) {
 #pragma unroll
-          for (int c = 0; c < kN / 32; ++c) {
-            const int key = t * kN + c * 32 + lane;
-            drop[c] = __ballot_sync(
-                0xffffffffu, key >= at.e.keys || (p.key_mask != nullptr &&
-                                                  __ldg(p.key_mask + at.e.k0 + key) == 0));
-          }
+          for (int c = 0; c < kN / 32; ++c)
+            sLimit[place * kN + c * 32 + lane] = seen >> c & 1 ? -neg_inf() : neg_inf();
+          __syncwarp();
         }
+        if (lane == 0) mbar_arrive(&l_full[place]);
+        if (t + 1 < at.t0 + at.n) next = mask_bytes(t + 1);
         wait(&v_full[s], (uint32_t)(k / L::kStages & 1), 25);
         if (!whole) {
-          if (lane < kN / 32)  // (the stage's words have been read: P V of its last tile is done)
-            sSeen[s * 4 + lane] = ~(lane == 0 ? drop[0] : lane == 1 ? drop[1] : lane == 2 ? drop[2] : drop[3]);
           uint8_t* tile = sV + s * L::kTile;
-#pragma unroll 1
-          for (int c = 0; c < kN / 32; ++c) {
-            uint32_t w = drop[0];
-            if (c == 1) w = drop[1];
-            if (c == 2) w = drop[2];
-            if (c == 3) w = drop[3];
-            // eight lanes a row of 128 bytes, four rows at a time
-            for (int i = lane >> 3; i < 32; i += 4)
-              if (w >> i & 1)
-                for (int x = 0; x < D / 64; ++x)
-                  *reinterpret_cast<uint4*>(tile + x * kSlab + (c * 32 + i) * 128 + (lane & 7) * 16) =
-                      make_uint4(0, 0, 0, 0);
+          // the lane's four rows, each lane's chunks in another order
+#pragma unroll 4
+          for (int i = 0; i < D / 8; ++i) {
+            uint8_t* to = tile + (i >> 3) * kSlab + lane * 128 + (((i ^ lane) & 7) << 4);
+#pragma unroll
+            for (int c = 0; c < kN / 32; ++c)
+              if ((seen >> c & 1) == 0)
+                *reinterpret_cast<uint4*>(to + c * 32 * 128) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
         }
@@ -554,10 +566,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       int n = g ? done[1] : done[0];
       for (int j = one ? g : 0; j < at.n && at.e.keys > 0; j += one ? 2 : 1) {
         const bool whole = p.key_mask == nullptr && (at.t0 + j + 1) * kN <= at.e.keys;
-        const int stage = (k + j) % L::kStages;
+        const int place = (k + j) % L::kLimits;
         wait(&s_full[g], (uint32_t)(n & 1), 60 + g);
-        // (behind the scores, whose issue waited for the stage's tile before)
-        if (!whole) wait(&v_ready[stage], (uint32_t)((k + j) / L::kStages & 1), 66);
+        // (behind the scores: P V of the last tile with this place has been issued then)
+        if (!whole) wait(&l_full[place], (uint32_t)((k + j) / L::kLimits & 1), 66);
         tc::fence_after_sync();
         const uint32_t ts = tS(g) + lane_off;
         uint64_t sum2[4] = {0, 0, 0, 0};  // four pairs of sums
@@ -565,10 +577,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         float v[32];
         // 32 scores at a time, in a rolled loop (unrolled, the roles' code passes
         // what the instruction caches hold)
-        auto probabilities = [&](auto masked, int key0, uint32_t bits) {
+        auto probabilities = [&](auto masked, int key0) {
           if constexpr (masked) {
+            // -inf where a key is not seen, whatever the score is (NaN too), else at most inf
+            const float4* limit = reinterpret_cast<const float4*>(sLimit + place * kN + key0);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = bits >> i & 1 ? v[i] : neg_inf();
+            for (int i = 0; i < 8; ++i) {
+              const float4 x = limit[i];
+              v[4 * i] = fminf(v[4 * i], x.x);
+              v[4 * i + 1] = fminf(v[4 * i + 1], x.y);
+              v[4 * i + 2] = fminf(v[4 * i + 2], x.z);
+              v[4 * i + 3] = fminf(v[4 * i + 3], x.w);
+            }
           }
           // The exponentials do not wait for the largest score: the chunk is done
           // again where it passes the reference by more than the slack.
@@ -614,11 +634,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int c = 0; c < kN; c += 32) {
             tc::tmem_ld32(ts + c, v);
-            uint32_t bits = 0;
-            if constexpr (masked) bits = sSeen[stage * 4 + c / 32];
             tc::tmem_wait_ld();
             arrived(v);
-            probabilities(masked, c, bits);
+            probabilities(masked, c);
           }
         };
         if (whole) row(std::false_type{});
