@@ -589,7 +589,8 @@ PA_API int pa_copy_pages(const int32_t* copies, int n, void* const* caches, int 
  * Rows without a key: O = 0, LSE = -inf.  Rows behind cu_seqlens_q[B] are not
  * written.  An entry with rows or keys outside q and k, or more than the bounds,
  * is reported (PA_DEVERR_LENGTH, the entry, the length): its rows that lie in q
- * and within max_seqlen_q have no keys then.
+ * and within max_seqlen_q have no keys then.  At most 2^30 tiles of 256 rows per
+ * kv head by 128 keys, by the bounds; more return PA_ERR_UNSUPPORTED.
  */
 PA_API int pa_fwd_cross(const void* q, int64_t q_st, int64_t q_sh, const void* k, int64_t k_st,
                         int64_t k_sh, const void* v, int64_t v_st, int64_t v_sh,

@@ -49,7 +49,7 @@ constexpr int kMaxBeams = 32;
 constexpr int kMaxOut = 64;
 constexpr int kParts = 64;         // of the block maxima: the N-th largest of their maxima is the bound
 constexpr int kMaxCandidates = 1024;
-constexpr int kMaxCluster = 16;
+constexpr int kMaxCluster = kClusterLimit;
 constexpr int kMaxUnits = 64;      // of a CTA
 constexpr uint32_t kAll = 0xffffffffu;
 
@@ -608,34 +608,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) select_kernel(const Sele
   }
 }
 
-// How many clusters of the configuration's size the device holds at a time; asked
-// once a device and size.
-template <typename K>
-int resident_clusters(K kernel, const cudaLaunchConfig_t& cfg, int size,
-                      std::atomic<int> (*known)[kMaxCluster + 1]) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return size <= 8 ? num_sms() / size : 0;
-  int n = known[dev][size].load(std::memory_order_relaxed);
-  if (n == 0) {
-    // (sizes above 8 are not portable)
-    const bool ok = (size <= 8 || cudaFuncSetAttribute(
-                                      kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
-                                      cudaSuccess) &&
-                    cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess;
-    if (!ok) {
-      cudaGetLastError();  // (not an error of the call's)
-      n = 0;
-    }
-    if (n <= 0) n = -1;
-    known[dev][size].store(n, std::memory_order_relaxed);
-  }
-  return n;
-}
-
 template <typename T>
 cudaError_t launch_select(SelectParams p, cudaStream_t st) {
   static std::atomic<uint64_t> allowed{0};
-  static std::atomic<int> resident[64][kMaxCluster + 1];  // by device and size; 0: not known
+  static std::atomic<int> resident[64][kClusterLimit + 1];  // by device and size; 0: not known
   constexpr int per = 16 / (int)sizeof(T);
   const int vecs = p.V / per + 1;
   const int steps = (vecs + kStepVecs - 1) / kStepVecs;  // of a row

@@ -11,7 +11,7 @@
 // What bounds it is the read of K and V, once for all rows of the entry.  The
 // G query heads of a kv head and the rows are packed into tiles of 16 rows, the M
 // of mma.sync m16n8k16; P passes from one product to the other in registers.
-// Each of a CTA's four warps has its own kv head and its own ring of three
+// Each of a CTA's four warps has its own kv head and its own ring of two
 // 8 KB stages, filled by TMA and refilled as soon as the warp has read a stage:
 // no wait between warps, and neighbouring heads (which lie behind one another in
 // a row of k) are read at about the same time.  Where there are fewer than four
@@ -38,12 +38,11 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 3;
+constexpr int kStages = 2;
 constexpr int kStageBytes = 8192;  // K and V of a tile of one head
 constexpr int kRows = 16;          // packed rows of an entry and kv head
-constexpr int kCtasPerSm = 2;
-constexpr int kFill = 2;
-constexpr int kMaxCluster = 16;
+constexpr int kCtasPerSm = 3;
+constexpr int kMaxCluster = kClusterLimit;
 constexpr float kRescale = 8.f;
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -331,7 +330,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 template <int D, typename T>
 cudaError_t launch_t(const CrossParams& p, const CUtensorMap& tmk, const CUtensorMap& tmv,
                      cudaStream_t st) {
-  static std::atomic<uint64_t> asked{0}, wide{0}, allowed{0};
+  static std::atomic<uint64_t> allowed{0};
+  static std::atomic<int> resident[64][kClusterLimit + 1];  // by device and size; 0: not known
   constexpr int smem = kWarps * kStages * kStageBytes + 1024;
   const cudaError_t e =
       allow_shared(reinterpret_cast<const void*>(cross_kernel<D, T>), smem, &allowed);
@@ -340,12 +340,6 @@ cudaError_t launch_t(const CrossParams& p, const CUtensorMap& tmk, const CUtenso
   while (p.Hkv % hs != 0) hs /= 2;
   const long long items = (long long)p.B * (p.Hkv / hs);
   if (items > 0x7fffffffll / kMaxCluster) return cudaErrorInvalidValue;
-  // as many CTAs as are resident, with two tiles a warp at least
-  const int tiles = (p.max_k + cross_narrow_box(D) - 1) / cross_narrow_box(D);
-  int ctas = 1;
-  while (ctas < kMaxCluster && items * ctas * 2 <= kFill * num_sms() &&
-         tiles >= ctas * 2 * 2 * (kWarps / hs))
-    ctas *= 2;
   cudaLaunchConfig_t cfg{};
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
@@ -355,12 +349,17 @@ cudaError_t launch_t(const CrossParams& p, const CUtensorMap& tmk, const CUtenso
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  for (;;) {
-    cfg.gridDim = dim3((unsigned)(items * ctas));
+  // as many CTAs as are resident together, with two tiles a warp at least
+  const int tiles = (p.max_k + cross_narrow_box(D) - 1) / cross_narrow_box(D);
+  int ctas = tiles / (2 * (kWarps / hs));
+  ctas = ctas < 1 ? 1 : ctas < kMaxCluster ? ctas : kMaxCluster;
+  for (; ctas > 1; --ctas) {
+    cfg.gridDim = dim3((unsigned)ctas);
     at.val.clusterDim.x = (unsigned)ctas;
-    if (ctas <= 8 || wide_clusters(cross_kernel<D, T>, cfg, &asked, &wide)) break;
-    ctas = 8;
+    if (items <= resident_clusters(cross_kernel<D, T>, cfg, ctas, resident)) break;
   }
+  cfg.gridDim = dim3((unsigned)(items * ctas));
+  at.val.clusterDim.x = (unsigned)ctas;
   return cudaLaunchKernelEx(&cfg, cross_kernel<D, T>, p, hs, tmk, tmv);
 }
 
@@ -452,6 +451,12 @@ extern "C" PA_API int pa_fwd_cross(const void* q, int64_t q_st, int64_t q_sh, co
                (reinterpret_cast<uintptr_t>(workspace) & 255) != 0))
     return set_error(PA_ERR_WORKSPACE, "workspace of %zu bytes, 256-byte aligned, is needed",
                      cross_wide_workspace(D));
+  if (wide) {  // (tiles are counted in 32 bits)
+    const long long pair = 2 * (128 / heads);
+    if ((long long)B * Hkv * (G / heads) * ((max_q + pair - 1) / pair) >
+        (1 << 30) / (max_k / 128 + 1))
+      return set_error(PA_ERR_UNSUPPORTED, "more than 2^30 tiles of 256 rows per kv head by 128 keys");
+  }
   CrossParams p{};
   p.q = q;
   p.q_st = q_st;

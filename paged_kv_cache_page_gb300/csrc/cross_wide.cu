@@ -13,9 +13,12 @@
 // Bound: the tensor cores, 4 D operations a (row, key) pair, and next to them the
 // exponentials.  One persistent CTA an SM:
 //   warps 0-7  softmax: one thread a row, group g = warp / 4 takes tile g
-//   warp 8     K and Q tiles by TMA, warp 9 V tiles
+//   warp 8     K and Q tiles by TMA, warp 9 V tiles (one thread for both would hold K
+//              back until V's place is free)
 //   warp 10    issues O_g += P_g V (P_g from TMEM over S_g) and S_g = Q_g K^T
-//   warp 11    clears rows of V that no row sees (0 times what they hold may be NaN)
+//   warp 11    limits of masked scores; clears rows of V that no row sees (0 times
+//              what they hold may be NaN); tells that parts of cut streams are
+//              written
 // TMEM: S_0, S_1, O_0, O_1.  While one group's softmax runs, the tensor core works
 // on the other group.  Where a pair has rows for one tile only, the groups take
 // its tiles of keys in turn and their results are brought together at the end.
@@ -36,10 +39,12 @@ namespace {
 constexpr int kM = 128;  // rows of a query tile
 constexpr int kN = 128;  // keys of a tile
 constexpr int kSlab = 128 * 128;
+constexpr int kSoft = 8;  // softmax warps
 constexpr int kWarpK = 8, kWarpV = 9, kWarpMma = 10, kWarpFix = 11;
 constexpr int kThreads = 12 * 32;
 constexpr int kMinShare = 2;  // tiles
-constexpr int kSnap = 4;      // tiles that a cut moves to an end of its stream
+constexpr int kSnap = 2;      // tiles that a cut moves to an end of its stream
+constexpr int kEnds = 3;      // what a stream's begin and end cost, in tiles
 
 template <int D>
 struct Layout {
@@ -48,19 +53,20 @@ struct Layout {
   static constexpr int kOffQ = 0;                   // [2]
   static constexpr int kOffK = 2 * kTile;
   static constexpr int kOffV = kOffK + kStages * kTile;
-  static constexpr int kOffOut = kOffV + kStages * kTile;  // [8 warps][32 rows][128 bytes]
-  static constexpr int kOffBar = kOffOut + 8 * 4096;
+  static constexpr int kOffOut = kOffV + kStages * kTile;  // [warps][2][32 rows][64 bytes]
+  static constexpr int kOffBar = kOffOut + kSoft * 4096;
   static constexpr int kLimits = kStages + 1;              // tiles whose limits are held
   // q_full, q_empty; k_full, k_empty, v_full, v_ready, v_empty [kStages];
-  // s_full, p_full, pv_done, o_free [2]; l_full [kLimits]
-  static constexpr int kBars = 2 + 5 * kStages + 8 + kLimits;
-  static constexpr int kOffSums = kOffBar + kBars * 8;  // long long [16]
-  static constexpr int kOffLimit = (kOffSums + 16 * 8 + 15) & ~15;  // float [kLimits][kN] of scores
-  static constexpr int kOffMisc = kOffLimit + kLimits * kN * 4;  // start; TMEM base, flag
-  static constexpr int kBytes = kOffMisc + 32 + 1024;
+  // s_full, p_full, pv_done, o_free [2]; l_full [kLimits]; part_full [2], told
+  static constexpr int kBars = 2 + 5 * kStages + 8 + kLimits + 3;
+  static constexpr int kOffSums = kOffBar + kBars * 8;      // int [24]
+  static constexpr int kOffLimit = (kOffSums + 24 * 4 + 15) & ~15;  // float [kLimits][kN] of scores
+  static constexpr int kOffPlain = kOffLimit + kLimits * kN * 4;    // int [kLimits] no limits in the tile
+  static constexpr int kOffCut = kOffPlain + kLimits * 4;           // Cut [2]
+  static constexpr int kOffMisc = kOffCut + 2 * 48;         // start [2], TMEM base
+  static constexpr int kBytes = kOffMisc + 16 + 1024;
   static_assert(kBytes <= 232448, "shared memory");
   static_assert(kOffOut % 16 == 0 && kOffLimit % 16 == 0, "read 16 bytes at a time");
-  static_assert(kOffSums % 8 == 0 && kOffMisc % 8 == 0, "64-bit values");
 };
 
 // P of the type: the largest score is brought to 2^shift at first, and may pass
@@ -185,18 +191,18 @@ __device__ __forceinline__ int entry_tiles(const CrossEntry& e) {
   return max(1, (e.keys + kN - 1) / kN);  // (without keys: one, to write the empty rows)
 }
 
-// A part of a CTA's share: tiles [t0, t0 + n) of a stream.  The cuts are at whole
-// multiples of `share`; one that lies at most kSnap tiles behind a stream's begin
+// A part of a CTA's share: tiles [t0, t0 + n) of a stream.  A stream counts as its
+// tiles and kEnds.  The cuts are at whole multiples of `share`; one that lies at most kSnap tiles behind a stream's begin
 // counts as there, else one that lies at most kSnap in front of its end as there.
 struct Walk {
   int b, h, pair, t0, n, all, pairs;  // all: tiles of the stream; n = 0: no more
-  long long begin;                    // tiles of the streams in front
-  long long stop;                     // the cut behind the share; -1: none
+  int begin;                          // what the streams in front count
+  int stop;                           // the cut behind the share; -1: none
   CrossEntry e;
 
   __device__ __forceinline__ void take() {
-    const long long d = stop - begin;
-    n = stop < 0 || d >= all ? all - t0 : d <= kSnap ? 0 : d >= all - kSnap ? all - t0 : (int)d - t0;
+    const int d = stop - begin;
+    n = stop < 0 || d >= all ? all - t0 : d <= kSnap ? 0 : d >= all - kSnap ? all - t0 : d - t0;
   }
   __device__ __forceinline__ void next(const CrossParams& p) {
     if (t0 + n < all) {  // (cut)
@@ -207,7 +213,7 @@ struct Walk {
   }
   __device__ __forceinline__ void next_stream(const CrossParams& p) {
     n = 0;
-    begin += all;
+    begin += all + kEnds;
     t0 = 0;
     if (++pair == pairs) {
       pair = 0;
@@ -224,6 +230,12 @@ struct Walk {
     take();
   }
 };
+
+// What a join needs of a cut stream: its rows and the CTAs of its parts.
+struct Cut {
+  int q0, rows, h, pair, cta0, cta1, last;
+};
+static_assert(sizeof(Cut) <= 48, "kOffCut");
 
 template <int D, typename T>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -251,11 +263,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* pv_done = p_full + 2;
   uint64_t* o_free = pv_done + 2;
   uint64_t* l_full = o_free + 2;
-  long long* sSums = reinterpret_cast<long long*>(smem + L::kOffSums);
-  long long* sStart = reinterpret_cast<long long*>(smem + L::kOffMisc);  // entry, tiles in front of it
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc + 16);
-  int* sFlag = reinterpret_cast<int*>(smem + L::kOffMisc + 20);
+  uint64_t* part_full = l_full + L::kLimits;  // [2]: the rows of the first, last part are written
+  uint64_t* told = part_full + 2;             // what is to be joined is known
+  int* sSums = reinterpret_cast<int*>(smem + L::kOffSums);
+  Cut* sCut = reinterpret_cast<Cut*>(smem + L::kOffCut);       // the first part, the last
+  int* sStart = reinterpret_cast<int*>(smem + L::kOffMisc);    // entry, tiles in front of it
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc + 8);
   float* sLimit = reinterpret_cast<float*>(smem + L::kOffLimit);
+  int* sPlain = reinterpret_cast<int*>(smem + L::kOffPlain);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -270,73 +285,92 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int g = 0; g < 2; ++g) {
       mbar_init(&s_full[g], 1);
-      mbar_init(&p_full[g], 4);
+      mbar_init(&p_full[g], kSoft / 2);
       mbar_init(&pv_done[g], 1);
-      mbar_init(&o_free[g], 8);
+      mbar_init(&o_free[g], kSoft);
     }
     for (int i = 0; i < L::kLimits; ++i) mbar_init(&l_full[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&part_full[i], kSoft);
+    mbar_init(told, 1);
     fence_mbar_init();
   }
 
-  // ---- the CTA's share: the tiles of all entries, then the entry it begins in
-  long long total = 0, share = 0, start = 0;
+  if (warp == kWarpMma) {
+    tc::tmem_alloc(tslot, 512);
+    tc::tmem_relinquish();
+  }
+
+  // ---- the CTA's share: the tiles of all entries, then the entry it begins in.  Up
+  // to 32 entries every warp finds them by itself.
+  int total = 0, share = 0, start = 0, b_start = 0, b_begin = 0;
   {
-    long long cost = 0, x = 0;  // of entry b, and up to and with it
+    auto cost_of = [&](int b, bool rep) {
+      if (b >= p.B) return 0;
+      const CrossEntry e = cross_entry(p, b, rep);
+      return entry_pairs(p, e) * p.Hkv * (entry_tiles(e) + kEnds);
+    };
+    auto upto = [&](int x) {  // with the lanes in front
 #pragma unroll 1
-    for (int pass = 0; pass < 2; ++pass) {
-      long long before = 0;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      return x;
+    };
+    auto deal = [&]() {
+      share = max(kMinShare, (total + (int)gridDim.x - 1) / (int)gridDim.x);
+      start = share * (int)blockIdx.x;
+    };
+    if (p.B <= 32) {
+      const int cost = cost_of(lane, warp == 0 && blockIdx.x == 0), x = upto(cost);
+      total = __shfl_sync(0xffffffffu, x, 31);
+      deal();
+      const uint32_t mine = __ballot_sync(0xffffffffu, start >= x - cost && start < x);
+      b_start = mine != 0 ? __ffs((int)mine) - 1 : 0;
+      b_begin = __shfl_sync(0xffffffffu, x - cost, b_start);
+    } else {
 #pragma unroll 1
-      for (int b0 = 0; b0 < p.B; b0 += kThreads) {
-        const int b = b0 + tid;
-        if (pass == 0 || p.B > kThreads) {
-          cost = 0;
-          if (b < p.B) {
-            const CrossEntry e = cross_entry(p, b, pass == 0 && blockIdx.x == 0);
-            cost = (long long)entry_pairs(p, e) * p.Hkv * entry_tiles(e);
-          }
-          x = cost;
+      for (int pass = 0; pass < 2; ++pass) {
+        int before = 0;
 #pragma unroll 1
-          for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-          }
+        for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+          const int cost = cost_of(b0 + tid, pass == 0 && blockIdx.x == 0);
+          int x = upto(cost);
           __syncthreads();  // (sSums have been read)
           if (lane == 31) sSums[warp] = x;
           __syncthreads();
-          x += before;
-#pragma unroll 1
-          for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) x += sSums[w];
-            before += sSums[w];
+          const int sum = lane < kThreads / 32 ? sSums[lane] : 0;
+          x += before + __reduce_add_sync(0xffffffffu, lane < warp ? sum : 0);
+          before += __reduce_add_sync(0xffffffffu, sum);
+          if (pass == 1 && start >= x - cost && start < x) {
+            sStart[0] = b0 + tid;
+            sStart[1] = x - cost;
           }
         }
-        if (pass == 1 && cost > 0 && start >= x - cost && start < x) {
-          sStart[0] = b;
-          sStart[1] = x - cost;
+        if (pass == 0) {
+          total = before;
+          deal();
         }
       }
-      if (pass == 0) {
-        total = before;
-        share = max((long long)kMinShare, (total + gridDim.x - 1) / gridDim.x);
-        start = share * blockIdx.x;
-        if (start >= total) return;  // (the whole CTA)
-      }
+      __syncthreads();
+      b_start = start < total ? sStart[0] : 0;
+      b_begin = start < total ? sStart[1] : 0;
     }
   }
-  __syncthreads();
   Walk at;
-  at.b = (int)sStart[0];
-  at.e = cross_entry(p, at.b, false);
-  at.pairs = entry_pairs(p, at.e);
-  at.all = entry_tiles(at.e);
-  at.stop = start + share < total ? start + share : -1;
-  {
-    const long long off = start - sStart[1], stream = off / at.all;
-    at.begin = sStart[1] + stream * at.all;
-    at.t0 = (int)(off - stream * at.all);
-    at.h = (int)(stream / at.pairs);
-    at.pair = (int)(stream - (long long)at.h * at.pairs);
-    if (at.t0 <= kSnap) at.t0 = 0;
+  at.n = 0;
+  if (start < total) {
+    at.b = b_start;
+    at.e = cross_entry(p, at.b, false);
+    at.pairs = entry_pairs(p, at.e);
+    at.all = entry_tiles(at.e);
+    at.stop = start + share < total ? start + share : -1;
+    const int off = start - b_begin, stream = off / (at.all + kEnds);
+    at.begin = b_begin + stream * (at.all + kEnds);
+    at.t0 = off - stream * (at.all + kEnds);
+    at.h = stream / at.pairs;
+    at.pair = stream - at.h * at.pairs;
+    if (at.t0 < at.all && at.t0 <= kSnap) at.t0 = 0;
     if (at.t0 > 0 && at.t0 >= at.all - kSnap) at.next_stream(p);
     else at.take();
   }
@@ -348,14 +382,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       *reinterpret_cast<uint4*>(sQ + i * 16) = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
   }
-  if (warp == kWarpMma) {
-    tc::tmem_alloc(tslot, 512);
-    tc::tmem_relinquish();
-  }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tbase = *tslot;
+  if (tid < 2) sCut[tid].last = 0;  // (before the first part's end, which is behind barriers)
   auto tS = [&](int g) { return tbase + (uint32_t)(g * 128); };
   auto tO = [&](int g) { return tbase + 256u + (uint32_t)(g * D); };
   // One tile of rows: the groups take its tiles of keys in turn.
@@ -415,7 +446,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == kWarpFix) {
     // ======================= limits of scores, rows of V that no row sees =====
-    int k = 0;
+    int k = 0, parts = 0;
+    // The softmax warps do not wait until their part's writes have arrived: this warp
+    // arrives for the CTA some time later.
+    Cut cut = {};
+    int pending = -1;  // the part: 0 first, 1 last
+    auto tell = [&]() {
+      if (pending < 0) return;
+      wait(&part_full[pending], 0, 27);
+      if (lane == 0) {
+        __threadfence();
+        cut.last = arrive_last(p.words + cut.cta0, launch_tag(), cut.cta1 - cut.cta0 + 1) ? 1 : 0;
+        __threadfence();
+        sCut[pending] = cut;
+      }
+      __syncwarp();
+      pending = -1;
+    };
     for (; at.n > 0; at.next(p)) {
       if (at.e.keys == 0) continue;
       auto mask_bytes = [&](int t) -> uint32_t {  // of the lane's four keys of tile t
@@ -432,10 +479,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int t = at.t0; t < at.t0 + at.n; ++t, ++k) {
         const int s = k % L::kStages, place = k % L::kLimits;
-        const bool whole = p.key_mask == nullptr && (t + 1) * kN <= at.e.keys;
         const uint32_t seen = next;
+        const bool whole = __all_sync(0xffffffffu, seen == 0xfu);
         // (V of the tile before has arrived, so P V of the last tile with these
         // limits is done)
+        if (lane == 0) sPlain[place] = whole ? 1 : 0;
         if (!whole) {
 #pragma unroll
           for (int c = 0; c < kN / 32; ++c)
@@ -460,8 +508,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&v_ready[s]);
+        if (pending >= 0 && __all_sync(0xffffffffu, mbar_try_wait(&part_full[pending], 0))) tell();
+      }
+      if (at.t0 > 0 || at.n < at.all) {
+        tell();
+        pending = at.t0 == 0 ? 1 : 0;
+        cut = {at.e.q0, at.e.rows, at.h, at.pair, (at.begin + min(kSnap, at.all - 1)) / share, 0, 0};
+        cut.cta1 = max(cut.cta0, (at.begin + at.all - kSnap - 1) / share);
+        ++parts;
       }
     }
+    tell();
+    if (parts > 0 && lane == 0) mbar_arrive(told);
   } else if (warp == kWarpMma) {
     // ======================= MMA issuer =======================
     // Per tile and group: O_g += P_g V, then S_g of the next tile.  One thread's
@@ -556,7 +614,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const float f = p.scale_log2;
     uint8_t* staged = smem + L::kOffOut + warp * 4096;
+    // 32 columns of the warp's rows by way of shared memory: a thread holds a row,
+    // and whole sectors of few rows are written at a time
+    auto write = [&](long long my_row, int col, const float (&x)[32], float by) {
+      uint8_t* buf = staged + (col >> 5 & 1) * 2048;
+#pragma unroll
+      for (int e = 0; e < 32; e += 8)
+        *reinterpret_cast<uint4*>(buf + lane * 64 + (((e >> 3) ^ (lane >> 1 & 3)) << 4)) =
+            make_uint4(E::from_f2(x[e] * by, x[e + 1] * by), E::from_f2(x[e + 2] * by, x[e + 3] * by),
+                       E::from_f2(x[e + 4] * by, x[e + 5] * by),
+                       E::from_f2(x[e + 6] * by, x[e + 7] * by));
+      __syncwarp();
+      const int c = lane & 3;
+#pragma unroll
+      for (int i = lane >> 2; i < 32; i += 8) {
+        const long long to = __shfl_sync(0xffffffffu, my_row, i);
+        const uint4 y = *reinterpret_cast<const uint4*>(buf + i * 64 + ((c ^ (i >> 1 & 3)) << 4));
+        if (to >= 0)
+          *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.out) + to * D + col + c * 8) = y;
+      }
+      __syncwarp();
+    };
+    auto weight = [](float2 x, float ref) {
+      return x.y == 0.f ? 0.f : x.x == ref ? 1.f : ex2(x.x - ref);
+    };
     int done[2] = {0, 0}, k = 0;  // tiles of either group, of the CTA
+    bool cut = false;
     for (; at.n > 0; at.next(p)) {
       const bool one = solo(at);
       const int tile = one ? 0 : g;  // the group's rows
@@ -565,11 +648,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = neg_inf(), l = 0.f;
       int n = g ? done[1] : done[0];
       for (int j = one ? g : 0; j < at.n && at.e.keys > 0; j += one ? 2 : 1) {
-        const bool whole = p.key_mask == nullptr && (at.t0 + j + 1) * kN <= at.e.keys;
+        bool whole = p.key_mask == nullptr && (at.t0 + j + 1) * kN <= at.e.keys;
         const int place = (k + j) % L::kLimits;
         wait(&s_full[g], (uint32_t)(n & 1), 60 + g);
         // (behind the scores: P V of the last tile with this place has been issued then)
-        if (!whole) wait(&l_full[place], (uint32_t)((k + j) / L::kLimits & 1), 66);
+        if (!whole) {
+          wait(&l_full[place], (uint32_t)((k + j) / L::kLimits & 1), 66);
+          whole = sPlain[place] != 0;
+        }
         tc::fence_after_sync();
         const uint32_t ts = tS(g) + lane_off;
         uint64_t sum2[4] = {0, 0, 0, 0};  // four pairs of sums
@@ -675,27 +761,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool whole = at.t0 == 0 && at.n == at.all;
       const int col0 = one ? g * (D / 2) : 0, cols = one ? D / 2 : D;
       const long long my_row = valid ? (long long)(at.e.q0 + token) * p.Hq + head : -1;
-      // 32 columns of the warp's rows by way of shared memory: a thread holds a row,
-      // and whole sectors of few rows are written at a time
-      auto write = [&](int col, const float (&x)[32], float by) {
-        uint8_t* buf = staged + (col >> 5 & 1) * 2048;
-#pragma unroll
-        for (int e = 0; e < 32; e += 8)
-          *reinterpret_cast<uint4*>(buf + lane * 64 + (((e >> 3) ^ (lane >> 1 & 3)) << 4)) =
-              make_uint4(E::from_f2(x[e] * by, x[e + 1] * by), E::from_f2(x[e + 2] * by, x[e + 3] * by),
-                         E::from_f2(x[e + 4] * by, x[e + 5] * by),
-                         E::from_f2(x[e + 6] * by, x[e + 7] * by));
-        __syncwarp();
-        const int c = lane & 3;
-#pragma unroll
-        for (int i = lane >> 2; i < 32; i += 8) {
-          const long long to = __shfl_sync(0xffffffffu, my_row, i);
-          const uint4 y = *reinterpret_cast<const uint4*>(buf + i * 64 + ((c ^ (i >> 1 & 3)) << 4));
-          if (to >= 0)
-            *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.out) + to * D + col + c * 8) = y;
-        }
-        __syncwarp();
-      };
       auto put_lse = [&](float ref, float sum) {
         if (valid && (!one || g == 0) && p.lse != nullptr)
           p.lse[(int64_t)head * p.total_q + at.e.q0 + token] =
@@ -706,7 +771,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int e = 0; e < 32; ++e) zero[e] = 0.f;
 #pragma unroll 1
-        for (int col = col0; col < col0 + cols; col += 32) write(col, zero, 0.f);
+        for (int col = col0; col < col0 + cols; col += 32) write(my_row, col, zero, 0.f);
         put_lse(m, l);
         continue;
       }
@@ -723,9 +788,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         named_barrier(1, 256);  // (read, before it is written again)
         m = fmaxf(half[0].x, half[1].x);
       }
-      auto weight = [](float2 x, float ref) {
-        return x.y == 0.f ? 0.f : x.x == ref ? 1.f : ex2(x.x - ref);
-      };
       const float weight0 = weight(half[0], m), weight1 = weight(half[1], m);
       if (one) l = fmaf(weight0, half[0].y, weight1 * half[1].y);
       // P V of either group's last tile (the other group's softmax of it is done)
@@ -753,7 +815,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (whole) {
-          write(col, o, by);
+          write(my_row, col, o, by);
         } else if (valid) {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
@@ -776,60 +838,69 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       if (valid && (!one || g == 0)) p.part_ml[my_part + r] = make_float2(m, l);
-      const int cta0 = (int)((at.begin + min(kSnap, at.all - 1)) / share),
-                cta1 = max(cta0, (int)((at.begin + at.all - kSnap - 1) / share));
-      named_barrier(1, 256);  // the partial rows of the CTA before its arrival
-      if (tid == 0) {
-        __threadfence();
-        *sFlag = arrive_last(p.words + cta0, launch_tag(), cta1 - cta0 + 1) ? 1 : 0;
-        __threadfence();
-      }
-      named_barrier(1, 256);
-      const bool join = *sFlag != 0;
-      named_barrier(1, 256);  // the flag has been read
-      if (!join) continue;
-      // the row's place in part `cta`
-      auto from = [&](int cta) {
-        return ((int64_t)(2 * cta + (cta == cta0 ? 1 : 0)) * 2 + tile) * kM + r;
-      };
-      float ref = neg_inf(), sum = 0.f;
-      if (valid) {
-        for (int cta = cta0; cta <= cta1; ++cta) ref = fmaxf(ref, __ldcg(p.part_ml + from(cta)).x);
-        for (int cta = cta0; cta <= cta1; ++cta) {
-          const float2 ml = __ldcg(p.part_ml + from(cta));
-          sum = fmaf(weight(ml, ref), ml.y, sum);
-        }
-      }
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      cut = true;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&part_full[at.t0 == 0 ? 1 : 0]);
+    }
+
+    // ---- joins: of streams whose last part was this CTA's
+    if (cut) {
+      wait(told, 0, 68);
 #pragma unroll 1
-      for (int col = col0; col < col0 + cols; col += 32) {
-        float o[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = 0.f;
+      for (int x = 0; x < 2; ++x) {
+        const Cut c = sCut[x];
+        if (!c.last) continue;
+        const bool one = (2 * c.pair + 1) * tokens >= c.rows;
+        const int tile = one ? 0 : g;
+        const int token = (2 * c.pair + tile) * tokens + r / p.G, head = c.h * p.G + r % p.G;
+        const bool valid = r < tile_rows && token < c.rows;
+        const int col0 = one ? g * (D / 2) : 0, cols = one ? D / 2 : D;
+        const long long my_row = valid ? (long long)(c.q0 + token) * p.Hq + head : -1;
+        // the row tile's place in part `cta`
+        auto from = [&](int cta) {
+          return ((int64_t)(2 * cta + (cta == c.cta0 ? 1 : 0)) * 2 + tile) * kM;
+        };
+        float ref = neg_inf(), sum = 0.f;
         if (valid) {
-#pragma unroll 1
-          for (int cta = cta0; cta <= cta1; ++cta) {
-            float4 y[8];
-            const float2 ml = __ldcg(p.part_ml + from(cta));
-            const int64_t row = from(cta) - r;
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              y[e] = load16_l2(p.part_o + (row * (D / 4) + (col / 4 + e) * kM + r) * 4);
-            if (ml.y == 0.f) continue;
-            const float w = weight(ml, ref);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              o[4 * e] = fmaf(w, y[e].x, o[4 * e]);
-              o[4 * e + 1] = fmaf(w, y[e].y, o[4 * e + 1]);
-              o[4 * e + 2] = fmaf(w, y[e].z, o[4 * e + 2]);
-              o[4 * e + 3] = fmaf(w, y[e].w, o[4 * e + 3]);
-            }
+          for (int cta = c.cta0; cta <= c.cta1; ++cta)
+            ref = fmaxf(ref, __ldcg(p.part_ml + from(cta) + r).x);
+          for (int cta = c.cta0; cta <= c.cta1; ++cta) {
+            const float2 ml = __ldcg(p.part_ml + from(cta) + r);
+            sum = fmaf(weight(ml, ref), ml.y, sum);
           }
         }
-        __syncwarp();
-        write(col, o, inv);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll 1
+        for (int col = col0; col < col0 + cols; col += 32) {
+          float o[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0.f;
+          if (valid) {
+#pragma unroll 1
+            for (int cta = c.cta0; cta <= c.cta1; ++cta) {
+              float4 y[8];
+              const float2 ml = __ldcg(p.part_ml + from(cta) + r);
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                y[e] = load16_l2(p.part_o + (from(cta) * (D / 4) + (col / 4 + e) * kM + r) * 4);
+              if (ml.y == 0.f) continue;
+              const float w = weight(ml, ref);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                o[4 * e] = fmaf(w, y[e].x, o[4 * e]);
+                o[4 * e + 1] = fmaf(w, y[e].y, o[4 * e + 1]);
+                o[4 * e + 2] = fmaf(w, y[e].z, o[4 * e + 2]);
+                o[4 * e + 3] = fmaf(w, y[e].w, o[4 * e + 3]);
+              }
+            }
+          }
+          __syncwarp();
+          write(my_row, col, o, inv);
+        }
+        if (valid && (!one || g == 0) && p.lse != nullptr)
+          p.lse[(int64_t)head * p.total_q + c.q0 + token] =
+              sum == 0.f ? neg_inf() : (ref + log2f(sum)) * kLn2;
       }
-      put_lse(ref, sum);
     }
   }
 

@@ -146,6 +146,31 @@ bool wide_clusters(K kernel, const cudaLaunchConfig_t& cfg, std::atomic<uint64_t
   return (wide->load(std::memory_order_relaxed) & bit) != 0;
 }
 
+constexpr int kClusterLimit = 16;  // CTAs of a cluster at most
+// How many clusters of the configuration's size the device holds at a time; asked
+// once a device and size.
+template <typename K>
+int resident_clusters(K kernel, const cudaLaunchConfig_t& cfg, int size,
+                      std::atomic<int> (*known)[kClusterLimit + 1]) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return size <= 8 ? num_sms() / size : 0;
+  int n = known[dev][size].load(std::memory_order_relaxed);
+  if (n == 0) {
+    // (sizes above 8 are not portable)
+    const bool ok = (size <= 8 || cudaFuncSetAttribute(
+                                      kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
+                                      cudaSuccess) &&
+                    cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess;
+    if (!ok) {
+      cudaGetLastError();  // (not an error of the call's)
+      n = 0;
+    }
+    if (n <= 0) n = -1;
+    known[dev][size].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
 bool encode_cache_map(CUtensorMap* map, const void* base, int dtype, int D, int Hkv, int64_t dim2,
                       int64_t dim3, int64_t stride_h, int64_t stride_t, int64_t stride_b,
                       int box_d, int box_rows, bool swizzle128);

@@ -121,6 +121,8 @@ def test_cross_refusals(lib):
     assert cross(lib, tq=2 ** 31 - 1) == pa.PA_ERR_UNSUPPORTED
     assert cross(lib, tk=2 ** 31 - 1) == pa.PA_ERR_UNSUPPORTED
     assert cross(lib, B=1 << 20, tq=1 << 30, mq=1 << 20) == pa.PA_ERR_UNSUPPORTED
+    wide = dict(tq=1 << 28, tk=1 << 28, mq=1 << 28, mk=1 << 28, ws=P, ws_bytes=1 << 40)
+    assert cross(lib, **wide) == pa.PA_ERR_UNSUPPORTED
     # many rows need a workspace
     size = lib.pa_fwd_cross_workspace_size(500, 400, 4, 2, 64)
     assert size > 0 and lib.pa_fwd_cross_workspace_size(5, 4, 4, 2, 64) == 0
