@@ -188,6 +188,8 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const ReorderParams p
   const int slots = kWarps / p.warps;  // requests at a time
   const int slot = warp / p.warps, part = warp % p.warps;
 
+  griddep_launch_dependents();
+  griddep_wait();
   int free_now = *p.free_count;
   if (free_now < 0 || free_now > p.num_pages) {
     if (rank == 0 && tid == 0) report(p.err, PA_DEVERR_CAPACITY, -1, free_now);
@@ -411,10 +413,12 @@ cudaError_t launch_reorder(ReorderParams p, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
   cfg.blockDim = dim3(kThreads);
   cfg.stream = st;
-  cudaLaunchAttribute at{};
+  cudaLaunchAttribute attrs[2] = {};
+  cudaLaunchAttribute& at = attrs[0];
   at.id = cudaLaunchAttributeClusterDimension;
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
+  overlap_launch(&attrs[1]);
+  cfg.attrs = attrs;
   cfg.numAttrs = 1;
   auto shape = [&] {
     const int per = (p.B + ctas - 1) / ctas;
@@ -433,6 +437,7 @@ cudaError_t launch_reorder(ReorderParams p, cudaStream_t st) {
     ctas = 8;
     shape();
   }
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, reorder_kernel<KM>, p);
 }
 
@@ -450,6 +455,8 @@ struct CopyParams {
 };
 
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ CopyParams p) {
+  griddep_launch_dependents();
+  griddep_wait();
   const int entry = blockIdx.x;
   const int src = p.copies[3 * entry], dst = p.copies[3 * entry + 1],
             tokens = p.copies[3 * entry + 2];
@@ -590,9 +597,15 @@ PA_API int pa_copy_pages(const int32_t* copies, int n, void* const* caches, int 
   for (int at = 0; at < n_caches; at += kMaxCaches) {
     p.n_caches = n_caches - at < kMaxCaches ? n_caches - at : kMaxCaches;
     for (int i = 0; i < p.n_caches; ++i) p.caches[i] = caches[at + i];
-    copy_kernel<<<dim3((unsigned)n, (unsigned)p.n_caches), kCopyThreads, 0,
-                  reinterpret_cast<cudaStream_t>(stream)>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)n, (unsigned)p.n_caches);
+    cfg.blockDim = dim3(kCopyThreads);
+    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr{};
+    overlap_launch(&attr);
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, copy_kernel, p);
     if (e != cudaSuccess) return set_error(PA_ERR_CUDA, "copy launch: %s", cudaGetErrorString(e));
   }
   return PA_OK;

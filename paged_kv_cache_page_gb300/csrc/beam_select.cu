@@ -288,6 +288,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) select_kernel(const Sele
   const int b = blockIdx.x / ranks;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
+  griddep_launch_dependents();
+  griddep_wait();
   // the beams that live: a finite score, and not finished
   float cum = neg_inf();
   bool done = false;
@@ -621,10 +623,12 @@ cudaError_t launch_select(SelectParams p, cudaStream_t st) {
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = sizeof(SelectShared);
   cfg.stream = st;
-  cudaLaunchAttribute at{};
+  cudaLaunchAttribute attrs[2] = {};
+  cudaLaunchAttribute& at = attrs[0];
   at.id = cudaLaunchAttributeClusterDimension;
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
+  overlap_launch(&attrs[1]);
+  cfg.attrs = attrs;
   cfg.numAttrs = 1;
   const cudaError_t e = allow_shared(reinterpret_cast<const void*>(select_kernel<T>),
                                      (int)sizeof(SelectShared), &allowed);
@@ -645,6 +649,7 @@ cudaError_t launch_select(SelectParams p, cudaStream_t st) {
   }
   cfg.gridDim = dim3((unsigned)(p.B * ctas));
   at.val.clusterDim.x = (unsigned)ctas;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, select_kernel<T>, p);
 }
 

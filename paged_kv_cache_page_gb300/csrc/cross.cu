@@ -93,6 +93,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
+  griddep_launch_dependents();
+  griddep_wait();
   // cluster -> entry, group of heads
   const int item = blockIdx.x / ranks;
   const int groups = p.Hkv / hs;
@@ -282,36 +284,50 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   }
   cluster.sync();
 
-  // ---- join: the CTAs share the rows of all heads
+  // ---- join: the CTAs share the rows of all heads, four values a thread, and where
+  // there are more threads than that several share a row's parts
   constexpr int kVec = D / 4;
-  const int work = rows * hs;
-  const int parts = ranks * slices;
-  for (int w = rank * kThreads + tid; w < work * kVec; w += ranks * kThreads) {
+  const int work = rows * hs * kVec, parts = ranks * slices;
+  int lanes = 1;
+  while (lanes < 16 && lanes < parts && work * lanes * 2 <= ranks * kThreads) lanes *= 2;
+  const int my_part = lane & (lanes - 1);
+#pragma unroll 1
+  for (int w0 = rank * kThreads + warp * 32; w0 < work * lanes; w0 += ranks * kThreads) {
+    const int w = min((w0 + lane) / lanes, work - 1);
     const int rh = w / kVec, c = w - rh * kVec;
     const int r = rh / hs, hh = rh - r * hs;
-    auto from = [&](int i) {  // part i of the head's ring
-      const int cta = i / slices, wp = (i - cta * slices) * hs + hh;
-      return cluster.map_shared_rank(reinterpret_cast<float*>(smem + wp * kStages * kStageBytes),
-                                     cta);
-    };
-    float top = neg_inf();
-    for (int i = 0; i < parts; ++i) top = fmaxf(top, from(i)[kRows * D + 2 * r]);
-    float sum = 0.f;
+    float m = neg_inf(), sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = 0; i < parts; ++i) {
-      const float* f = from(i);
-      const float mi = f[kRows * D + 2 * r], li = f[kRows * D + 2 * r + 1];
-      // (a part without a seen key counts for nothing; a NaN in one without any
-      // number reaches the result)
-      if (li == 0.f) continue;
-      const float x = mi == top ? 1.f : ex2(mi - top);
-      sum += x * li;
+    // a part without a seen key counts for nothing; a NaN in one without any number
+    // reaches the result
+    auto add = [&](float mi, float li, float4 y) {
+      const float top = fmaxf(m, mi);
+      const float a = m == top ? 1.f : ex2(m - top), x = mi == top ? 1.f : ex2(mi - top);
+      sum = fmaf(sum, a, x * li);
+      acc.x = fmaf(acc.x, a, x * y.x);
+      acc.y = fmaf(acc.y, a, x * y.y);
+      acc.z = fmaf(acc.z, a, x * y.z);
+      acc.w = fmaf(acc.w, a, x * y.w);
+      m = top;
+    };
+#pragma unroll 2
+    for (int i = my_part; i < parts; i += lanes) {
+      const int cta = i / slices, wp = (i - cta * slices) * hs + hh;
+      const float* f = cluster.map_shared_rank(
+          reinterpret_cast<float*>(smem + wp * kStages * kStageBytes), cta);
+      const float2 ml = *reinterpret_cast<const float2*>(f + kRows * D + 2 * r);
       const float4 y = *reinterpret_cast<const float4*>(f + r * D + 4 * c);
-      acc.x += x * y.x;
-      acc.y += x * y.y;
-      acc.z += x * y.z;
-      acc.w += x * y.w;
+      if (ml.y != 0.f) add(ml.x, ml.y, y);
     }
+#pragma unroll 1
+    for (int o = 1; o < lanes; o <<= 1) {
+      const float mi = __shfl_xor_sync(0xffffffffu, m, o), li = __shfl_xor_sync(0xffffffffu, sum, o);
+      const float4 y = make_float4(
+          __shfl_xor_sync(0xffffffffu, acc.x, o), __shfl_xor_sync(0xffffffffu, acc.y, o),
+          __shfl_xor_sync(0xffffffffu, acc.z, o), __shfl_xor_sync(0xffffffffu, acc.w, o));
+      if (li != 0.f) add(mi, li, y);
+    }
+    if (my_part != 0 || (w0 + lane) / lanes >= work) continue;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const int at = r / p.G, g = r - at * p.G;
     const int head = (h - warp % hs + hh) * p.G + g;
@@ -322,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     *reinterpret_cast<uint2*>(dst) = u;
     if (c == 0 && p.lse != nullptr)
       p.lse[(int64_t)head * p.total_q + e.q0 + at] =
-          sum == 0.f ? neg_inf() : (top + log2f(sum)) * kLn2;
+          sum == 0.f ? neg_inf() : (m + log2f(sum)) * kLn2;
   }
   cluster.sync();  // no CTA leaves while its parts are read
 }
@@ -344,10 +360,12 @@ cudaError_t launch_t(const CrossParams& p, const CUtensorMap& tmk, const CUtenso
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute at{};
+  cudaLaunchAttribute attrs[2] = {};
+  cudaLaunchAttribute& at = attrs[0];
   at.id = cudaLaunchAttributeClusterDimension;
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
+  overlap_launch(&attrs[1]);
+  cfg.attrs = attrs;
   cfg.numAttrs = 1;
   // as many CTAs as are resident together, with two tiles a warp at least
   const int tiles = (p.max_k + cross_narrow_box(D) - 1) / cross_narrow_box(D);
@@ -360,6 +378,7 @@ cudaError_t launch_t(const CrossParams& p, const CUtensorMap& tmk, const CUtenso
   }
   cfg.gridDim = dim3((unsigned)(items * ctas));
   at.val.clusterDim.x = (unsigned)ctas;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, cross_kernel<D, T>, p, hs, tmk, tmv);
 }
 

@@ -300,6 +300,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::tmem_relinquish();
   }
 
+  griddep_launch_dependents();
+  griddep_wait();
   // ---- the CTA's share: the tiles of all entries, then the entry it begins in.  Up
   // to 32 entries every warp finds them by itself.
   int total = 0, share = 0, start = 0, b_start = 0, b_begin = 0;
@@ -917,8 +919,16 @@ cudaError_t launch(const CrossParams& p, const CUtensorMap& tmq, const CUtensorM
   const cudaError_t e = allow_shared(reinterpret_cast<const void*>(wide_kernel<D, T>),
                                      Layout<D>::kBytes, &devices);
   if (e != cudaSuccess) return e;
-  wide_kernel<D, T><<<(unsigned)num_sms(), kThreads, Layout<D>::kBytes, st>>>(p, tmq, tmk, tmv);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)num_sms());
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Layout<D>::kBytes;
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  overlap_launch(&at);
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, wide_kernel<D, T>, p, tmq, tmk, tmv);
 }
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }

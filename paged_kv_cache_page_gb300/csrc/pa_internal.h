@@ -146,6 +146,12 @@ bool wide_clusters(K kernel, const cudaLaunchConfig_t& cfg, std::atomic<uint64_t
   return (wide->load(std::memory_order_relaxed) & bit) != 0;
 }
 
+// Lets a launch begin before the kernel in front of it in its stream has ended: the
+// kernel waits for that (griddep_wait) before it reads anything.
+inline void overlap_launch(cudaLaunchAttribute* at) {
+  at->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at->val.programmaticStreamSerializationAllowed = 1;
+}
 constexpr int kClusterLimit = 16;  // CTAs of a cluster at most
 // How many clusters of the configuration's size the device holds at a time; asked
 // once a device and size.
