@@ -62,6 +62,12 @@ struct ReorderParams {
   int warps;  // of a request (a power of two)
 };
 
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 // A load that sees what other threads of the cluster have stored.
 __device__ __forceinline__ int load_l2(const int32_t* p) { return __ldcg(p); }
 
@@ -153,20 +159,23 @@ __device__ __forceinline__ void load_column(const ReorderParams& p, const Beams&
   }
 }
 
-// Whether child `lane` copies its last page.  entry(i, j): child i's page at
-// column j.
-template <typename F>
-__device__ __forceinline__ bool copies_page(const ReorderParams& p, const Beams& s, int lane,
-                                            F&& entry) {
+// Whether child `lane` copies its last page, and that page (-1: it has no partly
+// filled one).
+__device__ __forceinline__ bool copies_page(const ReorderParams& p, const Beams& s, int g, int lane,
+                                            int& page) {
+  const int32_t* rows = p.table + (int64_t)g * p.K * p.bt_stride;
   const bool partly = s.partial >= 0;
-  const int mine = partly ? entry(lane, s.parent, s.partial) : -1;
+  page = partly ? load_l2(rows + s.parent * p.bt_stride + s.partial) : -1;
   bool clash = false;
-#pragma unroll 4
+#pragma unroll 1
   for (int i = 0; i < p.K; ++i) {
     const int held = __shfl_sync(kAll, s.new_held, i), part = __shfl_sync(kAll, s.partial, i);
     const int par = __shfl_sync(kAll, s.parent, i);
-    if (partly && i != lane && s.partial < held && (i < lane || part != s.partial))
-      clash = clash || entry(i, par, s.partial) == mine;
+    int other = __shfl_sync(kAll, page, i);  // child i's page in the lane's column, if that is its last
+    if (!partly || i == lane || s.partial >= held) continue;
+    if (part != s.partial) other = load_l2(rows + par * p.bt_stride + s.partial);
+    else if (i > lane) continue;
+    clash = clash || other == page;
   }
   return clash;
 }
@@ -176,43 +185,46 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const ReorderParams p
   extern __shared__ int sm[];
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = (int)blockDim.x;
   const int per = (p.B + ranks - 1) / ranks;             // requests of a CTA
   const int g0 = min(p.B, rank * per), g1 = min(p.B, g0 + per);
   int* s_given = sm;                   // [B] pages given back, then those in front
   int* s_taken = sm + p.B;             // [B] fresh pages, then those in front
-  int* s_part = sm + 2 * p.B;          // [per][warps] pages given back by a warp's columns
+  int* s_need = sm + 2 * p.B;          // [per] fresh pages of the CTA's requests
+  int* s_part = s_need + per;          // [per][warps] pages given back by a warp's columns
   uint8_t* s_bad = reinterpret_cast<uint8_t*>(s_part + per * p.warps);  // [per]
   __shared__ int s_sums[2][32];
   __shared__ int s_fail;
-  const int slots = kWarps / p.warps;  // requests at a time
+  const int slots = threads / 32 / p.warps;  // requests at a time
   const int slot = warp / p.warps, part = warp % p.warps;
 
+  cluster_arrive();  // (the others' shared memory is written once they have started)
   griddep_launch_dependents();
-  griddep_wait();
-  int free_now = *p.free_count;
-  if (free_now < 0 || free_now > p.num_pages) {
-    if (rank == 0 && tid == 0) report(p.err, PA_DEVERR_CAPACITY, -1, free_now);
-    free_now = free_now < 0 ? 0 : p.num_pages;
-  }
-  for (int i = tid; i < per; i += kThreads) s_bad[i] = 0;
+  for (int i = tid; i < per; i += threads) s_bad[i] = 0;
+  for (int i = tid; i < 64; i += threads) s_sums[i >> 5][i & 31] = 0;
   if (tid == 0) s_fail = p.B;
-  // (also: every CTA has started before its shared memory is written)
-  cluster.sync();
+  __syncthreads();
+  griddep_wait();
+  int free_now = load_l2(p.free_count);
 
-  auto in_entry = [&](int g) {
-    return [&p, g](int, int par, int j) {
-      return load_l2(p.table + ((int64_t)g * p.K + par) * p.bt_stride + j);
-    };
-  };
+  // Where a warp has one request it keeps what it has found out, and with 32 columns
+  // at most loads nothing again.  (More requests than warps are a warp each.)
+  const bool single = g0 + slot + slots >= g1;
+  Beams s;
+  Column<KM> c;
+  Range r = {0, 0};
+  int page = -1;  // the child's partly filled page
+  bool copy = false;
   // ---- pages given back and fresh ones, request by request
+#pragma unroll 1
   for (int g = g0 + slot; g < g1; g += slots) {
-    const Beams s = beams_of(p, g, lane, part == 0);
+    s = beams_of(p, g, lane, part == 0);
+    r = {0, 0};
     int given = 0;
     if (s.ok) {
-      const Range r = columns_of(s.columns, part, p.warps);
+      r = columns_of(s.columns, part, p.warps);
+#pragma unroll 1
       for (int j = r.begin + lane; j - lane < r.end; j += 32) {
-        Column<KM> c;
         load_column<KM>(p, s, g, j < r.end ? j : 0x7fffffff, c);
         given += __popc(c.gone);
         uint32_t bad = 0;
@@ -230,26 +242,30 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const ReorderParams p
     given = __reduce_add_sync(kAll, given);
     if (lane == 0) s_part[(g - g0) * p.warps + part] = given;
     if (part == 0) {
-      const bool copy = s.ok && copies_page(p, s, lane, in_entry(g));
+      copy = s.ok && copies_page(p, s, g, lane, page);
       const int taken = __popc(__ballot_sync(kAll, copy));
-      if (lane == 0) s_taken[g] = taken;
+      if (lane == 0) s_need[g - g0] = taken;
     }
   }
+  if (free_now < 0 || free_now > p.num_pages) {
+    if (rank == 0 && tid == 0) report(p.err, PA_DEVERR_CAPACITY, -1, free_now);
+    free_now = free_now < 0 ? 0 : p.num_pages;
+  }
   __syncthreads();
-  for (int g = g0 + tid; g < g1; g += kThreads) {
-    int given = 0, taken = s_taken[g];
-    for (int i = 0; i < p.warps; ++i) given += s_part[(g - g0) * p.warps + i];
-    if (s_bad[g - g0]) given = taken = 0;
-    for (int r = 0; r < ranks; ++r) {
-      cluster.map_shared_rank(s_given, r)[g] = given;
-      cluster.map_shared_rank(s_taken, r)[g] = taken;
-    }
+  cluster_wait();
+#pragma unroll 1
+  for (int i = tid; i < (g1 - g0) * ranks; i += threads) {  // a request for a CTA
+    const int g = i / ranks, to = i - g * ranks;
+    int given = 0;
+    for (int w = 0; w < p.warps; ++w) given += s_part[g * p.warps + w];
+    cluster.map_shared_rank(s_given, to)[g0 + g] = s_bad[g] ? 0 : given;
+    cluster.map_shared_rank(s_taken, to)[g0 + g] = s_bad[g] ? 0 : s_need[g];
   }
   cluster.sync();
 
   // ---- the sums in front of each request, and how far the pool goes
   int given[kPer], taken[kPer], my_given = 0, my_taken = 0;
-  const int each = (p.B + kThreads - 1) / kThreads;
+  const int each = (p.B + threads - 1) / threads;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int g = tid * each + i;
@@ -262,12 +278,12 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const ReorderParams p
     my_taken += taken[i];
   }
   int sum_given = my_given, sum_taken = my_taken;
-#pragma unroll
+#pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
-    const int a = __shfl_up_sync(kAll, sum_given, o), b = __shfl_up_sync(kAll, sum_taken, o);
+    const int x = __shfl_up_sync(kAll, sum_given, o), y = __shfl_up_sync(kAll, sum_taken, o);
     if (lane >= o) {
-      sum_given += a;
-      sum_taken += b;
+      sum_given += x;
+      sum_taken += y;
     }
   }
   if (lane == 31) {
@@ -309,71 +325,80 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const ReorderParams p
   top += free_now;
 
   // ---- abandoned pages onto the pool, children's entries
+#pragma unroll 1
   for (int g = g0 + slot; g < g1; g += slots) {
-    Beams s = beams_of(p, g, lane, false);
-    const bool moved = g < fail && !s_bad[g - g0];
-    if (!moved) {  // every beam stays itself
-      s.parent = lane < p.K ? lane : -1;
-      s.new_held = s.held;
-      s.used = kAll;
+    if (!single) {
+      s = beams_of(p, g, lane, false);
+      copy = s.ok && copies_page(p, s, g, lane, page);
     }
-    const Range r = columns_of(s.columns, part, p.warps);
+    const bool moved = g < fail && !s_bad[g - g0];
+    int parent = s.parent, new_held = s.new_held;
+    if (!moved) {  // every beam stays itself
+      parent = lane < p.K ? lane : -1;
+      new_held = s.held;
+    }
+    const bool held = single && s.ok && r.end - r.begin <= 32;  // the columns are in registers
+    r = columns_of(s.columns, part, p.warps);
     int at = s_given[g];
     for (int i = 0; i < part; ++i) at += s_part[(g - g0) * p.warps + i];
+#pragma unroll 1
     for (int j = r.begin + lane; j - lane < r.end; j += 32) {
       const int col = j < r.end ? j : 0x7fffffff;
+      if (!held) load_column<KM>(p, s, g, col, c);
       if (moved) {
-        Column<KM> c;
-        load_column<KM>(p, s, g, col, c);
         const int mine = __popc(c.gone);
-        int upto = mine;
+        if (__any_sync(kAll, mine != 0)) {
+          int upto = mine;
+#pragma unroll 1
+          for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(kAll, upto, o);
+            if (lane >= o) upto += x;
+          }
+          int to = at + upto - mine;
+          for (uint32_t left = c.gone; left != 0; left &= left - 1) {
+            const int k = __ffs((int)left) - 1;
+            int e = c.e[0];
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int x = __shfl_up_sync(kAll, upto, o);
-          if (lane >= o) upto += x;
-        }
-        int to = at + upto - mine;
-#pragma unroll
-        for (int k = 0; k < KM; ++k)
-          if (c.gone >> k & 1) {
-            if (to < room) p.free_pages[free_now + to] = c.e[k];
+            for (int q = 1; q < KM; ++q) e = q == k ? c.e[q] : e;
+            if (to < room) p.free_pages[free_now + to] = e;
             ++to;
           }
-        at += __shfl_sync(kAll, upto, 31);
-      }
-      // all of the column is read before any of it is written
-      int n[KM];
-      uint32_t write = 0;
-#pragma unroll
-      for (int i = 0; i < KM; ++i) {
-        const int par = __shfl_sync(kAll, s.parent, i), held = __shfl_sync(kAll, s.new_held, i);
-        n[i] = 0;
-        if (col < held && !(par == i && p.table == p.table_out)) {
-          n[i] = load_l2(p.table + ((int64_t)g * p.K + par) * p.bt_stride + col);
-          write |= 1u << i;
+          at += __shfl_sync(kAll, upto, 31);
         }
       }
+      // (all of the column has been read before any of it is written)
 #pragma unroll
-      for (int i = 0; i < KM; ++i)
-        if (write >> i & 1) p.table_out[((int64_t)g * p.K + i) * p.bto_stride + col] = n[i];
+      for (int i = 0; i < KM; ++i) {
+        const int par = __shfl_sync(kAll, parent, i), end = __shfl_sync(kAll, new_held, i);
+        if (col < end && !(par == i && p.table == p.table_out)) {
+          int e = c.e[0];
+#pragma unroll
+          for (int q = 1; q < KM; ++q) e = q == par ? c.e[q] : e;
+          p.table_out[((int64_t)g * p.K + i) * p.bto_stride + col] = e;
+        }
+      }
     }
+    if (!single && lane < p.K) p.copies[3 * (g * p.K + lane)] = moved && copy ? page : -1;
   }
   cluster.sync();
 
   // ---- fresh pages, copies, lengths
   if (rank == 0 && tid == 0) *p.free_count_out = max(0, top - used);
+#pragma unroll 1
   for (int g = g0 + slot; g < g1; g += slots) {
     if (part != 0) continue;
-    const Beams s = beams_of(p, g, lane, false);
     const bool moved = g < fail && !s_bad[g - g0];
     const int row = g * p.K + lane;
-    int32_t* out = p.table_out + (int64_t)g * p.K * p.bto_stride;
-    auto out_entry = [&](int i, int, int j) { return load_l2(out + i * p.bto_stride + j); };
+    if (!single) {
+      s = beams_of(p, g, lane, false);
+      page = lane < p.K ? load_l2(p.copies + 3 * row) : -1;
+      copy = page >= 0;
+    }
     int src = -1, dst = -1, tokens = 0;
-    if (moved) {
-      const bool copy = copies_page(p, s, lane, out_entry);
+    if (moved && __any_sync(kAll, copy)) {
       // fresh pages by column, then by child
       int before = 0;
+#pragma unroll 1
       for (int i = 0; i < p.K; ++i) {
         const int part_i = __shfl_sync(kAll, s.partial, i);
         const bool copy_i = __shfl_sync(kAll, (int)copy, i) != 0;
@@ -381,19 +406,18 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const ReorderParams p
       }
       if (copy) {
         const int at = top - 1 - (s_taken[g] + before);
-        const int page = at >= 0 ? load_l2(p.free_pages + at) : -1;
-        if (page >= 0 && page < p.num_pages) {
-          src = out_entry(lane, 0, s.partial);
-          dst = page;
+        const int fresh = at >= 0 ? load_l2(p.free_pages + at) : -1;
+        if (fresh >= 0 && fresh < p.num_pages) {
+          src = page;
+          dst = fresh;
           tokens = s.new_len & ((1 << p.page_log2) - 1);
+          p.table_out[(int64_t)row * p.bto_stride + s.partial] = dst;
         } else {
           report(p.err, PA_DEVERR_PAGE_OOB, row, s.partial);
         }
       }
     }
-    __syncwarp();  // the lanes' entries have been read
     if (lane < p.K) {
-      if (dst >= 0) out[(int64_t)lane * p.bto_stride + s.partial] = dst;
       p.copies[3 * row] = src;
       p.copies[3 * row + 1] = dst;
       p.copies[3 * row + 2] = tokens;
@@ -405,13 +429,12 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const ReorderParams p
 template <int KM>
 cudaError_t launch_reorder(ReorderParams p, cudaStream_t st) {
   static std::atomic<uint64_t> asked{0}, wide{0}, allowed{0};
-  // A warp for each 32 columns as far as they go, and as many CTAs as that fills.
+  // A warp for each 32 columns as far as they go, and as many CTAs of eight warps as
+  // that fills (barriers of few warps are short); then larger ones.
   const int chunks = (p.max_pages + 31) / 32;
   int ctas = 1;
-  while (ctas < kMaxCluster && ctas < p.B && (long long)p.B * chunks > (long long)ctas * kWarps)
-    ctas *= 2;
+  while (ctas < kMaxCluster && ctas < p.B && (long long)p.B * chunks > (long long)ctas * 8) ctas *= 2;
   cudaLaunchConfig_t cfg{};
-  cfg.blockDim = dim3(kThreads);
   cfg.stream = st;
   cudaLaunchAttribute attrs[2] = {};
   cudaLaunchAttribute& at = attrs[0];
@@ -424,12 +447,15 @@ cudaError_t launch_reorder(ReorderParams p, cudaStream_t st) {
     const int per = (p.B + ctas - 1) / ctas;
     p.warps = 1;
     while (p.warps < kWarps && p.warps < chunks && p.warps * 2 * per <= kWarps) p.warps *= 2;
-    cfg.dynamicSmemBytes = (size_t)p.B * 8 + (size_t)per * p.warps * 4 + (size_t)per;
+    const int warps = per * p.warps < 4 ? 4 : per * p.warps < kWarps ? per * p.warps : kWarps;
+    cfg.blockDim = dim3((unsigned)(warps + p.warps - 1) / p.warps * p.warps * 32);
+    cfg.dynamicSmemBytes = (size_t)p.B * 8 + (size_t)per * (p.warps + 1) * 4 + (size_t)per;
     cfg.gridDim = dim3((unsigned)ctas);
     at.val.clusterDim.x = (unsigned)ctas;
   };
-  // 8 B a request, and of a CTA 4 B a warp's part (at most kWarps or one a request) and a flag
-  const int most = kMaxRows * 8 + kMaxRows * 4 + kMaxRows;
+  // 8 B a request, and of a CTA 4 B a warp's part (kWarps at most, or one a request), 4 B
+  // and a flag a request
+  const int most = kMaxRows * (8 + 4 + 4 + 1);
   cudaError_t e = allow_shared(reinterpret_cast<const void*>(reorder_kernel<KM>), most, &allowed);
   if (e != cudaSuccess) return e;
   shape();
