@@ -359,11 +359,11 @@ def _load_native():
     spec = importlib.util.spec_from_file_location("_binding", path, loader=loader)
     native = importlib.util.module_from_spec(spec)
     loader.exec_module(native)
-    native.bind(*[ctypes.cast(fn, _vp).value for fn in (
-        lib.pa_plan_step, lib.pa_release_pages, lib.pa_rotary_append_varlen,
-        lib.pa_fwd_varlen_e4m3, lib.pa_fwd_varlen_e4m3_workspace_size, lib.pa_beam_select,
-        lib.pa_beam_reorder, lib.pa_copy_pages, lib.pa_fwd_cross,
-        lib.pa_fwd_cross_workspace_size)])
+    address = lambda *fns: [ctypes.cast(f, _vp).value for f in fns]  # noqa: E731
+    native.bind(*address(lib.pa_plan_step, lib.pa_release_pages, lib.pa_rotary_append_varlen,
+                         lib.pa_fwd_varlen_e4m3, lib.pa_fwd_varlen_e4m3_workspace_size))
+    native.bind_beam(*address(lib.pa_beam_select, lib.pa_beam_reorder, lib.pa_copy_pages,
+                              lib.pa_fwd_cross, lib.pa_fwd_cross_workspace_size))
     _native = native
     return native
 

@@ -160,22 +160,34 @@ bool count_is(Py_ssize_t n, Py_ssize_t expected) {
   return false;
 }
 
-// bind(plan, release, append, attend, attend_workspace, select, reorder, copy, cross,
-//      cross_workspace): entry addresses
+uintptr_t address_of(PyObject* o) { return (uintptr_t)(unsigned long long)integer(o); }
+template <typename F>
+void entry(F& f, PyObject* address) {
+  f = reinterpret_cast<F>(address_of(address));
+}
+
+// bind(plan, release, append, attend, attend_workspace): entry addresses
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (!count_is(n, 10)) return nullptr;
+  if (!count_is(n, 5)) return nullptr;
   return guarded([&]() -> PyObject* {
-    auto at = [&](int i) { return (uintptr_t)(unsigned long long)integer(a[i]); };
-    g_entries.plan = reinterpret_cast<decltype(g_entries.plan)>(at(0));
-    g_entries.release = reinterpret_cast<decltype(g_entries.release)>(at(1));
-    g_entries.append = reinterpret_cast<decltype(g_entries.append)>(at(2));
-    g_entries.attend = reinterpret_cast<decltype(g_entries.attend)>(at(3));
-    g_entries.attend_workspace = reinterpret_cast<decltype(g_entries.attend_workspace)>(at(4));
-    g_entries.select = reinterpret_cast<decltype(g_entries.select)>(at(5));
-    g_entries.reorder = reinterpret_cast<decltype(g_entries.reorder)>(at(6));
-    g_entries.copy = reinterpret_cast<decltype(g_entries.copy)>(at(7));
-    g_entries.cross = reinterpret_cast<decltype(g_entries.cross)>(at(8));
-    g_entries.cross_workspace = reinterpret_cast<decltype(g_entries.cross_workspace)>(at(9));
+    entry(g_entries.plan, a[0]);
+    entry(g_entries.release, a[1]);
+    entry(g_entries.append, a[2]);
+    entry(g_entries.attend, a[3]);
+    entry(g_entries.attend_workspace, a[4]);
+    Py_RETURN_NONE;
+  });
+}
+
+// bind_beam(select, reorder, copy, cross, cross_workspace): entry addresses
+PyObject* bind_beam(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count_is(n, 5)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    entry(g_entries.select, a[0]);
+    entry(g_entries.reorder, a[1]);
+    entry(g_entries.copy, a[2]);
+    entry(g_entries.cross, a[3]);
+    entry(g_entries.cross_workspace, a[4]);
     Py_RETURN_NONE;
   });
 }
@@ -568,6 +580,7 @@ PyCFunction as_method() {
 
 PyMethodDef g_methods[] = {
     {"bind", as_method<bind>(), METH_FASTCALL, nullptr},
+    {"bind_beam", as_method<bind_beam>(), METH_FASTCALL, nullptr},
     {"plan_step", as_method<plan_step>(), METH_FASTCALL, nullptr},
     {"release_pages", as_method<release_pages>(), METH_FASTCALL, nullptr},
     {"rotary_append_varlen", as_method<rotary_append_varlen>(), METH_FASTCALL, nullptr},
