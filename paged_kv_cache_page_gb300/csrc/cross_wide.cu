@@ -43,7 +43,7 @@ constexpr int kSoft = 8;  // softmax warps
 constexpr int kWarpK = 8, kWarpV = 9, kWarpMma = 10, kWarpFix = 11;
 constexpr int kThreads = 12 * 32;
 constexpr int kMinShare = 2;  // tiles
-constexpr int kSnap = 2;      // tiles that a cut moves to an end of its stream
+constexpr int kSnap = 1;      // tiles that a cut moves to an end of its stream
 constexpr int kEnds = 3;      // what a stream's begin and end cost, in tiles
 
 template <int D>
@@ -862,46 +862,56 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto from = [&](int cta) {
           return ((int64_t)(2 * cta + (cta == c.cta0 ? 1 : 0)) * 2 + tile) * kM;
         };
-        float ref = neg_inf(), sum = 0.f;
-        if (valid) {
-          for (int cta = c.cta0; cta <= c.cta1; ++cta)
-            ref = fmaxf(ref, __ldcg(p.part_ml + from(cta) + r).x);
-          for (int cta = c.cta0; cta <= c.cta1; ++cta) {
-            const float2 ml = __ldcg(p.part_ml + from(cta) + r);
-            sum = fmaf(weight(ml, ref), ml.y, sum);
-          }
-        }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        // 64 columns at a time (32 where there are no more): what a part has of them is
+        // one wait for L2
+        constexpr int kAtOnce = D == 128 ? 16 : 8;
 #pragma unroll 1
-        for (int col = col0; col < col0 + cols; col += 32) {
-          float o[32];
+        for (int col = col0; col < col0 + cols; col += 4 * kAtOnce) {
+          float ref = neg_inf(), sum = 0.f;
+          float4 acc[kAtOnce];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0.f;
+          for (int e = 0; e < kAtOnce; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
           if (valid) {
 #pragma unroll 1
             for (int cta = c.cta0; cta <= c.cta1; ++cta) {
-              float4 y[8];
+              float4 y[kAtOnce];
               const float2 ml = __ldcg(p.part_ml + from(cta) + r);
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
+              for (int e = 0; e < kAtOnce; ++e)
                 y[e] = load16_l2(p.part_o + (from(cta) * (D / 4) + (col / 4 + e) * kM + r) * 4);
+              // (a part without a seen key counts for nothing, its O may hold nothing)
               if (ml.y == 0.f) continue;
-              const float w = weight(ml, ref);
+              const float to = fmaxf(ref, ml.x);
+              const float v = ref == to ? 1.f : ex2(ref - to), w = ml.x == to ? 1.f : ex2(ml.x - to);
+              ref = to;
+              sum = fmaf(sum, v, w * ml.y);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                o[4 * e] = fmaf(w, y[e].x, o[4 * e]);
-                o[4 * e + 1] = fmaf(w, y[e].y, o[4 * e + 1]);
-                o[4 * e + 2] = fmaf(w, y[e].z, o[4 * e + 2]);
-                o[4 * e + 3] = fmaf(w, y[e].w, o[4 * e + 3]);
+              for (int e = 0; e < kAtOnce; ++e) {
+                acc[e].x = fmaf(acc[e].x, v, w * y[e].x);
+                acc[e].y = fmaf(acc[e].y, v, w * y[e].y);
+                acc[e].z = fmaf(acc[e].z, v, w * y[e].z);
+                acc[e].w = fmaf(acc[e].w, v, w * y[e].w);
               }
             }
           }
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          if (valid && col == 0 && p.lse != nullptr)
+            p.lse[(int64_t)head * p.total_q + c.q0 + token] =
+                sum == 0.f ? neg_inf() : (ref + log2f(sum)) * kLn2;
           __syncwarp();
-          write(my_row, col, o, inv);
+#pragma unroll
+          for (int x = 0; x < kAtOnce; x += 8) {
+            float o[32];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              o[4 * e] = acc[x + e].x;
+              o[4 * e + 1] = acc[x + e].y;
+              o[4 * e + 2] = acc[x + e].z;
+              o[4 * e + 3] = acc[x + e].w;
+            }
+            write(my_row, col + 4 * x, o, inv);
+          }
         }
-        if (valid && (!one || g == 0) && p.lse != nullptr)
-          p.lse[(int64_t)head * p.total_q + c.q0 + token] =
-              sum == 0.f ? neg_inf() : (ref + log2f(sum)) * kLn2;
       }
     }
   }
