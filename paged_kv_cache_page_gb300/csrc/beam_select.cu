@@ -40,9 +40,9 @@ int set_error(int code, const char* fmt, ...);
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kCtasPerSm = 2;
+constexpr int kCtasPerSm = 1;
 constexpr int kVecs = 8;           // 16-byte vectors of a lane in a step
 constexpr int kStepVecs = 32 * kVecs;
 constexpr int kMaxBeams = 32;
@@ -559,8 +559,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) select_kernel(const Sele
       for (int o = 16; o > 0; o >>= 1) fold(o);
       if (lane == 0) sm.warp_best[warp] = best;
       __syncthreads();
-      best = sm.warp_best[lane % kWarps];
-      for (int o = kWarps / 2; o > 0; o >>= 1) fold(o);
+      for (int w = 0; w < kWarps; ++w)
+        if (better(sm.warp_best[w], best)) best = sm.warp_best[w];
       if (tid == 0) lists[out] = best;
       last = best;  // (more than kMaxCandidates pass, so there is one)
       __syncthreads();
