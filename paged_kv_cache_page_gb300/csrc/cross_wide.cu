@@ -49,24 +49,24 @@ constexpr int kEnds = 3;      // what a stream's begin and end cost, in tiles
 template <int D>
 struct Layout {
   static constexpr int kTile = D / 64 * kSlab;
-  static constexpr int kStages = D == 128 ? 2 : 3;  // of K and of V
-  static constexpr int kOffQ = 0;                   // [2]
+  static constexpr int kK = D == 128 ? 2 : 3;  // tiles of K
+  static constexpr int kV = D == 128 ? 3 : 4;  // and of V, which stay longer
+  static constexpr int kOffQ = 0;              // [2]
   static constexpr int kOffK = 2 * kTile;
-  static constexpr int kOffV = kOffK + kStages * kTile;
-  static constexpr int kOffOut = kOffV + kStages * kTile;  // [warps][2][32 rows][64 bytes]
-  static constexpr int kOffBar = kOffOut + kSoft * 4096;
-  static constexpr int kLimits = kStages + 1;              // tiles whose limits are held
-  // q_full, q_empty; k_full, k_empty, v_full, v_ready, v_empty [kStages];
-  // s_full, p_full, pv_done, o_free [2]; l_full [kLimits]; part_full [2], told
-  static constexpr int kBars = 2 + 5 * kStages + 8 + kLimits + 3;
-  static constexpr int kOffSums = kOffBar + kBars * 8;      // int [24]
-  static constexpr int kOffLimit = (kOffSums + 24 * 4 + 15) & ~15;  // float [kLimits][kN] of scores
-  static constexpr int kOffPlain = kOffLimit + kLimits * kN * 4;    // int [kLimits] no limits in the tile
-  static constexpr int kOffCut = kOffPlain + kLimits * 4;           // Cut [2]
-  static constexpr int kOffMisc = kOffCut + 2 * 48;         // start [2], TMEM base
-  static constexpr int kBytes = kOffMisc + 16 + 1024;
+  static constexpr int kOffV = kOffK + kK * kTile;
+  static constexpr int kOffLimit = kOffV + kV * kTile;        // float [kV][kN] of scores
+  static constexpr int kOffHalf = kOffLimit + kV * kN * 4;    // float2 [kM] m and l of a group
+  static constexpr int kOffBar = kOffHalf + kM * 8;
+  // q_full, q_empty; k_full, k_empty [kK]; v_full, v_ready, v_empty [kV]; s_full, p_full,
+  // pv_done, o_free [2]; part_full [2], told
+  static constexpr int kBars = 2 + 2 * kK + 3 * kV + 8 + 3;
+  static constexpr int kOffSums = kOffBar + kBars * 8;        // int [kThreads / 32]
+  static constexpr int kOffPlain = kOffSums + 12 * 4;         // int [kV] no limits in the tile
+  static constexpr int kOffCut = kOffPlain + kV * 4;          // Cut [2]
+  static constexpr int kOffMisc = kOffCut + 2 * 28;           // start [2], TMEM base
+  static constexpr int kBytes = kOffMisc + 12;                // (the base is aligned to 1024)
   static_assert(kBytes <= 232448, "shared memory");
-  static_assert(kOffOut % 16 == 0 && kOffLimit % 16 == 0, "read 16 bytes at a time");
+  static_assert(kOffLimit % 16 == 0 && kOffBar % 8 == 0, "read 16 bytes at a time; 64-bit words");
 };
 
 // P of the type: the largest score is brought to 2^shift at first, and may pass
@@ -235,7 +235,7 @@ struct Walk {
 struct Cut {
   int q0, rows, h, pair, cta0, cta1, last;
 };
-static_assert(sizeof(Cut) <= 48, "kOffCut");
+static_assert(sizeof(Cut) == 28, "kOffCut");
 
 template <int D, typename T>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -245,8 +245,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   using E = Elem<T>;
   using R = Range<T>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
+  uint8_t* smem = smem_raw;
+  if ((smem_u32(smem) & 1023) != 0) {  // (what swizzled tiles ask for; no room is left to move them)
+    if (threadIdx.x == 0) report(p.err, PA_DEVERR_TIMEOUT, -1, 99);
+    return;
+  }
   uint8_t* sQ = smem + L::kOffQ;
   uint8_t* sK = smem + L::kOffK;
   uint8_t* sV = smem + L::kOffV;
@@ -254,31 +257,33 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* q_full = bars;
   uint64_t* q_empty = bars + 1;
   uint64_t* k_full = bars + 2;
-  uint64_t* k_empty = k_full + L::kStages;
-  uint64_t* v_full = k_empty + L::kStages;
-  uint64_t* v_ready = v_full + L::kStages;
-  uint64_t* v_empty = v_ready + L::kStages;
-  uint64_t* s_full = v_empty + L::kStages;
+  uint64_t* k_empty = k_full + L::kK;
+  uint64_t* v_full = k_empty + L::kK;
+  uint64_t* v_ready = v_full + L::kV;
+  uint64_t* v_empty = v_ready + L::kV;
+  uint64_t* s_full = v_empty + L::kV;
   uint64_t* p_full = s_full + 2;
   uint64_t* pv_done = p_full + 2;
   uint64_t* o_free = pv_done + 2;
-  uint64_t* l_full = o_free + 2;
-  uint64_t* part_full = l_full + L::kLimits;  // [2]: the rows of the first, last part are written
+  uint64_t* part_full = o_free + 2;           // [2]: the rows of the first, last part are written
   uint64_t* told = part_full + 2;             // what is to be joined is known
   int* sSums = reinterpret_cast<int*>(smem + L::kOffSums);
   Cut* sCut = reinterpret_cast<Cut*>(smem + L::kOffCut);       // the first part, the last
   int* sStart = reinterpret_cast<int*>(smem + L::kOffMisc);    // entry, tiles in front of it
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc + 8);
   float* sLimit = reinterpret_cast<float*>(smem + L::kOffLimit);
+  float2* sHalf = reinterpret_cast<float2*>(smem + L::kOffHalf);
   int* sPlain = reinterpret_cast<int*>(smem + L::kOffPlain);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
-    for (int i = 0; i < L::kStages; ++i) {
+    for (int i = 0; i < L::kK; ++i) {
       mbar_init(&k_full[i], 1);
       mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < L::kV; ++i) {
       mbar_init(&v_full[i], 1);
       mbar_init(&v_ready[i], 1);
       mbar_init(&v_empty[i], 1);
@@ -289,7 +294,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&pv_done[g], 1);
       mbar_init(&o_free[g], kSoft);
     }
-    for (int i = 0; i < L::kLimits; ++i) mbar_init(&l_full[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&part_full[i], kSoft);
     mbar_init(told, 1);
     fence_mbar_init();
@@ -410,20 +414,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* empty = is_v ? v_empty : k_empty;
     uint8_t* ring = is_v ? sV : sK;
     const CUtensorMap* map = is_v ? &tmv : &tmk;
-    int k = 0, a = 0;
+    const int stages = is_v ? L::kV : L::kK;
+    int s = 0, a = 0;     // place in the ring,
+    uint32_t round = 0;   // and how often it has come round
+    int behind = 0;       // tiles issued, up to the ring's places
     if (lane == 0) {
       tma_prefetch_desc(map);
       if (!is_v) tma_prefetch_desc(&tmq);
       for (; at.n > 0; at.next(p)) {
         if (at.e.keys == 0) continue;
-        for (int t = at.t0; t < at.t0 + at.n; ++t, ++k) {
-          const int s = k % L::kStages;
-          wait(&empty[s], (uint32_t)((k / L::kStages & 1) ^ 1), is_v ? 21 : 20);
+        for (int t = at.t0; t < at.t0 + at.n; ++t) {
+          wait(&empty[s], (round & 1) ^ 1, is_v ? 21 : 20);
           if (failed) break;
           mbar_arrive_expect_tx(&full[s], L::kTile);
           for (int c = 0; c < D / 64; ++c)
             tma_load_4d(ring + s * L::kTile + c * kSlab, map, &full[s], c * 64, at.h / p.kv_split,
                         at.e.k0 + t * kN, 0, keep);
+          if (++s == stages) {
+            s = 0;
+            ++round;
+          }
+          behind = min(behind + 1, stages);
           if (!is_v && t == at.t0) {
             if (a >= 1) wait(q_empty, (uint32_t)((a - 1) & 1), 10);
             if (failed) break;
@@ -437,13 +448,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ++a;
       }
-      // every copy must land before the CTA leaves
-      if (!failed)
-        for (int i = 0; i < L::kStages; ++i, ++k)
-          wait(&empty[k % L::kStages], (uint32_t)((k / L::kStages & 1) ^ 1), 30);
-      else
-        for (int i = max(0, k - L::kStages); i < k; ++i)
-          mbar_wait(&full[i % L::kStages], (uint32_t)(i / L::kStages & 1));
+      // every copy must land before the CTA leaves: the last `behind` tiles
+      for (int i = 0; i < behind; ++i) {
+        if (s-- == 0) {
+          s = stages - 1;
+          --round;
+        }
+        if (failed) mbar_wait(&full[s], round & 1);
+        else wait(&empty[s], round & 1, 30);
+      }
     }
     __syncwarp();
   } else if (warp == kWarpFix) {
@@ -480,21 +493,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t next = mask_bytes(at.t0);
 #pragma unroll 1
       for (int t = at.t0; t < at.t0 + at.n; ++t, ++k) {
-        const int s = k % L::kStages, place = k % L::kLimits;
+        const int s = k % L::kV;
         const uint32_t seen = next;
         const bool whole = __all_sync(0xffffffffu, seen == 0xfu);
-        // (V of the tile before has arrived, so P V of the last tile with these
-        // limits is done)
-        if (lane == 0) sPlain[place] = whole ? 1 : 0;
+        if (t + 1 < at.t0 + at.n) next = mask_bytes(t + 1);
+        wait(&v_full[s], (uint32_t)(k / L::kV & 1), 25);
+        // (V's place has been free: the scores of the tile before in it are used up)
+        if (lane == 0) sPlain[s] = whole ? 1 : 0;
         if (!whole) {
 #pragma unroll
           for (int c = 0; c < kN / 32; ++c)
-            sLimit[place * kN + c * 32 + lane] = seen >> c & 1 ? -neg_inf() : neg_inf();
-          __syncwarp();
+            sLimit[s * kN + c * 32 + lane] = seen >> c & 1 ? -neg_inf() : neg_inf();
         }
-        if (lane == 0) mbar_arrive(&l_full[place]);
-        if (t + 1 < at.t0 + at.n) next = mask_bytes(t + 1);
-        wait(&v_full[s], (uint32_t)(k / L::kStages & 1), 25);
         if (!whole) {
           uint8_t* tile = sV + s * L::kTile;
           // the lane's four rows, each lane's chunks in another order
@@ -578,8 +588,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool one = solo(at);
       wait(q_full, (uint32_t)(a & 1), 40);
       auto first = [&](int g, int t, bool last_of_tile) {
-        const int s = (k + t) % L::kStages;
-        wait(&k_full[s], (uint32_t)((k + t) / L::kStages & 1), 41);
+        const int s = (k + t) % L::kK;
+        wait(&k_full[s], (uint32_t)((k + t) / L::kK & 1), 41);
         tc::fence_after_sync();
         scores(g, one ? 0 : g, s);
         if (last_of_tile) release(&k_empty[s]);
@@ -591,10 +601,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int i = 0; i < (one ? at.n : 2 * at.n); ++i) {
         const int g = i & 1, t = one ? i : i >> 1, next_t = one ? i + 2 : t + 1;
-        const int s = (k + t) % L::kStages;
+        const int s = (k + t) % L::kV;
         const int n = g ? n1 : n0, m = g ? m1 : m0;
         const bool fresh = one ? i < 2 : t == 0;
-        if (one || g == 0) wait(&v_ready[s], (uint32_t)((k + t) / L::kStages & 1), 50);
+        if (one || g == 0) wait(&v_ready[s], (uint32_t)((k + t) / L::kV & 1), 50);
         wait(&p_full[g], (uint32_t)(n & 1), 51 + g);
         if (fresh && m >= 1) wait(&o_free[g], (uint32_t)((m - 1) & 1), 53 + g);
         tc::fence_after_sync();
@@ -615,27 +625,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = quarter * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const float f = p.scale_log2;
-    uint8_t* staged = smem + L::kOffOut + warp * 4096;
-    // 32 columns of the warp's rows by way of shared memory: a thread holds a row,
-    // and whole sectors of few rows are written at a time
+    // 32 columns of a row a thread: four threads exchange 16-byte chunks, so that each
+    // has the same chunk of their four rows, and 64 bytes of a row are written at a time
     auto write = [&](long long my_row, int col, const float (&x)[32], float by) {
-      uint8_t* buf = staged + (col >> 5 & 1) * 2048;
+      uint4 c[4];
 #pragma unroll
-      for (int e = 0; e < 32; e += 8)
-        *reinterpret_cast<uint4*>(buf + lane * 64 + (((e >> 3) ^ (lane >> 1 & 3)) << 4)) =
-            make_uint4(E::from_f2(x[e] * by, x[e + 1] * by), E::from_f2(x[e + 2] * by, x[e + 3] * by),
-                       E::from_f2(x[e + 4] * by, x[e + 5] * by),
-                       E::from_f2(x[e + 6] * by, x[e + 7] * by));
-      __syncwarp();
-      const int c = lane & 3;
+      for (int i = 0; i < 4; ++i)
+        c[i] = make_uint4(E::from_f2(x[8 * i] * by, x[8 * i + 1] * by),
+                          E::from_f2(x[8 * i + 2] * by, x[8 * i + 3] * by),
+                          E::from_f2(x[8 * i + 4] * by, x[8 * i + 5] * by),
+                          E::from_f2(x[8 * i + 6] * by, x[8 * i + 7] * by));
 #pragma unroll
-      for (int i = lane >> 2; i < 32; i += 8) {
-        const long long to = __shfl_sync(0xffffffffu, my_row, i);
-        const uint4 y = *reinterpret_cast<const uint4*>(buf + i * 64 + ((c ^ (i >> 1 & 3)) << 4));
+      for (int bit = 1; bit < 4; bit *= 2)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (i & bit) continue;
+          const bool up = (lane & bit) != 0;
+          uint4 send = up ? c[i] : c[i | bit];
+          send.x = __shfl_xor_sync(0xffffffffu, send.x, bit);
+          send.y = __shfl_xor_sync(0xffffffffu, send.y, bit);
+          send.z = __shfl_xor_sync(0xffffffffu, send.z, bit);
+          send.w = __shfl_xor_sync(0xffffffffu, send.w, bit);
+          if (up) c[i] = send;
+          else c[i | bit] = send;
+        }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const long long to = __shfl_sync(0xffffffffu, my_row, (lane & 28) + i);
         if (to >= 0)
-          *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.out) + to * D + col + c * 8) = y;
+          *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.out) + to * D + col + (lane & 3) * 8) = c[i];
       }
-      __syncwarp();
     };
     auto weight = [](float2 x, float ref) {
       return x.y == 0.f ? 0.f : x.x == ref ? 1.f : ex2(x.x - ref);
@@ -651,11 +670,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       int n = g ? done[1] : done[0];
       for (int j = one ? g : 0; j < at.n && at.e.keys > 0; j += one ? 2 : 1) {
         bool whole = p.key_mask == nullptr && (at.t0 + j + 1) * kN <= at.e.keys;
-        const int place = (k + j) % L::kLimits;
+        const int place = (k + j) % L::kV;
         wait(&s_full[g], (uint32_t)(n & 1), 60 + g);
-        // (behind the scores: P V of the last tile with this place has been issued then)
+        // (behind the scores: P V of the last tile in this place has been issued then)
         if (!whole) {
-          wait(&l_full[place], (uint32_t)((k + j) / L::kLimits & 1), 66);
+          wait(&v_ready[place], (uint32_t)((k + j) / L::kV & 1), 66);
           whole = sPlain[place] != 0;
         }
         tc::fence_after_sync();
@@ -781,13 +800,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       // and its O may hold nothing).
       float2 half[2] = {make_float2(m, l), make_float2(m, l)};
       if (one) {
-        // (by way of the warps' places for results)
-        reinterpret_cast<float2*>(staged)[lane] = half[0];
-        named_barrier(1, 256);
+        // (each group's in turn, in one place)
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-          half[x] = reinterpret_cast<const float2*>(smem + L::kOffOut + (4 * x + quarter) * 4096)[lane];
-        named_barrier(1, 256);  // (read, before it is written again)
+        for (int x = 0; x < 2; ++x) {
+          if (g == x) sHalf[r] = half[g];
+          named_barrier(1, 256);
+          if (g != x) half[x] = sHalf[r];
+          if (x == 0) named_barrier(1, 256);
+        }
         m = fmaxf(half[0].x, half[1].x);
       }
       const float weight0 = weight(half[0], m), weight1 = weight(half[1], m);
