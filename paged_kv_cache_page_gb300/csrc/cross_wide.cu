@@ -57,9 +57,9 @@ struct Layout {
   static constexpr int kOffLimit = kOffV + kV * kTile;        // float [kV][kN] of scores
   static constexpr int kOffHalf = kOffLimit + kV * kN * 4;    // float2 [kM] m and l of a group
   static constexpr int kOffBar = kOffHalf + kM * 8;
-  // q_full, q_empty; k_full, k_empty [kK]; v_full, v_ready, v_empty [kV]; s_full, p_full,
-  // pv_done, o_free [2]; part_full [2], told
-  static constexpr int kBars = 2 + 2 * kK + 3 * kV + 8 + 3;
+  // q_full, q_empty; k_full, k_empty [kK]; v_full, v_ready, v_empty, l_full [kV]; s_full,
+  // p_full, pv_done, o_free [2]; part_full [2], told
+  static constexpr int kBars = 2 + 2 * kK + 4 * kV + 8 + 3;
   static constexpr int kOffSums = kOffBar + kBars * 8;        // int [kThreads / 32]
   static constexpr int kOffPlain = kOffSums + 12 * 4;         // int [kV] no limits in the tile
   static constexpr int kOffCut = kOffPlain + kV * 4;          // Cut [2]
@@ -261,7 +261,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* v_full = k_empty + L::kK;
   uint64_t* v_ready = v_full + L::kV;
   uint64_t* v_empty = v_ready + L::kV;
-  uint64_t* s_full = v_empty + L::kV;
+  uint64_t* l_full = v_empty + L::kV;  // the tile's limits
+  uint64_t* s_full = l_full + L::kV;
   uint64_t* p_full = s_full + 2;
   uint64_t* pv_done = p_full + 2;
   uint64_t* o_free = pv_done + 2;
@@ -287,6 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&v_full[i], 1);
       mbar_init(&v_ready[i], 1);
       mbar_init(&v_empty[i], 1);
+      mbar_init(&l_full[i], 1);
     }
     for (int g = 0; g < 2; ++g) {
       mbar_init(&s_full[g], 1);
@@ -496,15 +498,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int s = k % L::kV;
         const uint32_t seen = next;
         const bool whole = __all_sync(0xffffffffu, seen == 0xfu);
-        if (t + 1 < at.t0 + at.n) next = mask_bytes(t + 1);
-        wait(&v_full[s], (uint32_t)(k / L::kV & 1), 25);
-        // (V's place has been free: the scores of the tile before in it are used up)
+        // V's place is free, so the limits of the last tile in it are used up; the
+        // softmax warps can go on while V is on its way
+        wait(&v_empty[s], (uint32_t)((k / L::kV & 1) ^ 1), 24);
         if (lane == 0) sPlain[s] = whole ? 1 : 0;
         if (!whole) {
 #pragma unroll
           for (int c = 0; c < kN / 32; ++c)
             sLimit[s * kN + c * 32 + lane] = seen >> c & 1 ? -neg_inf() : neg_inf();
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&l_full[s]);
+        if (t + 1 < at.t0 + at.n) next = mask_bytes(t + 1);
+        wait(&v_full[s], (uint32_t)(k / L::kV & 1), 25);
         if (!whole) {
           uint8_t* tile = sV + s * L::kTile;
           // the lane's four rows, each lane's chunks in another order
@@ -674,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait(&s_full[g], (uint32_t)(n & 1), 60 + g);
         // (behind the scores: P V of the last tile in this place has been issued then)
         if (!whole) {
-          wait(&v_ready[place], (uint32_t)((k + j) / L::kV & 1), 66);
+          wait(&l_full[place], (uint32_t)((k + j) / L::kV & 1), 66);
           whole = sPlain[place] != 0;
         }
         tc::fence_after_sync();
