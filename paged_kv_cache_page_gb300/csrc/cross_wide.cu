@@ -168,6 +168,13 @@ __device__ __noinline__ void scale_p(uint32_t t, int cols, float by) {
   tc::tmem_wait_st();
 }
 
+// A load that stays where it is written (see load16).
+__device__ __forceinline__ uint32_t load_byte(const uint8_t* src) {
+  uint32_t x;
+  asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(x) : "l"(src));
+  return x;
+}
+
 __device__ __forceinline__ void mbar_arrive_2(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], 2;" ::"r"(smem_u32(bar)) : "memory");
 }
@@ -482,21 +489,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     for (; at.n > 0; at.next(p)) {
       if (at.e.keys == 0) continue;
-      auto mask_bytes = [&](int t) -> uint32_t {  // of the lane's four keys of tile t
-        uint32_t x = 0;
+      // The mask of the lane's four keys of a tile is read two tiles ahead and looked at
+      // only then: while the memory is busy with K and V a byte takes as long as a tile.
+      uint32_t mask[2][kN / 32];
+      auto read_mask = [&](int t, uint32_t (&x)[kN / 32]) {
 #pragma unroll
         for (int c = 0; c < kN / 32; ++c) {
           const int key = t * kN + c * 32 + lane;
-          if (key < at.e.keys && (p.key_mask == nullptr || __ldg(p.key_mask + at.e.k0 + key) != 0))
-            x |= 1u << c;
+          x[c] = 1;
+          if (p.key_mask != nullptr && key < at.e.keys) x[c] = load_byte(p.key_mask + at.e.k0 + key);
         }
-        return x;
       };
-      uint32_t next = mask_bytes(at.t0);
+      read_mask(at.t0, mask[0]);
+      read_mask(at.t0 + 1, mask[1]);
 #pragma unroll 1
       for (int t = at.t0; t < at.t0 + at.n; ++t, ++k) {
         const int s = k % L::kV;
-        const uint32_t seen = next;
+        uint32_t seen = 0;
+#pragma unroll
+        for (int c = 0; c < kN / 32; ++c) {
+          if (t * kN + c * 32 + lane < at.e.keys && mask[0][c] != 0) seen |= 1u << c;
+          mask[0][c] = mask[1][c];
+        }
         const bool whole = __all_sync(0xffffffffu, seen == 0xfu);
         // V's place is free, so the limits of the last tile in it are used up; the
         // softmax warps can go on while V is on its way
@@ -509,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&l_full[s]);
-        if (t + 1 < at.t0 + at.n) next = mask_bytes(t + 1);
+        if (t + 2 < at.t0 + at.n) read_mask(t + 2, mask[1]);
         wait(&v_full[s], (uint32_t)(k / L::kV & 1), 25);
         if (!whole) {
           uint8_t* tile = sV + s * L::kTile;
