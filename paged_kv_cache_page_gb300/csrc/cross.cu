@@ -155,20 +155,24 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
   m_use[0] = m_use[1] = neg_inf();
   l[0] = l[1] = 0.f;
-  // the lane's key of tile i: whether it is seen
-  auto seen = [&](int i) -> bool {
-    const int key = (t_begin + i * slices) * TK + lane;
-    if (i >= n || lane >= TK || key >= e.keys) return false;
-    return p.key_mask == nullptr || __ldg(p.key_mask + e.k0 + key) != 0;
+  // The lane's key of tile i: its mask is read two tiles ahead and looked at only
+  // then (while the memory is busy with K and V a byte takes as long as a tile).
+  auto key_of = [&](int i) { return (t_begin + i * slices) * TK + lane; };
+  auto mask_of = [&](int i) -> uint32_t {
+    if (p.key_mask == nullptr || i >= n || lane >= TK || key_of(i) >= e.keys) return 1;
+    return load_byte(p.key_mask + e.k0 + key_of(i));
   };
   constexpr uint32_t kAllKeys = TK == 32 ? 0xffffffffu : (1u << TK) - 1;
-  bool ok = true, next = seen(0);
+  bool ok = true;
+  uint32_t mask0 = mask_of(0), mask1 = mask_of(1);
 
   int i = 0;
   for (; i < n && ok; ++i) {
     const int s = i % kStages;
-    const uint32_t bits = __ballot_sync(0xffffffffu, next);
-    next = seen(i + 1);
+    const uint32_t bits =
+        __ballot_sync(0xffffffffu, lane < TK && key_of(i) < e.keys && mask0 != 0);
+    mask0 = mask1;
+    mask1 = mask_of(i + 2);
     if (!mbar_wait(&full[s], (uint32_t)(i / kStages & 1))) {
       report(p.err, PA_DEVERR_TIMEOUT, b, 80);
       ok = false;
@@ -367,9 +371,9 @@ cudaError_t launch_t(const CrossParams& p, const CUtensorMap& tmk, const CUtenso
   overlap_launch(&attrs[1]);
   cfg.attrs = attrs;
   cfg.numAttrs = 1;
-  // as many CTAs as are resident together, with two tiles a warp at least
+  // as many CTAs as are resident together, with a tile a warp at least
   const int tiles = (p.max_k + cross_narrow_box(D) - 1) / cross_narrow_box(D);
-  int ctas = tiles / (2 * (kWarps / hs));
+  int ctas = tiles / (kWarps / hs);
   ctas = ctas < 1 ? 1 : ctas < kMaxCluster ? ctas : kMaxCluster;
   for (; ctas > 1; --ctas) {
     cfg.gridDim = dim3((unsigned)ctas);

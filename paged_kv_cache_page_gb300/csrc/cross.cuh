@@ -27,6 +27,13 @@ struct CrossParams {
   float* part_o;
 };
 
+// A load that stays where it is written (see load16).
+__device__ __forceinline__ uint32_t load_byte(const uint8_t* src) {
+  uint32_t x;
+  asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(x) : "l"(src));
+  return x;
+}
+
 // Rows [q0, q0 + rows) of q and keys [k0, k0 + keys) of k and v.
 struct CrossEntry {
   int q0, rows, k0, keys;

@@ -168,13 +168,6 @@ __device__ __noinline__ void scale_p(uint32_t t, int cols, float by) {
   tc::tmem_wait_st();
 }
 
-// A load that stays where it is written (see load16).
-__device__ __forceinline__ uint32_t load_byte(const uint8_t* src) {
-  uint32_t x;
-  asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(x) : "l"(src));
-  return x;
-}
-
 __device__ __forceinline__ void mbar_arrive_2(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], 2;" ::"r"(smem_u32(bar)) : "memory");
 }
