@@ -301,13 +301,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
 
+  // TMEM is taken behind the wait (a kernel in front may have yet to take its own),
+  // and a dependent grid may start once it is taken.
+  griddep_wait();
   if (warp == kWarpMma) {
     tc::tmem_alloc(tslot, 512);
     tc::tmem_relinquish();
   }
-
-  griddep_launch_dependents();
-  griddep_wait();
   // ---- the CTA's share: the tiles of all entries, then the entry it begins in.  Up
   // to 32 entries every warp finds them by itself.
   int total = 0, share = 0, start = 0, b_start = 0, b_begin = 0;
@@ -393,6 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
+  griddep_launch_dependents();
   const uint32_t tbase = *tslot;
   if (tid < 2) sCut[tid].last = 0;  // (before the first part's end, which is behind barriers)
   auto tS = [&](int g) { return tbase + (uint32_t)(g * 128); };
