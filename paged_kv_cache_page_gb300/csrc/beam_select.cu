@@ -7,7 +7,8 @@
 // k * V + v first among equal ones.  exp is taken as 2^(x log2(e) - n) against
 // a whole number n, so that sums under different references are brought
 // together by exact powers of two; log2(e) is a sum of two fp32 values, which
-// leaves one rounding of the exponent.  Next to the border candidates of
+// leaves one rounding of the exponent.  (Where the largest logit is beyond 2^29 an
+// fp32 n is too coarse: see Reference.)  Next to the border candidates of
 // different beams lie so close that 32 bits would often choose another one: the
 // sums of a row's parts and its logarithm (ln f = 2 atanh((f - 1) / (f + 1)))
 // are in pairs of fp32 values, the candidates' scores in 64 bits.  (FP64 is slow
@@ -150,14 +151,38 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 
 // A sum in a pair of fp32 values (the second is what the first lacks), times
-// 2^n.
+// 4^h (h the half of a whole number), or e^h where |h| >= kFar.
 struct Sum {
-  float n, hi, lo;
+  float h, hi, lo;
 };
-constexpr float kNothing = -3e38f;  // the reference where there is nothing but -inf
-// 2^d for a whole d <= 0 (0 below the normal range).
-__device__ __forceinline__ float pow2_whole(float d) {
-  return d < -126.f ? 0.f : __int_as_float((127 + (int)d) << 23);
+constexpr float kFar = 0x1p29f;
+constexpr float kNothing = -3.402823466e38f;  // h where there is nothing but -inf
+// 4^d for a half of a whole number d <= 0 (0 below the normal range).
+__device__ __forceinline__ float pow4(float d) {
+  return d < -63.f ? 0.f : __int_as_float((127 + (int)(2.f * d)) << 23);
+}
+// What the exponentials of values whose largest is `top` are taken against:
+// x stands for 2^(x hi + x lo - minus).  Nearer to 0 than kFar that is e^x / 4^h.
+// Beyond it h is top itself (behind those of smaller values, 0.72 x), and for
+// e^(x - top) stands 4^(x - top), or 2^((x - top) 2^-20) where 2 x might not be
+// finite: 1 at top, and no more than 2^-64 at any other x, which lies 32 below at
+// least, where e^-32 adds 2^-22 to a sum even as one of 2^24.  (lo: -inf times 0
+// would be NaN.)
+struct Reference {
+  float h, hi, lo, minus;
+};
+template <typename T>
+__device__ __forceinline__ Reference reference_of(float top) {
+  const float n = rintf(top * kLog2eHi);
+  if constexpr (std::is_same<T, __half>::value) {  // (finite ones lie above -2^17)
+    const float m = fmaxf(n, -0x1p20f);
+    return {m == n ? 0.5f * m : kNothing, kLog2eHi, kLog2eLo, m};
+  } else {
+    const float t = fmaxf(top, kNothing);
+    if (fabsf(t) < kFar) return {0.5f * n, kLog2eHi, kLog2eLo, n};
+    const float by = fabsf(t) < 0x1p60f ? 2.f : 0x1p-20f;
+    return {t, by, 0x1p-126f, t * by};
+  }
 }
 __device__ __forceinline__ float warp_max(float x) {
 #pragma unroll 1
@@ -167,7 +192,7 @@ __device__ __forceinline__ float warp_max(float x) {
 // Over the warp, the same in every lane (x + y and what it lacks do not depend
 // on their order).
 __device__ __noinline__ Sum warp_total(Sum s) {
-  const float n = warp_max(s.n), f = pow2_whole(s.n - n);
+  const float h = warp_max(s.h), f = pow4(s.h - h);
   float hi = s.hi * f, lo = s.lo * f;
 #pragma unroll 1
   for (int o = 16; o > 0; o >>= 1) {
@@ -177,7 +202,7 @@ __device__ __noinline__ Sum warp_total(Sum s) {
     hi = t + e;
     lo = e - (hi - t);
   }
-  return {n, hi, lo};
+  return {h, hi, lo};
 }
 // ln(s), s positive and finite.
 __device__ __forceinline__ double ln_of(const Sum& s) {
@@ -192,7 +217,10 @@ __device__ __forceinline__ double ln_of(const Sum& s) {
   const float r = __fdividef(fmaf(-q, den, num) + (g - q * den_lo), den);
   const float z = q * q;
   const float t = fmaf(fmaf(fmaf(fmaf(z, 1.f / 11, 1.f / 9), z, 1.f / 7), z, 1.f / 5), z, 1.f / 3);
-  return ((double)s.n + e) * kLn2d + (2.0 * (double)q + (double)(2.f * (r + q * z * t)));
+  const bool far = fabsf(s.h) >= kFar;
+  const double whole = far ? (double)e : 2.0 * (double)s.h + e;
+  const double ln = whole * kLn2d + (2.0 * (double)q + (double)(2.f * (r + q * z * t)));
+  return far ? (double)s.h + ln : ln;  // (rounded to h's size once)
 }
 
 // Larger is better; a score's order as a whole number (+0 and -0 alike).
@@ -248,12 +276,12 @@ struct Row {
 struct SelectShared {
   uint8_t row[kMaxBeams * 32];                // Row of each living beam
   float max[kMaxUnits * 32];                  // block maxima
-  float unit_n[kMaxUnits], unit_s[kMaxUnits];
+  float unit_h[kMaxUnits], unit_s[kMaxUnits];
   int unit_at[kMaxUnits];                     // a unit's first vector
   uint8_t unit_r[kMaxUnits];                  // and its row
   float4 rows[kMaxCluster][kMaxBeams];        // every CTA's sums of every row
-  double base[kMaxBeams];
-  float base32[kMaxBeams];
+  double lse[kMaxBeams];                      // inf: no candidates
+  float lse32[kMaxBeams], cum[kMaxBeams];
   int parts[kParts / 32][kMaxBeams][32];      // maxima of the even and the odd units of every row
   Candidate cand[kMaxCandidates];
   Candidate lists[kMaxCluster * kMaxOut];     // of every CTA, in order (CTA 0's are used)
@@ -356,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) select_kernel(const Sele
     }
     advance(next);
   };
-  float top = neg_inf(), n = kNothing, sum = 0.f;
+  float top = neg_inf(), h = kNothing, sum = 0.f;
   auto compute = [&](const uint4 (&v)[kVecs]) {
     float x_extra = neg_inf();
     if (now.at == 0) {
@@ -364,11 +392,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) select_kernel(const Sele
       if (e >= 0) x_extra = L::one(rows[now.r].p + e);
     }
     top = fmaxf(top, fmaxf(L::largest(v), x_extra));
-    const float ref = fmaxf(rintf(top * kLog2eHi), kNothing);
-    sum *= pow2_whole(n - ref);
-    n = ref;
-    const float2 hi = make_float2(kLog2eHi, kLog2eHi), lo = make_float2(kLog2eLo, kLog2eLo);
-    const float2 minus = make_float2(-n, -n);
+    const Reference ref = reference_of<T>(top);
+    sum *= pow4(h - ref.h);
+    h = ref.h;
+    const float2 hi = make_float2(ref.hi, ref.hi), lo = make_float2(ref.lo, ref.lo);
+    const float2 minus = make_float2(-ref.minus, -ref.minus);
     float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
@@ -383,25 +411,25 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) select_kernel(const Sele
     }
     const float2 both = add2(acc[0], acc[1]);
     sum += both.x + both.y;
-    if (now.at == 0) sum += ex2(fmaf(x_extra, kLog2eLo, fmaf(x_extra, kLog2eHi, -n)));
+    if (now.at == 0) sum += ex2(fmaf(x_extra, ref.lo, fmaf(x_extra, ref.hi, -ref.minus)));
     const int u = now.u, r = now.r, odd = now.i & 1, at = now.at - now.s * kStepVecs;
     advance(now);
     if (now.u == u) return;
     // the unit's maxima, and its sum under the largest of the lanes' references
     sm.max[u * 32 + lane] = top;
     atomicMax(&sm.parts[odd][r][lane], order32(top));
-    const float un = warp_max(n);
-    sum *= pow2_whole(n - un);
+    const float uh = warp_max(h);
+    sum *= pow4(h - uh);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
     if (lane == 0) {
-      sm.unit_n[u] = un;
+      sm.unit_h[u] = uh;
       sm.unit_s[u] = sum;
       sm.unit_at[u] = at;
       sm.unit_r[u] = (uint8_t)r;
     }
     top = neg_inf();
-    n = kNothing;
+    h = kNothing;
     sum = 0.f;
   };
   {
@@ -426,14 +454,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) select_kernel(const Sele
     // (at most two units a lane)
 #pragma unroll 1
     for (int u = lane * live + r; u < units; u += 32 * live) {
-      const float n = sm.unit_n[u], m = fmaxf(n, s.n);
-      const float x = s.hi * pow2_whole(s.n - m), y = sm.unit_s[u] * pow2_whole(n - m);
+      const float h = sm.unit_h[u], m = fmaxf(h, s.h);
+      const float x = s.hi * pow4(s.h - m), y = sm.unit_s[u] * pow4(h - m);
       const float t = x + y;
       s = {m, t, (x - (t - (t - x))) + (y - (t - x))};
     }
     s = warp_total(s);
     if (lane < ranks)
-      *cluster.map_shared_rank(&sm.rows[rank][r], lane) = make_float4(s.n, s.hi, s.lo, 0.f);
+      *cluster.map_shared_rank(&sm.rows[rank][r], lane) = make_float4(s.h, s.hi, s.lo, 0.f);
   }
   cluster.sync();
 #pragma unroll 1
@@ -447,11 +475,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) select_kernel(const Sele
     const float row_cum = __shfl_sync(kAll, cum, rows[r].k);
     if (lane == 0) {
       // a row without a distribution (NaN or +inf in it, or nothing but -inf) has no candidates
-      double base = -INFINITY;
-      if (s.hi > 0.f && isfinite(s.hi) && isfinite(s.n)) base = (double)row_cum - ln_of(s);
+      double lse = INFINITY;
+      if (s.hi > 0.f && isfinite(s.hi) && isfinite(s.h)) lse = ln_of(s);
       else if (rank == 0 && s.hi != 0.f) report(p.err, PA_DEVERR_VALUE, b * p.K + rows[r].k, 0);
-      sm.base[r] = base;
-      sm.base32[r] = (float)base;
+      sm.lse[r] = lse;
+      sm.lse32[r] = (float)lse;
+      sm.cum[r] = row_cum;
     }
   }
   __syncthreads();
@@ -463,11 +492,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) select_kernel(const Sele
     float size = 0.f, part[2] = {neg_inf(), neg_inf()};
 #pragma unroll 1
     for (int r = 0; r < live; ++r) {
-      const float base = sm.base32[r];
-      if (base == neg_inf()) continue;
-      size = fmaxf(size, fabsf(base));
-      part[0] = fmaxf(part[0], base + value32(sm.parts[0][r][lane]));
-      part[1] = fmaxf(part[1], base + value32(sm.parts[1][r][lane]));
+      const float lse = sm.lse32[r], s = sm.cum[r];
+      if (lse == -neg_inf()) continue;
+      size = fmaxf(size, fmaxf(fabsf(lse), fabsf(s)));
+      part[0] = fmaxf(part[0], s + (value32(sm.parts[0][r][lane]) - lse));
+      part[1] = fmaxf(part[1], s + (value32(sm.parts[1][r][lane]) - lse));
     }
     int even = order32(part[0]), odd = order32(part[1]), top = order32(neg_inf());
     // the largest ones, one value after the other, until N parts have gone
@@ -480,15 +509,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) select_kernel(const Sele
       if (odd == top) odd = order32(neg_inf());
     }
     bound = value32(top);
-    // fp32 scores are off by 2^-24 of the base and of the sum; the N-th best
-    // element and the blocks that bound it each once
-    bound -= fmaxf(size, fabsf(bound)) * 0x1p-21f;
+    // fp32 scores are off by 2^-24 of lse, of x - lse (which is no larger than the
+    // score and s together) and of the score; the N-th best element and the blocks
+    // that bound it each once
+    bound -= fmaxf(size, fabsf(bound)) * 0x1p-20f;
   }
   // (a score of -inf: nothing to choose, or a row without a distribution)
   auto passes = [&](float s) { return s > neg_inf() && s >= bound; };
 #pragma unroll 1
   for (int u = warp; u < units; u += kWarps)
-    if (passes(sm.base32[sm.unit_r[u]] + sm.max[u * 32 + lane]))
+    if (const int r = sm.unit_r[u]; passes(sm.cum[r] + (sm.max[u * 32 + lane] - sm.lse32[r])))
       sm.list[atomicAdd(&sm.blocks, 1)] = (uint16_t)(u * 32 + lane);
   __syncthreads();
 
@@ -499,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) select_kernel(const Sele
     for (int i = tid >> 3; i < sm.blocks; i += kThreads / 8) {
       const int blk = sm.list[i], u = blk >> 5, l = blk & 31, r = sm.unit_r[u], at = sm.unit_at[u];
       const Row<T>& row = rows[r];
-      const float base = sm.base32[r];
+      const float lse = sm.lse32[r], s = sm.cum[r];
 #pragma unroll 1
       for (int j = tid & 7; j < per_block; j += 8) {
         uint4 v = L::none();
@@ -514,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) select_kernel(const Sele
         L::expand(v, x);
         uint32_t in = 0;
 #pragma unroll
-        for (int c = 0; c < per; ++c) in |= passes(base + x[c]) ? 1u << c : 0u;
+        for (int c = 0; c < per; ++c) in |= passes(s + (x[c] - lse)) ? 1u << c : 0u;
         for (; in != 0; in &= in - 1) {
           const int c = __ffs((int)in) - 1;
           f(r, e + c, L::one(row.p + e + c));
@@ -523,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) select_kernel(const Sele
     }
   };
   auto candidate = [&](int r, int e, float x) {
-    return Candidate{order_of(sm.base[r] + (double)x), rows[r].k * p.V + e, rows[r].k};
+    return Candidate{order_of((double)sm.cum[r] + ((double)x - sm.lse[r])), rows[r].k * p.V + e, rows[r].k};
   };
   each_element([&](int r, int e, float x) {
     const int at = atomicAdd(&sm.count, 1);
@@ -682,6 +712,8 @@ extern "C" PA_API int pa_beam_select(const void* logits, int64_t stride_b, int64
     return set_error(PA_ERR_INVALID_ARG, "negative strides");
   if (end_token >= V || (finished != nullptr && end_token < 0))
     return set_error(PA_ERR_INVALID_ARG, "end_token must be a token of the vocabulary");
+  if (scores_out == scores || (finished != nullptr && finished_out == finished))
+    return set_error(PA_ERR_INVALID_ARG, "scores and finished may not be replaced");
   SelectParams p{};
   p.logits = logits;
   p.stride_b = stride_b;

@@ -150,6 +150,25 @@ def test_extreme_values():
     check(x, [[0.0] * 3, [0.0, -1.0, -2.0]], 6)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("size", [2.0 ** 27, 2.0 ** 28.9, 2.0 ** 29, 1e9, 1e10, 1e15, 2.0 ** 61, 1e30, 2e38,
+                                  "the type's largest"])
+def test_logits_far_from_zero(size, dtype):
+    """Next to each other such logits differ by 32 and more from 2^29 on: lse is the largest and the logarithm
+    of how many there are.  Up to there the exponent 2^t has |t| <= 32 + 2: 2^-24 34 ln 2 < 2^-19."""
+    lowest = torch.finfo(TYPES[dtype]).min
+    size = -lowest if isinstance(size, str) else size
+    near = size * (1 + 2.0 ** -21 * logits(20, 2, 3, 3001, "f32", spread=4.0).double())
+    near = near.clamp(max=-lowest).to(TYPES[dtype])
+    for x in (near, -near):
+        x = x.clone()
+        x[0, 1, 100:] = 3.0     # ordinary ones beside them
+        x[1, 0, ::2] = -math.inf
+        x[1, 1] = lowest        # nothing but the mask's value
+        x[1, 2, 7:] = lowest
+        check(x, some_scores(11, 2, 3), 5)
+
+
 def test_streams_and_graph_replays():
     x = logits(17, 4, 4, 8001, "bf16")
     s = some_scores(9, 4, 4).to(DEV)
