@@ -47,6 +47,13 @@ def test_select_refusals(lib):
     assert lib.pa_last_error_string()
 
 
+def test_select_refuses_to_replace_its_inputs(lib):
+    assert select(lib, so=P) == pa.PA_ERR_INVALID_ARG
+    assert b"replaced" in lib.pa_last_error_string()
+    assert select(lib, so=2 * P, fin=P, fo=P, end=3) == pa.PA_ERR_INVALID_ARG
+    assert b"replaced" in lib.pa_last_error_string()
+
+
 def reorder(lib, **kw):
     a = dict(par=P, lens=P, B=2, K=4, table=P, bt=8, pages=8, ps=16, free=P, count=P, pool=64, out=P, bto=8,
              lo=P, copies=P, co=P, err=None)
