@@ -224,7 +224,7 @@ cudaError_t allow_shared(const void* kernel, int bytes, std::atomic<uint64_t>* d
 
 bool encode_map(CUtensorMap* map, const void* base, int dtype, int D, int H, int64_t dim2,
                 int64_t dim3, int64_t stride_h, int64_t stride_t, int64_t stride_b, int box_d,
-                int box_h, int box_rows, bool swz = true) {
+                int box_h, int box_rows, bool swz = true, int l2_bytes = 256) {
   PFN_cuTensorMapEncodeTiled_v12000 fn = get_encode_fn();
   if (fn == nullptr) return false;
   const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)dim2, (cuuint64_t)dim3};
@@ -239,7 +239,9 @@ bool encode_map(CUtensorMap* map, const void* base, int dtype, int D, int H, int
                         4, const_cast<void*>(base), dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE,
                         swz ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                        l2_bytes == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                        : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 

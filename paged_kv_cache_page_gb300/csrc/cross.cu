@@ -32,7 +32,7 @@ namespace pa {
 int set_error(int code, const char* fmt, ...);
 bool encode_map(CUtensorMap* map, const void* base, int dtype, int D, int H, int64_t dim2,
                 int64_t dim3, int64_t stride_h, int64_t stride_t, int64_t stride_b, int box_d,
-                int box_h, int box_rows, bool swz);
+                int box_h, int box_rows, bool swz, int l2_bytes);
 
 namespace {
 
@@ -507,10 +507,11 @@ extern "C" PA_API int pa_fwd_cross(const void* q, int64_t q_st, int64_t q_sh, co
   const void* vb = total_k > 0 ? v : q;
   const int64_t rows = total_k > 0 ? total_k : 1;
   const int box = wide ? 128 : cross_narrow_box(D);
+  const int l2 = wide && D == 64 ? 128 : 256;
   CUtensorMap tmq, tmk, tmv;
-  if (!encode_map(&tmk, kb, dtype, D, Hkv, rows, 1, k_sh, k_st, k_st, 64, 1, box, true) ||
-      !encode_map(&tmv, vb, dtype, D, Hkv, rows, 1, v_sh, v_st, v_st, 64, 1, box, true) ||
-      (wide && !encode_map(&tmq, q, dtype, D, Hq, total_q, 1, q_sh, q_st, q_st, 64, p.G, 128 / p.G, true)))
+  if (!encode_map(&tmk, kb, dtype, D, Hkv, rows, 1, k_sh, k_st, k_st, 64, 1, box, true, l2) ||
+      !encode_map(&tmv, vb, dtype, D, Hkv, rows, 1, v_sh, v_st, v_st, 64, 1, box, true, l2) ||
+      (wide && !encode_map(&tmq, q, dtype, D, Hq, total_q, 1, q_sh, q_st, q_st, 64, p.G, 128 / p.G, true, 256)))
     return set_error(PA_ERR_CUDA, "the tensor maps of q, k and v could not be encoded");
   const cudaError_t e = wide ? launch_cross_wide(p, tmq, tmk, tmv, D, dtype, workspace, st)
                              : launch_cross_narrow(p, tmk, tmv, D, dtype, st);
