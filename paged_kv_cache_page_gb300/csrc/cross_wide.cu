@@ -23,11 +23,15 @@
 // on the other group.  Where a pair has rows for one tile only, the groups take
 // its tiles of keys in turn and their results are brought together at the end.
 //
-// Work: the streams (entry, kv head, pair of tiles) laid end to end in 128-key
-// tiles and dealt to the CTAs in equal shares, with cuts near an end of a stream
-// moved there; a stream that is cut is joined by the CTA that finishes last.
-// Whole streams dealt in turn would leave the last round of a few hundred streams
-// half empty.
+// Work: the streams (entry, kv head, pair of tiles) of up to 32 entries are dealt
+// whole, the dearest first, to the CTAs in order and back again, where that comes
+// within a join's time of equal shares.  Else they are laid end to end in 128-key
+// tiles and dealt in equal shares, with cuts near an end of a stream moved there; a
+// stream that is cut is joined by the CTA that finishes last.  The parts of a cut
+// stream and its join are 8 to 15 thousand cycles of a CTA, as much as its tiles in
+// a batch of a few hundred streams.  Whole and cut: 12 entries of 1 to 257 rows, 32/8
+// heads of 128: 41 and 54 us; 32 of them: 84 and 104; 16 of 16 to 40 rows, 12 heads
+// of 64: 21.6 and 28, the same with 2048 keys each: 35 and 32.
 #include <type_traits>
 
 #include "cross.cuh"
@@ -43,8 +47,18 @@ constexpr int kSoft = 8;  // softmax warps
 constexpr int kWarpK = 8, kWarpV = 9, kWarpMma = 10, kWarpFix = 11;
 constexpr int kThreads = 12 * 32;
 constexpr int kMinShare = 2;  // tiles
-constexpr int kSnap = 1;      // tiles that a cut moves to an end of its stream
-constexpr int kEnds = 3;      // what a stream's begin and end cost, in tiles
+// Tiles that a cut moves to an end of its stream (0, 1, 2 and 4: 59, 57, 62 and 65 us
+// for 12 entries of 1 to 257 rows), and what a stream's begin and end cost in tiles (0,
+// 3 and 5: 69.5, 65 and 66 us; 32 entries of 24 rows 55, 40 and 41).
+constexpr int kSnap = 1;
+constexpr int kEnds = 3;
+// Whole streams of a CTA at most (4 and 8: 103 and 84 us for 32 entries of 1 to 257
+// rows), what a stream's begin and end cost (3 to 6 alike) and what a cut one's parts
+// and join do (4: 54 us for what 8 to 24 do in 41; 16: 35 for what 8 does in 32), both
+// in tiles of keys of one tile of rows.
+constexpr int kRounds = 8;
+constexpr int kWholeEnds = 4;
+constexpr int kJoin = 8;
 
 template <int D>
 struct Layout {
@@ -61,7 +75,8 @@ struct Layout {
   // p_full, pv_done, o_free [2]; part_full [2], told
   static constexpr int kBars = 2 + 2 * kK + 4 * kV + 8 + 3;
   static constexpr int kOffSums = kOffBar + kBars * 8;        // int [kThreads / 32]
-  static constexpr int kOffPlain = kOffSums + 12 * 4;         // int [kV] no limits in the tile
+  static constexpr int kOffList = kOffSums + 12 * 4;          // int [kRounds][3] whole streams, -1
+  static constexpr int kOffPlain = kOffList + kRounds * 12 + 4;   // int [kV] no limits in the tile
   static constexpr int kOffCut = kOffPlain + kV * 4;          // Cut [2]
   static constexpr int kOffMisc = kOffCut + 2 * 28;           // start [2], TMEM base
   static constexpr int kBytes = kOffMisc + 12;                // (the base is aligned to 1024)
@@ -198,13 +213,30 @@ struct Walk {
   int b, h, pair, t0, n, all, pairs;  // all: tiles of the stream; n = 0: no more
   int begin;                          // what the streams in front count
   int stop;                           // the cut behind the share; -1: none
+  const int* list;                    // whole streams, or null
   CrossEntry e;
+
+  __device__ __forceinline__ void open(const CrossParams& p, const int* at) {
+    list = at;
+    n = 0;
+    if (*at < 0) return;
+    b = at[0];
+    h = at[1];
+    pair = at[2];
+    e = cross_entry(p, b, false);
+    t0 = 0;
+    n = all = entry_tiles(e);
+  }
 
   __device__ __forceinline__ void take() {
     const int d = stop - begin;
     n = stop < 0 || d >= all ? all - t0 : d <= kSnap ? 0 : d >= all - kSnap ? all - t0 : d - t0;
   }
   __device__ __forceinline__ void next(const CrossParams& p) {
+    if (list != nullptr) {
+      open(p, list + 3);
+      return;
+    }
     if (t0 + n < all) {  // (cut)
       n = 0;
       return;
@@ -230,6 +262,94 @@ struct Walk {
     take();
   }
 };
+
+// Whether the streams are dealt whole, by one warp of every CTA in the same way: in
+// descending order of their cost to CTAs 0, 1, .. and back again.  They are where the
+// CTA with the most has no more than an equal share and a join.  (A lane has an
+// entry.)
+__device__ __noinline__ void deal_whole(const CrossParams& p, const CrossEntry e, int* scratch,
+                                        int* list) {
+  constexpr uint32_t kAll = 0xffffffffu;
+  const int lane = threadIdx.x & 31, ctas = (int)gridDim.x;
+  const int tokens = kM / p.G, pairs = entry_pairs(p, e), tiles = entry_tiles(e);
+  // the entry's pairs with rows for two tiles, and the last one if it has rows for one
+  const int single = pairs > 0 && (2 * pairs - 1) * tokens >= e.rows ? 1 : 0;
+  const int count0 = (pairs - single) * p.Hkv, count1 = single * p.Hkv;
+  const int cost0 = count0 > 0 ? 2 * tiles + kWholeEnds : 0, cost1 = single ? tiles + kWholeEnds : 0;
+  const int streams = __reduce_add_sync(kAll, count0 + count1);
+  const int rounds = (streams + ctas - 1) / ctas;
+  const unsigned all = __reduce_add_sync(kAll, (unsigned)count0 * cost0 + (unsigned)count1 * cost1);
+  const int bound = (int)(all / ctas) + kJoin;
+  list += lane * 3;
+  if (lane <= kRounds) *list = -1;
+  // (no CTA has less than the dearest stream, one has `rounds`)
+  const int least = __reduce_min_sync(kAll, min(cost1 > 0 ? cost1 : 1 << 30, cost0 > 0 ? cost0 : 1 << 30));
+  if (streams == 0 || rounds > kRounds || __reduce_max_sync(kAll, max(cost0, cost1)) > bound ||
+      rounds * (long long)least > bound) {
+    if (lane == 0) list[1] = 0;
+    return;
+  }
+  // kinds of streams in order
+  int rank0 = 0, rank1 = 0;
+#pragma unroll 4
+  for (int k = 0; k < 32; ++k) {
+    const int a = __shfl_sync(kAll, cost0, k), b = __shfl_sync(kAll, cost1, k);
+    rank0 += (a > cost0 || (a == cost0 && k < lane)) + (b > cost0);
+    rank1 += (a >= cost1) + (b > cost1 || (b == cost1 && k < lane));
+  }
+  int* kind = scratch;             // [64] entry, and 32 for its last pair
+  int* cost = scratch + 64;        // [64]
+  int* count = scratch + 128;      // [64], then those in front
+  kind[rank0] = lane;
+  cost[rank0] = cost0;
+  count[rank0] = count0;
+  kind[rank1] = lane + 32;
+  cost[rank1] = cost1;
+  count[rank1] = count1;
+  __syncwarp();
+  const int c0 = count[2 * lane], c1 = count[2 * lane + 1];
+  int upto = c0 + c1;
+#pragma unroll 1
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(kAll, upto, o);
+    if (lane >= o) upto += x;
+  }
+  __syncwarp();
+  count[2 * lane] = upto - c0 - c1;
+  count[2 * lane + 1] = upto - c1;
+  __syncwarp();
+  auto place = [&](int r, int cta) { return r * ctas + (r & 1 ? ctas - 1 - cta : cta); };
+  auto find = [&](int i) {  // (kinds without streams are behind the last)
+    int k = 0;
+#pragma unroll
+    for (int step = 32; step > 0; step >>= 1)
+      if (count[k + step] <= i) k += step;
+    return k;
+  };
+  // the largest load, of 64 CTAs spread over the order
+  int most = 0;
+#pragma unroll 1
+  for (int r = 0, load0 = 0, load1 = 0; r < rounds; ++r) {
+    const int i0 = place(r, 2 * lane * (ctas - 1) / 63), i1 = place(r, (2 * lane + 1) * (ctas - 1) / 63);
+    const int x = cost[find(min(i0, streams - 1))], y = cost[find(min(i1, streams - 1))];
+    load0 += i0 < streams ? x : 0;
+    load1 += i1 < streams ? y : 0;
+    most = max(load0, load1);
+  }
+  most = __reduce_max_sync(kAll, most);
+  const bool whole = most <= bound;
+  const int i = place(lane & (kRounds - 1), (int)blockIdx.x), k = find(min(i, streams - 1));
+  const int of = kind[k] & 31, off = i - count[k];
+  const int of_pairs = __shfl_sync(kAll, pairs, of), full = of_pairs - __shfl_sync(kAll, single, of);
+  if (lane < kRounds && whole && i < streams) {
+    list[0] = of;
+    list[1] = kind[k] < 32 ? off / full : off;
+    list[2] = kind[k] < 32 ? off % full : of_pairs - 1;
+  } else if (lane == 0) {
+    list[1] = whole ? 1 : 0;
+  }
+  fence_proxy_async_smem();  // (the scratch is V's place)
+}
 
 // What a join needs of a cut stream: its rows and the CTAs of its parts.
 struct Cut {
@@ -275,6 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* sLimit = reinterpret_cast<float*>(smem + L::kOffLimit);
   float2* sHalf = reinterpret_cast<float2*>(smem + L::kOffHalf);
   int* sPlain = reinterpret_cast<int*>(smem + L::kOffPlain);
+  int* sList = reinterpret_cast<int*>(smem + L::kOffList);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -312,9 +433,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   // to 32 entries every warp finds them by itself.
   int total = 0, share = 0, start = 0, b_start = 0, b_begin = 0;
   {
+    CrossEntry e = {};
     auto cost_of = [&](int b, bool rep) {
       if (b >= p.B) return 0;
-      const CrossEntry e = cross_entry(p, b, rep);
+      e = cross_entry(p, b, rep);
       return entry_pairs(p, e) * p.Hkv * (entry_tiles(e) + kEnds);
     };
     auto upto = [&](int x) {  // with the lanes in front
@@ -336,7 +458,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t mine = __ballot_sync(0xffffffffu, start >= x - cost && start < x);
       b_start = mine != 0 ? __ffs((int)mine) - 1 : 0;
       b_begin = __shfl_sync(0xffffffffu, x - cost, b_start);
+      if (warp == kWarpFix) deal_whole(p, e, reinterpret_cast<int*>(sV), sList);
     } else {
+      if (tid < 2) sList[tid] = tid - 1;
 #pragma unroll 1
       for (int pass = 0; pass < 2; ++pass) {
         int before = 0;
@@ -367,6 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   Walk at;
   at.n = 0;
+  at.list = nullptr;
   if (start < total) {
     at.b = b_start;
     at.e = cross_entry(p, at.b, false);
@@ -394,6 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::fence_after_sync();
   griddep_launch_dependents();
+  if (sList[0] >= 0 || sList[1] != 0) at.open(p, sList);
   const uint32_t tbase = *tslot;
   if (tid < 2) sCut[tid].last = 0;  // (before the first part's end, which is behind barriers)
   auto tS = [&](int g) { return tbase + (uint32_t)(g * 128); };
