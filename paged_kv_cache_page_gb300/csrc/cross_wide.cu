@@ -265,88 +265,84 @@ struct Walk {
 
 // Whether the streams are dealt whole, by one warp of every CTA in the same way: in
 // descending order of their cost to CTAs 0, 1, .. and back again.  They are where the
-// CTA with the most has no more than an equal share and a join.  (A lane has an
-// entry.)
-__device__ __noinline__ void deal_whole(const CrossParams& p, const CrossEntry e, int* scratch,
-                                        int* list) {
+// CTA with the most has no more than an equal share and a join.  (A lane has an entry
+// and its pairs of tiles.  Divisions are left out where they can be: their code is
+// cold.)
+__device__ __noinline__ void deal_whole(const CrossParams& p, const CrossEntry e, const int pairs,
+                                        const int tokens, int* scratch, int* list) {
   constexpr uint32_t kAll = 0xffffffffu;
   const int lane = threadIdx.x & 31, ctas = (int)gridDim.x;
-  const int tokens = kM / p.G, pairs = entry_pairs(p, e), tiles = entry_tiles(e);
+  const int tiles = entry_tiles(e);
   // the entry's pairs with rows for two tiles, and the last one if it has rows for one
   const int single = pairs > 0 && (2 * pairs - 1) * tokens >= e.rows ? 1 : 0;
   const int count0 = (pairs - single) * p.Hkv, count1 = single * p.Hkv;
   const int cost0 = count0 > 0 ? 2 * tiles + kWholeEnds : 0, cost1 = single ? tiles + kWholeEnds : 0;
   const int streams = __reduce_add_sync(kAll, count0 + count1);
-  const int rounds = (streams + ctas - 1) / ctas;
   const unsigned all = __reduce_add_sync(kAll, (unsigned)count0 * cost0 + (unsigned)count1 * cost1);
-  const int bound = (int)(all / ctas) + kJoin;
-  list += lane * 3;
-  if (lane <= kRounds) *list = -1;
-  // (no CTA has less than the dearest stream, one has `rounds`)
-  const int least = __reduce_min_sync(kAll, min(cost1 > 0 ? cost1 : 1 << 30, cost0 > 0 ? cost0 : 1 << 30));
-  if (streams == 0 || rounds > kRounds || __reduce_max_sync(kAll, max(cost0, cost1)) > bound ||
-      rounds * (long long)least > bound) {
+  auto within = [&](int load) { return (long long)(load - kJoin) * ctas <= all; };
+  if (lane <= kRounds) list[3 * lane] = -1;
+  __syncwarp();
+  // (no CTA has less than the dearest stream)
+  if (streams == 0 || streams > kRounds * ctas ||
+      !within(__reduce_max_sync(kAll, max(cost0, cost1)))) {
     if (lane == 0) list[1] = 0;
     return;
   }
-  // kinds of streams in order
-  int rank0 = 0, rank1 = 0;
-#pragma unroll 4
-  for (int k = 0; k < 32; ++k) {
-    const int a = __shfl_sync(kAll, cost0, k), b = __shfl_sync(kAll, cost1, k);
-    rank0 += (a > cost0 || (a == cost0 && k < lane)) + (b > cost0);
-    rank1 += (a >= cost1) + (b > cost1 || (b == cost1 && k < lane));
-  }
-  int* kind = scratch;             // [64] entry, and 32 for its last pair
-  int* cost = scratch + 64;        // [64]
-  int* count = scratch + 128;      // [64], then those in front
-  kind[rank0] = lane;
-  cost[rank0] = cost0;
+  // kinds of streams in order; those of the lanes from `some` on, without an entry,
+  // have no streams and are last
+  const int some = (p.B + 7) / 8 * 8, over = max(0, lane - some);
+  int rank0 = over, rank1 = over + (cost1 == 0 ? 32 - some : 0);
+#pragma unroll 1
+  for (int k0 = 0; k0 < some; k0 += 8)
+#pragma unroll
+    for (int k = k0; k < k0 + 8; ++k) {
+      const int a = __shfl_sync(kAll, cost0, k), b = __shfl_sync(kAll, cost1, k);
+      rank0 += (a > cost0 || (a == cost0 && k < lane)) + (b > cost0);
+      rank1 += (a >= cost1) + (b > cost1 || (b == cost1 && k < lane));
+    }
+  // {entry, cost, pairs a head, first pair}; streams of the kind, then those in front
+  int4* kind = reinterpret_cast<int4*>(scratch);  // [64]
+  int* count = scratch + 4 * 64;                  // [64]
+  kind[rank0] = make_int4(lane, cost0, pairs - single, 0);
   count[rank0] = count0;
-  kind[rank1] = lane + 32;
-  cost[rank1] = cost1;
+  kind[rank1] = make_int4(lane, cost1, 1, pairs - 1);
   count[rank1] = count1;
   __syncwarp();
-  const int c0 = count[2 * lane], c1 = count[2 * lane + 1];
-  int upto = c0 + c1;
+  const int2 c = reinterpret_cast<int2*>(count)[lane];
+  int upto = c.x + c.y;
 #pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
     const int x = __shfl_up_sync(kAll, upto, o);
     if (lane >= o) upto += x;
   }
+  reinterpret_cast<int2*>(count)[lane] = make_int2(upto - c.x - c.y, upto - c.y);
   __syncwarp();
-  count[2 * lane] = upto - c0 - c1;
-  count[2 * lane + 1] = upto - c1;
-  __syncwarp();
-  auto place = [&](int r, int cta) { return r * ctas + (r & 1 ? ctas - 1 - cta : cta); };
-  auto find = [&](int i) {  // (kinds without streams are behind the last)
-    int k = 0;
+  // the loads of 31 CTAs spread over the order and, in the last lane, the CTA's own
+  const int cta = lane == 31 ? (int)blockIdx.x : lane * (ctas - 1) / 30;
+  int load = 0;
+#pragma unroll 1
+  for (int r = 0; r < kRounds; ++r) {
+    const int i = r * ctas + (r & 1 ? ctas - 1 - cta : cta);
+    if (i >= streams) break;
+    int k = 0;  // (kinds without streams are behind the last)
 #pragma unroll
     for (int step = 32; step > 0; step >>= 1)
       if (count[k + step] <= i) k += step;
-    return k;
-  };
-  // the largest load, of 64 CTAs spread over the order
-  int most = 0;
-#pragma unroll 1
-  for (int r = 0, load0 = 0, load1 = 0; r < rounds; ++r) {
-    const int i0 = place(r, 2 * lane * (ctas - 1) / 63), i1 = place(r, (2 * lane + 1) * (ctas - 1) / 63);
-    const int x = cost[find(min(i0, streams - 1))], y = cost[find(min(i1, streams - 1))];
-    load0 += i0 < streams ? x : 0;
-    load1 += i1 < streams ? y : 0;
-    most = max(load0, load1);
+    const int4 x = kind[k];
+    load += x.y;
+    if (lane == 31) {
+      const int off = i - count[k];
+      const int h = (int)__fdividef((float)off + 0.5f, (float)x.z);  // (exact: off < 2^20)
+      list[3 * r] = x.x;
+      list[3 * r + 1] = h;
+      list[3 * r + 2] = x.w + off - h * x.z;
+    }
   }
-  most = __reduce_max_sync(kAll, most);
-  const bool whole = most <= bound;
-  const int i = place(lane & (kRounds - 1), (int)blockIdx.x), k = find(min(i, streams - 1));
-  const int of = kind[k] & 31, off = i - count[k];
-  const int of_pairs = __shfl_sync(kAll, pairs, of), full = of_pairs - __shfl_sync(kAll, single, of);
-  if (lane < kRounds && whole && i < streams) {
-    list[0] = of;
-    list[1] = kind[k] < 32 ? off / full : off;
-    list[2] = kind[k] < 32 ? off % full : of_pairs - 1;
-  } else if (lane == 0) {
-    list[1] = whole ? 1 : 0;
+  // (of the same CTAs in all of them: every CTA comes to the same answer)
+  const bool whole = within(__reduce_max_sync(kAll, lane < 31 ? load : 0));
+  if (lane == 31) {
+    if (!whole) list[0] = -1;
+    if (list[0] < 0) list[1] = whole ? 1 : 0;
   }
   fence_proxy_async_smem();  // (the scratch is V's place)
 }
@@ -434,10 +430,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   int total = 0, share = 0, start = 0, b_start = 0, b_begin = 0;
   {
     CrossEntry e = {};
+    int pairs = 0;
     auto cost_of = [&](int b, bool rep) {
       if (b >= p.B) return 0;
       e = cross_entry(p, b, rep);
-      return entry_pairs(p, e) * p.Hkv * (entry_tiles(e) + kEnds);
+      pairs = entry_pairs(p, e);
+      return pairs * p.Hkv * (entry_tiles(e) + kEnds);
     };
     auto upto = [&](int x) {  // with the lanes in front
 #pragma unroll 1
@@ -458,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t mine = __ballot_sync(0xffffffffu, start >= x - cost && start < x);
       b_start = mine != 0 ? __ffs((int)mine) - 1 : 0;
       b_begin = __shfl_sync(0xffffffffu, x - cost, b_start);
-      if (warp == kWarpFix) deal_whole(p, e, reinterpret_cast<int*>(sV), sList);
+      if (warp == kWarpFix) deal_whole(p, e, pairs, kM / p.G, reinterpret_cast<int*>(sV), sList);
     } else {
       if (tid < 2) sList[tid] = tid - 1;
 #pragma unroll 1
