@@ -5,10 +5,10 @@
 // Mathematics as in cross.cu: softmax(scale Q K^T) V in one pass over the keys.
 // The rows of a tile are packed over the G heads of a kv head (row i G + g of an
 // entry; 128 / G whole tokens a tile), so that all rows of a CTA's two tiles share
-// every K and V tile.  A row's reference m is a whole number that follows the
-// largest score only where that passes it by more than the slack of P's type: P
-// and O are then scaled by exact powers of two, which is rare, and the exponentials
-// do not wait for the maximum.
+// every K and V tile.  A row's reference m is the first 32 keys' largest score (so
+// that a single key's P is exact) and follows larger ones, by whole numbers, only
+// where they pass it by more than the slack of P's type: P and O are then scaled by
+// powers of two, which is rare, and the exponentials do not wait for the maximum.
 //
 // Bound: the tensor cores, 4 D operations a (row, key) pair, and next to them the
 // exponentials.  One persistent CTA an SM:
@@ -858,9 +858,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!__any_sync(0xffffffffu, far)) break;
             float by = 1.f;
             if (far) {
-              const float to = ceilf(top) - R::kShift;
-              if (m != neg_inf()) by = ex2(m - to);
-              m = to;
+              if (m == neg_inf()) {
+                m = top - R::kShift;
+              } else {
+                const float up = ceilf(top - m) - R::kShift;
+                by = ex2(-up);
+                m += up;
+              }
             }
             alpha *= by;
             l *= by;

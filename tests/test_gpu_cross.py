@@ -111,6 +111,19 @@ def test_many_entries(rows):
           "f16", spare=1)
 
 
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("rows,d", [(3, 64), (3, 128), (40, 64), (200, 128)])
+def test_a_single_key_is_its_value(rows, d, dtype):
+    """O = P V / l with one P, a power of two to 2^-21: V itself, whose half a step is 2^-12 of it or more."""
+    q, k, v = inputs(12, [rows, rows], [1, 150], 4, 2, d, dtype)
+    mask = torch.zeros(151, dtype=torch.bool, device=DEV)
+    mask[0] = mask[90] = True
+    out, _ = pa.pa_fwd_cross(q, k, v, i32([0, rows, 2 * rows]), i32([0, 1, 151]), rows, 150, key_mask=mask)
+    for b, at in ((0, 0), (1, 90)):
+        want = v[at].repeat_interleave(2, 0).expand(rows, 4, d)
+        assert torch.equal(out[b * rows:(b + 1) * rows], want)
+
+
 @pytest.mark.parametrize("rows", [5, 80])
 def test_nan_in_seen_places_reaches_its_rows(rows):
     q, k, v = inputs(9, [rows, rows], [300, 200], 4, 2, 64, "bf16")
