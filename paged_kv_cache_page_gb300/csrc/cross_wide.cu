@@ -206,7 +206,10 @@ __device__ __forceinline__ int entry_tiles(const CrossEntry& e) {
   return max(1, (e.keys + kN - 1) / kN);  // (without keys: one, to write the empty rows)
 }
 
-// A part of a CTA's share: tiles [t0, t0 + n) of a stream.  A stream counts as its
+// A part of a CTA's share: tiles [t0, t0 + n) of a stream.  Of an entry's streams the
+// pairs of one head lie as far apart as they can: side by side they would be one CTA's,
+// one after the other, and each would read K and V from memory again (4 entries of
+// 1024 rows and 4096 keys: 1.1 GB of reads where K and V are 268 MB, 213 us; 204 this way).  A stream counts as its
 // tiles and kEnds.  The cuts are at whole multiples of `share`; one that lies at most kSnap tiles behind a stream's begin
 // counts as there, else one that lies at most kSnap in front of its end as there.
 struct Walk {
@@ -247,10 +250,10 @@ struct Walk {
     n = 0;
     begin += all + kEnds;
     t0 = 0;
-    if (++pair == pairs) {
-      pair = 0;
-      if (++h == p.Hkv) {
-        h = 0;
+    if (++h == p.Hkv) {
+      h = 0;
+      if (++pair == pairs) {
+        pair = 0;
         do {
           if (++b >= p.B) return;
           e = cross_entry(p, b, false);
@@ -499,8 +502,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int off = start - b_begin, stream = off / (at.all + kEnds);
     at.begin = b_begin + stream * (at.all + kEnds);
     at.t0 = off - stream * (at.all + kEnds);
-    at.h = stream / at.pairs;
-    at.pair = stream - at.h * at.pairs;
+    at.pair = stream / p.Hkv;
+    at.h = stream - at.pair * p.Hkv;
     if (at.t0 < at.all && at.t0 <= kSnap) at.t0 = 0;
     if (at.t0 > 0 && at.t0 >= at.all - kSnap) at.next_stream(p);
     else at.take();
