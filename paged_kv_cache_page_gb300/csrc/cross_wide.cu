@@ -206,12 +206,13 @@ __device__ __forceinline__ int entry_tiles(const CrossEntry& e) {
   return max(1, (e.keys + kN - 1) / kN);  // (without keys: one, to write the empty rows)
 }
 
-// A part of a CTA's share: tiles [t0, t0 + n) of a stream.  Of an entry's streams the
-// pairs of one head lie as far apart as they can: side by side they would be one CTA's,
-// one after the other, and each would read K and V from memory again (4 entries of
-// 1024 rows and 4096 keys: 1.1 GB of reads where K and V are 268 MB, 213 us; 204 this way).  A stream counts as its
-// tiles and kEnds.  The cuts are at whole multiples of `share`; one that lies at most kSnap tiles behind a stream's begin
-// counts as there, else one that lies at most kSnap in front of its end as there.
+// A part of a CTA's share: tiles [t0, t0 + n) of a stream.  A stream counts as its
+// tiles and kEnds.  The cuts are at whole multiples of `share`; one that lies at most
+// kSnap tiles behind a stream's begin counts as there, else one that lies at most kSnap
+// in front of its end as there.  Of an entry's streams the pairs of one head lie as far
+// apart as they can: side by side they would be one CTA's, one after the other, and
+// each would read K and V from memory again (4 entries of 1024 rows and 4096 keys: 1.1
+// GB of reads where K and V are 268 MB, 213 us; 202 this way).
 struct Walk {
   int b, h, pair, t0, n, all, pairs;  // all: tiles of the stream; n = 0: no more
   int begin;                          // what the streams in front count
