@@ -30,8 +30,8 @@
 // stream that is cut is joined by the CTA that finishes last.  The parts of a cut
 // stream and its join are 8 to 15 thousand cycles of a CTA, as much as its tiles in
 // a batch of a few hundred streams.  Whole and cut: 12 entries of 1 to 257 rows, 32/8
-// heads of 128: 41 and 54 us; 32 of them: 84 and 104; 16 of 16 to 40 rows, 12 heads
-// of 64: 21.6 and 28, the same with 2048 keys each: 35 and 32.
+// heads of 128: 40.5 and 52 us; 32 of them: 84 and 103; 16 of 16 to 40 rows, 12 heads
+// of 64: 21 and 26, the same with 2048 keys each: 35 and 31.
 #include <type_traits>
 
 #include "cross.cuh"
@@ -422,6 +422,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
 
+  if (tid == 32) {
+    tma_prefetch_desc(&tmq);
+    tma_prefetch_desc(&tmk);
+    tma_prefetch_desc(&tmv);
+  }
   // TMEM is taken behind the wait (a kernel in front may have yet to take its own),
   // and a dependent grid may start once it is taken.
   griddep_wait();
@@ -454,13 +459,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       start = share * (int)blockIdx.x;
     };
     if (p.B <= 32) {
-      const int cost = cost_of(lane, warp == 0 && blockIdx.x == 0), x = upto(cost);
+      const int cost = cost_of(lane, warp == 0 && blockIdx.x == 0);
+      if (warp == kWarpFix) deal_whole(p, e, pairs, kM / p.G, reinterpret_cast<int*>(sV), sList);
+      const int x = upto(cost);
       total = __shfl_sync(0xffffffffu, x, 31);
       deal();
       const uint32_t mine = __ballot_sync(0xffffffffu, start >= x - cost && start < x);
       b_start = mine != 0 ? __ffs((int)mine) - 1 : 0;
       b_begin = __shfl_sync(0xffffffffu, x - cost, b_start);
-      if (warp == kWarpFix) deal_whole(p, e, pairs, kM / p.G, reinterpret_cast<int*>(sV), sList);
     } else {
       if (tid < 2) sList[tid] = tid - 1;
 #pragma unroll 1
@@ -550,8 +556,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t round = 0;   // and how often it has come round
     int behind = 0;       // tiles issued, up to the ring's places
     if (lane == 0) {
-      tma_prefetch_desc(map);
-      if (!is_v) tma_prefetch_desc(&tmq);
       for (; at.n > 0; at.next(p)) {
         if (at.e.keys == 0) continue;
         for (int t = at.t0; t < at.t0 + at.n; ++t) {
