@@ -28,9 +28,9 @@
 // CTAs in the same way, so equal rows have bitwise equal sums and their ties go
 // to the lower index.
 //
-// Measured: 64 requests of 8 beams, 128000 bf16 logits: 37.8 us (3.5 TB/s, bound by
-// the pass: long loads and barriers, 128 of 152 SMs); one of 4 beams, 32000: 8.1 us,
-// launch and latency.
+// Measured: 64 requests of 8 beams, 128000 bf16 logits: 36.0 us, 20 of them the pass
+// (6.5 TB/s), the others start, sums, bound, candidates and the join, as in 8.1 us for
+// one request of 4 beams of 32000.
 #include <cooperative_groups.h>
 
 #include <type_traits>
@@ -526,20 +526,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) select_kernel(const Sele
       sm.list[atomicAdd(&sm.blocks, 1)] = (uint16_t)(u * 32 + lane);
   __syncthreads();
 
-  // elements of these blocks: eight lanes a block, one vector each at a time
-  const int per_block = p.steps * kVecs + 1;
+  // elements of these blocks: 16 lanes a block, or 32 where it has more vectors, one
+  // vector each at a time (the loads are misses, one after the other: 8 lanes took
+  // 8200 cycles for 33 vectors)
+  const int per_block = p.steps * kVecs + 1, lanes_log2 = per_block > 16 ? 5 : 4;
   auto each_element = [&](auto&& f) {  // f(row, element, logit)
 #pragma unroll 1
-    for (int i = tid >> 3; i < sm.blocks; i += kThreads / 8) {
+    for (int i = tid >> lanes_log2; i < sm.blocks; i += kThreads >> lanes_log2) {
       const int blk = sm.list[i], u = blk >> 5, l = blk & 31, r = sm.unit_r[u], at = sm.unit_at[u];
       const Row<T>& row = rows[r];
       const float lse = sm.lse32[r], s = sm.cum[r];
 #pragma unroll 1
-      for (int j = tid & 7; j < per_block; j += 8) {
+      for (int j = tid & ((1 << lanes_log2) - 1); j < per_block - (at != 0);
+           j += 1 << lanes_log2) {
         uint4 v = L::none();
         int e = row.head + (at + j * 32 + l) * per;
-        if (j == per_block - 1) {  // the extra element
-          e = at == 0 ? row.extra(l) : -1;
+        if (j == per_block - 1) {  // the extra element, of a row's first unit
+          e = row.extra(l);
           if (e >= 0) v.x = L::alone(row.p + e);
         } else if (at + j * 32 + l < row.vecs) {
           v = load16(row.vec() + at + j * 32 + l);
