@@ -111,6 +111,18 @@ def test_many_entries(rows):
           "f16", spare=1)
 
 
+@pytest.mark.parametrize("n,rows,keys,hq,hkv,d", [
+    (20, lambda i: 18 + i % 20, lambda i: 100 + 37 * i, 12, 12, 64),
+    (32, lambda i: 300 if i % 7 == 0 else 5 + i, lambda i: 50 + 29 * i, 16, 4, 128),
+    (33, lambda i: 300 if i % 7 == 0 else 5 + i, lambda i: 50 + 29 * i, 16, 4, 128),
+    (32, lambda i: 10 + i % 3, lambda i: 150 * (i % 9 != 4), 40, 20, 64),
+])
+def test_hundreds_of_streams(n, rows, keys, hq, hkv, d):
+    """Two to five streams a CTA, of one and two tiles of rows, dealt whole (up to 32 entries) and cut."""
+    rows, keys = [rows(i) for i in range(n)], [keys(i) for i in range(n)]
+    check(rows, keys, hq, hkv, d, "bf16", seed=n, spare=2)
+
+
 @pytest.mark.parametrize("dtype", list(TYPES))
 @pytest.mark.parametrize("rows,d", [(3, 64), (3, 128), (40, 64), (200, 128)])
 def test_a_single_key_is_its_value(rows, d, dtype):
