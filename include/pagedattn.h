@@ -72,7 +72,7 @@ enum {
 
 /* PA_E4M3: 8-bit cache values (four exponent, three mantissa bits, largest 448), each
  * standing for itself times its kv head's fp32 scale; only where a call says so.
- * PA_F32: rotary tables of pa_rotary_append_varlen. */
+ * PA_F32: rotary tables of pa_rotary_append_varlen, logits of pa_beam_select. */
 enum { PA_F16 = 0, PA_BF16 = 1, PA_E4M3 = 2, PA_F32 = 3 };
 
 /* Codes written to err_word[0] by the kernels. */
