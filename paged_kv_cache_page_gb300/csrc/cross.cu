@@ -20,7 +20,7 @@
 // distributed shared memory, so there is no scratch memory and no second launch.
 // A ring that the warps share was 1.6 times slower.  Measured: 32 entries of 5 rows
 // and 100 to 1500 keys, 16 heads of 64: 23.2 us (4.5 TB/s); 64 of one row and 4096
-// keys, 32/8 heads of 128: 162 us (6.6 TB/s); one of 4 rows and 1000 keys, 12 heads of
+// keys, 32/8 heads of 128: 159 us (6.7 TB/s); one of 4 rows and 1000 keys, 12 heads of
 // 64: 6.4 us, most of it launch, first keys and join.
 #include "cross.cuh"
 
@@ -376,16 +376,25 @@ cudaError_t launch_t(const CrossParams& p, const CUtensorMap& tmk, const CUtenso
   overlap_launch(&attrs[1]);
   cfg.attrs = attrs;
   cfg.numAttrs = 1;
-  // as many CTAs as are resident together, with a tile a warp at least (two: 6.9 us
+  // As many CTAs as are resident together, with a tile a warp at least (two: 6.9 us
   // instead of 6.2 for 200 keys; no more than 1.5 an SM: 64 entries of one row 153 us
-  // instead of 162, but 32 of five rows 27.7 instead of 23.6)
+  // instead of 162, but 32 of five rows 27.7 instead of 23.6).  Twice as many where a
+  // warp has kLong tiles even so, for entries of unlike lengths (one and two rounds: 64
+  // entries of 100 to 1500 keys, 16 heads of 64, 47 tiles a warp, 48 and 40 us; 64 of
+  // 100 to 4096 keys, 8 heads of 128, 99 and 93; 32 of 1500 keys, 16 tiles, 35 and 39).
+  constexpr int kLong = 32;
   const int tiles = (p.max_k + cross_narrow_box(D) - 1) / cross_narrow_box(D);
-  int ctas = tiles / (kWarps / hs);
-  ctas = ctas < 1 ? 1 : ctas < kMaxCluster ? ctas : kMaxCluster;
-  for (; ctas > 1; --ctas) {
-    cfg.gridDim = dim3((unsigned)ctas);
-    at.val.clusterDim.x = (unsigned)ctas;
-    if (items <= resident_clusters(cross_kernel<D, T>, cfg, ctas, resident)) break;
+  const int slices = kWarps / hs;
+  int most = tiles / slices, ctas = 1;
+  most = most < 1 ? 1 : most < kMaxCluster ? most : kMaxCluster;
+  for (int rounds = 1; rounds <= 2; ++rounds) {
+    for (ctas = most; ctas > 1; --ctas) {
+      cfg.gridDim = dim3((unsigned)ctas);
+      at.val.clusterDim.x = (unsigned)ctas;
+      const int held = resident_clusters(cross_kernel<D, T>, cfg, ctas, resident);
+      if (items <= (long long)rounds * held) break;
+    }
+    if (tiles / (ctas * slices) < kLong) break;
   }
   cfg.gridDim = dim3((unsigned)(items * ctas));
   at.val.clusterDim.x = (unsigned)ctas;
