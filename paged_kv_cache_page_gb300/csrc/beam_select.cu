@@ -406,7 +406,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) select_kernel(const Sele
     }
     advance(next);
   };
-  float top = neg_inf(), h = kNothing, sum = 0.f;
+  // (a lane may have thousands of steps: what its sum lacks is carried along)
+  float top = neg_inf(), h = kNothing, sum = 0.f, lack = 0.f;
   // (rows that lie a multiple of 16 bytes apart are cut alike: 36.2 us without, 38.0 with codes)
   const bool coded = p.stride_k * sizeof(T) % 16 != 0;
   uint32_t code = 0;
@@ -421,7 +422,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) select_kernel(const Sele
     }
     top = fmaxf(top, fmaxf(L::largest(v), x_extra));
     const Reference ref = reference_of<T>(top);
-    sum *= pow4(h - ref.h);
+    const float down = pow4(h - ref.h);
+    sum *= down;
+    lack *= down;
     h = ref.h;
     const float2 hi = make_float2(ref.hi, ref.hi), lo = make_float2(ref.lo, ref.lo);
     const float2 minus = make_float2(-ref.minus, -ref.minus);
@@ -442,8 +445,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) select_kernel(const Sele
       for (int j = 0; j < kVecs; ++j) code = L::code(v[j], code);
     }
     const float2 both = add2(acc[0], acc[1]);
-    sum += both.x + both.y;
-    if (now.at == 0) sum += ex2(fmaf(x_extra, ref.lo, fmaf(x_extra, ref.hi, -ref.minus)));
+    float step = both.x + both.y;
+    if (now.at == 0) step += ex2(fmaf(x_extra, ref.lo, fmaf(x_extra, ref.hi, -ref.minus)));
+    const float upto = sum + step, added = upto - sum;
+    lack += (sum - (upto - added)) + (step - added);
+    sum = upto;
     const int u = now.u, r = now.r, odd = now.i & 1, at = now.at - now.s * kStepVecs;
     advance(now);
     if (now.u == u) return;
@@ -451,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) select_kernel(const Sele
     sm.max[u * 32 + lane] = top;
     atomicMax(&sm.parts[odd][r][lane], order32(top));
     const float uh = warp_max(h);
-    sum *= pow4(h - uh);
+    sum = (sum + lack) * pow4(h - uh);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
     code = __reduce_add_sync(kAll, code);
@@ -464,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) select_kernel(const Sele
     }
     top = neg_inf();
     h = kNothing;
-    sum = 0.f;
+    sum = lack = 0.f;
     code = 0;
   };
   {
