@@ -4,9 +4,9 @@
 //
 // Mathematics.  O = softmax(scale Q K^T) V over the keys of the entry that are not
 // masked, in one pass: a running maximum m and sum l of 2^(s - m), s the scores
-// times scale log2(e); O is brought to a new maximum only where that is more than
-// 2^8 above the one in use, so P stays below 2^8.  Partial results (O, m, l) of
-// different keys are joined exactly.
+// times scale log2(e); O is brought to a new maximum only where P would pass a limit
+// of its type otherwise (Range).  Partial results (O, m, l) of different keys are
+// joined exactly.
 //
 // What bounds it is the read of K and V, once for all rows of the entry.  The
 // G query heads of a kv head and the rows are packed into tiles of 16 rows, the M
@@ -47,7 +47,18 @@ constexpr int kStageBytes = 8192;  // K and V of a tile of one head
 constexpr int kRows = 16;          // packed rows of an entry and kv head
 constexpr int kCtasPerSm = 3;
 constexpr int kMaxCluster = kClusterLimit;
-constexpr float kRescale = 8.f;
+
+// The largest score is brought to 2^kShift, and may pass that by 2^kSlack before O is
+// brought to a new maximum.  fp16 has no numbers below 2^-24, and l counts the P that
+// vanish: so the largest is 2^8 at first and 2^15 at most, and keys of 2^-30 of its
+// weight still count.
+template <typename T> struct Range;
+template <> struct Range<__half> {
+  static constexpr float kShift = 8.f, kSlack = 7.f;
+};
+template <> struct Range<__nv_bfloat16> {
+  static constexpr float kShift = 0.f, kSlack = 8.f;
+};
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -82,6 +93,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     cross_kernel(const __grid_constant__ CrossParams p, const int hs,
                  const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
   using E = Elem<T>;
+  using R = Range<T>;
   constexpr int TK = cross_narrow_box(D);  // keys of a tile
   constexpr int NT = TK / 8;               // its n-tiles
   constexpr int KD = D / 16;               // k-steps of Q K^T
@@ -221,10 +233,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       top *= p.scale_log2;
       float& mu = m_use[half];
-      const bool lift = top > mu + kRescale || (mu == neg_inf() && top != neg_inf());
+      const bool lift = top > mu + (R::kShift + R::kSlack) || (mu == neg_inf() && top != neg_inf());
       if (__any_sync(0xffffffffu, lift)) {
-        const float f = lift ? ex2(mu - top) : 1.f;
-        if (lift) mu = top;
+        const float to = top - R::kShift, f = lift ? ex2(mu - to) : 1.f;
+        if (lift) mu = to;
         l[half] *= f;
 #pragma unroll
         for (int d = 0; d < ND; ++d) {
