@@ -535,7 +535,9 @@ PA_API int pa_beam_select(const void* logits, int64_t stride_b, int64_t stride_k
  *                 fresh page and the number of tokens; -1, -1, 0: none.
  * Requests are taken in order while the pool holds their fresh pages; the first
  * that does not fit and every later one stay as they are, without copies
- * (PA_DEVERR_CAPACITY, the request and its fresh pages).  A request with a parent
+ * (PA_DEVERR_CAPACITY, the request and its fresh pages).  An entry of the pool that is
+ * no page of it counts as the pool's end (PA_DEVERR_PAGE_OOB, the first row that wants
+ * a fresh page, the column, where that stops a request).  A request with a parent
  * outside [-1, K) (PA_DEVERR_VALUE, the row, the parent), a length outside its
  * table row (PA_DEVERR_LENGTH, the row, the length) or an entry outside the pool
  * (PA_DEVERR_PAGE_OOB, the row, the column) stays as it is, too, and does not

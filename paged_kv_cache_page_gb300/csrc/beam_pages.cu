@@ -85,14 +85,21 @@ struct Beams {
   int columns;    // the largest held
   bool ok;        // (uniform) lengths and parents are sound
 };
-__device__ __forceinline__ Beams beams_of(const ReorderParams& p, int g, int lane, bool rep) {
+struct Given {  // of beam and child `lane`
+  int len, parent;
+};
+__device__ __forceinline__ Given given_of(const ReorderParams& p, int g, int lane) {
+  if (lane >= p.K) return {0, -1};
+  return {p.seqlens[g * p.K + lane], p.parents[g * p.K + lane]};
+}
+__device__ __forceinline__ Beams beams_of(const ReorderParams& p, int g, int lane, Given given,
+                                          bool rep) {
   Beams s;
   const int ps = 1 << p.page_log2;
   const long long cap = (long long)p.max_pages << p.page_log2;
   const int row = g * p.K + lane;
-  const bool mine = lane < p.K;
-  s.len = mine ? p.seqlens[row] : 0;
-  s.parent = mine ? p.parents[row] : -1;
+  s.len = given.len;
+  s.parent = given.parent;
   const bool len_ok = s.len >= 0 && s.len <= cap;
   const bool par_ok = s.parent >= -1 && s.parent < p.K;
   if (rep && !len_ok) report(p.err, PA_DEVERR_LENGTH, row, s.len);
@@ -197,7 +204,8 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const ReorderParams p
   int* s_part = s_need + per;          // [per][warps] pages given back by a warp's columns
   uint8_t* s_bad = reinterpret_cast<uint8_t*>(s_part + per * p.warps);  // [per]
   __shared__ int s_sums[2][32];
-  __shared__ int s_fail;
+  __shared__ int s_fail, s_usable;
+  __shared__ int s_usable_of[kMaxCluster];  // by CTA
   const int slots = threads / 32 / p.warps;  // requests at a time
   const int slot = warp / p.warps, part = warp % p.warps;
 
@@ -205,10 +213,20 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const ReorderParams p
   griddep_launch_dependents();
   for (int i = tid; i < per; i += threads) s_bad[i] = 0;
   for (int i = tid; i < 64; i += threads) s_sums[i >> 5][i & 31] = 0;
-  if (tid == 0) s_fail = p.B;
+  if (tid == 0) {
+    s_fail = p.B;
+    s_usable = kMaxItems;
+  }
   __syncthreads();
   griddep_wait();
   int free_now = load_l2(p.free_count);
+  Given given0 = {0, -1};
+  if (g0 + slot < g1) given0 = given_of(p, g0 + slot, lane);
+  // The free pages that this call may take (no more than rows) are looked at while the
+  // tables are read: the stack's usable part ends at an entry outside the pool.
+  const int most = min(free_now < 0 ? 0 : min(free_now, p.num_pages), p.B * p.K);
+  const int depth0 = rank * threads + tid;
+  const int page0 = depth0 < most ? load_l2(p.free_pages + min(free_now, p.num_pages) - 1 - depth0) : 0;
 
   // Where a warp has one request it keeps what it has found out, and with 32 columns
   // at most loads nothing again.  (More requests than warps are a warp each.)
@@ -221,7 +239,7 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const ReorderParams p
   // ---- pages given back and fresh ones, request by request
 #pragma unroll 1
   for (int g = g0 + slot; g < g1; g += slots) {
-    s = beams_of(p, g, lane, part == 0);
+    s = beams_of(p, g, lane, g == g0 + slot ? given0 : given_of(p, g, lane), part == 0);
     r = {0, 0};
     int given = 0;
     if (s.ok) {
@@ -254,8 +272,15 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const ReorderParams p
     if (rank == 0 && tid == 0) report(p.err, PA_DEVERR_CAPACITY, -1, free_now);
     free_now = free_now < 0 ? 0 : p.num_pages;
   }
+  if (page0 < 0 || page0 >= p.num_pages) atomicMin(&s_usable, depth0);
+#pragma unroll 1
+  for (int i = depth0 + ranks * threads; i < most; i += ranks * threads) {
+    const int e = load_l2(p.free_pages + free_now - 1 - i);
+    if (e < 0 || e >= p.num_pages) atomicMin(&s_usable, i);
+  }
   __syncthreads();
   cluster_wait();
+  if (tid < ranks) cluster.map_shared_rank(s_usable_of, tid)[rank] = s_usable;
 #pragma unroll 1
   for (int i = tid; i < (g1 - g0) * ranks; i += threads) {  // a request for a CTA
     const int g = i / ranks, to = i - g * ranks;
@@ -267,6 +292,9 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const ReorderParams p
   cluster.sync();
 
   // ---- the sums in front of each request, and how far the pool goes
+  const int room = p.num_pages - free_now;
+  const int usable =
+      min(free_now, __reduce_min_sync(kAll, lane < ranks ? s_usable_of[lane] : kMaxItems));
   int given[kPer], taken[kPer], my_given = 0, my_taken = 0;
   const int each = (p.B + threads - 1) / threads;
 #pragma unroll
@@ -306,7 +334,8 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const ReorderParams p
     s_taken[g] = at_taken;
     at_given += given[i];
     at_taken += taken[i];
-    if (taken[i] > 0 && (long long)free_now + at_given < at_taken) atomicMin(&s_fail, g);
+    if (taken[i] > 0 && (long long)usable + min(at_given, room) < at_taken)
+      atomicMin(&s_fail, g);
   }
   __syncthreads();
   const int fail = s_fail;  // requests [fail, B) stay as they are
@@ -314,13 +343,12 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const ReorderParams p
   if (fail < p.B) {
     top = s_given[fail];
     used = s_taken[fail];
-    if (rank == 0) {
+    if (rank == 0 && usable == free_now) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
         if (i < each && tid * each + i == fail) report(p.err, PA_DEVERR_CAPACITY, fail, taken[i]);
     }
   }
-  const int room = p.num_pages - free_now;
   if (top > room) {  // (pages that are in the tables and the pool twice)
     if (rank == 0 && tid == 0) report(p.err, PA_DEVERR_CAPACITY, -1, top);
     top = room;
@@ -331,10 +359,14 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const ReorderParams p
 #pragma unroll 1
   for (int g = g0 + slot; g < g1; g += slots) {
     if (!single) {
-      s = beams_of(p, g, lane, false);
+      s = beams_of(p, g, lane, given_of(p, g, lane), false);
       copy = s.ok && copies_page(p, s, g, lane, page);
     }
     const bool moved = g < fail && !s_bad[g - g0];
+    if (g == fail && usable < free_now && part == 0) {  // a page outside the pool stopped it
+      const uint32_t first = __ballot_sync(kAll, copy);
+      if (lane == __ffs((int)first) - 1) report(p.err, PA_DEVERR_PAGE_OOB, g * p.K + lane, s.partial);
+    }
     int parent = s.parent, new_held = s.new_held;
     if (!moved) {  // every beam stays itself
       parent = lane < p.K ? lane : -1;
@@ -393,7 +425,7 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const ReorderParams p
     const bool moved = g < fail && !s_bad[g - g0];
     const int row = g * p.K + lane;
     if (!single) {
-      s = beams_of(p, g, lane, false);
+      s = beams_of(p, g, lane, given_of(p, g, lane), false);
       page = lane < p.K ? load_l2(p.copies + 3 * row) : -1;
       copy = page >= 0;
     }
@@ -408,16 +440,10 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const ReorderParams p
         if (copy_i && (part_i < s.partial || (part_i == s.partial && i < lane))) ++before;
       }
       if (copy) {
-        const int at = top - 1 - (s_taken[g] + before);
-        const int fresh = at >= 0 ? load_l2(p.free_pages + at) : -1;
-        if (fresh >= 0 && fresh < p.num_pages) {
-          src = page;
-          dst = fresh;
-          tokens = s.new_len & ((1 << p.page_log2) - 1);
-          p.table_out[(int64_t)row * p.bto_stride + s.partial] = dst;
-        } else {
-          report(p.err, PA_DEVERR_PAGE_OOB, row, s.partial);
-        }
+        src = page;
+        dst = load_l2(p.free_pages + top - 1 - (s_taken[g] + before));
+        tokens = s.new_len & ((1 << p.page_log2) - 1);
+        p.table_out[(int64_t)row * p.bto_stride + s.partial] = dst;
       }
     }
     if (lane < p.K) {
