@@ -513,8 +513,8 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
   griddep_launch_dependents();
   griddep_wait();
   const int entry = blockIdx.x;
-  const int src = p.copies[3 * entry], dst = p.copies[3 * entry + 1],
-            tokens = p.copies[3 * entry + 2];
+  const int32_t* copy = p.copies + 3 * (int64_t)entry;
+  const int src = copy[0], dst = copy[1], tokens = copy[2];
   if (src < 0 || dst < 0 || tokens == 0) return;
   const bool first = blockIdx.y == 0 && threadIdx.x == 0;
   if (src >= p.num_pages || dst >= p.num_pages) {
