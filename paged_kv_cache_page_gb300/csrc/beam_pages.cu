@@ -471,7 +471,7 @@ cudaError_t launch_reorder(ReorderParams p, cudaStream_t st) {
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   overlap_launch(&attrs[1]);
   cfg.attrs = attrs;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   auto shape = [&] {
     const int per = (p.B + ctas - 1) / ctas;
     p.warps = 1;
@@ -488,11 +488,11 @@ cudaError_t launch_reorder(ReorderParams p, cudaStream_t st) {
   cudaError_t e = allow_shared(reinterpret_cast<const void*>(reorder_kernel<KM>), most, &allowed);
   if (e != cudaSuccess) return e;
   shape();
-  if (ctas > 8 && !wide_clusters(reorder_kernel<KM>, cfg, &asked, &wide)) {
+  if (ctas > 8 &&
+      !wide_clusters(reorder_kernel<KM>, kMaxCluster, kThreads, most, &asked, &wide)) {
     ctas = 8;
     shape();
   }
-  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, reorder_kernel<KM>, p);
 }
 

@@ -125,15 +125,27 @@ int num_sms();
 // Lets `kernel` use `bytes` of dynamic shared memory on the current device;
 // `devices` remembers (a bit each) where that has been done.
 cudaError_t allow_shared(const void* kernel, int bytes, std::atomic<uint64_t>* devices);
-// Whether the device schedules clusters of more than 8 CTAs of the kernel
-// (sizes that are not portable); asked once a device.
+// Whether the device schedules clusters of `size` (more than 8, which is not portable)
+// CTAs of the kernel, with the most threads and shared memory that its launches have:
+// the answer is asked for once a device and holds for all of them.  (What the kernel may
+// use of shared memory has been raised to that before.)
 template <typename K>
-bool wide_clusters(K kernel, const cudaLaunchConfig_t& cfg, std::atomic<uint64_t>* asked,
-                   std::atomic<uint64_t>* wide) {
+bool wide_clusters(K kernel, int size, int most_threads, int most_shared,
+                   std::atomic<uint64_t>* asked, std::atomic<uint64_t>* wide) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return false;
   const uint64_t bit = uint64_t(1) << dev;
   if ((asked->load(std::memory_order_acquire) & bit) == 0) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)size);
+    cfg.blockDim = dim3((unsigned)most_threads);
+    cfg.dynamicSmemBytes = (size_t)most_shared;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = (unsigned)size;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
     int n = 0;
     const bool ok =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==

@@ -396,13 +396,14 @@ cudaError_t launch_cluster(void (*kernel)(P), const P& p, long long items, int e
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  if (cfg.dynamicSmemBytes > (40 << 10)) {  // with the static arrays more than the 48 KB of a plain launch
+  // (with the static arrays more than the 48 KB of a plain launch, or asked about below)
+  if (cfg.dynamicSmemBytes > (40 << 10) || ctas > 8) {
     // (the largest batch's: another thread's launch may be on its way)
     const cudaError_t e =
         allow_shared(reinterpret_cast<const void*>(kernel), kMaxB * entry_bytes, &allowed);
     if (e != cudaSuccess) return e;
   }
-  if (ctas > 8 && !wide_clusters(kernel, cfg, &asked, &wide)) {
+  if (ctas > 8 && !wide_clusters(kernel, kCluster, kThreads, kMaxB * entry_bytes, &asked, &wide)) {
     cfg.gridDim = dim3(8);
     at.val.clusterDim.x = 8;
   }
