@@ -510,8 +510,9 @@ PA_API int pa_beam_select(const void* logits, int64_t stride_b, int64_t stride_k
  *
  * Row b * K + i of the tables becomes child i of request b: the tokens and
  * pages of row b * K + parents[b, i].  Beams of a request share pages only at
- * the same column of their tables, and other requests' rows share none with
- * them but such as all of the request's beams hold.
+ * the same column of their tables.  No page is in the tables of two requests, a
+ * common prompt's neither: nothing counts references, so the request that ends
+ * first would give back what the other still reads and writes.
  *   - A page of a column that no child holds there goes back to the pool: pushed
  *     onto free_pages behind the first *free_count, by request, column, beam.
  *   - A child's last page that is partly filled will be written to.  Where an

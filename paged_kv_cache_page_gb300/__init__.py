@@ -506,7 +506,8 @@ def pa_beam_reorder(parents, seqlens, block_table, free_pages, free_count, page_
                     err=None):
     """Block tables, lengths and page pool after each request's beams have been replaced by their
     continuations: row ``b * K + i`` becomes row ``b * K + parents[b, i]`` (-1: dropped).  Returns
-    ``(block_table_out, seqlens_out, copies)``; ``pa_copy_pages`` then makes the ``copies``.
+    ``(block_table_out, seqlens_out, copies)``; ``pa_copy_pages`` then makes the ``copies``.  Beams of a
+    request share pages; two requests share none, not those of a common prompt either.
 
     ``parents`` int32 ``[B, K]``; ``seqlens`` int32 ``[B * K]``; ``block_table`` int32
     ``[B * K, max_pages]``; ``free_pages`` and ``free_count`` as in ``pa_plan_step``.  Outputs that
