@@ -224,7 +224,7 @@ cudaError_t allow_shared(const void* kernel, int bytes, std::atomic<uint64_t>* d
 
 bool encode_map(CUtensorMap* map, const void* base, int dtype, int D, int H, int64_t dim2,
                 int64_t dim3, int64_t stride_h, int64_t stride_t, int64_t stride_b, int box_d,
-                int box_h, int box_rows, bool swz = true, int l2_bytes = 256) {
+                int box_h, int box_rows, bool swz, int l2_bytes) {
   PFN_cuTensorMapEncodeTiled_v12000 fn = get_encode_fn();
   if (fn == nullptr) return false;
   const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)dim2, (cuuint64_t)dim3};

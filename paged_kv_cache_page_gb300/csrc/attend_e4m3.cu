@@ -48,8 +48,6 @@
 #include "attend_e4m3.cuh"
 
 namespace pa {
-int set_error(int code, const char* fmt, ...);
-
 namespace {
 
 constexpr int kWarps = 8;

@@ -35,8 +35,6 @@
 namespace cg = cooperative_groups;
 
 namespace pa {
-int set_error(int code, const char* fmt, ...);
-
 namespace {
 
 constexpr int kMaxBeams = 32;

@@ -45,8 +45,6 @@
 namespace cg = cooperative_groups;
 
 namespace pa {
-int set_error(int code, const char* fmt, ...);
-
 namespace {
 
 constexpr int kThreads = 512;      // (two CTAs of 256 an SM: 26.7 us for 21.8, 8 requests of 16 beams)

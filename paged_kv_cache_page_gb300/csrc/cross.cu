@@ -33,11 +33,6 @@
 namespace cg = cooperative_groups;
 
 namespace pa {
-int set_error(int code, const char* fmt, ...);
-bool encode_map(CUtensorMap* map, const void* base, int dtype, int D, int H, int64_t dim2,
-                int64_t dim3, int64_t stride_h, int64_t stride_t, int64_t stride_b, int box_d,
-                int box_h, int box_rows, bool swz, int l2_bytes);
-
 namespace {
 
 constexpr int kWarps = 4;

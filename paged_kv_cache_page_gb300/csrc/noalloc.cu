@@ -33,7 +33,6 @@
 
 namespace pa {
 // Records a message for pa_last_error_string() (defined in api.cu).
-int set_error(int code, const char* fmt, ...);
 }  // namespace pa
 
 namespace {

@@ -121,6 +121,8 @@ constexpr int kDecodeMaxRows = 16;
 constexpr int kDecodeMaxSchedB = 512;
 
 // Host helpers (api.cu).
+// Keeps the text of a call's error for pa_last_error_string; returns `code`.
+int set_error(int code, const char* fmt, ...);
 int num_sms();
 // Lets `kernel` use `bytes` of dynamic shared memory on the current device;
 // `devices` remembers (a bit each) where that has been done.
@@ -189,6 +191,11 @@ int resident_clusters(K kernel, const cudaLaunchConfig_t& cfg, int size,
   return n;
 }
 
+// A 4-D map of 16-bit values, in boxes of box_d columns, box_h heads and box_rows rows:
+// `swz`: with the 128-byte swizzle; l2_bytes: what L2 fetches at a time (128 or 256).
+bool encode_map(CUtensorMap* map, const void* base, int dtype, int D, int H, int64_t dim2,
+                int64_t dim3, int64_t stride_h, int64_t stride_t, int64_t stride_b, int box_d,
+                int box_h, int box_rows, bool swz = true, int l2_bytes = 256);
 bool encode_cache_map(CUtensorMap* map, const void* base, int dtype, int D, int Hkv, int64_t dim2,
                       int64_t dim3, int64_t stride_h, int64_t stride_t, int64_t stride_b,
                       int box_d, int box_rows, bool swizzle128);

@@ -30,8 +30,6 @@
 #include "pa_internal.h"
 
 namespace pa {
-int set_error(int code, const char* fmt, ...);
-
 namespace {
 
 constexpr int kMaxAxes = 4;
