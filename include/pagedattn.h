@@ -593,6 +593,7 @@ PA_API int pa_copy_pages(const int32_t* copies, int n, void* const* caches, int 
  *   workspace     pa_fwd_cross_workspace_size bytes, 256-byte aligned (NULL where
  *                 that is 0); its contents on entry do not matter.  Calls that may
  *                 overlap on the GPU need one each.
+ *   scale         positive, and finite times log2(e).
  * Rows without a key: O = 0, LSE = -inf.  Rows behind cu_seqlens_q[B] are not
  * written.  An entry with rows or keys outside q and k, or more than the bounds,
  * is reported (PA_DEVERR_LENGTH, the entry, the length): its rows that lie in q

@@ -470,8 +470,8 @@ extern "C" PA_API int pa_fwd_cross(const void* q, int64_t q_st, int64_t q_sh, co
     return set_error(PA_ERR_UNSUPPORTED, "Hq %d not a multiple of Hkv %d", Hq, Hkv);
   if (B < 0 || total_q < 0 || total_k < 0 || max_seqlen_q < 0 || max_seqlen_k < 0)
     return set_error(PA_ERR_INVALID_ARG, "negative size");
-  if (!(scale > 0.f) || !std::isfinite(scale))
-    return set_error(PA_ERR_INVALID_ARG, "scale must be positive and finite");
+  if (!(scale > 0.f) || !std::isfinite(scale * kLog2e))
+    return set_error(PA_ERR_INVALID_ARG, "scale must be positive, and finite times log2(e)");
   if (B == 0 || total_q == 0 || max_seqlen_q == 0) return PA_OK;
   if (q == nullptr || cu_seqlens_q == nullptr || cu_seqlens_k == nullptr || out == nullptr)
     return set_error(PA_ERR_INVALID_ARG, "q, cu_seqlens_q, cu_seqlens_k and out must be non-NULL");
