@@ -131,18 +131,22 @@ struct Logits {
       return fmaxf(f.x, f.y);
     }
   }
-  // The sum of the values' bits, on top of c.
+  // The sum of the values' bits but for their signs (+0 and -0 are equal), on top of c.
+  // (Of fp32 values it counts modulo 2^31.)
   static __device__ __forceinline__ uint32_t code(const uint4& v, uint32_t c) {
     if constexpr (std::is_same<T, float>::value) return c + v.x + v.y + v.z + v.w;
-    else
-      return __dp2a_lo(v.x, 0x101u, __dp2a_lo(v.y, 0x101u, __dp2a_lo(v.z, 0x101u, __dp2a_lo(v.w, 0x101u, c))));
+    else {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c = __dp2a_lo(w[i] & 0x7fff7fffu, 0x101u, c);
+      return c;
+    }
   }
   static __device__ __forceinline__ uint32_t bits(const T* p) {
     if constexpr (std::is_same<T, float>::value) return __float_as_uint(*p);
     else return *reinterpret_cast<const uint16_t*>(p);
   }
-  // Of a sum of bits those that no value's sign counts in (+0 and -0 are equal).
-  static constexpr uint32_t kCode = std::is_same<T, float>::value ? 0x7fffffffu : 0x7fffu;
+  static constexpr uint32_t kCode = std::is_same<T, float>::value ? 0x7fffffffu : 0xffffffffu;
   static __device__ __forceinline__ float one(const T* p) { return (float)*p; }
   // A first word whose first value is *p, the others -inf.
   static __device__ __forceinline__ uint32_t alone(const T* p) {
@@ -407,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) select_kernel(const Sele
   // (a lane may have thousands of steps: what its sum lacks is carried along)
   float top = neg_inf(), h = kNothing, sum = 0.f, lack = 0.f;
   // (rows that lie a multiple of 16 bytes apart are cut alike: 36.2 us without, 38.0 with codes)
-  const bool coded = p.stride_k * sizeof(T) % 16 != 0;
+  const bool coded = p.K > 1 && p.stride_k * sizeof(T) % 16 != 0;
   uint32_t code = 0;
   auto compute = [&](const uint4 (&v)[kVecs]) {
     float x_extra = neg_inf();
@@ -415,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) select_kernel(const Sele
       const int e = rows[now.r].extra(lane);
       if (e >= 0) {
         x_extra = L::one(rows[now.r].p + e);
-        code += L::bits(rows[now.r].p + e);
+        code += L::bits(rows[now.r].p + e) & (std::is_same<T, float>::value ? ~0u : 0x7fffu);
       }
     }
     top = fmaxf(top, fmaxf(L::largest(v), x_extra));
@@ -534,7 +538,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) select_kernel(const Sele
       const double lse = lane < live ? sm.lse[lane] : INFINITY;
       const uint32_t same = __match_any_sync(kAll, lane < live ? sm.code[lane] & L::kCode : ~0u);
       const double first = __shfl_sync(kAll, lse, __ffs((int)same) - 1);
-      if (isfinite(first) && fabs(lse - first) <= 0x1p-16 + fabs(first) * 0x1p-50) {
+      // (each is off by less than 2^-18)
+      if (isfinite(first) && fabs(lse - first) <= 0x1p-17 + fabs(first) * 0x1p-50) {
         sm.lse[lane] = first;
         sm.lse32[lane] = (float)first;
       }

@@ -2,9 +2,9 @@
 
 Scores.  A step of a lane adds at most 64 exponentials and an extra one in four sums, 16 deep, and these
 in two more steps: (16 + 3) 2^-24 of the sum.  What a lane's steps add up to lacks 2^-24, however many
-they are; a warp's sum 5 2^-24, and the row's parts nothing that counts.  An exponent is rounded once
-(2^-24 |t| ln 2 of a term that weighs 2^t, at most log2(V) on the mean: 17 for 2^24), 2^t is good to
-2^-22: together (19 + 1 + 5 + 17 + 4) 2^-24 < 2^-18, so of lse.  The fp32 score is off by 2^-24 of itself.
+they are; a warp's sum 5 2^-24, and the row's parts nothing that counts.  An exponent is rounded twice
+(2^-24 |t| ln 2 of a term that weighs 2^t, |t| at most log2(V) on the mean: 17 for 2^24), 2^t is good to
+2^-22: together (19 + 1 + 5 + 34 + 4) 2^-24 < 2^-18, so of lse.  The fp32 score is off by 2^-24 of itself.
 """
 
 import numpy as np
