@@ -8,11 +8,12 @@
 // a whole number n, so that sums under different references are brought
 // together by exact powers of two; log2(e) is a sum of two fp32 values, which
 // leaves one rounding of the exponent.  (Where the largest logit is beyond 2^29 an
-// fp32 n is too coarse: see Reference.)  Next to the border candidates of
-// different beams lie so close that 32 bits would often choose another one: the
-// sums of a row's parts and its logarithm (ln f = 2 atanh((f - 1) / (f + 1)))
-// are in pairs of fp32 values, the candidates' scores in 64 bits.  (FP64 is slow
-// here: log() of a double took 5500 cycles, the pairs take 700.)
+// fp32 n is too coarse: see Reference.)  The exponentials, and the 64 of a lane's step,
+// are fp32: lse is good to 2^-17, and so is the order of two beams' candidates.  Nothing
+// behind them adds to that, whatever the row's length: what a lane's steps add up to, the
+// sums of a row's parts and its logarithm (ln f = 2 atanh((f - 1) / (f + 1))) are in pairs
+// of fp32 values, the candidates' scores in 64 bits, so the order within a beam is that of
+// 64 bits.  (FP64 is slow here: log() of a double took 5500 cycles, the pairs take 700.)
 //
 // One pass over the logits, 4 KB of a warp on their way while it computes with the
 // 4 KB before.  A lane finds the maximum of its elements, then their sum.  Only the
@@ -32,9 +33,13 @@
 // order: rows of one code whose lse agree within what the sums may be off have the lse
 // of the first.
 //
-// Measured: 64 requests of 8 beams, 128000 bf16 logits: 36.0 us, 20 of them the pass
-// (6.5 TB/s), the others start, sums, bound, candidates and the join, as in 8.1 us for
-// one request of 4 beams of 32000.
+// Measured: 64 requests of 8 beams, 128000 bf16 logits: 36.5 us, 20 of them the pass
+// (6.5 TB/s), the others start, sums, bound, candidates and the join, as in 8.2 us for
+// one request of 4 beams of 32000.  16 of 5 beams of an odd number of logits 12.8 (12.1
+// without codes and pairs).  More than 32 candidates where a CTA has one unit of a row:
+// half of the parts are empty, nothing bounds the candidates, and all elements are
+// compared N times (32 beams of 32000 bf16 logits, one request: N = 32 36 us, 33 5200 us,
+// 64 10060 us).
 #include <cooperative_groups.h>
 
 #include <type_traits>
@@ -410,7 +415,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) select_kernel(const Sele
   };
   // (a lane may have thousands of steps: what its sum lacks is carried along)
   float top = neg_inf(), h = kNothing, sum = 0.f, lack = 0.f;
-  // (rows that lie a multiple of 16 bytes apart are cut alike: 36.2 us without, 38.0 with codes)
+  // (rows that lie a multiple of 16 bytes apart are cut alike; with codes even so 64 x 8
+  // beams of 128000 logits took 38.0 us instead of 36.6)
   const bool coded = p.K > 1 && p.stride_k * sizeof(T) % 16 != 0;
   uint32_t code = 0;
   auto compute = [&](const uint4 (&v)[kVecs]) {

@@ -12,8 +12,9 @@
 //
 // Bound: the tensor cores, 4 D operations a (row, key) pair, and next to them the
 // exponentials; with few rows the read of K and V.  Measured: 4 entries of 1024 rows
-// and 4096 keys, 32 heads of 128: 202 us (1.36 PFLOP/s, tensor pipe busy 58 %: a tile's
-// chain of scores, softmax and values, two of them in turn); 64 of 8 rows and 4096
+// and 4096 keys, 32 heads of 128: 202 to 206 us in a graph of a few launches (1.36 PFLOP/s, tensor
+// pipe busy 58 %: a tile's chain of scores, softmax and values, two of them in turn), 217 to
+// 225 us call by call, under the power cap (1.22 PFLOP/s); 64 of 8 rows and 4096
 // masked keys, 32/8 heads of 128: 178 us (6.1 TB/s).  One persistent CTA an SM:
 //   warps 0-7  softmax: one thread a row, group g = warp / 4 takes tile g
 //   warp 8     K and Q tiles by TMA, warp 9 V tiles (one thread for both would hold K
