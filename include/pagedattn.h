@@ -599,10 +599,10 @@ PA_API int pa_copy_pages(const int32_t* copies, int n, void* const* caches, int 
  *                 overlap on the GPU need one each.
  *   scale         positive, and finite times log2(e).
  * Sums of p v are fp32, with p up to 2^40 (bf16) or 2^15 (fp16): bf16 values of v above
- * 2^60 may overflow.  Rows without a key: O = 0, LSE = -inf.  Rows behind cu_seqlens_q[B] are not
- * written.  An entry with rows or keys outside q and k, or more than the bounds,
- * is reported (PA_DEVERR_LENGTH, the entry, the length): its rows that lie in q
- * and within max_seqlen_q have no keys then.  At most 2^30 tiles of 256 rows per
+ * 2^60 may overflow.  Rows without a key: O = 0, LSE = -inf.  Rows behind
+ * cu_seqlens_q[B] are not written.  An entry with rows or keys outside q and k, or more
+ * than the bounds, is reported (PA_DEVERR_LENGTH, the entry, the length): its rows that
+ * lie in q and within max_seqlen_q have no keys then.  At most 2^30 tiles of 256 rows per
  * kv head by 128 keys, by the bounds; more return PA_ERR_UNSUPPORTED.
  */
 PA_API int pa_fwd_cross(const void* q, int64_t q_st, int64_t q_sh, const void* k, int64_t k_st,
